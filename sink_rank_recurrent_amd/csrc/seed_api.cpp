@@ -9,6 +9,7 @@
 #include <stdio.h>
 
 #include "../../include/seed.h"
+#include "seed_error.h"
 #include "seed_launch.h"
 
 namespace {
@@ -81,6 +82,10 @@ seed_status device_status(const char* fn, hipError_t e) {
 }
 
 }  // namespace
+
+seed_status seed::set_error(seed_status status, const char* text) {
+  return fail(status, "%s", text);
+}
 
 namespace {
 

@@ -1,0 +1,54 @@
+// The recurrence over sequences: workspace layout and the order of its phases.
+#include "seed_scan.h"
+
+namespace seed {
+
+ScanLayout scan_layout(int rule, int n_seq, int heads, int key_heads, int d_k, int d_v, int tokens,
+                       bool backward) {
+  const bool kda = rule == kKDA, delta = rule != kMAMBA2;
+  const size_t slots = (size_t)(tokens / kScanChunk) + (size_t)n_seq;
+  const size_t units = slots * heads;
+  size_t at = 0;
+  auto part = [&](bool used, size_t bytes) {
+    const size_t here = at;
+    if (used) at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t pack = (size_t)6 * 3 * 512 * 2;
+  const size_t per_token = units * kScanChunk * sizeof(float);
+  const size_t per_head = (size_t)tokens * heads * d_k * sizeof(float);
+  ScanLayout l{};
+  l.n_pack = part(delta, units * pack);
+  l.nt_pack = part(delta && backward, units * pack);
+  l.m_pack = part(true, units * pack);
+  l.p = part(true, per_token * (kda ? d_k : 1));
+  l.f = part(true, per_token * (kda ? d_k : 1));
+  l.state = part(backward, units * d_k * d_v * sizeof(float));
+  l.grad = part(backward, units * d_k * d_v * sizeof(float));
+  l.e = part(backward && delta, per_token * d_v);
+  l.y = part(backward && delta, per_token * d_v);
+  l.dq = part(backward && (kda || heads != key_heads), per_head);
+  l.dk = part(backward && (kda || heads != key_heads), per_head);
+  l.tp = part(backward && kda, per_token * d_k);
+  l.tf = part(backward && kda, per_token * d_k);
+  l.bytes = at;
+  return l;
+}
+
+hipError_t launch_scan(const ScanArgs& a, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (a.tokens > 0) e = launch_scan_prep(a, false, stream);
+  if (e == hipSuccess) e = launch_scan_forward(a, false, stream);
+  return e;
+}
+
+hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (a.tokens > 0) e = launch_scan_prep(a, true, stream);
+  if (e == hipSuccess && a.tokens > 0) e = launch_scan_forward(a, true, stream);
+  if (e == hipSuccess) e = launch_scan_reverse(a, stream);
+  if (e == hipSuccess && a.tokens > 0) e = launch_scan_grads(a, stream);
+  return e;
+}
+
+}  // namespace seed
