@@ -17,9 +17,9 @@
 //                                        dL = -dR u^T (s < t).
 //
 // Arithmetic: v_mfma_f32_16x16x32_bf16 with fp32 accumulators.  An fp32
-// operand is the exact sum of three bf16 terms (its 24 significant bits cut
-// into three times 8); the products whose weight is 2^-24 or less are left
-// out, so a product of two fp32 operands takes six MFMAs, one with a bf16
+// operand is the sum of three bf16 terms, each rounding what the ones before
+// leave (2^-27 of it at last); the products whose weight is 2^-27 or less are
+// left out, so a product of two fp32 operands takes six MFMAs, one with a bf16
 // input three.
 #pragma once
 
@@ -45,17 +45,15 @@ struct Frag {
   u32x4 t[N];
 };
 
-__device__ __forceinline__ uint32_t pack_hi(float lo, float hi) {
-  // the upper halves of two floats in one word
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+// Two floats rounded to nearest bf16, in one word.
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-__device__ __forceinline__ float cut(float x) {
-  return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-}
-
-// x as N truncated bf16 terms: exact for N = 3 (and for bf16 values with
-// N = 1); N = 2 leaves at most 2^-16 of x.
+// x as N bf16 terms, each what the ones before leave, rounded to nearest:
+// N terms leave at most 2^-9N of x (nothing of a bf16 value).
 template <int N>
 __device__ __forceinline__ Frag<N> split(const float (&x)[8]) {
   Frag<N> f;
@@ -65,10 +63,13 @@ __device__ __forceinline__ Frag<N> split(const float (&x)[8]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.t[n][j] = pack_hi(r[2 * j], r[2 * j + 1]);
-    if (n + 1 < N) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] -= cut(r[j]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t p = round_pair(r[2 * j], r[2 * j + 1]);
+      f.t[n][j] = p;
+      if (n + 1 < N) {
+        r[2 * j] -= __uint_as_float(p << 16);
+        r[2 * j + 1] -= __uint_as_float(p & 0xffff0000u);
+      }
     }
   }
   return f;
@@ -139,7 +140,7 @@ __device__ __forceinline__ void load_col8(const T* __restrict__ base, size_t ld,
 
 __device__ __forceinline__ void store_scalar(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_scalar(bf16_t* p, float x) {
-  *p = (bf16_t)round_nearest16<kStoreBF16>(x);
+  *p = (bf16_t)round_pair(x, 0.f);
 }
 
 // Index of the fragment (row tile mt, contracted block ks) of a lower
@@ -202,6 +203,128 @@ __device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& a, int slot) {
   if (c < 0 || c * kC >= r.len) return {lo, 0, 0, 0};
   const int left = r.len - c * kC;
   return {lo, r.start + c * kC, left < kC ? left : kC, c};
+}
+
+// ---------------------------------------------------------------------------
+// A 64 x DK operand in LDS: one bf16 plane per term, rows of DK / 8 pieces of
+// 16 bytes.  Piece c of row t lies at c ^ swizzle(t): the 16 rows a fragment
+// reads at one c then cover all 64 banks.
+template <int DK>
+__device__ __forceinline__ int swizzle(int t) {
+  return DK == 128 ? t & 15 : (t >> 1) & 7;
+}
+template <int DK>
+__device__ __forceinline__ int piece_at(int t, int c) {   // in bytes
+  return t * (DK * 2) + ((c ^ swizzle<DK>(t)) << 4);
+}
+template <int DK>
+constexpr int kPlane = kC * DK * 2;   // bytes
+
+// The channel of row 4 g + r of state tile m.  Tiles 2 ks and 2 ks + 1 hold
+// channels 32 ks + 8 g + 0..7 in a lane, so that the state's fragments
+// contract over 16-byte pieces of K's rows.
+__device__ __forceinline__ int state_row(int m) {
+  return 32 * (m >> 1) + 8 * (lane_id() >> 4) + 4 * (m & 1);
+}
+
+// Rows 16 mt .. + 15 as a fragment, contracted over channels 32 ks .. + 31.
+template <int DK, int N>
+__device__ __forceinline__ Frag<N> lds_rows(const char* planes, int mt, int ks) {
+  const int l = lane_id(), at = piece_at<DK>(16 * mt + (l & 15), 4 * ks + (l >> 4));
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const u32x4*>(planes + n * kPlane<DK> + at);
+  return f;
+}
+
+// The transpose: state tile m's channels as rows, contracted over tokens
+// 32 ks .. + 31 in accumulator order, by transposing LDS reads (a block of
+// 16 lanes reads 4 rows of 16 values, lane i gets the 4 of column i).
+template <int DK, int N>
+__device__ __forceinline__ Frag<N> lds_cols(const char* planes, int m, int ks) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const int l = lane_id(), i = l & 15, g = l >> 4;
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 32 * ks + 16 * h + 4 * g + (i >> 2);
+      const char* at = planes + n * kPlane<DK> + piece_at<DK>(t, 4 * (m >> 1) + (i & 3)) + 8 * (m & 1);
+      const u32x2 x = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                     (__attribute__((address_space(3))) bf16x4*)(at)));
+      f.t[n][2 * h] = x[0];
+      f.t[n][2 * h + 1] = x[1];
+    }
+  return f;
+}
+
+// One fragment of a pack in LDS ([frag][term][lane][8]).
+template <int N>
+__device__ __forceinline__ Frag<N> lds_pack(const char* pack, int frag) {
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    f.t[n] = *reinterpret_cast<const u32x4*>(pack + (frag * N + n) * (kFrag * 2) + lane_id() * 16);
+  return f;
+}
+
+// Global memory to LDS without registers: 16 bytes (or 4) a lane, the LDS
+// side 64 consecutive places from `to` (the same in every lane).  Written as
+// asm because the compiler would make every later LDS read wait for it,
+// another buffer's too; the caller waits (async_wait, then a barrier).  The
+// s_nop is the wait state an LDS load needs after M0 is written.
+template <int BYTES>
+__device__ __forceinline__ void async_copy(const void* from, const char* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to);
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 ::"v"(from), "s"(at) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                 ::"v"(from), "s"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void async_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A chunk's rows of a bf16 array [tokens][heads][DK] into a plane, `waves`
+// waves together; rows from n on repeat row n - 1.
+template <int DK>
+__device__ __forceinline__ void async_rows(const bf16_t* rows, size_t ld, int n, const char* plane,
+                                           int wave, int waves) {
+  constexpr int PR = DK / 8, PER = 64 / PR;   // pieces a row, rows a step
+  for (int i = wave; i < kC / PER; i += waves) {
+    const int t = i * PER + lane_id() / PR, c = (lane_id() % PR) ^ swizzle<DK>(t);
+    async_copy<16>(rows + (size_t)(t < n ? t : n - 1) * ld + c * 8, plane + i * 1024);
+  }
+}
+
+// `frags` fragments of a pack with N of the three terms it holds.
+template <int N>
+__device__ __forceinline__ void async_pack(const uint16_t* pack, const char* to, int wave, int waves) {
+  for (int i = wave; i < kTriFrags * N; i += waves)
+    async_copy<16>(pack + (size_t)(i / N * 3 + i % N) * kFrag + lane_id() * 8, to + i * 1024);
+}
+
+// c[m] += a[m] b for MT row tiles, the tiles in turn so that consecutive
+// MFMAs do not wait for each other.
+template <int MT, int NA, int NB, int ORDER = 3>
+__device__ __forceinline__ void mma_tiles(f32x4 (&c)[MT], const Frag<NA> (&a)[MT],
+                                          const Frag<NB>& b) {
+#pragma unroll
+  for (int o = ORDER - 1; o >= 0; --o) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = o - i;
+      if (j < 0 || j >= NB) continue;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[m].t[i]),
+                                                       __builtin_bit_cast(bf16x8, b.t[j]), c[m], 0, 0, 0);
+    }
+  }
 }
 
 }  // namespace scan

@@ -1,0 +1,460 @@
+// The recurrence from chunk to chunk, and back, for bf16 inputs and scalar
+// gates (Gated DeltaNet, Mamba-2).  Columns of the state do not mix: a wave
+// owns 16 of them and carries them through a sequence's chunks in its
+// accumulators; every product's result is the next one's right operand in
+// the registers it is already in (seed_scan.h).  The left operands (K, Q, N,
+// M) are the same for all waves: they come through LDS, the next chunk's by
+// asynchronous loads while this one is computed.
+#include "seed_scan.h"
+
+namespace seed {
+namespace scan {
+namespace {
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+template <int N>
+__device__ __forceinline__ Frag<N> split_tiles(const f32x4& a, const f32x4& b) {
+  float x[8];
+  tiles_to_floats(a, b, x);
+  return split<N>(x);
+}
+
+// Rows 16 m + 4 g + r of a 64-vector in LDS.
+__device__ __forceinline__ f32x4 lds_vec(const char* vec, int m) {
+  return *reinterpret_cast<const f32x4*>(vec + 64 * m + 16 * (lane_id() >> 4));
+}
+
+// 16 columns of a bf16 array as raw accumulator tiles, rows from n on 0.
+struct RawTiles {
+  uint16_t x[4][4];
+};
+// p: the same address in every lane; `lane`: the lane's offset, 4 g rows and
+// its column.
+__device__ __forceinline__ RawTiles load_raw(const bf16_t* p, size_t ld, uint32_t lane, int n) {
+  RawTiles v;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * m + 4 * (lane_id() >> 4) + r;
+      const bf16_t* row = p + (size_t)(16 * m + r) * ld;
+      v.x[m][r] = t < n ? row[lane] : 0;
+    }
+  return v;
+}
+__device__ __forceinline__ f32x4 tile_of(const RawTiles& v, int m) {
+  f32x4 x;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = bf16_bits_to_f32(v.x[m][r]);
+  return x;
+}
+__device__ __forceinline__ void store_tiles(bf16_t* p, size_t ld, uint32_t lane, int n,
+                                            const f32x4 (&x)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * m + 4 * (lane_id() >> 4) + r;
+      bf16_t* row = p + (size_t)(16 * m + r) * ld;
+      if (t < n) store_scalar(row + lane, x[m][r]);
+    }
+}
+// The same for the fp32 arrays of the workspace (every row) and for states
+// (rows in the order of state_row; `lane` 8 g rows and the column).
+__device__ __forceinline__ void keep_tiles(float* p, int ld, uint32_t lane, const f32x4 (&x)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float* row = p + (16 * m + r) * ld;
+      row[lane] = x[m][r];
+    }
+}
+template <int IT>
+__device__ __forceinline__ void keep_state(float* p, int ld, uint32_t lane, const f32x4 (&x)[IT]) {
+#pragma unroll
+  for (int m = 0; m < IT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float* row = p + (32 * (m >> 1) + 4 * (m & 1) + r) * ld;
+      row[lane] = x[m][r];
+    }
+}
+template <int IT>
+__device__ __forceinline__ void load_state(const float* p, int ld, uint32_t lane, f32x4 (&x)[IT]) {
+#pragma unroll
+  for (int m = 0; m < IT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float* row = p ? p + (32 * (m >> 1) + 4 * (m & 1) + r) * ld : nullptr;
+      x[m][r] = p ? row[lane] : 0.f;
+    }
+}
+// Rows from n on are no tokens: their results are dropped.
+__device__ __forceinline__ void drop_rows(f32x4 (&x)[4], int n) {
+  if (n < kC) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * m + 4 * (lane_id() >> 4) + r >= n) x[m][r] = 0.f;
+  }
+}
+
+// LDS of one chunk's operands.
+template <int RULE, int DK, bool K_Q, int MT, bool HAS_M>
+struct Stage {
+  static constexpr bool DELTA = RULE != kMAMBA2;
+  static constexpr int q = kPlane<DK>;
+  static constexpr int n = q + (K_Q ? kPlane<DK> : 0);
+  static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int vec = m + (HAS_M ? kTriFrags * MT * 1024 : 0);   // P, F, beta
+  static constexpr int bytes = vec + 768;
+
+  static __device__ __forceinline__ void load(const ScanArgs& a, char* to, const bf16_t* K,
+                                              const bf16_t* Q, size_t ld, size_t unit, int rows,
+                                              bool transposed, int w, int waves) {
+    async_rows<DK>(K, ld, rows, to, w, waves);
+    if (K_Q) async_rows<DK>(Q, ld, rows, to + q, w, waves);
+    constexpr size_t pack = kTriFrags * 3 * kFrag;
+    if (DELTA)
+      async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
+                        unit * pack, to + n, w, waves);
+    if (HAS_M)
+      async_pack<MT>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w,
+                     waves);
+    for (int i = w; i < (DELTA ? 3 : 2); i += waves)
+      async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
+                        (unit * kC + lane_id()) * sizeof(float), to + vec + 256 * i);
+  }
+};
+
+// Where a workgroup's columns are: grid n_seq * heads * (d_v / (16 NW)).
+template <int NW>
+struct Place {
+  int seq, head, hk, col;
+  __device__ __forceinline__ explicit Place(const ScanArgs& a) {
+    const int blocks = a.d_v / (16 * NW);
+    const int sh = blockIdx.x / blocks;
+    seq = sh / a.heads;
+    head = sh % a.heads;
+    hk = head / (a.heads / a.key_heads);
+    col = (blockIdx.x % blocks) * 16 * NW + (threadIdx.x >> 6) * 16 + (lane_id() & 15);
+  }
+};
+
+// SAVE keeps each chunk's incoming state and E for the backward pass and
+// writes no read-outs.
+template <int RULE, int DK, int NW, bool SAVE>
+__global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
+  constexpr bool DELTA = RULE != kMAMBA2;
+  constexpr int IT = DK / 16;
+  using St = Stage<RULE, DK, !SAVE, 2, !SAVE>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int w = threadIdx.x >> 6;
+  const Place<NW> at(a);
+  const Range rg = sequence(a, at.seq);
+  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
+  const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
+  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
+  const bf16_t* K = static_cast<const bf16_t*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const bf16_t* Q = static_cast<const bf16_t*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const bf16_t* V = static_cast<const bf16_t*>(a.v) + vat;
+  bf16_t* out = static_cast<bf16_t*>(a.o) + vat;
+
+  f32x4 S[IT];
+  load_state(a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+
+  RawTiles v{};
+  if (chunks > 0) {
+    St::load(a, lds, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w, NW);
+    v = load_raw(V, vld, row_lane, min(kC, rg.len));
+    async_wait();
+    __syncthreads();
+  }
+  f32x4 O[4];
+  for (int c = 0; c < chunks; ++c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    const char* now = lds + (c & 1) * St::bytes;
+    // the chunk before's read-outs leave while this one is computed
+    if (!SAVE && c > 0) store_tiles(out + (size_t)(c - 1) * kC * vld, vld, row_lane, kC, O);
+    RawTiles next = v;
+    if (c + 1 < chunks) {
+      const int rows = min(kC, rg.len - (c + 1) * kC);
+      St::load(a, lds + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
+               Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, rows, false, w, NW);
+      next = load_raw(V + (size_t)(c + 1) * kC * vld, vld, row_lane, rows);
+    }
+    if (SAVE)
+      keep_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, a.d_v, state_lane, S);
+
+    f32x4 R[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) R[m] = O[m] = zero4();
+    if (DELTA || !SAVE) {
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        const Frag<3> s = split_tiles<3>(S[2 * ks], S[2 * ks + 1]);
+        Frag<1> f[4];
+        if (DELTA) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
+          mma_tiles(R, f, s);
+        }
+        if (!SAVE) {   // the read-outs are rounded to 2^-9: two terms of S do
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now + St::q, m, ks);
+          mma_tiles<4, 1, 3, 2>(O, f, s);
+        }
+      }
+    }
+    f32x4 u[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 p = lds_vec(now + St::vec, m);
+      u[m] = tile_of(v, m);
+      if (DELTA) u[m] -= p * R[m];
+      O[m] *= p;
+    }
+    if (DELTA) {
+      f32x4 b[4], y[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        b[m] = lds_vec(now + St::vec + 512, m);
+        y[m] = zero4();
+      }
+      const Frag<3> x0 = split_tiles<3>(b[0] * u[0], b[1] * u[1]);
+      const Frag<3> x1 = split_tiles<3>(b[2] * u[2], b[3] * u[3]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::n, lower_frag(m, 0));
+      mma_tiles(y, f, x0);
+      f32x4 z[2] = {y[2], y[3]};
+      const Frag<3> h[2] = {lds_pack<3>(now + St::n, lower_frag(2, 1)),
+                            lds_pack<3>(now + St::n, lower_frag(3, 1))};
+      mma_tiles(z, h, x1);
+      u[0] -= y[0];
+      u[1] -= y[1];
+      u[2] -= z[0];
+      u[3] -= z[1];
+      drop_rows(u, n);
+      if (SAVE)
+        keep_tiles(reinterpret_cast<float*>(a.ws + a.at.e) + unit * kC * a.d_v, a.d_v, keep_lane, u);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) u[m] *= b[m];
+    }
+    if (!SAVE) {
+      constexpr int NU = DELTA ? 2 : 1;   // V itself is one term
+      const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
+      Frag<2> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<2>(now + St::m, lower_frag(m, 0));
+      mma_tiles<4, 2, NU, 2>(O, f, x0);
+      f32x4 z[2] = {O[2], O[3]};
+      const Frag<2> h[2] = {lds_pack<2>(now + St::m, lower_frag(2, 1)),
+                            lds_pack<2>(now + St::m, lower_frag(3, 1))};
+      mma_tiles<2, 2, NU, 2>(z, h, x1);
+      O[2] = z[0];
+      O[3] = z[1];
+    }
+    // S' = P_end S + K^T (F u)
+    const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
+#pragma unroll
+    for (int m = 0; m < 4; ++m) u[m] *= lds_vec(now + St::vec + 256, m);
+#pragma unroll
+    for (int m = 0; m < IT; ++m) S[m] *= last;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const Frag<3> x = split_tiles<3>(u[2 * ks], u[2 * ks + 1]);
+      Frag<1> f[IT];
+#pragma unroll
+      for (int m = 0; m < IT; ++m) f[m] = lds_cols<DK, 1>(now, m, ks);
+      mma_tiles(S, f, x);
+    }
+    v = next;
+    async_wait();
+    __syncthreads();
+  }
+  if (!SAVE) {
+    if (chunks > 0)
+      store_tiles(out + (size_t)(chunks - 1) * kC * vld, vld, row_lane, rg.len - (chunks - 1) * kC, O);
+    keep_state(a.S + state, a.d_v, state_lane, S);
+  }
+}
+
+// The chunks from the last to the first, H the gradient of the state behind
+// the chunk.  Keeps H and (delta rules) Y, writes dV and dS0.
+template <int RULE, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
+  constexpr bool DELTA = RULE != kMAMBA2;
+  constexpr int IT = DK / 16;
+  using St = Stage<RULE, DK, true, 3, true>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int w = threadIdx.x >> 6;
+  const Place<NW> at(a);
+  const Range rg = sequence(a, at.seq);
+  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
+  const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
+  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
+  const bf16_t* K = static_cast<const bf16_t*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const bf16_t* Q = static_cast<const bf16_t*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const bf16_t* dO = static_cast<const bf16_t*>(a.dO) + vat;
+  bf16_t* dV = static_cast<bf16_t*>(a.dv) + vat;
+
+  f32x4 H[IT];
+  load_state(a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
+
+  RawTiles d{};
+  if (chunks > 0) {
+    const int c = chunks - 1, rows = rg.len - c * kC;
+    St::load(a, lds + (c & 1) * St::bytes, K + (size_t)c * kC * kld, Q + (size_t)c * kC * kld, kld,
+             (size_t)(base + c) * a.heads + at.head, rows, true, w, NW);
+    d = load_raw(dO + (size_t)c * kC * vld, vld, row_lane, rows);
+    async_wait();
+    __syncthreads();
+  }
+  for (int c = chunks - 1; c >= 0; --c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    const char* now = lds + (c & 1) * St::bytes;
+    RawTiles next = d;
+    if (c > 0) {
+      St::load(a, lds + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
+               Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w, NW);
+      next = load_raw(dO + (size_t)(c - 1) * kC * vld, vld, row_lane, kC);
+    }
+    keep_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, a.d_v, state_lane, H);
+
+    // dU = F (K H) + M^T dO
+    f32x4 y[4], go[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      y[m] = zero4();
+      go[m] = tile_of(d, m);
+    }
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) {
+      const Frag<3> h = split_tiles<3>(H[2 * ks], H[2 * ks + 1]);
+      Frag<1> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
+      mma_tiles(y, f, h);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y[m] *= lds_vec(now + St::vec + 256, m);
+    {
+      const Frag<1> x0 = split_tiles<1>(go[0], go[1]), x1 = split_tiles<1>(go[2], go[3]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::m, upper_frag(m, 1));
+      mma_tiles(y, f, x1);
+      f32x4 z[2] = {y[0], y[1]};
+      const Frag<3> h[2] = {lds_pack<3>(now + St::m, upper_frag(0, 0)),
+                            lds_pack<3>(now + St::m, upper_frag(1, 0))};
+      mma_tiles(z, h, x0);
+      y[0] = z[0];
+      y[1] = z[1];
+    }
+    if (DELTA) {
+      f32x4 b[4], t[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        b[m] = lds_vec(now + St::vec + 512, m);
+        t[m] = zero4();
+      }
+      const Frag<3> x0 = split_tiles<3>(b[0] * y[0], b[1] * y[1]);
+      const Frag<3> x1 = split_tiles<3>(b[2] * y[2], b[3] * y[3]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::n, upper_frag(m, 1));
+      mma_tiles(t, f, x1);
+      f32x4 z[2] = {t[0], t[1]};
+      const Frag<3> h[2] = {lds_pack<3>(now + St::n, upper_frag(0, 0)),
+                            lds_pack<3>(now + St::n, upper_frag(1, 0))};
+      mma_tiles(z, h, x0);
+      y[0] -= z[0];
+      y[1] -= z[1];
+      y[2] -= t[2];
+      y[3] -= t[3];
+      drop_rows(y, n);
+      keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[m] *= b[m];
+    }
+    store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+
+    // dS = P_end H + Q^T (P dO) - K^T (P dR)
+    const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 p = lds_vec(now + St::vec, m);
+      go[m] *= p;
+      y[m] *= -p;
+    }
+#pragma unroll
+    for (int m = 0; m < IT; ++m) H[m] *= last;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const Frag<3> x = split_tiles<3>(go[2 * ks], go[2 * ks + 1]);
+      Frag<1> f[IT];
+#pragma unroll
+      for (int m = 0; m < IT; ++m) f[m] = lds_cols<DK, 1>(now + St::q, m, ks);
+      mma_tiles(H, f, x);
+      if (DELTA) {
+        const Frag<3> z = split_tiles<3>(y[2 * ks], y[2 * ks + 1]);
+#pragma unroll
+        for (int m = 0; m < IT; ++m) f[m] = lds_cols<DK, 1>(now, m, ks);
+        mma_tiles(H, f, z);
+      }
+    }
+    d = next;
+    async_wait();
+    __syncthreads();
+  }
+  if (a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
+}
+
+template <typename F>
+hipError_t launch(F kernel, const ScanArgs& a, int waves, size_t lds, hipStream_t stream) {
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  const size_t grid = (size_t)a.n_seq * a.heads * (a.d_v / (16 * waves));
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * waves), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <int RULE, int DK, int NW>
+hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
+  if (what == 0)
+    return launch(chain_forward_kernel<RULE, DK, NW, false>, a, NW,
+                  2 * Stage<RULE, DK, true, 2, true>::bytes, stream);
+  if (what == 1)
+    return launch(chain_forward_kernel<RULE, DK, NW, true>, a, NW,
+                  2 * Stage<RULE, DK, false, 2, false>::bytes, stream);
+  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, true>::bytes,
+                stream);
+}
+template <int RULE>
+hipError_t chain_shape(const ScanArgs& a, int what, hipStream_t stream) {
+  if (a.d_k == 64) return chain<RULE, 64, 4>(a, what, stream);
+  return a.d_v == 128 ? chain<RULE, 128, 8>(a, what, stream) : chain<RULE, 128, 4>(a, what, stream);
+}
+
+}  // namespace
+}  // namespace scan
+
+hipError_t launch_scan_chain(const ScanArgs& a, int what, hipStream_t stream) {
+  return a.rule == kGDN ? scan::chain_shape<kGDN>(a, what, stream)
+                        : scan::chain_shape<kMAMBA2>(a, what, stream);
+}
+
+}  // namespace seed

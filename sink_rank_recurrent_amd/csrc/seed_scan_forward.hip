@@ -373,9 +373,11 @@ hipError_t chain_any(const ScanArgs& a, int what, hipStream_t stream) {
 }  // namespace scan
 
 hipError_t launch_scan_forward(const ScanArgs& a, bool save, hipStream_t stream) {
+  if (a.bf16 && a.rule != kKDA) return launch_scan_chain(a, save ? 1 : 0, stream);
   return scan::chain_any(a, save ? 1 : 0, stream);
 }
 hipError_t launch_scan_reverse(const ScanArgs& a, hipStream_t stream) {
+  if (a.bf16 && a.rule != kKDA) return launch_scan_chain(a, 2, stream);
   return scan::chain_any(a, 2, stream);
 }
 

@@ -81,7 +81,10 @@ __global__ __launch_bounds__(64) void prep_scalar_kernel(ScanArgs a) {
   }
   reinterpret_cast<float*>(a.ws + a.at.p)[unit * kC + l] = p;
   reinterpret_cast<float*>(a.ws + a.at.f)[unit * kC + l] = cur;
-  if (RULE != kMAMBA2) bt[l] = l < ch.n ? a.beta[gate] : 0.f;
+  if (RULE != kMAMBA2) {
+    bt[l] = l < ch.n ? a.beta[gate] : 0.f;
+    reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + l] = bt[l];
+  }
   __syncthreads();
 
   if (RULE != kMAMBA2) {
@@ -164,8 +167,10 @@ __global__ __launch_bounds__(256) void prep_kda_kernel(ScanArgs a) {
     kk[t * LR + i] = live ? load_scalar(K + (size_t)t * a.key_heads * DK + i) : 0.f;
     qq[t * LR + i] = live ? load_scalar(Q + (size_t)t * a.key_heads * DK + i) : 0.f;
   }
-  if (tid < kC)
+  if (tid < kC) {
     bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
+    reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + tid] = bt[tid];
+  }
   __syncthreads();
 
   float* P = reinterpret_cast<float*>(a.ws + a.at.p) + unit * kC * DK;

@@ -19,6 +19,7 @@ struct ScanLayout {
   size_t nt_pack;    // N^T
   size_t m_pack;     // M (forward) or M^T (backward)
   size_t p, f;       // P, F: one float a token, d_k for KDA
+  size_t b;          // beta: one float a token, 0 behind the sequence's end
   size_t state;      // S before each chunk (backward)
   size_t grad;       // H behind each chunk (backward)
   size_t e, y;       // E, Y: d_v floats a token (backward, delta rules)
@@ -58,6 +59,8 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t stream);
 // Phases of the recurrence (seed_scan_*.hip).
 hipError_t launch_scan_prep(const ScanArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_scan_forward(const ScanArgs& a, bool save, hipStream_t stream);
+// The same for bf16 inputs and scalar gates, whose keys need one term.
+hipError_t launch_scan_chain(const ScanArgs& a, int what, hipStream_t stream);
 hipError_t launch_scan_reverse(const ScanArgs& a, hipStream_t stream);
 hipError_t launch_scan_grads(const ScanArgs& a, hipStream_t stream);
 
