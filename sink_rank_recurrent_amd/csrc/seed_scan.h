@@ -192,11 +192,15 @@ struct Chunk {
   int seq, tok, n, index;
 };
 __device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& a, int slot) {
-  int lo = 0, hi = a.n_seq - 1;   // the last sequence whose base is <= slot
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (slot_base(sequence(a, mid), mid) <= slot) lo = mid;
-    else hi = mid - 1;
+  // the last sequence whose base is <= slot: a wave tries 64 at a time
+  int lo = 0, span = a.n_seq;
+  while (span > 1) {
+    const int step = (span + 63) >> 6;
+    const int i = lo + lane_id() * step;
+    const bool at = lane_id() * step < span && slot_base(sequence(a, i), i) <= slot;
+    const int last = 63 - __builtin_clzll(__ballot(at) | 1);
+    lo += last * step;
+    span = min(step, span - last * step);
   }
   const Range r = sequence(a, lo);
   const int c = slot - slot_base(r, lo);

@@ -5,6 +5,13 @@
 // the registers it is already in (seed_scan.h).  The left operands (K, Q, N,
 // M) are the same for all waves: they come through LDS, the next chunk's by
 // asynchronous loads while this one is computed.
+//
+// Terms: what is added to the state takes all three terms of F u.  Forward,
+// K S and N (beta R) only correct u and take two (at most 2^-18 of an
+// operand's value is left out, its sign at random: the states stay within
+// 1e-6), as do the read-outs' products, which are rounded to 2^-9 after all.
+// The backward pass keeps three throughout: dbeta and dg are inner products
+// of these results and would lose digits (1.1e-6 instead of 3e-7).
 #include "seed_scan.h"
 
 namespace seed {
@@ -33,6 +40,16 @@ struct RawTiles {
 // its column.
 __device__ __forceinline__ RawTiles load_raw(const bf16_t* p, size_t ld, uint32_t lane, int n) {
   RawTiles v;
+  if (n >= kC) {   // a whole chunk: no row to test
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bf16_t* row = p + (size_t)(16 * m + r) * ld;
+        v.x[m][r] = row[lane];
+      }
+    return v;
+  }
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -103,12 +120,12 @@ __device__ __forceinline__ void drop_rows(f32x4 (&x)[4], int n) {
 }
 
 // LDS of one chunk's operands.
-template <int RULE, int DK, bool K_Q, int MT, bool HAS_M>
+template <int RULE, int DK, bool K_Q, int NT, int MT, bool HAS_M>
 struct Stage {
   static constexpr bool DELTA = RULE != kMAMBA2;
   static constexpr int q = kPlane<DK>;
   static constexpr int n = q + (K_Q ? kPlane<DK> : 0);
-  static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int m = n + (DELTA ? kTriFrags * NT * 1024 : 0);
   static constexpr int vec = m + (HAS_M ? kTriFrags * MT * 1024 : 0);   // P, F, beta
   static constexpr int bytes = vec + 768;
 
@@ -119,7 +136,7 @@ struct Stage {
     if (K_Q) async_rows<DK>(Q, ld, rows, to + q, w, waves);
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
+      async_pack<NT>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
                         unit * pack, to + n, w, waves);
     if (HAS_M)
       async_pack<MT>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w,
@@ -149,8 +166,8 @@ struct Place {
 template <int RULE, int DK, int NW, bool SAVE>
 __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
   constexpr bool DELTA = RULE != kMAMBA2;
-  constexpr int IT = DK / 16;
-  using St = Stage<RULE, DK, !SAVE, 2, !SAVE>;
+  constexpr int IT = DK / 16, NT = SAVE ? 3 : 2;   // terms of the corrections
+  using St = Stage<RULE, DK, !SAVE, NT, 2, !SAVE>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = threadIdx.x >> 6;
   const Place<NW> at(a);
@@ -199,17 +216,17 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     if (DELTA || !SAVE) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        const Frag<3> s = split_tiles<3>(S[2 * ks], S[2 * ks + 1]);
+        const Frag<NT> s = split_tiles<NT>(S[2 * ks], S[2 * ks + 1]);
         Frag<1> f[4];
         if (DELTA) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
-          mma_tiles(R, f, s);
+          mma_tiles<4, 1, NT, NT>(R, f, s);
         }
-        if (!SAVE) {   // the read-outs are rounded to 2^-9: two terms of S do
+        if (!SAVE) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now + St::q, m, ks);
-          mma_tiles<4, 1, 3, 2>(O, f, s);
+          mma_tiles<4, 1, NT, 2>(O, f, s);
         }
       }
     }
@@ -228,16 +245,16 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
         b[m] = lds_vec(now + St::vec + 512, m);
         y[m] = zero4();
       }
-      const Frag<3> x0 = split_tiles<3>(b[0] * u[0], b[1] * u[1]);
-      const Frag<3> x1 = split_tiles<3>(b[2] * u[2], b[3] * u[3]);
-      Frag<3> f[4];
+      const Frag<NT> x0 = split_tiles<NT>(b[0] * u[0], b[1] * u[1]);
+      const Frag<NT> x1 = split_tiles<NT>(b[2] * u[2], b[3] * u[3]);
+      Frag<NT> f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::n, lower_frag(m, 0));
-      mma_tiles(y, f, x0);
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NT>(now + St::n, lower_frag(m, 0));
+      mma_tiles<4, NT, NT, NT>(y, f, x0);
       f32x4 z[2] = {y[2], y[3]};
-      const Frag<3> h[2] = {lds_pack<3>(now + St::n, lower_frag(2, 1)),
-                            lds_pack<3>(now + St::n, lower_frag(3, 1))};
-      mma_tiles(z, h, x1);
+      const Frag<NT> h[2] = {lds_pack<NT>(now + St::n, lower_frag(2, 1)),
+                            lds_pack<NT>(now + St::n, lower_frag(3, 1))};
+      mma_tiles<2, NT, NT, NT>(z, h, x1);
       u[0] -= y[0];
       u[1] -= y[1];
       u[2] -= z[0];
@@ -293,7 +310,7 @@ template <int RULE, int DK, int NW>
 __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   constexpr bool DELTA = RULE != kMAMBA2;
   constexpr int IT = DK / 16;
-  using St = Stage<RULE, DK, true, 3, true>;
+  using St = Stage<RULE, DK, true, 3, 3, true>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = threadIdx.x >> 6;
   const Place<NW> at(a);
@@ -436,11 +453,11 @@ template <int RULE, int DK, int NW>
 hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
   if (what == 0)
     return launch(chain_forward_kernel<RULE, DK, NW, false>, a, NW,
-                  2 * Stage<RULE, DK, true, 2, true>::bytes, stream);
+                  2 * Stage<RULE, DK, true, 2, 2, true>::bytes, stream);
   if (what == 1)
     return launch(chain_forward_kernel<RULE, DK, NW, true>, a, NW,
-                  2 * Stage<RULE, DK, false, 2, false>::bytes, stream);
-  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, true>::bytes,
+                  2 * Stage<RULE, DK, false, 3, 2, false>::bytes, stream);
+  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, 3, true>::bytes,
                 stream);
 }
 template <int RULE>

@@ -6,134 +6,267 @@ namespace seed {
 namespace scan {
 namespace {
 
-constexpr int kLd = kC + 1;   // LDS rows, padded against bank conflicts
+constexpr int kRow = kC + 4;   // LDS rows of 16-byte vectors, off the banks' stride
 
-// N = (I + L beta)^-1 L in place of L: row t is L_t - sum_{s<t} L_ts beta_s N_s.
-// Lane c holds column c of beta N; one wave.
-__device__ __forceinline__ void solve(float* Lm, const float* beta) {
-  const int c = lane_id();
-  float m[kC];
+// A 16 x 16 x 16 product in fp32: a's rows from LDS, b an accumulator tile.
+__device__ __forceinline__ void mma_f32(f32x4& c, const f32x4& a, const f32x4& b) {
 #pragma unroll
-  for (int t = 0; t < kC; ++t) {
-    float x = Lm[t * kLd + c];
-#pragma unroll
-    for (int s = 0; s < t; ++s) x -= Lm[t * kLd + s] * m[s];
-    m[t] = beta[t] * x;
-    Lm[t * kLd + c] = x;
-  }
+  for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
 }
 
-// The triangle of an LDS matrix as a pack (upper: of its transpose).
+// N = (I + L beta)^-1 L in place of L [64][kRow], by blocks of 16:
+//   N_ic = X_ii (L_ic - sum over c <= j < i of L_ij beta_j N_jc),
+// X_ii = (I + L_ii beta_i)^-1 by substitution.  Wave w inverts block w, then
+// takes column w of blocks, its tiles staying in registers as the next
+// product's right operand.  X: [4][16][20].
+__device__ __forceinline__ void solve(float* L, float* X, const float* beta, int w) {
+  const int l = lane_id(), l16 = l & 15, g = l >> 4;
+  if (l < 16) {   // lane c: column c of X_ww
+    float x[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      float v = t == l ? 1.f : 0.f;
+#pragma unroll
+      for (int s = 0; s < t; ++s) v -= L[(16 * w + t) * kRow + 16 * w + s] * x[s];
+      X[(w * 16 + t) * 20 + l] = v;
+      x[t] = v * beta[16 * w + t];
+    }
+  }
+  __syncthreads();
+  f32x4 N[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    N[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (i < w) continue;
+    f32x4 acc;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = L[(16 * i + 4 * g + r) * kRow + 16 * w + l16];
+#pragma unroll
+    for (int j = 0; j < i; ++j) {
+      if (j < w) continue;
+      const f32x4 a = *reinterpret_cast<const f32x4*>(L + (16 * i + l16) * kRow + 16 * j + 4 * g);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(beta + 16 * j + 4 * g);
+      mma_f32(acc, -(a * b), N[j]);
+    }
+    mma_f32(N[i], *reinterpret_cast<const f32x4*>(X + (i * 16 + l16) * 20 + 4 * g), acc);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) L[(16 * i + 4 * g + r) * kRow + 16 * w + l16] = N[i][r];
+  __syncthreads();
+}
+
+// The triangle of an LDS matrix as a pack (transposed: of its transpose).
 __device__ __forceinline__ void pack_triangle(uint16_t* __restrict__ pack, const float* mat,
                                               bool transposed, int mt, int ks) {
   const int frag = transposed ? upper_frag(mt, ks) : lower_frag(mt, ks);
   if (frag < 0) return;
   const int row = 16 * mt + (lane_id() & 15), g = lane_id() >> 4;
   float x[8];
+  if (transposed) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int col = 32 * ks + 16 * (j >> 2) + 4 * g + (j & 3);
-    x[j] = transposed ? mat[col * kLd + row] : mat[row * kLd + col];
+    for (int j = 0; j < 8; ++j) x[j] = mat[(32 * ks + 16 * (j >> 2) + 4 * g + (j & 3)) * kRow + row];
+  } else {
+    tiles_to_floats(*reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 4 * g),
+                    *reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 16 + 4 * g), x);
   }
   store_pack(pack, frag, split<3>(x));
 }
 
-// One 16 x 16 tile A B^T of rows of two row-major arrays, DK long.
-template <int DK, int NT, typename T>
-__device__ __forceinline__ f32x4 row_product(const T* __restrict__ a, const T* __restrict__ b,
-                                             size_t ld, int ta, int tb, int n) {
-  const int r = lane_id() & 15;
-  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+// Half a fragment (slots 4 h .. 4 h + 3): one accumulator tile of the
+// transposed product.
+__device__ __forceinline__ void store_half(uint16_t* __restrict__ pack, int frag, int h,
+                                           const f32x4& c) {
+  const float x[8] = {c[0], c[1], c[2], c[3], 0.f, 0.f, 0.f, 0.f};
+  const Frag<3> f = split<3>(x);
 #pragma unroll
-  for (int ks = 0; ks < DK / 32; ++ks) {
-    float x[8], y[8];
-    load_row8(a + (size_t)(16 * ta + r) * ld, 32 * ks, 16 * ta + r < n, x);
-    load_row8(b + (size_t)(16 * tb + r) * ld, 32 * ks, 16 * tb + r < n, y);
-    mma(c, split<NT>(x), split<NT>(y));
-  }
-  return c;
+  for (int n = 0; n < 3; ++n)
+    *reinterpret_cast<uint2*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8 + 4 * h) =
+        make_uint2(f.t[n][0], f.t[n][1]);
 }
 
+// Eight channels from col0 + 8 g of a row.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* __restrict__ row, int col0, bool live,
+                                           float (&x)[8]) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 0.f;
+  if (live) {
+    float a[4], b[4];
+    load_vec<4>(row + col0 + 8 * g, a);
+    load_vec<4>(row + col0 + 8 * g + 4, b);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = a[r];
+      x[4 + r] = b[r];
+    }
+  }
+}
+
+// Decay factors of a chunk for scalar gates, for pairs in different blocks
+// of 16: G_ts = pre[t] mid[block t][block s] suf[s], pre from t's block's
+// start through t, suf behind s to its block's end; within a block, G_ts is
+// multiplied up (inside).
+struct __attribute__((aligned(16))) Decay {
+  float gate[kC + 4], pre[kC], suf[kC], mid[16];   // gate: read 3 past a block
+};
+// The decay behind s through t of one block, and (rows: along t, else along
+// s) of the three tokens that follow it in a lane.
+template <bool ROWS>
+__device__ __forceinline__ f32x4 inside(const float* gate, int t, int s) {
+  const float* g = gate + (t & ~15);
+  t &= 15;
+  s &= 15;
+  const int last = ROWS ? s : s + 3;   // the pair with the shortest stretch
+  float x = 1.f;
+#pragma unroll
+  for (int o = 1; o < 16; ++o) {
+    const float y = g[o];
+    x *= o > last && o <= t ? y : 1.f;
+  }
+  f32x4 out;
+  if (ROWS) {
+    out[0] = x;
+#pragma unroll
+    for (int r = 1; r < 4; ++r) {
+      const float y = g[t + r];
+      out[r] = out[r - 1] * (t + r > s ? y : 1.f);
+    }
+  } else {
+    out[3] = x;
+#pragma unroll
+    for (int r = 2; r >= 0; --r) {
+      const float y = g[s + r + 1];
+      out[r] = out[r + 1] * (s + r < t ? y : 1.f);
+    }
+  }
+  return out;
+}
+// One wave; lane l holds gate l.  P and F of token l come back.
+__device__ __forceinline__ void decays(Decay& d, float gate, float& P, float& F) {
+  const int l = lane_id(), l16 = l & 15;
+  float p = gate, s = gate;
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) {
+    const float x = __shfl_up(p, o), y = __shfl_down(s, o);
+    p *= l16 >= o ? x : 1.f;
+    s *= l16 + o < 16 ? y : 1.f;
+  }
+  const float next = __shfl_down(s, 1);
+  s = l16 == 15 ? 1.f : next;   // behind l only
+  const float t0 = __shfl(p, 15), t1 = __shfl(p, 31), t2 = __shfl(p, 47), t3 = __shfl(p, 63);
+  d.gate[l] = gate;
+  d.pre[l] = p;
+  d.suf[l] = s;
+  if (l < 16) {
+    const int a = l >> 2, b = l & 3;   // blocks between b and a
+    d.mid[l] = (b < 1 && a > 1 ? t1 : 1.f) * (b < 2 && a > 2 ? t2 : 1.f);
+  }
+  const int blk = l >> 4;
+  P = p * (blk > 0 ? t0 : 1.f) * (blk > 1 ? t1 : 1.f) * (blk > 2 ? t2 : 1.f);
+  F = s * (blk < 1 ? t1 : 1.f) * (blk < 2 ? t2 : 1.f) * (blk < 3 ? t3 : 1.f);
+}
+
+// Four waves a (chunk, head); wave a has the tokens 16 a .. + 15 as rows.
 template <int RULE, int DK, typename T, bool BWD>
-__global__ __launch_bounds__(64) void prep_scalar_kernel(ScanArgs a) {
+__global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   constexpr int NT = sizeof(T) == 2 ? 1 : 3;
-  __shared__ float G[kC * kLd];
-  __shared__ float Lm[kC * kLd];
-  __shared__ float bt[kC];
+  constexpr bool DELTA = RULE != kMAMBA2;
+  __shared__ __attribute__((aligned(16))) float L[DELTA ? kC * kRow : 4];
+  __shared__ __attribute__((aligned(16))) float X[DELTA ? 64 * 20 : 4];
+  __shared__ __attribute__((aligned(16))) float bt[kC];
+  __shared__ __attribute__((aligned(16))) uint16_t kl[4 * (DK / 32) * NT * kFrag];   // K's fragments
+  __shared__ Decay dec;
   const Chunk ch = chunk_of_slot(a, blockIdx.x);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, l = threadIdx.x, g16 = l >> 4, l16 = l & 15;
+  const int head = blockIdx.y, w = threadIdx.x >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
   const size_t unit = (size_t)blockIdx.x * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t ld = (size_t)a.key_heads * DK;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
-  const size_t gate = ((size_t)ch.tok + l) * a.heads + head;
+  uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
 
-  // the decays: lane s multiplies its own column G_.s downwards
-  const float gl = l < ch.n ? a.g[gate] : 1.f;
-  float cur = 1.f, p = 1.f;
-  for (int t = 0; t < kC; ++t) {
-    const float gt = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gl), t));
-    cur = t > l ? cur * gt : 1.f;
-    p = t <= l ? p * gt : p;
-    G[t * kLd + l] = t >= l ? cur : 0.f;
+  // the wave's rows of K and Q
+  const int t0 = 16 * w + l16;
+  Frag<NT> kt[DK / 32], qt[DK / 32];
+#pragma unroll
+  for (int ks = 0; ks < DK / 32; ++ks) {
+    float x[8];
+    load_piece(K + (size_t)t0 * ld, 32 * ks, t0 < ch.n, x);
+    kt[ks] = split<NT>(x);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<u32x4*>(kl + (((w * (DK / 32) + ks) * NT + n) * 64 + l) * 8) = kt[ks].t[n];
+    load_piece(Q + (size_t)t0 * ld, 32 * ks, t0 < ch.n, x);
+    qt[ks] = split<NT>(x);
   }
-  reinterpret_cast<float*>(a.ws + a.at.p)[unit * kC + l] = p;
-  reinterpret_cast<float*>(a.ws + a.at.f)[unit * kC + l] = cur;
-  if (RULE != kMAMBA2) {
-    bt[l] = l < ch.n ? a.beta[gate] : 0.f;
-    reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + l] = bt[l];
+  if (w == 0) {
+    const size_t gate = ((size_t)ch.tok + l) * a.heads + head;
+    float P, F;
+    decays(dec, l < ch.n ? a.g[gate] : 1.f, P, F);
+    reinterpret_cast<float*>(a.ws + a.at.p)[unit * kC + l] = P;
+    reinterpret_cast<float*>(a.ws + a.at.f)[unit * kC + l] = F;
+    if (DELTA) {
+      bt[l] = l < ch.n ? a.beta[gate] : 0.f;
+      reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + l] = bt[l];
+    }
   }
   __syncthreads();
 
-  if (RULE != kMAMBA2) {
-    for (int ta = 0; ta < 4; ++ta) {
-      for (int tb = 0; tb < 4; ++tb) {
-        const int t = 16 * ta + l16;
-        f32x4 c = {0.f, 0.f, 0.f, 0.f};
-        if (tb <= ta) c = row_product<DK, NT>(K, K, ld, tb, ta, ch.n);
+  for (int b = 0; b < 4; ++b) {
+    // lane (t, s): its row of the right operand and four rows of the left;
+    // backward the left operand is Q, and M's tile comes out transposed
+    f32x4 ll = {0.f, 0.f, 0.f, 0.f}, mm = ll;
+    if (b <= w) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int s = 16 * tb + 4 * g16 + r;
-          Lm[t * kLd + s] = s < t ? c[r] * G[t * kLd + s] : 0.f;
-        }
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        Frag<NT> kb;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          kb.t[n] = *reinterpret_cast<const u32x4*>(kl + (((b * (DK / 32) + ks) * NT + n) * 64 + l) * 8);
+        if (DELTA) mma(ll, kb, kt[ks]);
+        if (BWD) mma(mm, qt[ks], kb);
+        else mma(mm, kb, qt[ks]);
       }
     }
+    f32x4 gl = {0.f, 0.f, 0.f, 0.f}, gm = gl;
+    const int t = 16 * w + l16, s = 16 * b + 4 * g16;        // L, and M forward
+    const int tm = 16 * w + 4 * g16, sm = 16 * b + l16;      // M backward
+    if (b < w) {
+      const float mid = dec.mid[4 * w + b];
+      gl = *reinterpret_cast<const f32x4*>(dec.suf + s) * (dec.pre[t] * mid);
+      gm = BWD ? *reinterpret_cast<const f32x4*>(dec.pre + tm) * (dec.suf[sm] * mid) : gl;
+    } else if (b == w) {
+      gl = inside<false>(dec.gate, t, s);
+      gm = BWD ? inside<true>(dec.gate, tm, sm) : gl;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        gm[r] = (BWD ? sm <= tm + r : s + r <= t) ? gm[r] : 0.f;
+        gl[r] = s + r < t ? gl[r] : 0.f;
+      }
+    }
+    if (DELTA) *reinterpret_cast<f32x4*>(L + (16 * w + l16) * kRow + 16 * b + 4 * g16) = ll * gl;
+    mm *= gm;
+    if (BWD) {
+      // rows s of tile b, tokens of tile w; a block's zero half is written too
+      if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
+    } else {
+      if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
+    }
+  }
+  if (DELTA) {
     __syncthreads();
-    solve(Lm, bt);
-    __syncthreads();
+    solve(L, X, bt, w);
     uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-    for (int i = 0; i < 8; ++i) pack_triangle(np, Lm, false, i >> 1, i & 1);
+    for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
     if (BWD) {
       uint16_t* tp =
           reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
-      for (int i = 0; i < 8; ++i) pack_triangle(tp, Lm, true, i >> 1, i & 1);
-    }
-    __syncthreads();
-  }
-
-  // M (or M^T), already in fragment order as the product K Q^T (Q K^T)
-  uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
-  for (int mt = 0; mt < 4; ++mt) {
-    for (int ks = 0; ks < 2; ++ks) {
-      const int frag = BWD ? upper_frag(mt, ks) : lower_frag(mt, ks);
-      if (frag < 0) continue;
-      float x[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kt = 2 * ks + h;
-        f32x4 c = {0.f, 0.f, 0.f, 0.f};
-        if (BWD ? kt >= mt : kt <= mt)
-          c = BWD ? row_product<DK, NT>(Q, K, ld, kt, mt, ch.n)
-                  : row_product<DK, NT>(K, Q, ld, kt, mt, ch.n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * mt + l16, col = 16 * kt + 4 * g16 + r;
-          x[4 * h + r] = c[r] * (BWD ? G[col * kLd + row] : G[row * kLd + col]);
-        }
-      }
-      store_pack(mp, frag, split<3>(x));
+      for (int i = w; i < 8; i += 4) pack_triangle(tp, L, true, i >> 1, i & 1);
     }
   }
 }
@@ -148,9 +281,10 @@ __global__ __launch_bounds__(256) void prep_kda_kernel(ScanArgs a) {
   float* gs = lds;                 // [64][DK + 1]
   float* kk = gs + kC * LR;
   float* qq = kk + kC * LR;
-  float* Lm = qq + kC * LR;        // [64][65]
-  float* Mm = Lm + kC * kLd;
-  float* bt = Mm + kC * kLd;
+  float* Lm = qq + ((kC * LR + 3) & ~3);   // [64][kRow]
+  float* Mm = Lm + kC * kRow;
+  float* bt = Mm + kC * kRow;
+  float* X = bt + kC;                      // [4][16][20]
   const Chunk ch = chunk_of_slot(a, blockIdx.x);
   if (ch.n == 0) return;
   const int head = blockIdx.y, tid = threadIdx.x, l = tid & 63, w = tid >> 6;
@@ -206,14 +340,13 @@ __global__ __launch_bounds__(256) void prep_kda_kernel(ScanArgs a) {
 #pragma unroll
       for (int t = 0; t < kC; ++t) {
         const float x = t > l ? accL[t] : 0.f, y = accM[t];
-        Lm[t * kLd + l] = turn == 0 ? x : Lm[t * kLd + l] + x;
-        Mm[t * kLd + l] = turn == 0 ? y : Mm[t * kLd + l] + y;
+        Lm[t * kRow + l] = turn == 0 ? x : Lm[t * kRow + l] + x;
+        Mm[t * kRow + l] = turn == 0 ? y : Mm[t * kRow + l] + y;
       }
     }
     __syncthreads();
   }
-  if (w == 0) solve(Lm, bt);
-  __syncthreads();
+  solve(Lm, X, bt, w);
   uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
   uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
   for (int i = w; i < 8; i += 4) {
@@ -231,15 +364,15 @@ template <int DK, typename T, bool BWD>
 hipError_t prep(const ScanArgs& a, hipStream_t stream) {
   const dim3 grid(a.slots, a.heads);
   if (a.rule == kKDA) {
-    const size_t lds = (3 * kC * (DK + 1) + 2 * kC * kLd + kC) * sizeof(float);
+    const size_t lds = (3 * kC * (DK + 1) + 2 * kC * kRow + kC + 64 * 20) * sizeof(float);
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prep_kda_kernel<DK, T, BWD>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((prep_kda_kernel<DK, T, BWD>), grid, dim3(256), lds, stream, a);
   } else if (a.rule == kGDN) {
-    hipLaunchKernelGGL((prep_scalar_kernel<kGDN, DK, T, BWD>), grid, dim3(64), 0, stream, a);
+    hipLaunchKernelGGL((prep_scalar_kernel<kGDN, DK, T, BWD>), grid, dim3(256), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((prep_scalar_kernel<kMAMBA2, DK, T, BWD>), grid, dim3(64), 0, stream, a);
+    hipLaunchKernelGGL((prep_scalar_kernel<kMAMBA2, DK, T, BWD>), grid, dim3(256), 0, stream, a);
   }
   return hipGetLastError();
 }
