@@ -35,6 +35,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kC = kScanChunk;
 constexpr int kFrag = 512;        // bf16 values of one 16 x 32 operand fragment
+constexpr int kRow = kC + 4;      // fp32 LDS rows of 64: 16-byte vectors, off the banks' stride
 constexpr int kTriFrags = 6;      // fragments of a 64 x 64 triangle
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
@@ -265,6 +266,28 @@ __device__ __forceinline__ Frag<N> lds_cols(const char* planes, int m, int ks) {
   return f;
 }
 
+// The transpose with the channels 16 m .. + 15 in their own order.
+template <int DK, int N>
+__device__ __forceinline__ Frag<N> lds_channels(const char* planes, int m, int ks) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const int l = lane_id(), i = l & 15, g = l >> 4;
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 32 * ks + 16 * h + 4 * g + (i >> 2);
+      const char* at = planes + n * kPlane<DK> + piece_at<DK>(t, 2 * m + ((i & 3) >> 1)) + 8 * (i & 1);
+      const u32x2 x = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                     (__attribute__((address_space(3))) bf16x4*)(at)));
+      f.t[n][2 * h] = x[0];
+      f.t[n][2 * h + 1] = x[1];
+    }
+  return f;
+}
+
 // One fragment of a pack in LDS ([frag][term][lane][8]).
 template <int N>
 __device__ __forceinline__ Frag<N> lds_pack(const char* pack, int frag) {
@@ -310,6 +333,89 @@ template <int N>
 __device__ __forceinline__ void async_pack(const uint16_t* pack, const char* to, int wave, int waves) {
   for (int i = wave; i < kTriFrags * N; i += waves)
     async_copy<16>(pack + (size_t)(i / N * 3 + i % N) * kFrag + lane_id() * 8, to + i * 1024);
+}
+
+// Eight channels from col0 + 8 g of a row.
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* __restrict__ row, int col0, bool live,
+                                           float (&x)[8]) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 0.f;
+  if (live) {
+    float a[4], b[4];
+    load_vec<4>(row + col0 + 8 * g, a);
+    load_vec<4>(row + col0 + 8 * g + 4, b);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = a[r];
+      x[4 + r] = b[r];
+    }
+  }
+}
+
+// Decay factors of a chunk for scalar gates, for pairs in different blocks
+// of 16: G_ts = pre[t] mid[block t][block s] suf[s], pre from t's block's
+// start through t, suf behind s to its block's end; within a block, G_ts is
+// multiplied up (inside).
+struct __attribute__((aligned(16))) Decay {
+  float gate[kC + 4], pre[kC], suf[kC], mid[16];   // gate: read 3 past a block
+};
+// The decay behind s through t of one block, and (rows: along t, else along
+// s) of the three tokens that follow it in a lane.
+template <bool ROWS>
+__device__ __forceinline__ f32x4 inside(const float* gate, int t, int s) {
+  const float* g = gate + (t & ~15);
+  t &= 15;
+  s &= 15;
+  const int last = ROWS ? s : s + 3;   // the pair with the shortest stretch
+  float x = 1.f;
+#pragma unroll
+  for (int o = 1; o < 16; ++o) {
+    const float y = g[o];
+    x *= o > last && o <= t ? y : 1.f;
+  }
+  f32x4 out;
+  if (ROWS) {
+    out[0] = x;
+#pragma unroll
+    for (int r = 1; r < 4; ++r) {
+      const float y = g[t + r];
+      out[r] = out[r - 1] * (t + r > s ? y : 1.f);
+    }
+  } else {
+    out[3] = x;
+#pragma unroll
+    for (int r = 2; r >= 0; --r) {
+      const float y = g[s + r + 1];
+      out[r] = out[r + 1] * (s + r < t ? y : 1.f);
+    }
+  }
+  return out;
+}
+// One wave; lane l holds gate l.  P and F of token l come back.
+__device__ __forceinline__ void decays(Decay& d, float gate, float& P, float& F) {
+  const int l = lane_id(), l16 = l & 15;
+  float p = gate, s = gate;
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) {
+    const float x = __shfl_up(p, o), y = __shfl_down(s, o);
+    p *= l16 >= o ? x : 1.f;
+    s *= l16 + o < 16 ? y : 1.f;
+  }
+  const float next = __shfl_down(s, 1);
+  s = l16 == 15 ? 1.f : next;   // behind l only
+  const float t0 = __shfl(p, 15), t1 = __shfl(p, 31), t2 = __shfl(p, 47), t3 = __shfl(p, 63);
+  d.gate[l] = gate;
+  d.pre[l] = p;
+  d.suf[l] = s;
+  if (l < 16) {
+    const int a = l >> 2, b = l & 3;   // blocks between b and a
+    d.mid[l] = (b < 1 && a > 1 ? t1 : 1.f) * (b < 2 && a > 2 ? t2 : 1.f);
+  }
+  const int blk = l >> 4;
+  P = p * (blk > 0 ? t0 : 1.f) * (blk > 1 ? t1 : 1.f) * (blk > 2 ? t2 : 1.f);
+  F = s * (blk < 1 ? t1 : 1.f) * (blk < 2 ? t2 : 1.f) * (blk < 3 ? t3 : 1.f);
 }
 
 // c[m] += a[m] b for MT row tiles, the tiles in turn so that consecutive

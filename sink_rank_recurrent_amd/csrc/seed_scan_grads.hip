@@ -26,7 +26,7 @@ __device__ __forceinline__ float sum64(float x) {
 }
 
 // Rows of an LDS matrix [64][65] (or of its transpose) as a fragment.
-__device__ __forceinline__ void lds_rows(const float* mat, int mt, int ks, bool transposed,
+__device__ __forceinline__ void mat65_rows(const float* mat, int mt, int ks, bool transposed,
                                          float (&x)[8]) {
   const int row = 16 * mt + (lane_id() & 15), g = lane_id() >> 4;
 #pragma unroll
@@ -227,13 +227,13 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
         load_col8(K + i, kld, 32 * ks, n, kc);
         load_col8(Q + i, kld, 32 * ks, n, qc);
         const Frag<NT> kf = split<NT>(kc);
-        lds_rows(dM, w, ks, false, x);
+        mat65_rows(dM, w, ks, false, x);
         mma(dq, split<3>(x), kf);
-        lds_rows(dM, w, ks, true, x);
+        mat65_rows(dM, w, ks, true, x);
         mma(dk, split<3>(x), split<NT>(qc));
         if (DELTA) {
-          lds_rows(dL, w, ks, false, x);
-          lds_rows(dL, w, ks, true, y);
+          mat65_rows(dL, w, ks, false, x);
+          mat65_rows(dL, w, ks, true, y);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] += y[j];
           mma(dk, split<3>(x), kf);
@@ -377,6 +377,371 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
   }
 }
 
+// Rows [row][kRow] of fp32 in LDS as a left fragment contracted over columns
+// 32 ks .. + 31, or the transpose.
+__device__ __forceinline__ void mat_rows(const float* mat, int row, int ks, float (&x)[8]) {
+  const float* at = mat + row * kRow + 32 * ks + 4 * (lane_id() >> 4);
+  tiles_to_floats(*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 16), x);
+}
+__device__ __forceinline__ void mat_cols(const float* mat, int col, int ks, float (&x)[8]) {
+  const float* at = mat + (32 * ks + 4 * (lane_id() >> 4)) * kRow + col;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = at[(16 * (j >> 2) + (j & 3)) * kRow];
+}
+
+// Scalar gates.  Eight waves a (chunk, head): wave (rows 16 w4, half) has the
+// 16 tokens' rows of dO, dR and u in registers and every other 16 columns of
+// each result.  First the pairs inside the chunk (K and Q in LDS, u of the
+// other waves' rows through LDS), then 32 channels of S and H at a time.
+template <int RULE, int DK, int DV, typename T>
+struct GradLds {
+  static constexpr int NT = sizeof(T) == 2 ? 1 : 3, NE = RULE != kMAMBA2 ? 3 : NT;
+  static constexpr int kq = 2 * NT * kPlane<DK>;
+  static constexpr int u = 3 * (DV / 32) * NE * 1024;
+  static constexpr int mats = 2 * kC * kRow * 4;
+  static constexpr int plane = 32 * DV * 2;          // 32 channels of S or H, one term
+  static constexpr int pairs = kq + (u > mats ? u : mats);
+  static constexpr int small = pairs > 6 * plane ? pairs : 6 * plane;
+  static constexpr int bytes = small + (int)sizeof(Decay) + (2 + 4 + 4) * kC * 4 + 64;
+};
+
+template <int RULE, int DK, int DV, typename T>
+__global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
+  constexpr bool DELTA = RULE != kMAMBA2;
+  using Lds = GradLds<RULE, DK, DV, T>;
+  constexpr int NT = Lds::NT, NE = Lds::NE, KS = DV / 32, MT = DK / 32;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  char* Kp = smem;
+  char* Qp = smem + NT * kPlane<DK>;
+  char* Up = smem + Lds::kq;
+  float* m0 = reinterpret_cast<float*>(Up);   // two fp32 matrices where u was
+  float* m1 = m0 + kC * kRow;
+  Decay& dec = *reinterpret_cast<Decay*>(smem + Lds::small);
+  float* Pv = reinterpret_cast<float*>(smem + Lds::small + sizeof(Decay));
+  float* Fv = Pv + kC;
+  float* red = Fv + kC;       // [4][64]
+  float* dPF = red + 4 * kC;  // [half][dP, dF][64]
+  float* hs = dPF + 4 * kC;   // [8]
+  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  if (ch.n == 0) return;
+  const int head = blockIdx.y, tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
+  const int w4 = (tid >> 6) & 3, half = tid >> 8, n = ch.n;
+  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const int hk = head / (a.heads / a.key_heads);
+  const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * DV;
+  const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
+  const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
+  const float* Sc = reinterpret_cast<const float*>(a.ws + a.at.state) + unit * DK * DV;
+  const float* Hc = reinterpret_cast<const float*>(a.ws + a.at.grad) + unit * DK * DV;
+
+  // K and Q into LDS
+  if constexpr (NT == 1) {
+    async_rows<DK>(K, kld, n, Kp, tid >> 6, 8);
+    async_rows<DK>(Q, kld, n, Qp, tid >> 6, 8);
+  } else {
+    for (int i = tid; i < 2 * kC * (DK / 8); i += 512) {
+      const int which = i / (kC * (DK / 8)), t = i / (DK / 8) % kC, c = i % (DK / 8);
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t < n) {
+        const T* from = (which ? Q : K) + (size_t)t * kld + 8 * c;
+        float y[4], z[4];
+        load_vec<4>(from, y);
+        load_vec<4>(from + 4, z);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[r] = y[r];
+          x[4 + r] = z[r];
+        }
+      }
+      const Frag<NT> f = split<NT>(x);
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        *reinterpret_cast<u32x4*>((which ? Qp : Kp) + m * kPlane<DK> + piece_at<DK>(t, c)) = f.t[m];
+    }
+  }
+  // the wave's rows of dO, dR and u
+  const int row = 16 * w4 + l16;
+  Frag<NT> ado[KS];
+  Frag<3> adr[DELTA ? KS : 1];
+  Frag<NE> au[KS];
+  {
+    const bool live = row < n;
+    const T* dO = static_cast<const T*>(a.dO) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
+    const T* V = static_cast<const T*>(a.v) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
+    const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
+    const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
+    const float b = DELTA ? reinterpret_cast<const float*>(a.ws + a.at.b)[unit * kC + row] : 0.f;
+    float db = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      float x[8], y[8];
+      load_piece(dO, 32 * ks, live, x);
+      ado[ks] = split<NT>(x);
+      if constexpr (DELTA) {
+        load_piece(E, 32 * ks, live, x);
+        load_piece(Y, 32 * ks, live, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          db += x[j] * y[j];
+          x[j] *= b;
+          y[j] *= b;
+        }
+        adr[ks] = split<3>(y);
+      } else {
+        load_piece(V, 32 * ks, live, x);
+      }
+      au[ks] = split<NE>(x);
+      if (w4 < 3 && half == 0) {
+#pragma unroll
+        for (int m = 0; m < NE; ++m)
+          *reinterpret_cast<u32x4*>(Up + (((w4 * KS + ks) * NE + m) * 64 + l) * 16) = au[ks].t[m];
+      }
+    }
+    if (DELTA) {   // dbeta = Y . E
+      db += __shfl_xor(db, 16);
+      db += __shfl_xor(db, 32);
+      if (half == 0 && g == 0 && live) a.dbeta[((size_t)ch.tok + row) * a.heads + head] = db;
+    }
+  }
+  if (tid < 64) {
+    const float gate = tid < n ? a.g[((size_t)ch.tok + tid) * a.heads + head] : 1.f;
+    float P, F;
+    decays(dec, gate, P, F);
+    Pv[tid] = P;
+    Fv[tid] = F;
+  }
+  if (tid < 4 * kC) red[tid] = 0.f;
+  async_wait();
+  __syncthreads();
+
+  // the pairs: row tile w4, column tiles b = half, half + 2
+  f32x4 pl[2], pm[2], pw[2], pg[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = 2 * i + half;
+    pl[i] = pm[i] = pw[i] = pg[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b > w4) continue;
+    f32x4 kk = pl[i], qk = pl[i];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      Frag<NE> u = au[ks];
+      if (b < w4) {
+#pragma unroll
+        for (int m = 0; m < NE; ++m)
+          u.t[m] = *reinterpret_cast<const u32x4*>(Up + (((b * KS + ks) * NE + m) * 64 + l) * 16);
+      }
+      mma(pm[i], ado[ks], u);
+      if constexpr (DELTA) mma(pl[i], adr[ks], u);
+    }
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) {
+      const Frag<NT> k = lds_rows<DK, NT>(Kp, b, ks);
+      if (DELTA) mma(kk, lds_rows<DK, NT>(Kp, w4, ks), k);
+      mma(qk, lds_rows<DK, NT>(Qp, w4, ks), k);
+    }
+    const int t = 16 * w4 + 4 * g, s = 16 * b + l16;
+    if (b < w4) {
+      pg[i] = *reinterpret_cast<const f32x4*>(dec.pre + t) * (dec.suf[s] * dec.mid[4 * w4 + b]);
+    } else {
+      pg[i] = inside<true>(dec.gate, t, s);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (s > t + r) pg[i][r] = pm[i][r] = 0.f;
+        if (s >= t + r) pl[i][r] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) pw[i][r] = s < t + r ? pm[i][r] * qk[r] - pl[i][r] * kk[r] : 0.f;
+    pl[i] *= -pg[i];
+    pm[i] *= pg[i];
+  }
+  __syncthreads();
+  auto put = [&](float* mat, int i, const f32x4& x) {
+    const int b = 2 * i + half;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) mat[(16 * w4 + 4 * g + r) * kRow + 16 * b + l16] = x[r];
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    put(m0, i, pg[i]);
+    put(m1, i, pw[i]);
+  }
+  __syncthreads();
+  // dg from the pairs: sum over r >= t > s of G_rt W_rs G_{t-1,s}
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = 2 * i + half, t = 16 * b + l16;
+    if (b > w4) continue;
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    for (int ks = 0; ks <= (b >> 1); ++ks) {
+      float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      mat_rows(m1, 16 * w4 + l16, ks, x);
+      if (t > 0) mat_rows(m0, t - 1, ks, y);
+      mma(d, split<3>(x), split<3>(y));
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum += d[r] * pg[i][r];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (g == 0) red[w4 * kC + t] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    put(m0, i, pl[i]);
+    put(m1, i, pm[i]);
+  }
+  __syncthreads();
+
+  // dQ and dK from the pairs; column tiles it = half, half + 2, ...
+  f32x4 dq[MT], dk[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    float x[8], y[8];
+    Frag<3> fm, ft, fl;
+    const bool low = ks <= (w4 >> 1), up = ks >= (w4 >> 1);
+    if (low) {
+      mat_rows(m1, row, ks, x);
+      fm = split<3>(x);
+    }
+    if (up) {
+      mat_cols(m1, row, ks, x);
+      ft = split<3>(x);
+    }
+    if (DELTA) {
+      mat_rows(m0, row, ks, x);
+      mat_cols(m0, row, ks, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += y[j];
+      fl = split<3>(x);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int it = 2 * i + half;
+      const Frag<NT> k = lds_channels<DK, NT>(Kp, it, ks);
+      if (low) mma(dq[i], fm, k);
+      if (up) mma(dk[i], ft, lds_channels<DK, NT>(Qp, it, ks));
+      if (DELTA) mma(dk[i], fl, k);
+    }
+  }
+
+  // through the states, 32 channels at a time: rows of 8 values a thread
+  constexpr int PR = DV / 8;
+  const bool stager = tid < 32 * PR;
+  float sv[8], hv[8], hsum = 0.f;
+  auto fetch = [&](int part) {
+    if (!stager) return;
+    const size_t at = (size_t)(32 * part + tid / PR) * DV + 8 * (tid % PR);
+    float y[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load_vec<4>(Sc + at + 4 * h, y);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sv[4 * h + r] = y[r];
+      load_vec<4>(Hc + at + 4 * h, y);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) hv[4 * h + r] = y[r];
+    }
+  };
+  fetch(0);
+  f32x4 dp = {0.f, 0.f, 0.f, 0.f}, df = dp;
+  const f32x4 pt = *reinterpret_cast<const f32x4*>(Pv + 16 * w4 + 4 * g);
+  const f32x4 ft = *reinterpret_cast<const f32x4*>(Fv + 16 * w4 + 4 * g);
+  const bool shared = a.key_heads != a.heads;
+#pragma unroll
+  for (int part = 0; part < MT; ++part) {
+    __syncthreads();
+    if (stager) {
+      const int at = piece_at<DV>(tid / PR, tid % PR);
+      const Frag<3> s = split<3>(sv), h = split<3>(hv);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        *reinterpret_cast<u32x4*>(smem + m * Lds::plane + at) = s.t[m];
+        *reinterpret_cast<u32x4*>(smem + (3 + m) * Lds::plane + at) = h.t[m];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hsum += sv[j] * hv[j];
+    }
+    __syncthreads();
+    if (part + 1 < MT) fetch(part + 1);
+    // channels 32 part + 16 half + l16
+    f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int at = piece_at<DV>(16 * half + l16, 4 * ks + g);
+      Frag<3> s, h;
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        s.t[m] = *reinterpret_cast<const u32x4*>(smem + m * Lds::plane + at);
+        h.t[m] = *reinterpret_cast<const u32x4*>(smem + (3 + m) * Lds::plane + at);
+      }
+      mma(x1, ado[ks], s);
+      if constexpr (DELTA) mma(x2, adr[ks], s);
+      mma(x3, au[ks], h);
+    }
+    const int i = 32 * part + 16 * half + l16;
+    dq[part] += pt * x1;
+    dk[part] += ft * x3 - pt * x2;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * w4 + 4 * g + r;
+      if (t >= n) continue;
+      const float q = load_scalar(Q + (size_t)t * kld + i), k = load_scalar(K + (size_t)t * kld + i);
+      dp[r] += q * x1[r] - k * x2[r];
+      df[r] += k * x3[r];
+      if (shared) {
+        const size_t at = ((size_t)(ch.tok + t) * a.heads + head) * DK + i;
+        reinterpret_cast<float*>(a.ws + a.at.dq)[at] = dq[part][r];
+        reinterpret_cast<float*>(a.ws + a.at.dk)[at] = dk[part][r];
+      } else {
+        const size_t at = ((size_t)(ch.tok + t) * a.key_heads + hk) * DK + i;
+        store_scalar(static_cast<T*>(a.dq) + at, dq[part][r]);
+        store_scalar(static_cast<T*>(a.dk) + at, dk[part][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float x = sum16(dp[r]), y = sum16(df[r]);
+    if (l16 == 0) {
+      dPF[half * 2 * kC + 16 * w4 + 4 * g + r] = x;
+      dPF[half * 2 * kC + kC + 16 * w4 + 4 * g + r] = y;
+    }
+  }
+  hsum = sum64(hsum);
+  if (l == 0) hs[tid >> 6] = hsum;
+  __syncthreads();
+  if (tid >= 64) return;
+  // and from the states: c_t = dP_t + g_{t+1} c_{t+1} behind t (<H, S> at the
+  // end), b_{t+1} = g_t b_t + dF_t before it
+  const float gate = dec.gate[tid];
+  float A = __shfl_down(gate, 1), B = dPF[tid] + dPF[2 * kC + tid];
+  if (tid == 63) A = 1.f;
+  float A2 = gate, B2 = dPF[kC + tid] + dPF[3 * kC + tid];
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const float ax = __shfl_down(A, o), bx = __shfl_down(B, o);
+    const float ay = __shfl_up(A2, o), by = __shfl_up(B2, o);
+    if (tid + o < 64) {
+      B += A * bx;
+      A *= ax;
+    }
+    if (tid >= o) {
+      B2 += A2 * by;
+      A2 *= ay;
+    }
+  }
+  const float all = ((hs[0] + hs[1]) + (hs[2] + hs[3])) + ((hs[4] + hs[5]) + (hs[6] + hs[7]));
+  const float c = B + A * all, b0 = __shfl_up(B2, 1), b = tid ? b0 : 0.f;
+  const float before = tid ? Pv[tid - 1] : 1.f;
+  const float pairs = (red[tid] + red[kC + tid]) + (red[2 * kC + tid] + red[3 * kC + tid]);
+  if (tid < n)
+    a.dg[((size_t)ch.tok + tid) * a.heads + head] = pairs + (c * before + Fv[tid] * b);
+}
+
 // Gradients of keys and queries that several heads share: the sum over the
 // group in head order.  Rows outside every sequence are left as they were.
 template <typename T>
@@ -406,11 +771,21 @@ __global__ __launch_bounds__(256) void share_kernel(ScanArgs a) {
 template <int RULE, int DK, int DV, typename T>
 hipError_t grads(const ScanArgs& a, hipStream_t stream) {
   constexpr bool KDA = RULE == kKDA;
+  hipError_t e;
+  if constexpr (!KDA) {
+    constexpr size_t bytes = GradLds<RULE, DK, DV, T>::bytes;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_scalar_kernel<RULE, DK, DV, T>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((grads_scalar_kernel<RULE, DK, DV, T>), dim3(a.slots, a.heads), dim3(512),
+                       bytes, stream, a);
+  } else {
   const size_t lds = ((KDA ? 2 : 4) * kC * kLd + 6 * kC + DK + (KDA ? 3 * kC * DK : 0)) * sizeof(float);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kernel<RULE, DK, DV, T>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kernel<RULE, DK, DV, T>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((grads_kernel<RULE, DK, DV, T>), dim3(a.slots, a.heads), dim3(256), lds, stream, a);
+  }
   e = hipGetLastError();
   if (e != hipSuccess || a.key_heads == a.heads) return e;
   const size_t total = (size_t)a.tokens * a.key_heads * DK;
