@@ -36,18 +36,23 @@ ScanLayout scan_layout(int rule, int n_seq, int heads, int key_heads, int d_k, i
   return l;
 }
 
+static hipError_t walk(const ScanArgs& a, int what, hipStream_t stream) {
+  return a.bf16 && a.rule != kKDA ? launch_scan_chain(a, what, stream)
+                                  : launch_scan_wide(a, what, stream);
+}
+
 hipError_t launch_scan(const ScanArgs& a, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.tokens > 0) e = launch_scan_prep(a, false, stream);
-  if (e == hipSuccess) e = launch_scan_forward(a, false, stream);
+  if (e == hipSuccess) e = walk(a, 0, stream);
   return e;
 }
 
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.tokens > 0) e = launch_scan_prep(a, true, stream);
-  if (e == hipSuccess && a.tokens > 0) e = launch_scan_forward(a, true, stream);
-  if (e == hipSuccess) e = launch_scan_reverse(a, stream);
+  if (e == hipSuccess && a.tokens > 0) e = walk(a, 1, stream);
+  if (e == hipSuccess) e = walk(a, 2, stream);
   if (e == hipSuccess && a.tokens > 0) e = launch_scan_grads(a, stream);
   return e;
 }

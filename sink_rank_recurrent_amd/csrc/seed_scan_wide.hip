@@ -1,0 +1,519 @@
+// The recurrence from chunk to chunk, and back, where a key operand needs
+// more than one bf16 term: float32 inputs, and gates per key channel (K and
+// Q are scaled by the decays channel by channel).  As in seed_scan_chain.hip a
+// wave owns 16 columns; the operands are split into LDS planes by the whole
+// workgroup, from values loaded while the chunk before was computed.  With
+// gates per channel K serves twice, scaled by P and by F: the second fills
+// the same planes once the first is used up.
+#include "seed_scan_chain.h"
+
+namespace seed {
+namespace scan {
+namespace {
+
+// Eight values of an array as loaded.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f32x4*>(p);
+    b = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  __device__ __forceinline__ void clear() { a = b = zero4(); }
+  __device__ __forceinline__ void get(float (&x)[8]) const { tiles_to_floats(a, b, x); }
+};
+template <>
+struct Piece<bf16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void clear() { a = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(a[j] << 16);
+      x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+    }
+  }
+};
+
+// A thread's share of a 64 x DK operand: PPT pieces.
+template <int DK, int THREADS>
+constexpr int kShare = kC * DK / 8 / THREADS;
+template <int DK, int THREADS, typename T>
+struct Share {
+  Piece<T> x[kShare<DK, THREADS>];
+  // rows from n on are 0 (`pad`: hold no rows past the array)
+  __device__ __forceinline__ void load(const T* base, size_t ld, int n) {
+#pragma unroll
+    for (int i = 0; i < kShare<DK, THREADS>; ++i) {
+      const int e = i * THREADS + threadIdx.x, t = e / (DK / 8), c = e % (DK / 8);
+      if (t < n) x[i].load(base + (size_t)t * ld + 8 * c);
+      else x[i].clear();
+    }
+  }
+};
+// x (times `scale`) into N planes.
+template <int DK, int THREADS, int N, bool SCALED, typename T>
+__device__ __forceinline__ void fill(char* planes, const Share<DK, THREADS, T>& v,
+                                     const Share<DK, THREADS, float>& scale) {
+#pragma unroll
+  for (int i = 0; i < kShare<DK, THREADS>; ++i) {
+    const int e = i * THREADS + threadIdx.x, t = e / (DK / 8), c = e % (DK / 8);
+    float x[8];
+    v.x[i].get(x);
+    if (SCALED) {
+      float y[8];
+      scale.x[i].get(y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= y[j];
+    }
+    const Frag<N> f = split<N>(x);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      *reinterpret_cast<u32x4*>(planes + n * kPlane<DK> + piece_at<DK>(t, c)) = f.t[n];
+  }
+}
+
+template <typename T>
+struct Tiles {
+  T x[4][4];
+  __device__ __forceinline__ void load(const T* p, size_t ld, uint32_t lane, int n) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const T* row = p + (size_t)(16 * m + r) * ld;
+        x[m][r] = n >= kC || 16 * m + 4 * (lane_id() >> 4) + r < n ? row[lane] : T(0);
+      }
+  }
+  __device__ __forceinline__ f32x4 tile(int m) const {
+    return f32x4{load_scalar(&x[m][0]), load_scalar(&x[m][1]), load_scalar(&x[m][2]),
+                 load_scalar(&x[m][3])};
+  }
+};
+
+// Terms: as in seed_scan_chain.hip, two for the corrections and the read-outs
+// where the read-outs are bf16, three otherwise.
+template <int RULE, int DK, typename T, bool SAVE>
+struct Wide {
+  static constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
+  static constexpr bool OUT16 = sizeof(T) == 2 && !SAVE;
+  static constexpr int NC = OUT16 ? 2 : 3;                       // corrections
+  static constexpr int NV = sizeof(T) == 2 ? 1 : 3;              // a value or a gradient
+  static constexpr int q = 3 * kPlane<DK>;
+  static constexpr int n = q + (SAVE ? 0 : NC * kPlane<DK>);
+  static constexpr int m = n + (DELTA ? kTriFrags * NC * 1024 : 0);
+  static constexpr int vec = m + (SAVE ? 0 : kTriFrags * NC * 1024);
+  static constexpr int bytes = vec + 768;
+};
+
+template <int RULE, int DK, int NW, typename T, bool SAVE>
+__global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
+  using W = Wide<RULE, DK, T, SAVE>;
+  constexpr bool KDA = W::KDA, DELTA = W::DELTA;
+  constexpr int IT = DK / 16, NC = W::NC, TH = 64 * NW;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int w = threadIdx.x >> 6;
+  const Place<NW> at(a);
+  const Range rg = sequence(a, at.seq);
+  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
+  const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
+  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
+  const T* K = static_cast<const T*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const T* Q = static_cast<const T*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const T* V = static_cast<const T*>(a.v) + vat;
+  T* out = static_cast<T*>(a.o) + vat;
+
+  f32x4 S[IT];
+  load_state(a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+
+  Share<DK, TH, T> kr, qr;
+  Share<DK, TH, float> pr, fr;
+  Tiles<T> v;
+  f32x4 last[KDA ? IT : 1];
+  auto fetch = [&](int c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    kr.load(K + (size_t)c * kC * kld, kld, n);
+    if (!SAVE) qr.load(Q + (size_t)c * kC * kld, kld, n);
+    if (KDA) {
+      pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
+      fr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
+    }
+    v.load(V + (size_t)c * kC * vld, vld, row_lane, n);
+  };
+  if (chunks > 0) fetch(0);
+  for (int c = 0; c < chunks; ++c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    __syncthreads();   // the chunk before is done with the planes
+    constexpr size_t pack = kTriFrags * 3 * kFrag;
+    if (DELTA)
+      async_pack<NC>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds + W::n,
+                     w, NW);
+    if (!SAVE)
+      async_pack<NC>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds + W::m,
+                     w, NW);
+    for (int i = w; i < (DELTA ? 3 : 2); i += NW)
+      if (!KDA || i == 2)
+        async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
+                          (unit * kC + lane_id()) * sizeof(float), lds + W::vec + 256 * i);
+    if (KDA) {
+      if (DELTA) fill<DK, TH, NC, true>(lds, kr, pr);
+      if (!SAVE) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
+    } else {
+      fill<DK, TH, 3, false>(lds, kr, pr);
+      if (!SAVE) fill<DK, TH, NC, false>(lds + W::q, qr, pr);
+    }
+    f32x4 u[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) u[m] = v.tile(m);
+    async_wait();
+    __syncthreads();
+    if (SAVE)
+      keep_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, a.d_v, state_lane, S);
+    if (!KDA && c + 1 < chunks) fetch(c + 1);
+
+    f32x4 R[4], O[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) R[m] = O[m] = zero4();
+    if (DELTA || !SAVE) {
+#pragma unroll
+      for (int ks = 0; ks < DK / 32; ++ks) {
+        const Frag<NC> s = split_tiles<NC>(S[2 * ks], S[2 * ks + 1]);
+        Frag<NC> f[4];
+        if (DELTA) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds, m, ks);
+          mma_tiles<4, NC, NC, NC>(R, f, s);
+        }
+        if (!SAVE) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds + W::q, m, ks);
+          mma_tiles<4, NC, NC, NC>(O, f, s);
+        }
+      }
+    }
+    if (KDA) {   // K's planes are used up: F K takes their place
+#pragma unroll
+      for (int m = 0; m < IT; ++m)
+        last[m] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.ws + a.at.p) +
+                                                  (unit * kC + kC - 1) * DK + state_row(m));
+      __syncthreads();
+      fill<DK, TH, 3, true>(lds, kr, fr);
+      if (c + 1 < chunks) fetch(c + 1);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 p = KDA ? f32x4{1.f, 1.f, 1.f, 1.f} : lds_vec(lds + W::vec, m);
+      if (DELTA) u[m] -= p * R[m];
+      O[m] *= p;
+    }
+    if (DELTA) {
+      f32x4 b[4], y[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        b[m] = lds_vec(lds + W::vec + 512, m);
+        y[m] = zero4();
+      }
+      const Frag<NC> x0 = split_tiles<NC>(b[0] * u[0], b[1] * u[1]);
+      const Frag<NC> x1 = split_tiles<NC>(b[2] * u[2], b[3] * u[3]);
+      Frag<NC> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NC>(lds + W::n, lower_frag(m, 0));
+      mma_tiles<4, NC, NC, NC>(y, f, x0);
+      f32x4 z[2] = {y[2], y[3]};
+      const Frag<NC> h[2] = {lds_pack<NC>(lds + W::n, lower_frag(2, 1)),
+                             lds_pack<NC>(lds + W::n, lower_frag(3, 1))};
+      mma_tiles<2, NC, NC, NC>(z, h, x1);
+      u[0] -= y[0];
+      u[1] -= y[1];
+      u[2] -= z[0];
+      u[3] -= z[1];
+      drop_rows(u, n);
+      if (SAVE)
+        keep_tiles(reinterpret_cast<float*>(a.ws + a.at.e) + unit * kC * a.d_v, a.d_v, keep_lane, u);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) u[m] *= b[m];
+    }
+    if (!SAVE) {
+      constexpr int NU = DELTA ? NC : W::NV;   // V itself is one term
+      const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
+      Frag<NC> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NC>(lds + W::m, lower_frag(m, 0));
+      mma_tiles<4, NC, NU, NC>(O, f, x0);
+      f32x4 z[2] = {O[2], O[3]};
+      const Frag<NC> h[2] = {lds_pack<NC>(lds + W::m, lower_frag(2, 1)),
+                             lds_pack<NC>(lds + W::m, lower_frag(3, 1))};
+      mma_tiles<2, NC, NU, NC>(z, h, x1);
+      O[2] = z[0];
+      O[3] = z[1];
+      store_tiles(out + (size_t)c * kC * vld, vld, row_lane, n, O);
+    }
+    // S' = P_end S + (F K)^T u
+    if (KDA) {
+      __syncthreads();   // F K is in place
+#pragma unroll
+      for (int m = 0; m < IT; ++m) S[m] *= last[m];
+    } else {
+      const float end = *reinterpret_cast<const float*>(lds + W::vec + 4 * (kC - 1));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) u[m] *= lds_vec(lds + W::vec + 256, m);
+#pragma unroll
+      for (int m = 0; m < IT; ++m) S[m] *= end;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const Frag<3> x = split_tiles<3>(u[2 * ks], u[2 * ks + 1]);
+#pragma unroll
+      for (int mm = 0; mm < IT; mm += 4) {
+        Frag<3> f[4];
+        f32x4 s[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          f[m] = lds_cols<DK, 3>(lds, mm + m, ks);
+          s[m] = S[mm + m];
+        }
+        mma_tiles(s, f, x);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) S[mm + m] = s[m];
+      }
+    }
+  }
+  if (!SAVE) keep_state(a.S + state, a.d_v, state_lane, S);
+}
+
+template <int DK, int RULE>
+struct WideBack {
+  static constexpr bool DELTA = RULE != kMAMBA2;
+  static constexpr int q = 3 * kPlane<DK>;
+  static constexpr int n = 2 * q;
+  static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int vec = m + kTriFrags * 3 * 1024;
+  static constexpr int bytes = vec + 768;
+};
+
+// The chunks from the last to the first (see chain_reverse_kernel).
+template <int RULE, int DK, int NW, typename T>
+__global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
+  using W = WideBack<DK, RULE>;
+  constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
+  constexpr int IT = DK / 16, TH = 64 * NW, NV = sizeof(T) == 2 ? 1 : 3;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int w = threadIdx.x >> 6;
+  const Place<NW> at(a);
+  const Range rg = sequence(a, at.seq);
+  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
+  const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
+  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
+  const T* K = static_cast<const T*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const T* Q = static_cast<const T*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const T* dO = static_cast<const T*>(a.dO) + vat;
+  T* dV = static_cast<T*>(a.dv) + vat;
+
+  f32x4 H[IT];
+  load_state(a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
+
+  Share<DK, TH, T> kr, qr;
+  Share<DK, TH, float> pr, fr;
+  Tiles<T> d;
+  auto fetch = [&](int c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    kr.load(K + (size_t)c * kC * kld, kld, n);
+    qr.load(Q + (size_t)c * kC * kld, kld, n);
+    if (KDA) {
+      pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
+      fr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
+    }
+    d.load(dO + (size_t)c * kC * vld, vld, row_lane, n);
+  };
+  if (chunks > 0) fetch(chunks - 1);
+  for (int c = chunks - 1; c >= 0; --c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    __syncthreads();
+    constexpr size_t pack = kTriFrags * 3 * kFrag;
+    if (DELTA)
+      async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds + W::n,
+                    w, NW);
+    async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds + W::m, w,
+                  NW);
+    for (int i = w; i < (DELTA ? 3 : 2); i += NW)
+      if (!KDA || i == 2)
+        async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
+                          (unit * kC + lane_id()) * sizeof(float), lds + W::vec + 256 * i);
+    if (KDA) {
+      fill<DK, TH, 3, true>(lds, kr, fr);
+      fill<DK, TH, 3, true>(lds + W::q, qr, pr);
+    } else {
+      fill<DK, TH, 3, false>(lds, kr, pr);
+      fill<DK, TH, 3, false>(lds + W::q, qr, pr);
+    }
+    f32x4 y[4], go[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      y[m] = zero4();
+      go[m] = d.tile(m);
+    }
+    async_wait();
+    __syncthreads();
+    keep_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, a.d_v, state_lane, H);
+    if (!KDA && c > 0) fetch(c - 1);
+
+    // dU = F (K H) + M^T dO
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) {
+      const Frag<3> h = split_tiles<3>(H[2 * ks], H[2 * ks + 1]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 3>(lds, m, ks);
+      mma_tiles(y, f, h);
+    }
+    f32x4 last[KDA ? IT : 1];
+    if (KDA) {   // F K is used up: P K takes its place
+#pragma unroll
+      for (int m = 0; m < IT; ++m)
+        last[m] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.ws + a.at.p) +
+                                                  (unit * kC + kC - 1) * DK + state_row(m));
+      __syncthreads();
+      fill<DK, TH, 3, true>(lds, kr, pr);
+      if (c > 0) fetch(c - 1);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[m] *= lds_vec(lds + W::vec + 256, m);
+    }
+    {
+      const Frag<NV> x0 = split_tiles<NV>(go[0], go[1]), x1 = split_tiles<NV>(go[2], go[3]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(lds + W::m, upper_frag(m, 1));
+      mma_tiles(y, f, x1);
+      f32x4 z[2] = {y[0], y[1]};
+      const Frag<3> h[2] = {lds_pack<3>(lds + W::m, upper_frag(0, 0)),
+                            lds_pack<3>(lds + W::m, upper_frag(1, 0))};
+      mma_tiles(z, h, x0);
+      y[0] = z[0];
+      y[1] = z[1];
+    }
+    if (DELTA) {
+      f32x4 b[4], t[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        b[m] = lds_vec(lds + W::vec + 512, m);
+        t[m] = zero4();
+      }
+      const Frag<3> x0 = split_tiles<3>(b[0] * y[0], b[1] * y[1]);
+      const Frag<3> x1 = split_tiles<3>(b[2] * y[2], b[3] * y[3]);
+      Frag<3> f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(lds + W::n, upper_frag(m, 1));
+      mma_tiles(t, f, x1);
+      f32x4 z[2] = {t[0], t[1]};
+      const Frag<3> h[2] = {lds_pack<3>(lds + W::n, upper_frag(0, 0)),
+                            lds_pack<3>(lds + W::n, upper_frag(1, 0))};
+      mma_tiles(z, h, x0);
+      y[0] -= z[0];
+      y[1] -= z[1];
+      y[2] -= t[2];
+      y[3] -= t[3];
+      drop_rows(y, n);
+      keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[m] *= b[m];
+    }
+    store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+
+    // dS = P_end H + (P Q)^T dO - (P K)^T dR
+    if (KDA) {
+      __syncthreads();   // P K is in place
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[m] = -y[m];
+#pragma unroll
+      for (int m = 0; m < IT; ++m) H[m] *= last[m];
+    } else {
+      const float end = *reinterpret_cast<const float*>(lds + W::vec + 4 * (kC - 1));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const f32x4 p = lds_vec(lds + W::vec, m);
+        go[m] *= p;
+        y[m] *= -p;
+      }
+#pragma unroll
+      for (int m = 0; m < IT; ++m) H[m] *= end;
+    }
+    constexpr int NG = KDA ? NV : 3;   // dO itself, or times P
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const Frag<NG> x = split_tiles<NG>(go[2 * ks], go[2 * ks + 1]);
+      const Frag<3> z = split_tiles<3>(y[2 * ks], y[2 * ks + 1]);
+#pragma unroll
+      for (int mm = 0; mm < IT; mm += 4) {
+        Frag<3> f[4];
+        f32x4 s[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          f[m] = lds_cols<DK, 3>(lds + W::q, mm + m, ks);
+          s[m] = H[mm + m];
+        }
+        mma_tiles(s, f, x);
+        if (DELTA) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[m] = lds_cols<DK, 3>(lds, mm + m, ks);
+          mma_tiles(s, f, z);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) H[mm + m] = s[m];
+      }
+    }
+  }
+  if (a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
+}
+
+template <typename F>
+hipError_t launch(F kernel, const ScanArgs& a, int waves, size_t lds, hipStream_t stream) {
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  const size_t grid = (size_t)a.n_seq * a.heads * (a.d_v / (16 * waves));
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * waves), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <int RULE, int DK, int NW, typename T>
+hipError_t wide(const ScanArgs& a, int what, hipStream_t stream) {
+  if (what == 0)
+    return launch(wide_forward_kernel<RULE, DK, NW, T, false>, a, NW, Wide<RULE, DK, T, false>::bytes,
+                  stream);
+  if (what == 1)
+    return launch(wide_forward_kernel<RULE, DK, NW, T, true>, a, NW, Wide<RULE, DK, T, true>::bytes,
+                  stream);
+  return launch(wide_reverse_kernel<RULE, DK, NW, T>, a, NW, WideBack<DK, RULE>::bytes, stream);
+}
+template <int RULE, typename T>
+hipError_t wide_shape(const ScanArgs& a, int what, hipStream_t stream) {
+  if (a.d_k == 64) return wide<RULE, 64, 4, T>(a, what, stream);
+  return a.d_v == 128 ? wide<RULE, 128, 8, T>(a, what, stream) : wide<RULE, 128, 4, T>(a, what, stream);
+}
+
+}  // namespace
+}  // namespace scan
+
+hipError_t launch_scan_wide(const ScanArgs& a, int what, hipStream_t stream) {
+  using namespace scan;
+  if (a.rule == kKDA)
+    return a.bf16 ? wide_shape<kKDA, bf16_t>(a, what, stream) : wide_shape<kKDA, float>(a, what, stream);
+  return a.rule == kGDN ? wide_shape<kGDN, float>(a, what, stream)
+                        : wide_shape<kMAMBA2, float>(a, what, stream);
+}
+
+}  // namespace seed

@@ -58,10 +58,11 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t stream);
 
 // Phases of the recurrence (seed_scan_*.hip).
 hipError_t launch_scan_prep(const ScanArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_scan_forward(const ScanArgs& a, bool save, hipStream_t stream);
-// The same for bf16 inputs and scalar gates, whose keys need one term.
+// From chunk to chunk: what = 0 forward, 1 forward for the backward pass
+// (keeps S and E, writes no read-outs), 2 backward.  chain: bf16 inputs and
+// scalar gates; wide: the others.
 hipError_t launch_scan_chain(const ScanArgs& a, int what, hipStream_t stream);
-hipError_t launch_scan_reverse(const ScanArgs& a, hipStream_t stream);
+hipError_t launch_scan_wide(const ScanArgs& a, int what, hipStream_t stream);
 hipError_t launch_scan_grads(const ScanArgs& a, hipStream_t stream);
 
 enum NormAct { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
