@@ -36,6 +36,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kC = kScanChunk;
 constexpr int kFrag = 512;        // bf16 values of one 16 x 32 operand fragment
 constexpr int kRow = kC + 4;      // fp32 LDS rows of 64: 16-byte vectors, off the banks' stride
+constexpr float kSafe = 0x1p-60f;  // the least decay (and 1 / the largest) of a chunk that is divided by
 constexpr int kTriFrags = 6;      // fragments of a 64 x 64 triangle
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }

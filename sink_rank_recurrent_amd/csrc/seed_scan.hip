@@ -32,6 +32,7 @@ ScanLayout scan_layout(int rule, int n_seq, int heads, int key_heads, int d_k, i
   l.dk = part(backward && (kda || heads != key_heads), per_head);
   l.tp = part(backward && kda, per_token * d_k);
   l.tf = part(backward && kda, per_token * d_k);
+  l.slow = part(backward && kda, units * sizeof(int));
   l.bytes = at;
   return l;
 }

@@ -3,7 +3,7 @@
 // seed_scan.h).  A gate's gradient is summed over the pairs s < t <= r that
 // its decay lies between, each without the gate itself (the decays before
 // and behind it), so no quotient is taken and a gate of 0 has its gradient.
-#include "seed_scan.h"
+#include "seed_scan_chain.h"
 
 namespace seed {
 namespace scan {
@@ -55,6 +55,7 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
   const int head = blockIdx.y, tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int l16 = l & 15, g16 = l >> 4, n = ch.n;
   const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  if (KDA && !reinterpret_cast<const int*>(a.ws + a.at.slow)[unit]) return;
   const int hk = head / (a.heads / a.key_heads);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * DV;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
@@ -742,6 +743,345 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
     a.dg[((size_t)ch.tok + tid) * a.heads + head] = pairs + (c * before + Fv[tid] * b);
 }
 
+// Gates per key channel, chunks whose P lies in kSafe .. 1 / kSafe and whose
+// gates are 1/4 and more (the others are marked and left to grads_kernel).
+// With K~ = P K, Q~ = P Q, K' = K / P:
+//   dQ = P (dO S^T + dM K'),  dK = P (dL K' - dR S^T) + F (u H^T)
+//        + (dL^T K~ + dM^T Q~) / P
+// and with the parts of k.dK in this order called row, end and col,
+//   g_t dg_t = sum over r >= t of (q.dQ + row - col)_r + sum over s < t of
+//   end_s + P_end <H, S>, channel by channel: the pairs that lie behind t
+// cancel in the first sum, which is why small gates take the other way.
+template <int DK, int DV, typename T>
+struct KdaLds {
+  static constexpr int NT = sizeof(T) == 2 ? 1 : 3;
+  static constexpr int u = 3 * (DV / 32) * 3 * 1024;
+  static constexpr int mats = 2 * kC * kRow * 4;
+  static constexpr int plane = 32 * DV * 2, kplane = kC * 64;   // 32 channels of S or H, of K
+  static constexpr int s = u > mats ? u : mats;
+  static constexpr int k = s + 6 * plane;
+  static constexpr int small = k + 9 * kplane;
+  static constexpr int bytes = small + (4 * 2 * 32 + 32 + 8) * 4;
+};
+
+template <int DK, int DV, typename T>
+__global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
+  using Lds = KdaLds<DK, DV, T>;
+  constexpr int NT = Lds::NT, KS = DV / 32, MT = DK / 32;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  float* m0 = reinterpret_cast<float*>(smem);   // u of the waves, then dL and dM
+  float* m1 = m0 + kC * kRow;
+  char* Sp = smem + Lds::s;
+  char* Kp = smem + Lds::k;                     // K', K~, Q~: three planes each
+  float* tot = reinterpret_cast<float*>(smem + Lds::small);   // [x, z][4][32]
+  float* hs = tot + 4 * 2 * 32;                 // [32]
+  int* bad = reinterpret_cast<int*>(hs + 32);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  if (ch.n == 0) return;
+  const int head = blockIdx.y, tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
+  const int w4 = (tid >> 6) & 3, half = tid >> 8, n = ch.n;
+  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const int hk = head / (a.heads / a.key_heads);
+  const size_t kld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
+  const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
+  const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
+  const float* gates = a.g + ((size_t)ch.tok * a.heads + head) * DK;
+  const float* P = reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK;
+  const float* F = reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK;
+  const float* Sc = reinterpret_cast<const float*>(a.ws + a.at.state) + unit * DK * DV;
+  const float* Hc = reinterpret_cast<const float*>(a.ws + a.at.grad) + unit * DK * DV;
+
+  if (tid == 0) *bad = 0;
+  __syncthreads();
+  {
+    bool fine = true;
+    for (int e = tid; e < kC * DK / 4; e += 512) {
+      const int t = e / (DK / 4), i = 4 * (e % (DK / 4));
+      const f32x4 p = *reinterpret_cast<const f32x4*>(P + t * DK + i);
+      f32x4 q = {1.f, 1.f, 1.f, 1.f};
+      float k[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t < n) {
+        q = *reinterpret_cast<const f32x4*>(gates + (size_t)t * gld + i);
+        load_vec<4>(K + (size_t)t * kld + i, k);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        fine &= p[r] >= kSafe && p[r] <= 1.f / kSafe && q[r] >= 0.25f && fabsf(k[r]) <= 0x1p40f;
+    }
+    if (!fine) *bad = 1;
+  }
+  // the wave's rows of dO, dR and u
+  const int row = 16 * w4 + l16;
+  Frag<NT> ado[KS];
+  Frag<3> adr[KS], au[KS];
+  float db = 0.f;
+  {
+    const bool live = row < n;
+    const T* dO = static_cast<const T*>(a.dO) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
+    const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
+    const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
+    const float b = reinterpret_cast<const float*>(a.ws + a.at.b)[unit * kC + row];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      float x[8], y[8];
+      load_piece(dO, 32 * ks, live, x);
+      ado[ks] = split<NT>(x);
+      load_piece(E, 32 * ks, live, x);
+      load_piece(Y, 32 * ks, live, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        db += x[j] * y[j];
+        x[j] *= b;
+        y[j] *= b;
+      }
+      adr[ks] = split<3>(y);
+      au[ks] = split<3>(x);
+      if (w4 < 3 && half == 0) {
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          *reinterpret_cast<u32x4*>(smem + (((w4 * KS + ks) * 3 + m) * 64 + l) * 16) = au[ks].t[m];
+      }
+    }
+    db += __shfl_xor(db, 16);
+    db += __shfl_xor(db, 32);
+  }
+  __syncthreads();
+  if (tid == 0) reinterpret_cast<int*>(a.ws + a.at.slow)[unit] = *bad;
+  if (*bad) return;
+  if (half == 0 && g == 0 && row < n) a.dbeta[((size_t)ch.tok + row) * a.heads + head] = db;
+
+  // the pairs: row tile w4, column tiles half, half + 2
+  f32x4 pl[2], pm[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = 2 * i + half;
+    pl[i] = pm[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b > w4) continue;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      Frag<3> u = au[ks];
+      if (b < w4) {
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          u.t[m] = *reinterpret_cast<const u32x4*>(smem + (((b * KS + ks) * 3 + m) * 64 + l) * 16);
+      }
+      mma(pm[i], ado[ks], u);
+      mma(pl[i], adr[ks], u);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * g + r;
+      if (b == w4 && l16 > t) pm[i][r] = 0.f;
+      pl[i][r] = b == w4 && l16 >= t ? 0.f : -pl[i][r];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = 2 * i + half;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m0[(16 * w4 + 4 * g + r) * kRow + 16 * b + l16] = pl[i][r];
+      m1[(16 * w4 + 4 * g + r) * kRow + 16 * b + l16] = pm[i][r];
+    }
+  }
+
+  constexpr int PR = DV / 8;
+  const bool stager = tid < 32 * PR;
+  float sv[8], hv[8], pv[8];
+  Piece<T> kv, qv;
+  auto fetch = [&](int part) {
+    if (stager) {
+      const int at = (32 * part + tid / PR) * DV + 8 * (tid % PR);
+      float y[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load_vec<4>(Sc + at + 4 * h, y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sv[4 * h + r] = y[r];
+        load_vec<4>(Hc + at + 4 * h, y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) hv[4 * h + r] = y[r];
+      }
+    }
+    if (tid < 256) {
+      const int t = tid >> 2, c = 32 * part + 8 * (tid & 3);
+      float y[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load_vec<4>(P + t * DK + c + 4 * h, y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pv[4 * h + r] = y[r];
+      }
+      kv.clear();
+      qv.clear();
+      if (t < n) {
+        kv.load(K + (size_t)t * kld + c);
+        qv.load(Q + (size_t)t * kld + c);
+      }
+    }
+  };
+  auto kplane_at = [](int t, int c) { return t * 64 + ((c ^ ((t >> 2) & 3)) << 4); };
+  auto cols = [&](const char* planes, int ks) {   // channels 16 half .. + 15
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    Frag<3> f;
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = 32 * ks + 16 * h + 4 * g + (l16 >> 2);
+        const char* at = planes + m * Lds::kplane + kplane_at(t, 2 * half + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
+        const u32x2 x = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                       (__attribute__((address_space(3))) bf16x4*)(at)));
+        f.t[m][2 * h] = x[0];
+        f.t[m][2 * h + 1] = x[1];
+      }
+    return f;
+  };
+  const bool shared = a.key_heads != a.heads;
+  fetch(0);
+  for (int part = 0; part < MT; ++part) {
+    __syncthreads();
+    if (stager) {
+      const int at = piece_at<DV>(tid / PR, tid % PR);
+      const Frag<3> s = split<3>(sv), h = split<3>(hv);
+      float x = 0.f;
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        *reinterpret_cast<u32x4*>(Sp + m * Lds::plane + at) = s.t[m];
+        *reinterpret_cast<u32x4*>(Sp + (3 + m) * Lds::plane + at) = h.t[m];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x += sv[j] * hv[j];
+      // <H, S> of the thread's channel: PR neighbouring lanes
+#pragma unroll
+      for (int o = 1; o < PR; o *= 2) x += __shfl_xor(x, o);
+      if (tid % PR == 0) hs[tid / PR] = x;
+    }
+    if (tid < 256) {
+      float x[8], y[8], z[8];
+      kv.get(y);
+      qv.get(z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = y[j] / pv[j];
+        y[j] *= pv[j];
+        z[j] *= pv[j];
+      }
+      const int at = kplane_at(tid >> 2, tid & 3);
+      const Frag<3> f0 = split<3>(x), f1 = split<3>(y), f2 = split<3>(z);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        *reinterpret_cast<u32x4*>(Kp + m * Lds::kplane + at) = f0.t[m];
+        *reinterpret_cast<u32x4*>(Kp + (3 + m) * Lds::kplane + at) = f1.t[m];
+        *reinterpret_cast<u32x4*>(Kp + (6 + m) * Lds::kplane + at) = f2.t[m];
+      }
+    }
+    __syncthreads();
+    if (part + 1 < MT) fetch(part + 1);
+    f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1, a1 = x1, a2 = x1, a3 = x1;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int at = piece_at<DV>(16 * half + l16, 4 * ks + g);
+      Frag<3> s, h;
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        s.t[m] = *reinterpret_cast<const u32x4*>(Sp + m * Lds::plane + at);
+        h.t[m] = *reinterpret_cast<const u32x4*>(Sp + (3 + m) * Lds::plane + at);
+      }
+      mma(x1, ado[ks], s);
+      mma(x2, adr[ks], s);
+      mma(x3, au[ks], h);
+    }
+    const int i = 32 * part + 16 * half + l16, t0 = 16 * w4 + 4 * g;
+    float q[4], k[4], pt[4], ft[4], gt[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = t0 + r;
+      pt[r] = P[t * DK + i];
+      ft[r] = F[t * DK + i];
+      q[r] = t < n ? load_scalar(Q + (size_t)t * kld + i) : 0.f;
+      k[r] = t < n ? load_scalar(K + (size_t)t * kld + i) : 0.f;
+      gt[r] = t < n ? gates[(size_t)t * gld + i] : 1.f;
+    }
+    const float end = P[(kC - 1) * DK + i] * hs[16 * half + l16];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      float x[8];
+      if (ks <= (w4 >> 1)) {
+        const Frag<3> f = cols(Kp, ks);
+        mat_rows(m1, row, ks, x);
+        mma(a1, split<3>(x), f);
+        mat_rows(m0, row, ks, x);
+        mma(a2, split<3>(x), f);
+      }
+      if (ks >= (w4 >> 1)) {
+        mat_cols(m0, row, ks, x);
+        mma(a3, split<3>(x), cols(Kp + 3 * Lds::kplane, ks));
+        mat_cols(m1, row, ks, x);
+        mma(a3, split<3>(x), cols(Kp + 6 * Lds::kplane, ks));
+      }
+    }
+    float xs[4], zs[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = t0 + r;
+      const float dq = pt[r] * (x1[r] + a1[r]), rk = pt[r] * (a2[r] - x2[r]);
+      const float ck = a3[r] / pt[r], fk = ft[r] * x3[r];
+      xs[r] = q[r] * dq + k[r] * (rk - ck);
+      zs[r] = k[r] * fk;
+      if (t >= n) continue;
+      if (shared) {
+        const size_t at = ((size_t)(ch.tok + t) * a.heads + head) * DK + i;
+        reinterpret_cast<float*>(a.ws + a.at.dq)[at] = dq;
+        reinterpret_cast<float*>(a.ws + a.at.dk)[at] = rk + ck + fk;
+      } else {
+        const size_t at = ((size_t)(ch.tok + t) * a.key_heads + hk) * DK + i;
+        store_scalar(static_cast<T*>(a.dq) + at, dq);
+        store_scalar(static_cast<T*>(a.dk) + at, rk + ck + fk);
+      }
+    }
+    // sums of x over t and behind, of z before t: rows, lanes, waves
+    const float sx = (xs[0] + xs[1]) + (xs[2] + xs[3]), sz = (zs[0] + zs[1]) + (zs[2] + zs[3]);
+    float bx = 0.f, bz = 0.f, allx = sx, allz = sz;
+#pragma unroll
+    for (int o = 1; o < 4; ++o) {
+      const float x = __shfl(sx, (l16 + 16 * (g + o)) & 63), z = __shfl(sz, (l16 + 16 * (g - o)) & 63);
+      bx += g + o < 4 ? x : 0.f;
+      bz += g - o >= 0 ? z : 0.f;
+    }
+    allx += __shfl_xor(allx, 16);
+    allx += __shfl_xor(allx, 32);
+    allz += __shfl_xor(allz, 16);
+    allz += __shfl_xor(allz, 32);
+    if (g == 0) {
+      tot[w4 * 32 + 16 * half + l16] = allx;
+      tot[128 + w4 * 32 + 16 * half + l16] = allz;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+      bx += o > w4 ? tot[o * 32 + 16 * half + l16] : 0.f;
+      bz += o < w4 ? tot[128 + o * 32 + 16 * half + l16] : 0.f;
+    }
+    float ax = bx;
+#pragma unroll
+    for (int r = 3; r >= 0; --r) {
+      ax += xs[r];
+      xs[r] = ax;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = t0 + r;
+      if (t < n)
+        a.dg[((size_t)(ch.tok + t) * a.heads + head) * DK + i] = (xs[r] + bz + end) / gt[r];
+      bz += zs[r];
+    }
+  }
+}
+
 // Gradients of keys and queries that several heads share: the sum over the
 // group in head order.  Rows outside every sequence are left as they were.
 template <typename T>
@@ -780,6 +1120,13 @@ hipError_t grads(const ScanArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((grads_scalar_kernel<RULE, DK, DV, T>), dim3(a.slots, a.heads), dim3(512),
                        bytes, stream, a);
   } else {
+  constexpr size_t bytes = KdaLds<DK, DV, T>::bytes;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kda_kernel<DK, DV, T>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((grads_kda_kernel<DK, DV, T>), dim3(a.slots, a.heads), dim3(512), bytes, stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const size_t lds = ((KDA ? 2 : 4) * kC * kLd + 6 * kC + DK + (KDA ? 3 * kC * DK : 0)) * sizeof(float);
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kernel<RULE, DK, DV, T>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

@@ -187,92 +187,224 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   }
 }
 
-// Gates per key channel: every pair's decay differs by channel, so the
-// triangles are summed pair by pair, lane s running down column s.  A wave
-// takes a quarter of the channels.
-template <int DK, typename T, bool BWD>
-__global__ __launch_bounds__(256) void prep_kda_kernel(ScanArgs a) {
-  constexpr int LR = DK + 1;
-  extern __shared__ float lds[];
-  float* gs = lds;                 // [64][DK + 1]
+// Gates per key channel.  With P the decay from the chunk's start,
+// G_ts = P_t / P_s channel by channel, so L and M are products of K P, Q P and
+// K / P.  That is taken where every P of the chunk lies in 2^-60 .. 2^60 (the
+// quotient then costs one rounding; a masked pair stays finite).  Chunks with
+// smaller decays, zeros among them, are summed pair by pair (slow_triangles).
+
+// The product over the lanes of a row of 16 up to (and with) this one.
+__device__ __forceinline__ float row_prefix(float x) {
+#define SEED_STEP(CTRL)                                                                       \
+  x *= __int_as_float(__builtin_amdgcn_update_dpp(0x3f800000, __float_as_int(x), CTRL, 0xf, 0xf, \
+                                                  false))
+  SEED_STEP(0x111);   // row_shr 1, 2, 4, 8
+  SEED_STEP(0x112);
+  SEED_STEP(0x114);
+  SEED_STEP(0x118);
+#undef SEED_STEP
+  return x;
+}
+
+// L and M [64][kRow] (M only for s <= t) and P, F of a chunk, any gates: lane
+// s runs down column s, a wave has 16 rows; 32 channels at a time through
+// `buf` (3 * 64 * 33 floats).
+template <int DK, typename T>
+__device__ void slow_triangles(const T* __restrict__ K, const T* __restrict__ Q, size_t ld,
+                               const float* __restrict__ gates, size_t gld, int n, float* buf,
+                               float* L, float* M, float* __restrict__ P, float* __restrict__ F) {
+  constexpr int LR = 33;
+  float* gs = buf;
   float* kk = gs + kC * LR;
   float* qq = kk + kC * LR;
-  float* Lm = qq + ((kC * LR + 3) & ~3);   // [64][kRow]
-  float* Mm = Lm + kC * kRow;
-  float* bt = Mm + kC * kRow;
-  float* X = bt + kC;                      // [4][16][20]
+  const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  float accL[16], accM[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) accL[t] = accM[t] = 0.f;
+  for (int c0 = 0; c0 < DK; c0 += 32) {
+    __syncthreads();
+    for (int e = tid; e < kC * 32; e += 256) {
+      const int t = e >> 5, i = e & 31;
+      const bool live = t < n;
+      gs[t * LR + i] = live ? gates[(size_t)t * gld + c0 + i] : 1.f;
+      kk[t * LR + i] = live ? load_scalar(K + (size_t)t * ld + c0 + i) : 0.f;
+      qq[t * LR + i] = live ? load_scalar(Q + (size_t)t * ld + c0 + i) : 0.f;
+    }
+    __syncthreads();
+    if (tid < 32) {
+      float x = 1.f;
+#pragma unroll 1
+      for (int t = 0; t < kC; ++t) {
+        x *= gs[t * LR + tid];
+        P[t * DK + c0 + tid] = x;
+      }
+      x = 1.f;
+#pragma unroll 1
+      for (int t = kC - 1; t >= 0; --t) {
+        F[t * DK + c0 + tid] = x;
+        x *= gs[t * LR + tid];
+      }
+    }
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      const float ks = kk[l * LR + i];
+      float cur = 0.f;
+#pragma unroll 1
+      for (int t = 0; t < 16 * w; ++t) cur = t > l ? cur * gs[t * LR + i] : (t == l ? ks : 0.f);
+#pragma unroll
+      for (int o = 0; o < 16; ++o) {
+        const int t = 16 * w + o;
+        cur = t > l ? cur * gs[t * LR + i] : (t == l ? ks : 0.f);
+        accL[o] += kk[t * LR + i] * cur;
+        accM[o] += qq[t * LR + i] * cur;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < 16; ++o) {
+    const int t = 16 * w + o;
+    L[t * kRow + l] = l < t ? accL[o] : 0.f;
+    M[t * kRow + l] = accM[o];
+  }
+  __syncthreads();
+}
+
+// Four waves a (chunk, head); wave w has the tokens 16 w .. + 15 as rows.
+template <int DK, typename T, bool BWD>
+__global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
+  constexpr int KS = DK / 32;
+  constexpr int KBAR = 4 * KS * 3 * kFrag * 2, SLOW = (kC * kRow + 3 * kC * 33) * 4;   // bytes
+  __shared__ __attribute__((aligned(16))) char buf[KBAR > SLOW ? KBAR : SLOW];
+  __shared__ __attribute__((aligned(16))) float L[kC * kRow];
+  __shared__ __attribute__((aligned(16))) float X[64 * 20];
+  __shared__ __attribute__((aligned(16))) float tot[4][DK];
+  __shared__ __attribute__((aligned(16))) float bt[kC];
+  __shared__ int unsafe;
+  uint16_t* kl = reinterpret_cast<uint16_t*>(buf);   // K / P in fragments
   const Chunk ch = chunk_of_slot(a, blockIdx.x);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  const int head = blockIdx.y, tid = threadIdx.x, w = tid >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
   const size_t unit = (size_t)blockIdx.x * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
+  const size_t ld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
-  const float* gg = a.g + ((size_t)ch.tok * a.heads + head) * DK;
+  const float* gates = a.g + ((size_t)ch.tok * a.heads + head) * DK;
+  float* P = reinterpret_cast<float*>(a.ws + a.at.p) + unit * kC * DK;
+  float* F = reinterpret_cast<float*>(a.ws + a.at.f) + unit * kC * DK;
+  uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
 
-  for (int e = tid; e < kC * DK; e += 256) {
-    const int t = e / DK, i = e % DK;
-    const bool live = t < ch.n;
-    gs[t * LR + i] = live ? gg[(size_t)t * a.heads * DK + i] : 1.f;
-    kk[t * LR + i] = live ? load_scalar(K + (size_t)t * a.key_heads * DK + i) : 0.f;
-    qq[t * LR + i] = live ? load_scalar(Q + (size_t)t * a.key_heads * DK + i) : 0.f;
-  }
   if (tid < kC) {
     bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
     reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + tid] = bt[tid];
   }
+  if (tid == 0) unsafe = 0;
+  const int t0 = 16 * w + l16;
+  const bool live = t0 < ch.n;
+  float p[KS][8], k[KS][8], q[KS][8];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    load_piece(gates + (size_t)t0 * gld, 32 * ks, live, p[ks]);
+    load_piece(K + (size_t)t0 * ld, 32 * ks, live, k[ks]);
+    load_piece(Q + (size_t)t0 * ld, 32 * ks, live, q[ks]);
+  }
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[ks][j] = row_prefix(live ? p[ks][j] : 1.f);
+    if (l16 == 15) {
+      float* to = &tot[w][32 * ks + 8 * g16];
+      *reinterpret_cast<f32x4*>(to) = f32x4{p[ks][0], p[ks][1], p[ks][2], p[ks][3]};
+      *reinterpret_cast<f32x4*>(to + 4) = f32x4{p[ks][4], p[ks][5], p[ks][6], p[ks][7]};
+    }
+  }
+  __syncthreads();
+  bool fine = true;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    float end[8], kb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = 32 * ks + 8 * g16 + j;
+      float before = 1.f, all = 1.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float x = tot[b][c];
+        before *= b < w ? x : 1.f;
+        all *= x;
+      }
+      const float x = p[ks][j] * before, inv = 1.f / x;
+      fine &= x >= kSafe && inv >= kSafe;
+      p[ks][j] = x;
+      end[j] = all * inv;
+      kb[j] = k[ks][j] * inv;
+      fine &= fabsf(kb[j]) <= 0x1p100f;   // no overflow in a masked pair
+      k[ks][j] *= x;
+      q[ks][j] *= x;
+    }
+    const Frag<3> f = split<3>(kb);
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+      *reinterpret_cast<u32x4*>(kl + (((w * KS + ks) * 3 + m) * 64 + l) * 8) = f.t[m];
+    float* to = P + t0 * DK + 32 * ks + 8 * g16;
+    *reinterpret_cast<f32x4*>(to) = f32x4{p[ks][0], p[ks][1], p[ks][2], p[ks][3]};
+    *reinterpret_cast<f32x4*>(to + 4) = f32x4{p[ks][4], p[ks][5], p[ks][6], p[ks][7]};
+    to = F + t0 * DK + 32 * ks + 8 * g16;
+    *reinterpret_cast<f32x4*>(to) = f32x4{end[0], end[1], end[2], end[3]};
+    *reinterpret_cast<f32x4*>(to + 4) = f32x4{end[4], end[5], end[6], end[7]};
+  }
+  if (!fine) unsafe = 1;
   __syncthreads();
 
-  float* P = reinterpret_cast<float*>(a.ws + a.at.p) + unit * kC * DK;
-  float* F = reinterpret_cast<float*>(a.ws + a.at.f) + unit * kC * DK;
-  if (tid < DK) {
-    float x = 1.f;
-    for (int t = 0; t < kC; ++t) {
-      x *= gs[t * LR + tid];
-      P[t * DK + tid] = x;
-    }
-    x = 1.f;
-    for (int t = kC - 1; t >= 0; --t) {
-      F[t * DK + tid] = x;
-      x *= gs[t * LR + tid];
-    }
-  }
-
-  float accL[kC], accM[kC];
+  if (unsafe) {
+    float* M = reinterpret_cast<float*>(buf);
+    slow_triangles<DK>(K, Q, ld, gates, gld, ch.n, M + kC * kRow, L, M, P, F);
+    for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1);
+  } else {
+    f32x4 lt[4], mt[4];
 #pragma unroll
-  for (int t = 0; t < kC; ++t) accL[t] = accM[t] = 0.f;
-  for (int i = w * (DK / 4); i < (w + 1) * (DK / 4); ++i) {
-    const float ks = kk[l * LR + i];
-    float cur = 0.f;
+    for (int b = 0; b < 4; ++b) lt[b] = mt[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < kC; ++t) {
-      cur = t > l ? cur * gs[t * LR + i] : (t == l ? ks : 0.f);
-      accL[t] += kk[t * LR + i] * cur;
-      accM[t] += qq[t * LR + i] * cur;
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<3> kt = split<3>(k[ks]), qt = split<3>(q[ks]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (b > w) continue;
+        Frag<3> kb;
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          kb.t[m] = *reinterpret_cast<const u32x4*>(kl + (((b * KS + ks) * 3 + m) * 64 + l) * 8);
+        mma(lt[b], kb, kt);
+        if (BWD) mma(mt[b], qt, kb);
+        else mma(mt[b], kb, qt);
+      }
     }
-  }
-  for (int turn = 0; turn < 4; ++turn) {
-    if (w == turn) {
 #pragma unroll
-      for (int t = 0; t < kC; ++t) {
-        const float x = t > l ? accL[t] : 0.f, y = accM[t];
-        Lm[t * kRow + l] = turn == 0 ? x : Lm[t * kRow + l] + x;
-        Mm[t * kRow + l] = turn == 0 ? y : Mm[t * kRow + l] + y;
+    for (int b = 0; b < 4; ++b) {
+      f32x4 ll = lt[b], mm = mt[b];
+      if (b == w) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          ll[r] = 4 * g16 + r < l16 ? ll[r] : 0.f;
+          mm[r] = (BWD ? l16 <= 4 * g16 + r : 4 * g16 + r <= l16) ? mm[r] : 0.f;
+        }
+      }
+      *reinterpret_cast<f32x4*>(L + (16 * w + l16) * kRow + 16 * b + 4 * g16) = ll;
+      if (BWD) {
+        if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
+      } else {
+        if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
       }
     }
     __syncthreads();
   }
-  solve(Lm, X, bt, w);
+  solve(L, X, bt, w);
   uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-  uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
-  for (int i = w; i < 8; i += 4) {
-    pack_triangle(np, Lm, false, i >> 1, i & 1);
-    pack_triangle(mp, Mm, BWD, i >> 1, i & 1);
-    if (BWD) {
-      uint16_t* tp =
-          reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
-      pack_triangle(tp, Lm, true, i >> 1, i & 1);
-    }
+  for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
+  if (BWD) {
+    uint16_t* tp =
+        reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
+    for (int i = w; i < 8; i += 4) pack_triangle(tp, L, true, i >> 1, i & 1);
   }
 }
 
@@ -280,11 +412,7 @@ template <int DK, typename T, bool BWD>
 hipError_t prep(const ScanArgs& a, hipStream_t stream) {
   const dim3 grid(a.slots, a.heads);
   if (a.rule == kKDA) {
-    const size_t lds = (3 * kC * (DK + 1) + 2 * kC * kRow + kC + 64 * 20) * sizeof(float);
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prep_kda_kernel<DK, T, BWD>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((prep_kda_kernel<DK, T, BWD>), grid, dim3(256), lds, stream, a);
+    hipLaunchKernelGGL((prep_kda_kernel<DK, T, BWD>), grid, dim3(256), 0, stream, a);
   } else if (a.rule == kGDN) {
     hipLaunchKernelGGL((prep_scalar_kernel<kGDN, DK, T, BWD>), grid, dim3(256), 0, stream, a);
   } else {

@@ -11,33 +11,6 @@ namespace seed {
 namespace scan {
 namespace {
 
-// Eight values of an array as loaded.
-template <typename T>
-struct Piece;
-template <>
-struct Piece<float> {
-  f32x4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const f32x4*>(p);
-    b = *reinterpret_cast<const f32x4*>(p + 4);
-  }
-  __device__ __forceinline__ void clear() { a = b = zero4(); }
-  __device__ __forceinline__ void get(float (&x)[8]) const { tiles_to_floats(a, b, x); }
-};
-template <>
-struct Piece<bf16_t> {
-  u32x4 a;
-  __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const u32x4*>(p); }
-  __device__ __forceinline__ void clear() { a = u32x4{0, 0, 0, 0}; }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(a[j] << 16);
-      x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-    }
-  }
-};
-
 // A thread's share of a 64 x DK operand: PPT pieces.
 template <int DK, int THREADS>
 constexpr int kShare = kC * DK / 8 / THREADS;

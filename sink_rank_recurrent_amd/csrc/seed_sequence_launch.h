@@ -25,6 +25,7 @@ struct ScanLayout {
   size_t e, y;       // E, Y: d_v floats a token (backward, delta rules)
   size_t dq, dk;     // per-head gradients of keys and queries (backward: KDA, shared heads)
   size_t tp, tf;     // gradients of P and F (backward, KDA)
+  size_t slow;       // 1 where a chunk's gradients go pair by pair (backward, KDA): one int
   size_t bytes;
 };
 
