@@ -299,41 +299,63 @@ __device__ __forceinline__ Frag<N> lds_pack(const char* pack, int frag) {
   return f;
 }
 
-// Global memory to LDS without registers: 16 bytes (or 4) a lane, the LDS
-// side 64 consecutive places from `to` (the same in every lane).  Written as
-// asm because the compiler would make every later LDS read wait for it,
-// another buffer's too; the caller waits (async_wait, then a barrier).  The
-// s_nop is the wait state an LDS load needs after M0 is written.
+// Global memory to LDS without registers: 16 bytes (or 4) a lane from `from`
+// (the same in every lane) + `off`, to 64 consecutive places from LDS offset
+// `to` (the same in every lane).  Written as asm because the compiler would
+// make every later LDS read wait for it, another buffer's too; the caller
+// waits (async_wait, then a barrier).  M0 holds the LDS side; the s_nop is
+// the wait state such a load needs after M0 is written, and M0 is put back for
+// the compiler.
 template <int BYTES>
-__device__ __forceinline__ void async_copy(const void* from, const char* to) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(
-      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to);
+__device__ __forceinline__ void async_copy(const void* from, uint32_t off, uint32_t to) {
+  uint32_t kept;
+  const uint64_t p = reinterpret_cast<uint64_t>(from);
+  const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32 |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p);
+  to = __builtin_amdgcn_readfirstlane(to);
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 ::"v"(from), "s"(at) : "memory", "m0");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
-                 ::"v"(from), "s"(at) : "memory", "m0");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                 "global_load_lds_dword %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
 }
 __device__ __forceinline__ void async_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const char* p) {
+  return __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+// The wave's number in its workgroup, as a scalar.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// A chunk's rows of a bf16 array [tokens][heads][DK] into a plane, `waves`
-// waves together; rows from n on repeat row n - 1.
-template <int DK>
-__device__ __forceinline__ void async_rows(const bf16_t* rows, size_t ld, int n, const char* plane,
-                                           int wave, int waves) {
+// A chunk's rows of bf16 arrays [tokens][heads][DK] (K, and Q if it has a
+// place) into planes, W waves together; rows from n on repeat row n - 1.
+// ld: elements from row to row.
+template <int DK, int W>
+__device__ __forceinline__ void async_rows(const bf16_t* K, const bf16_t* Q, uint32_t ld, int n,
+                                           uint32_t k_to, uint32_t q_to, bool has_q, int wave) {
   constexpr int PR = DK / 8, PER = 64 / PR;   // pieces a row, rows a step
-  for (int i = wave; i < kC / PER; i += waves) {
-    const int t = i * PER + lane_id() / PR, c = (lane_id() % PR) ^ swizzle<DK>(t);
-    async_copy<16>(rows + (size_t)(t < n ? t : n - 1) * ld + c * 8, plane + i * 1024);
+#pragma unroll
+  for (int j = 0; j < kC / PER / W; ++j) {
+    const int i = wave + j * W, t = i * PER + lane_id() / PR;
+    const int c = (lane_id() % PR) ^ swizzle<DK>(t);
+    const uint32_t off = (uint32_t)min(t, n - 1) * (2 * ld) + 16 * c;
+    async_copy<16>(K, off, k_to + i * 1024);
+    if (has_q) async_copy<16>(Q, off, q_to + i * 1024);
   }
 }
 
-// `frags` fragments of a pack with N of the three terms it holds.
-template <int N>
-__device__ __forceinline__ void async_pack(const uint16_t* pack, const char* to, int wave, int waves) {
-  for (int i = wave; i < kTriFrags * N; i += waves)
-    async_copy<16>(pack + (size_t)(i / N * 3 + i % N) * kFrag + lane_id() * 8, to + i * 1024);
+// The first N of the three terms of a pack's fragments.
+template <int N, int W>
+__device__ __forceinline__ void async_pack(const uint16_t* pack, uint32_t to, int wave) {
+#pragma unroll
+  for (int j = 0; j < (kTriFrags * N + W - 1) / W; ++j) {
+    const int i = wave + j * W;
+    if (i < kTriFrags * N)
+      async_copy<16>(pack + (i / N * 3 + i % N) * kFrag, lane_id() * 16, to + i * 1024);
+  }
 }
 
 // Eight channels from col0 + 8 g of a row.

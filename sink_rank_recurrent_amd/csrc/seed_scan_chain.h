@@ -21,39 +21,41 @@ __device__ __forceinline__ f32x4 lds_vec(const char* vec, int m) {
   return *reinterpret_cast<const f32x4*>(vec + 64 * m + 16 * (lane_id() >> 4));
 }
 
-// 16 columns of a bf16 array as raw accumulator tiles, rows from n on 0.
-struct RawTiles {
-  uint16_t x[4][4];
-};
-// p: the same address in every lane; `lane`: the lane's offset, 4 g rows and
-// its column.
-__device__ __forceinline__ RawTiles load_raw(const bf16_t* p, size_t ld, uint32_t lane, int n) {
-  RawTiles v;
-  if (n >= kC) {   // a whole chunk: no row to test
+// A wave's 64 rows x 16 columns of a bf16 array, in 2 KB of LDS of its own
+// (rows of 32 bytes).  Loads repeat row n - 1 from row n on.
+__device__ __forceinline__ void wave_load(const bf16_t* p, uint32_t ld, int n, uint32_t to) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bf16_t* row = p + (size_t)(16 * m + r) * ld;
-        v.x[m][r] = row[lane];
-      }
-    return v;
+  for (int i = 0; i < 2; ++i) {
+    const int t = 32 * i + (lane_id() >> 1);
+    async_copy<16>(p, (uint32_t)min(t, n - 1) * (2 * ld) + 16 * (lane_id() & 1), to + 1024 * i);
   }
+}
+// As accumulator tiles, by transposing reads.
+__device__ __forceinline__ f32x4 wave_tile(const char* from, int m) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const int l = lane_id(), i = l & 15, g = l >> 4;
+  const char* at = from + (16 * m + 4 * g + (i >> 2)) * 32 + 8 * (i & 3);
+  const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                                                (__attribute__((address_space(3))) bf16x4*)(at)));
+  return f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u),
+               __uint_as_float(x[1] << 16), __uint_as_float(x[1] & 0xffff0000u)};
+}
+// Accumulator tiles out through the same place: rows of 16 bytes a lane.
+__device__ __forceinline__ void wave_store(bf16_t* p, size_t ld, int n, const f32x4 (&x)[4], char* by) {
+  const int l = lane_id();
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * m + 4 * (lane_id() >> 4) + r;
-      const bf16_t* row = p + (size_t)(16 * m + r) * ld;
-      v.x[m][r] = t < n ? row[lane] : 0;
-    }
-  return v;
-}
-__device__ __forceinline__ f32x4 tile_of(const RawTiles& v, int m) {
-  f32x4 x;
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<bf16_t*>(by + (16 * m + 4 * (l >> 4) + r) * 32 + 2 * (l & 15)) =
+          (bf16_t)round_pair(x[m][r], 0.f);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = bf16_bits_to_f32(v.x[m][r]);
-  return x;
+  for (int i = 0; i < 2; ++i) {
+    const int t = 32 * i + (l >> 1);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(by + 1024 * i + 16 * l);
+    if (t < n) *reinterpret_cast<u32x4*>(p + (size_t)t * ld + 8 * (l & 1)) = v;
+  }
 }
 template <typename T>
 __device__ __forceinline__ void store_tiles(T* p, size_t ld, uint32_t lane, int n,
@@ -87,6 +89,13 @@ __device__ __forceinline__ void keep_state(float* p, int ld, uint32_t lane, cons
       float* row = p + (32 * (m >> 1) + 4 * (m & 1) + r) * ld;
       row[lane] = x[m][r];
     }
+}
+// A chunk's state in the workspace, [d_v][DK]: four channels a lane in a row.
+template <int IT>
+__device__ __forceinline__ void keep_chunk_state(float* p, int col, const f32x4 (&x)[IT]) {
+#pragma unroll
+  for (int m = 0; m < IT; ++m)
+    *reinterpret_cast<f32x4*>(p + col * (16 * IT) + state_row(m)) = x[m];
 }
 template <int IT>
 __device__ __forceinline__ void load_state(const float* p, int ld, uint32_t lane, f32x4 (&x)[IT]) {
@@ -139,16 +148,26 @@ struct Piece<bf16_t> {
 // Where a workgroup's columns are: grid n_seq * heads * (d_v / (16 NW)).
 template <int NW>
 struct Place {
-  int seq, head, hk, col;
+  int seq, head, hk, col0, col;   // col0: the wave's first column
   __device__ __forceinline__ explicit Place(const ScanArgs& a) {
     const int blocks = a.d_v / (16 * NW);
     const int sh = blockIdx.x / blocks;
     seq = sh / a.heads;
     head = sh % a.heads;
     hk = head / (a.heads / a.key_heads);
-    col = (blockIdx.x % blocks) * 16 * NW + (threadIdx.x >> 6) * 16 + (lane_id() & 15);
+    col0 = (blockIdx.x % blocks) * 16 * NW + wave_id() * 16;
+    col = col0 + (lane_id() & 15);
   }
 };
+
+// Waves of a workgroup: all of a head's columns, or half of 128 where whole
+// heads would leave some of the 256 CUs idle (backward of 64 x 32 chunks of
+// 128 x 128 GDN heads: 212 us with four waves, 253 us with eight; forward of
+// 1024 x 8 chunks: 385 us with four, 234 us with eight).
+inline int walk_waves(const ScanArgs& a) {
+  const int all = a.d_v / 16;
+  return all == 8 && (long long)a.n_seq * a.heads < 256 ? 4 : all;
+}
 
 }  // namespace scan
 }  // namespace seed

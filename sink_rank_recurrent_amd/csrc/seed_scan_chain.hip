@@ -28,21 +28,20 @@ struct Stage {
   static constexpr int vec = m + (HAS_M ? kTriFrags * MT * 1024 : 0);   // P, F, beta
   static constexpr int bytes = vec + 768;
 
-  static __device__ __forceinline__ void load(const ScanArgs& a, char* to, const bf16_t* K,
-                                              const bf16_t* Q, size_t ld, size_t unit, int rows,
-                                              bool transposed, int w, int waves) {
-    async_rows<DK>(K, ld, rows, to, w, waves);
-    if (K_Q) async_rows<DK>(Q, ld, rows, to + q, w, waves);
+  template <int W>
+  static __device__ __forceinline__ void load(const ScanArgs& a, uint32_t to, const bf16_t* K,
+                                              const bf16_t* Q, uint32_t ld, size_t unit, int rows,
+                                              bool transposed, int w) {
+    async_rows<DK, W>(K, Q, ld, rows, to, to + q, K_Q, w);
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<NT>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
-                        unit * pack, to + n, w, waves);
+      async_pack<NT, W>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
+                            unit * pack, to + n, w);
     if (HAS_M)
-      async_pack<MT>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w,
-                     waves);
-    for (int i = w; i < (DELTA ? 3 : 2); i += waves)
-      async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
-                        (unit * kC + lane_id()) * sizeof(float), to + vec + 256 * i);
+      async_pack<MT, W>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w);
+    if (w < (DELTA ? 3 : 2))
+      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
+                    lane_id() * 4, to + vec + 256 * w);
   }
 };
 
@@ -54,50 +53,50 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
   constexpr int IT = DK / 16, NT = SAVE ? 3 : 2;   // terms of the corrections
   using St = Stage<RULE, DK, !SAVE, NT, 2, !SAVE>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int w = threadIdx.x >> 6;
+  const int w = wave_id();
   const Place<NW> at(a);
+  const uint32_t lds0 = lds_offset(lds), mine0 = lds0 + 2 * St::bytes + 2048 * w;
   const Range rg = sequence(a, at.seq);
   const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
-  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t g = lane_id() >> 4;
   const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
   const bf16_t* K = static_cast<const bf16_t*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
   const bf16_t* Q = static_cast<const bf16_t*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
-  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v + at.col0;
   const bf16_t* V = static_cast<const bf16_t*>(a.v) + vat;
   bf16_t* out = static_cast<bf16_t*>(a.o) + vat;
 
   f32x4 S[IT];
   load_state(a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
 
-  RawTiles v{};
+  char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of V, then of O
   if (chunks > 0) {
-    St::load(a, lds, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w, NW);
-    v = load_raw(V, vld, row_lane, min(kC, rg.len));
+    St::template load<NW>(a, lds0, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w);
+    wave_load(V, vld, min(kC, rg.len), mine0);
     async_wait();
     __syncthreads();
   }
-  f32x4 O[4];
   for (int c = 0; c < chunks; ++c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     const char* now = lds + (c & 1) * St::bytes;
-    // the chunk before's read-outs leave while this one is computed
-    if (!SAVE && c > 0) store_tiles(out + (size_t)(c - 1) * kC * vld, vld, row_lane, kC, O);
-    RawTiles next = v;
+    f32x4 u[4], R[4], O[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      u[m] = wave_tile(mine, m);
+      R[m] = O[m] = zero4();
+    }
+    drop_rows(u, n);
     if (c + 1 < chunks) {
       const int rows = min(kC, rg.len - (c + 1) * kC);
-      St::load(a, lds + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
-               Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, rows, false, w, NW);
-      next = load_raw(V + (size_t)(c + 1) * kC * vld, vld, row_lane, rows);
+      St::template load<NW>(a, lds0 + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
+                            Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, rows, false, w);
     }
     if (SAVE)
-      keep_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, a.d_v, state_lane, S);
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col, S);
 
-    f32x4 R[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) R[m] = O[m] = zero4();
     if (DELTA || !SAVE) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
@@ -115,11 +114,9 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
         }
       }
     }
-    f32x4 u[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const f32x4 p = lds_vec(now + St::vec, m);
-      u[m] = tile_of(v, m);
       if (DELTA) u[m] -= p * R[m];
       O[m] *= p;
     }
@@ -163,7 +160,10 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
       mma_tiles<2, 2, NU, 2>(z, h, x1);
       O[2] = z[0];
       O[3] = z[1];
+      wave_store(out + (size_t)c * kC * vld, vld, n, O, mine);
     }
+    if (c + 1 < chunks)
+      wave_load(V + (size_t)(c + 1) * kC * vld, vld, min(kC, rg.len - (c + 1) * kC), mine0);
     // S' = P_end S + K^T (F u)
     const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
 #pragma unroll
@@ -178,15 +178,10 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
       for (int m = 0; m < IT; ++m) f[m] = lds_cols<DK, 1>(now, m, ks);
       mma_tiles(S, f, x);
     }
-    v = next;
     async_wait();
     __syncthreads();
   }
-  if (!SAVE) {
-    if (chunks > 0)
-      store_tiles(out + (size_t)(chunks - 1) * kC * vld, vld, row_lane, rg.len - (chunks - 1) * kC, O);
-    keep_state(a.S + state, a.d_v, state_lane, S);
-  }
+  if (!SAVE) keep_state(a.S + state, a.d_v, state_lane, S);
 }
 
 // The chunks from the last to the first, H the gradient of the state behind
@@ -197,29 +192,31 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   constexpr int IT = DK / 16;
   using St = Stage<RULE, DK, true, 3, 3, true>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int w = threadIdx.x >> 6;
+  const int w = wave_id();
   const Place<NW> at(a);
+  const uint32_t lds0 = lds_offset(lds), mine0 = lds0 + 2 * St::bytes + 2048 * w;
   const Range rg = sequence(a, at.seq);
   const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
-  const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
+  const uint32_t g = lane_id() >> 4;
   const uint32_t keep_lane = 4 * g * a.d_v + at.col, state_lane = 8 * g * a.d_v + at.col;
   const bf16_t* K = static_cast<const bf16_t*>(a.k) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
   const bf16_t* Q = static_cast<const bf16_t*>(a.q) + ((size_t)rg.start * a.key_heads + at.hk) * DK;
-  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v;
+  const size_t vat = ((size_t)rg.start * a.heads + at.head) * a.d_v + at.col0;
   const bf16_t* dO = static_cast<const bf16_t*>(a.dO) + vat;
   bf16_t* dV = static_cast<bf16_t*>(a.dv) + vat;
 
   f32x4 H[IT];
   load_state(a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
 
-  RawTiles d{};
+  char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of dO, then of dV
   if (chunks > 0) {
     const int c = chunks - 1, rows = rg.len - c * kC;
-    St::load(a, lds + (c & 1) * St::bytes, K + (size_t)c * kC * kld, Q + (size_t)c * kC * kld, kld,
-             (size_t)(base + c) * a.heads + at.head, rows, true, w, NW);
-    d = load_raw(dO + (size_t)c * kC * vld, vld, row_lane, rows);
+    St::template load<NW>(a, lds0 + (c & 1) * St::bytes, K + (size_t)c * kC * kld,
+                          Q + (size_t)c * kC * kld, kld, (size_t)(base + c) * a.heads + at.head, rows,
+                          true, w);
+    wave_load(dO + (size_t)c * kC * vld, vld, rows, mine0);
     async_wait();
     __syncthreads();
   }
@@ -227,21 +224,20 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     const char* now = lds + (c & 1) * St::bytes;
-    RawTiles next = d;
     if (c > 0) {
-      St::load(a, lds + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
-               Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w, NW);
-      next = load_raw(dO + (size_t)(c - 1) * kC * vld, vld, row_lane, kC);
+      St::template load<NW>(a, lds0 + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
+                            Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w);
     }
-    keep_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, a.d_v, state_lane, H);
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col, H);
 
     // dU = F (K H) + M^T dO
     f32x4 y[4], go[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       y[m] = zero4();
-      go[m] = tile_of(d, m);
+      go[m] = wave_tile(mine, m);
     }
+    drop_rows(go, n);
 #pragma unroll
     for (int ks = 0; ks < DK / 32; ++ks) {
       const Frag<3> h = split_tiles<3>(H[2 * ks], H[2 * ks + 1]);
@@ -291,7 +287,8 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= b[m];
     }
-    store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+    wave_store(dV + (size_t)c * kC * vld, vld, n, y, mine);
+    if (c > 0) wave_load(dO + (size_t)(c - 1) * kC * vld, vld, kC, mine0);
 
     // dS = P_end H + Q^T (P dO) - K^T (P dR)
     const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
@@ -317,7 +314,6 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
         mma_tiles(H, f, z);
       }
     }
-    d = next;
     async_wait();
     __syncthreads();
   }
@@ -338,17 +334,18 @@ template <int RULE, int DK, int NW>
 hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
   if (what == 0)
     return launch(chain_forward_kernel<RULE, DK, NW, false>, a, NW,
-                  2 * Stage<RULE, DK, true, 2, 2, true>::bytes, stream);
+                  2 * Stage<RULE, DK, true, 2, 2, true>::bytes + 2048 * NW, stream);
   if (what == 1)
     return launch(chain_forward_kernel<RULE, DK, NW, true>, a, NW,
-                  2 * Stage<RULE, DK, false, 3, 2, false>::bytes, stream);
-  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, 3, true>::bytes,
+                  2 * Stage<RULE, DK, false, 3, 2, false>::bytes + 2048 * NW, stream);
+  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, 3, true>::bytes + 2048 * NW,
                 stream);
 }
 template <int RULE>
 hipError_t chain_shape(const ScanArgs& a, int what, hipStream_t stream) {
   if (a.d_k == 64) return chain<RULE, 64, 4>(a, what, stream);
-  return a.d_v == 128 ? chain<RULE, 128, 8>(a, what, stream) : chain<RULE, 128, 4>(a, what, stream);
+  return walk_waves(a) == 4 ? chain<RULE, 128, 4>(a, what, stream)
+                            : chain<RULE, 128, 8>(a, what, stream);
 }
 
 }  // namespace

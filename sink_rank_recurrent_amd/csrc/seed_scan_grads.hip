@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
     float all = 0.f;
     for (int i = w; i < DK; i += 4) {
       float x = 0.f;
-      for (int j = l; j < DV; j += 64) x += Sc[(size_t)i * DV + j] * Hc[(size_t)i * DV + j];
+      for (int j = l; j < DV; j += 64) x += Sc[(size_t)j * DK + i] * Hc[(size_t)j * DK + i];
       if (KDA) {
         x = sum64(x);
         if (l == 0) hs[i] = x;
@@ -197,11 +197,11 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
 #pragma unroll
     for (int ks = 0; ks < DV / 32; ++ks) {
       float x[8];
-      load_row8(Sc + (size_t)i * DV, 32 * ks, true, x);
+      load_col8(Sc + i, DK, 32 * ks, DV, x);
       const Frag<3> s = split<3>(x);
       mma(x1, rows_do(w, ks), s);
       if (DELTA) mma(x2, rows_dr(w, ks), s);
-      load_row8(Hc + (size_t)i * DV, 32 * ks, true, x);
+      load_col8(Hc + i, DK, 32 * ks, DV, x);
       mma(x3, rows_u(w, ks), split<3>(x));
     }
     f32x4 dq, dk;
@@ -390,6 +390,31 @@ __device__ __forceinline__ void mat_cols(const float* mat, int col, int ks, floa
   for (int j = 0; j < 8; ++j) x[j] = at[(16 * (j >> 2) + (j & 3)) * kRow];
 }
 
+// 32 channels of an array by rows of 64 bytes, pieces of 16: piece c of row t
+// at c ^ (t / 4) % 4.  As a fragment: channels 16 half .. + 15, contracted over
+// rows 32 ks .. + 31, by transposing reads.
+__device__ __forceinline__ int part_at(int t, int c) { return t * 64 + ((c ^ ((t >> 2) & 3)) << 4); }
+template <int PLANE>
+__device__ __forceinline__ Frag<3> part_cols(const char* planes, int half, int ks) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const int l = lane_id(), i = l & 15, g = l >> 4;
+  Frag<3> f;
+#pragma unroll
+  for (int m = 0; m < 3; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 32 * ks + 16 * h + 4 * g + (i >> 2);
+      const char* at = planes + m * PLANE + part_at(t, 2 * half + ((i & 3) >> 1)) + 8 * (i & 1);
+      const u32x2 x = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                     (__attribute__((address_space(3))) bf16x4*)(at)));
+      f.t[m][2 * h] = x[0];
+      f.t[m][2 * h + 1] = x[1];
+    }
+  return f;
+}
+
 // Scalar gates.  Eight waves a (chunk, head): wave (rows 16 w4, half) has the
 // 16 tokens' rows of dO, dR and u in registers and every other 16 columns of
 // each result.  First the pairs inside the chunk (K and Q in LDS, u of the
@@ -437,8 +462,7 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
 
   // K and Q into LDS
   if constexpr (NT == 1) {
-    async_rows<DK>(K, kld, n, Kp, tid >> 6, 8);
-    async_rows<DK>(Q, kld, n, Qp, tid >> 6, 8);
+    async_rows<DK, 8>(K, Q, kld, n, lds_offset(Kp), lds_offset(Qp), true, wave_id());
   } else {
     for (int i = tid; i < 2 * kC * (DK / 8); i += 512) {
       const int which = i / (kC * (DK / 8)), t = i / (DK / 8) % kC, c = i % (DK / 8);
@@ -476,11 +500,11 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       float x[8], y[8];
-      load_piece(dO, 32 * ks, live, x);
+      load_row8(dO, 32 * ks, live, x);
       ado[ks] = split<NT>(x);
       if constexpr (DELTA) {
-        load_piece(E, 32 * ks, live, x);
-        load_piece(Y, 32 * ks, live, y);
+        load_row8(E, 32 * ks, live, x);
+        load_row8(Y, 32 * ks, live, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           db += x[j] * y[j];
@@ -489,7 +513,7 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
         }
         adr[ks] = split<3>(y);
       } else {
-        load_piece(V, 32 * ks, live, x);
+        load_row8(V, 32 * ks, live, x);
       }
       au[ks] = split<NE>(x);
       if (w4 < 3 && half == 0) {
@@ -630,12 +654,11 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
   }
 
   // through the states, 32 channels at a time: rows of 8 values a thread
-  constexpr int PR = DV / 8;
-  const bool stager = tid < 32 * PR;
+  const bool stager = tid < 4 * DV;
   float sv[8], hv[8], hsum = 0.f;
   auto fetch = [&](int part) {
     if (!stager) return;
-    const size_t at = (size_t)(32 * part + tid / PR) * DV + 8 * (tid % PR);
+    const size_t at = (size_t)(tid >> 2) * DK + 32 * part + 8 * (tid & 3);
     float y[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -656,7 +679,7 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
   for (int part = 0; part < MT; ++part) {
     __syncthreads();
     if (stager) {
-      const int at = piece_at<DV>(tid / PR, tid % PR);
+      const int at = part_at(tid >> 2, tid & 3);
       const Frag<3> s = split<3>(sv), h = split<3>(hv);
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
@@ -672,13 +695,8 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
     f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int at = piece_at<DV>(16 * half + l16, 4 * ks + g);
-      Frag<3> s, h;
-#pragma unroll
-      for (int m = 0; m < 3; ++m) {
-        s.t[m] = *reinterpret_cast<const u32x4*>(smem + m * Lds::plane + at);
-        h.t[m] = *reinterpret_cast<const u32x4*>(smem + (3 + m) * Lds::plane + at);
-      }
+      const Frag<3> s = part_cols<Lds::plane>(smem, half, ks);
+      const Frag<3> h = part_cols<Lds::plane>(smem + 3 * Lds::plane, half, ks);
       mma(x1, ado[ks], s);
       if constexpr (DELTA) mma(x2, adr[ks], s);
       mma(x3, au[ks], h);
@@ -761,7 +779,7 @@ struct KdaLds {
   static constexpr int s = u > mats ? u : mats;
   static constexpr int k = s + 6 * plane;
   static constexpr int small = k + 9 * kplane;
-  static constexpr int bytes = small + (4 * 2 * 32 + 32 + 8) * 4;
+  static constexpr int bytes = small + (4 * 2 * 32 + 8 * 32 + 8) * 4;
 };
 
 template <int DK, int DV, typename T>
@@ -774,8 +792,8 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   char* Sp = smem + Lds::s;
   char* Kp = smem + Lds::k;                     // K', K~, Q~: three planes each
   float* tot = reinterpret_cast<float*>(smem + Lds::small);   // [x, z][4][32]
-  float* hs = tot + 4 * 2 * 32;                 // [32]
-  int* bad = reinterpret_cast<int*>(hs + 32);
+  float* hs = tot + 4 * 2 * 32;                 // [wave][32]
+  int* bad = reinterpret_cast<int*>(hs + 8 * 32);
   const Chunk ch = chunk_of_slot(a, blockIdx.x);
   if (ch.n == 0) return;
   const int head = blockIdx.y, tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
@@ -824,10 +842,10 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       float x[8], y[8];
-      load_piece(dO, 32 * ks, live, x);
+      load_row8(dO, 32 * ks, live, x);
       ado[ks] = split<NT>(x);
-      load_piece(E, 32 * ks, live, x);
-      load_piece(Y, 32 * ks, live, y);
+      load_row8(E, 32 * ks, live, x);
+      load_row8(Y, 32 * ks, live, y);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         db += x[j] * y[j];
@@ -886,13 +904,12 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
     }
   }
 
-  constexpr int PR = DV / 8;
-  const bool stager = tid < 32 * PR;
+  const bool stager = tid < 4 * DV;
   float sv[8], hv[8], pv[8];
   Piece<T> kv, qv;
   auto fetch = [&](int part) {
     if (stager) {
-      const int at = (32 * part + tid / PR) * DV + 8 * (tid % PR);
+      const int at = (tid >> 2) * DK + 32 * part + 8 * (tid & 3);
       float y[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -921,44 +938,26 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
       }
     }
   };
-  auto kplane_at = [](int t, int c) { return t * 64 + ((c ^ ((t >> 2) & 3)) << 4); };
-  auto cols = [&](const char* planes, int ks) {   // channels 16 half .. + 15
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    Frag<3> f;
-#pragma unroll
-    for (int m = 0; m < 3; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = 32 * ks + 16 * h + 4 * g + (l16 >> 2);
-        const char* at = planes + m * Lds::kplane + kplane_at(t, 2 * half + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
-        const u32x2 x = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                       (__attribute__((address_space(3))) bf16x4*)(at)));
-        f.t[m][2 * h] = x[0];
-        f.t[m][2 * h + 1] = x[1];
-      }
-    return f;
-  };
   const bool shared = a.key_heads != a.heads;
   fetch(0);
   for (int part = 0; part < MT; ++part) {
     __syncthreads();
     if (stager) {
-      const int at = piece_at<DV>(tid / PR, tid % PR);
+      const int at = part_at(tid >> 2, tid & 3);
       const Frag<3> s = split<3>(sv), h = split<3>(hv);
-      float x = 0.f;
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         *reinterpret_cast<u32x4*>(Sp + m * Lds::plane + at) = s.t[m];
         *reinterpret_cast<u32x4*>(Sp + (3 + m) * Lds::plane + at) = h.t[m];
       }
+      // <H, S> by channel: a wave's 16 rows
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x += sv[j] * hv[j];
-      // <H, S> of the thread's channel: PR neighbouring lanes
+      for (int j = 0; j < 8; ++j) {
+        float x = sv[j] * hv[j];
 #pragma unroll
-      for (int o = 1; o < PR; o *= 2) x += __shfl_xor(x, o);
-      if (tid % PR == 0) hs[tid / PR] = x;
+        for (int o = 4; o < 64; o *= 2) x += __shfl_xor(x, o);
+        if (l < 4) hs[(tid >> 6) * 32 + 8 * l + j] = x;
+      }
     }
     if (tid < 256) {
       float x[8], y[8], z[8];
@@ -970,7 +969,7 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
         y[j] *= pv[j];
         z[j] *= pv[j];
       }
-      const int at = kplane_at(tid >> 2, tid & 3);
+      const int at = part_at(tid >> 2, tid & 3);
       const Frag<3> f0 = split<3>(x), f1 = split<3>(y), f2 = split<3>(z);
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
@@ -984,13 +983,8 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
     f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1, a1 = x1, a2 = x1, a3 = x1;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int at = piece_at<DV>(16 * half + l16, 4 * ks + g);
-      Frag<3> s, h;
-#pragma unroll
-      for (int m = 0; m < 3; ++m) {
-        s.t[m] = *reinterpret_cast<const u32x4*>(Sp + m * Lds::plane + at);
-        h.t[m] = *reinterpret_cast<const u32x4*>(Sp + (3 + m) * Lds::plane + at);
-      }
+      const Frag<3> s = part_cols<Lds::plane>(Sp, half, ks);
+      const Frag<3> h = part_cols<Lds::plane>(Sp + 3 * Lds::plane, half, ks);
       mma(x1, ado[ks], s);
       mma(x2, adr[ks], s);
       mma(x3, au[ks], h);
@@ -1006,12 +1000,15 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
       k[r] = t < n ? load_scalar(K + (size_t)t * kld + i) : 0.f;
       gt[r] = t < n ? gates[(size_t)t * gld + i] : 1.f;
     }
-    const float end = P[(kC - 1) * DK + i] * hs[16 * half + l16];
+    float end = 0.f;
+#pragma unroll
+    for (int o = 0; o < DV / 16; ++o) end += hs[o * 32 + 16 * half + l16];
+    end *= P[(kC - 1) * DK + i];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       float x[8];
       if (ks <= (w4 >> 1)) {
-        const Frag<3> f = cols(Kp, ks);
+        const Frag<3> f = part_cols<Lds::kplane>(Kp, half, ks);
         mat_rows(m1, row, ks, x);
         mma(a1, split<3>(x), f);
         mat_rows(m0, row, ks, x);
@@ -1019,9 +1016,9 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
       }
       if (ks >= (w4 >> 1)) {
         mat_cols(m0, row, ks, x);
-        mma(a3, split<3>(x), cols(Kp + 3 * Lds::kplane, ks));
+        mma(a3, split<3>(x), part_cols<Lds::kplane>(Kp + 3 * Lds::kplane, half, ks));
         mat_cols(m1, row, ks, x);
-        mma(a3, split<3>(x), cols(Kp + 6 * Lds::kplane, ks));
+        mma(a3, split<3>(x), part_cols<Lds::kplane>(Kp + 6 * Lds::kplane, half, ks));
       }
     }
     float xs[4], zs[4];

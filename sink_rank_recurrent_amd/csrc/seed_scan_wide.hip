@@ -88,8 +88,9 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
   constexpr bool KDA = W::KDA, DELTA = W::DELTA;
   constexpr int IT = DK / 16, NC = W::NC, TH = 64 * NW;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int w = threadIdx.x >> 6;
+  const int w = wave_id();
   const Place<NW> at(a);
+  const uint32_t lds0 = lds_offset(lds);
   const Range rg = sequence(a, at.seq);
   const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
@@ -127,15 +128,12 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     __syncthreads();   // the chunk before is done with the planes
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<NC>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds + W::n,
-                     w, NW);
+      async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
     if (!SAVE)
-      async_pack<NC>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds + W::m,
-                     w, NW);
-    for (int i = w; i < (DELTA ? 3 : 2); i += NW)
-      if (!KDA || i == 2)
-        async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
-                          (unit * kC + lane_id()) * sizeof(float), lds + W::vec + 256 * i);
+      async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
+    if (w < (DELTA ? 3 : 2) && (!KDA || w == 2))
+      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
+                    lane_id() * 4, lds0 + W::vec + 256 * w);
     if (KDA) {
       if (DELTA) fill<DK, TH, NC, true>(lds, kr, pr);
       if (!SAVE) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
@@ -149,7 +147,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     async_wait();
     __syncthreads();
     if (SAVE)
-      keep_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, a.d_v, state_lane, S);
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col, S);
     if (!KDA && c + 1 < chunks) fetch(c + 1);
 
     f32x4 R[4], O[4];
@@ -279,8 +277,9 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
   constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
   constexpr int IT = DK / 16, TH = 64 * NW, NV = sizeof(T) == 2 ? 1 : 3;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int w = threadIdx.x >> 6;
+  const int w = wave_id();
   const Place<NW> at(a);
+  const uint32_t lds0 = lds_offset(lds);
   const Range rg = sequence(a, at.seq);
   const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
@@ -317,14 +316,11 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     __syncthreads();
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds + W::n,
-                    w, NW);
-    async_pack<3>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds + W::m, w,
-                  NW);
-    for (int i = w; i < (DELTA ? 3 : 2); i += NW)
-      if (!KDA || i == 2)
-        async_copy<4>(a.ws + (i == 0 ? a.at.p : i == 1 ? a.at.f : a.at.b) +
-                          (unit * kC + lane_id()) * sizeof(float), lds + W::vec + 256 * i);
+      async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds0 + W::n, w);
+    async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
+    if (w < (DELTA ? 3 : 2) && (!KDA || w == 2))
+      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
+                    lane_id() * 4, lds0 + W::vec + 256 * w);
     if (KDA) {
       fill<DK, TH, 3, true>(lds, kr, fr);
       fill<DK, TH, 3, true>(lds + W::q, qr, pr);
@@ -340,7 +336,7 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     }
     async_wait();
     __syncthreads();
-    keep_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, a.d_v, state_lane, H);
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col, H);
     if (!KDA && c > 0) fetch(c - 1);
 
     // dU = F (K H) + M^T dO
@@ -475,7 +471,8 @@ hipError_t wide(const ScanArgs& a, int what, hipStream_t stream) {
 template <int RULE, typename T>
 hipError_t wide_shape(const ScanArgs& a, int what, hipStream_t stream) {
   if (a.d_k == 64) return wide<RULE, 64, 4, T>(a, what, stream);
-  return a.d_v == 128 ? wide<RULE, 128, 8, T>(a, what, stream) : wide<RULE, 128, 4, T>(a, what, stream);
+  return walk_waves(a) == 4 ? wide<RULE, 128, 4, T>(a, what, stream)
+                            : wide<RULE, 128, 8, T>(a, what, stream);
 }
 
 }  // namespace
