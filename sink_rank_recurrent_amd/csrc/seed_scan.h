@@ -299,28 +299,22 @@ __device__ __forceinline__ Frag<N> lds_pack(const char* pack, int frag) {
   return f;
 }
 
-// Global memory to LDS without registers: 16 bytes (or 4) a lane from `from`
-// (the same in every lane) + `off`, to 64 consecutive places from LDS offset
-// `to` (the same in every lane).  Written as asm because the compiler would
-// make every later LDS read wait for it, another buffer's too; the caller
-// waits (async_wait, then a barrier).  M0 holds the LDS side; the s_nop is
-// the wait state such a load needs after M0 is written, and M0 is put back for
-// the compiler.
-template <int BYTES>
+// Global memory to LDS without registers: 16 bytes a lane from `from` (the
+// same in every lane) + `off`, to 64 consecutive places from LDS offset `to`
+// (the same in every lane).  Written as asm because the compiler would make
+// every later LDS read wait for it, another buffer's too; the caller waits
+// (async_wait, then a barrier).  M0 holds the LDS side; the s_nop is the wait
+// state such a load needs after M0 is written, and M0 is put back for the
+// compiler.
 __device__ __forceinline__ void async_copy(const void* from, uint32_t off, uint32_t to) {
   uint32_t kept;
   const uint64_t p = reinterpret_cast<uint64_t>(from);
   const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32 |
                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p);
   to = __builtin_amdgcn_readfirstlane(to);
-  if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
-                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
-                 : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
-  else
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
-                 "global_load_lds_dword %1, %2\n\ts_mov_b32 m0, %0"
-                 : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+               "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+               : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
 }
 __device__ __forceinline__ void async_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_offset(const char* p) {
@@ -342,8 +336,8 @@ __device__ __forceinline__ void async_rows(const bf16_t* K, const bf16_t* Q, uin
     const int i = wave + j * W, t = i * PER + lane_id() / PR;
     const int c = (lane_id() % PR) ^ swizzle<DK>(t);
     const uint32_t off = (uint32_t)min(t, n - 1) * (2 * ld) + 16 * c;
-    async_copy<16>(K, off, k_to + i * 1024);
-    if (has_q) async_copy<16>(Q, off, q_to + i * 1024);
+    async_copy(K, off, k_to + i * 1024);
+    if (has_q) async_copy(Q, off, q_to + i * 1024);
   }
 }
 
@@ -354,7 +348,7 @@ __device__ __forceinline__ void async_pack(const uint16_t* pack, uint32_t to, in
   for (int j = 0; j < (kTriFrags * N + W - 1) / W; ++j) {
     const int i = wave + j * W;
     if (i < kTriFrags * N)
-      async_copy<16>(pack + (i / N * 3 + i % N) * kFrag, lane_id() * 16, to + i * 1024);
+      async_copy(pack + (i / N * 3 + i % N) * kFrag, lane_id() * 16, to + i * 1024);
   }
 }
 

@@ -21,9 +21,9 @@ ScanLayout scan_layout(int rule, int n_seq, int heads, int key_heads, int d_k, i
   l.n_pack = part(delta, units * pack);
   l.nt_pack = part(delta && backward, units * pack);
   l.m_pack = part(true, units * pack);
-  l.p = part(true, per_token * (kda ? d_k : 1));
-  l.f = part(true, per_token * (kda ? d_k : 1));
-  l.b = part(delta, per_token);
+  l.vec = part(true, 4 * per_token);
+  l.p = part(kda, per_token * d_k);
+  l.f = part(kda, per_token * d_k);
   l.state = part(backward, units * d_k * d_v * sizeof(float));
   l.grad = part(backward, units * d_k * d_v * sizeof(float));
   l.e = part(backward && delta, per_token * d_v);

@@ -27,7 +27,7 @@ __device__ __forceinline__ void wave_load(const bf16_t* p, uint32_t ld, int n, u
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = 32 * i + (lane_id() >> 1);
-    async_copy<16>(p, (uint32_t)min(t, n - 1) * (2 * ld) + 16 * (lane_id() & 1), to + 1024 * i);
+    async_copy(p, (uint32_t)min(t, n - 1) * (2 * ld) + 16 * (lane_id() & 1), to + 1024 * i);
   }
 }
 // As accumulator tiles, by transposing reads.
@@ -90,12 +90,18 @@ __device__ __forceinline__ void keep_state(float* p, int ld, uint32_t lane, cons
       row[lane] = x[m][r];
     }
 }
-// A chunk's state in the workspace, [d_v][DK]: four channels a lane in a row.
+// A chunk's state in the workspace, in the order the waves hold it: 16
+// columns, then their tiles, 1 KB each.
 template <int IT>
-__device__ __forceinline__ void keep_chunk_state(float* p, int col, const f32x4 (&x)[IT]) {
+__device__ __forceinline__ void keep_chunk_state(float* p, int col0, const f32x4 (&x)[IT]) {
 #pragma unroll
   for (int m = 0; m < IT; ++m)
-    *reinterpret_cast<f32x4*>(p + col * (16 * IT) + state_row(m)) = x[m];
+    *reinterpret_cast<f32x4*>(p + (col0 / 16 * IT + m) * 256 + lane_id() * 4) = x[m];
+}
+// Four channels of state_row(m) of lanes 16 g .., column j, of such a state.
+template <int DK>
+__device__ __forceinline__ int chunk_state_at(int m, int g, int j) {
+  return ((j >> 4) * (DK / 16) + m) * 256 + (16 * g + (j & 15)) * 4;
 }
 template <int IT>
 __device__ __forceinline__ void load_state(const float* p, int ld, uint32_t lane, f32x4 (&x)[IT]) {

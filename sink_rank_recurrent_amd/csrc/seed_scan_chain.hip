@@ -18,6 +18,11 @@ namespace seed {
 namespace scan {
 namespace {
 
+template <int N>
+struct Part {
+  static constexpr int value = N;
+};
+
 // LDS of one chunk's operands.
 template <int RULE, int DK, bool K_Q, int NT, int MT, bool HAS_M>
 struct Stage {
@@ -26,22 +31,26 @@ struct Stage {
   static constexpr int n = q + (K_Q ? kPlane<DK> : 0);
   static constexpr int m = n + (DELTA ? kTriFrags * NT * 1024 : 0);
   static constexpr int vec = m + (HAS_M ? kTriFrags * MT * 1024 : 0);   // P, F, beta
-  static constexpr int bytes = vec + 768;
+  static constexpr int bytes = vec + 1024;
 
-  template <int W>
+  // The chunk's loads, PART 0 .. 2 of them (-1: all): spread over the chunk
+  // before, so that no wave waits for a full queue.
+  template <int W, int PART>
   static __device__ __forceinline__ void load(const ScanArgs& a, uint32_t to, const bf16_t* K,
                                               const bf16_t* Q, uint32_t ld, size_t unit, int rows,
                                               bool transposed, int w) {
-    async_rows<DK, W>(K, Q, ld, rows, to, to + q, K_Q, w);
     constexpr size_t pack = kTriFrags * 3 * kFrag;
-    if (DELTA)
-      async_pack<NT, W>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
-                            unit * pack, to + n, w);
-    if (HAS_M)
-      async_pack<MT, W>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w);
-    if (w < (DELTA ? 3 : 2))
-      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
-                    lane_id() * 4, to + vec + 256 * w);
+    if (PART <= 0) async_rows<DK, W>(K, Q, ld, rows, to, to + q, K_Q, w);
+    if (PART < 0 || PART == 1) {
+      if (DELTA)
+        async_pack<NT, W>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
+                              unit * pack, to + n, w);
+    }
+    if (PART < 0 || PART == 2) {
+      if (HAS_M)
+        async_pack<MT, W>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w);
+      if (w == W - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, to + vec);
+    }
   }
 };
 
@@ -73,7 +82,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
 
   char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of V, then of O
   if (chunks > 0) {
-    St::template load<NW>(a, lds0, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w);
+    St::template load<NW, -1>(a, lds0, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w);
     wave_load(V, vld, min(kC, rg.len), mine0);
     async_wait();
     __syncthreads();
@@ -89,13 +98,15 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
       R[m] = O[m] = zero4();
     }
     drop_rows(u, n);
-    if (c + 1 < chunks) {
-      const int rows = min(kC, rg.len - (c + 1) * kC);
-      St::template load<NW>(a, lds0 + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
-                            Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, rows, false, w);
-    }
+    auto stage = [&](auto part) {
+      if (c + 1 < chunks)
+        St::template load<NW, decltype(part)::value>(
+            a, lds0 + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
+            Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, min(kC, rg.len - (c + 1) * kC), false, w);
+    };
+    stage(Part<0>{});
     if (SAVE)
-      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col, S);
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
 
     if (DELTA || !SAVE) {
 #pragma unroll
@@ -114,6 +125,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
         }
       }
     }
+    stage(Part<1>{});
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const f32x4 p = lds_vec(now + St::vec, m);
@@ -147,6 +159,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) u[m] *= b[m];
     }
+    stage(Part<2>{});
     if (!SAVE) {
       constexpr int NU = DELTA ? 2 : 1;   // V itself is one term
       const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
@@ -213,7 +226,7 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of dO, then of dV
   if (chunks > 0) {
     const int c = chunks - 1, rows = rg.len - c * kC;
-    St::template load<NW>(a, lds0 + (c & 1) * St::bytes, K + (size_t)c * kC * kld,
+    St::template load<NW, -1>(a, lds0 + (c & 1) * St::bytes, K + (size_t)c * kC * kld,
                           Q + (size_t)c * kC * kld, kld, (size_t)(base + c) * a.heads + at.head, rows,
                           true, w);
     wave_load(dO + (size_t)c * kC * vld, vld, rows, mine0);
@@ -224,11 +237,14 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     const char* now = lds + (c & 1) * St::bytes;
-    if (c > 0) {
-      St::template load<NW>(a, lds0 + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
-                            Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w);
-    }
-    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col, H);
+    auto stage = [&](auto part) {
+      if (c > 0)
+        St::template load<NW, decltype(part)::value>(
+            a, lds0 + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
+            Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w);
+    };
+    stage(Part<0>{});
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
 
     // dU = F (K H) + M^T dO
     f32x4 y[4], go[4];
@@ -246,6 +262,7 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
       for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
       mma_tiles(y, f, h);
     }
+    stage(Part<1>{});
 #pragma unroll
     for (int m = 0; m < 4; ++m) y[m] *= lds_vec(now + St::vec + 256, m);
     {
@@ -287,6 +304,7 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= b[m];
     }
+    stage(Part<2>{});
     wave_store(dV + (size_t)c * kC * vld, vld, n, y, mine);
     if (c > 0) wave_load(dO + (size_t)(c - 1) * kC * vld, vld, kC, mine0);
 

@@ -25,6 +25,13 @@ __device__ __forceinline__ float sum64(float x) {
   return x;
 }
 
+// Element (channel i, column j) of a chunk's state in the workspace.
+template <int DK>
+__device__ __forceinline__ int state_at(int i, int j) {
+  const int m = 2 * (i >> 5) + ((i >> 2) & 1), g = (i >> 3) & 3;
+  return chunk_state_at<DK>(m, g, j) + (i & 3);
+}
+
 // Rows of an LDS matrix [64][65] (or of its transpose) as a fragment.
 __device__ __forceinline__ void mat65_rows(const float* mat, int mt, int ks, bool transposed,
                                          float (&x)[8]) {
@@ -85,7 +92,7 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
     float all = 0.f;
     for (int i = w; i < DK; i += 4) {
       float x = 0.f;
-      for (int j = l; j < DV; j += 64) x += Sc[(size_t)j * DK + i] * Hc[(size_t)j * DK + i];
+      for (int j = l; j < DV; j += 64) x += Sc[state_at<DK>(i, j)] * Hc[state_at<DK>(i, j)];
       if (KDA) {
         x = sum64(x);
         if (l == 0) hs[i] = x;
@@ -194,14 +201,19 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
   for (int it = 0; it < DK / 16; ++it) {
     const int i = 16 * it + l16;
     f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1;
+    auto load_state8 = [&](const float* p, int ks, float(&x)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = p[state_at<DK>(i, 32 * ks + 16 * (j >> 2) + 4 * g16 + (j & 3))];
+    };
 #pragma unroll
     for (int ks = 0; ks < DV / 32; ++ks) {
       float x[8];
-      load_col8(Sc + i, DK, 32 * ks, DV, x);
+      load_state8(Sc, ks, x);
       const Frag<3> s = split<3>(x);
       mma(x1, rows_do(w, ks), s);
       if (DELTA) mma(x2, rows_dr(w, ks), s);
-      load_col8(Hc + i, DK, 32 * ks, DV, x);
+      load_state8(Hc, ks, x);
       mma(x3, rows_u(w, ks), split<3>(x));
     }
     f32x4 dq, dk;
@@ -495,7 +507,7 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
     const T* V = static_cast<const T*>(a.v) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
     const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
     const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
-    const float b = DELTA ? reinterpret_cast<const float*>(a.ws + a.at.b)[unit * kC + row] : 0.f;
+    const float b = DELTA ? reinterpret_cast<const float*>(a.ws + a.at.vec)[unit * 256 + 128 + row] : 0.f;
     float db = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -658,14 +670,14 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
   float sv[8], hv[8], hsum = 0.f;
   auto fetch = [&](int part) {
     if (!stager) return;
-    const size_t at = (size_t)(tid >> 2) * DK + 32 * part + 8 * (tid & 3);
     float y[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load_vec<4>(Sc + at + 4 * h, y);
+      const int at = chunk_state_at<DK>(2 * part + h, tid & 3, tid >> 2);
+      load_vec<4>(Sc + at, y);
 #pragma unroll
       for (int r = 0; r < 4; ++r) sv[4 * h + r] = y[r];
-      load_vec<4>(Hc + at + 4 * h, y);
+      load_vec<4>(Hc + at, y);
 #pragma unroll
       for (int r = 0; r < 4; ++r) hv[4 * h + r] = y[r];
     }
@@ -838,7 +850,7 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
     const T* dO = static_cast<const T*>(a.dO) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
     const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
     const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
-    const float b = reinterpret_cast<const float*>(a.ws + a.at.b)[unit * kC + row];
+    const float b = reinterpret_cast<const float*>(a.ws + a.at.vec)[unit * 256 + 128 + row];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       float x[8], y[8];
@@ -909,14 +921,14 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   Piece<T> kv, qv;
   auto fetch = [&](int part) {
     if (stager) {
-      const int at = (tid >> 2) * DK + 32 * part + 8 * (tid & 3);
       float y[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        load_vec<4>(Sc + at + 4 * h, y);
+        const int at = chunk_state_at<DK>(2 * part + h, tid & 3, tid >> 2);
+        load_vec<4>(Sc + at, y);
 #pragma unroll
         for (int r = 0; r < 4; ++r) sv[4 * h + r] = y[r];
-        load_vec<4>(Hc + at + 4 * h, y);
+        load_vec<4>(Hc + at, y);
 #pragma unroll
         for (int r = 0; r < 4; ++r) hv[4 * h + r] = y[r];
       }

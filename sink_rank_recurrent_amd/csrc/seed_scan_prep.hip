@@ -123,12 +123,13 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   if (w == 0) {
     const size_t gate = ((size_t)ch.tok + l) * a.heads + head;
     float P, F;
+    float* vec = reinterpret_cast<float*>(a.ws + a.at.vec) + unit * 256;
     decays(dec, l < ch.n ? a.g[gate] : 1.f, P, F);
-    reinterpret_cast<float*>(a.ws + a.at.p)[unit * kC + l] = P;
-    reinterpret_cast<float*>(a.ws + a.at.f)[unit * kC + l] = F;
+    vec[l] = P;
+    vec[64 + l] = F;
     if (DELTA) {
       bt[l] = l < ch.n ? a.beta[gate] : 0.f;
-      reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + l] = bt[l];
+      vec[128 + l] = bt[l];
     }
   }
   __syncthreads();
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
 
   if (tid < kC) {
     bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
-    reinterpret_cast<float*>(a.ws + a.at.b)[unit * kC + tid] = bt[tid];
+    reinterpret_cast<float*>(a.ws + a.at.vec)[unit * 256 + 128 + tid] = bt[tid];
   }
   if (tid == 0) unsafe = 0;
   const int t0 = 16 * w + l16;

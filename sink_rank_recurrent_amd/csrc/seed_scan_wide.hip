@@ -79,7 +79,7 @@ struct Wide {
   static constexpr int n = q + (SAVE ? 0 : NC * kPlane<DK>);
   static constexpr int m = n + (DELTA ? kTriFrags * NC * 1024 : 0);
   static constexpr int vec = m + (SAVE ? 0 : kTriFrags * NC * 1024);
-  static constexpr int bytes = vec + 768;
+  static constexpr int bytes = vec + 1024;
 };
 
 template <int RULE, int DK, int NW, typename T, bool SAVE>
@@ -131,9 +131,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
     if (!SAVE)
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
-    if (w < (DELTA ? 3 : 2) && (!KDA || w == 2))
-      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
-                    lane_id() * 4, lds0 + W::vec + 256 * w);
+    if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
     if (KDA) {
       if (DELTA) fill<DK, TH, NC, true>(lds, kr, pr);
       if (!SAVE) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
@@ -147,7 +145,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     async_wait();
     __syncthreads();
     if (SAVE)
-      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col, S);
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
     if (!KDA && c + 1 < chunks) fetch(c + 1);
 
     f32x4 R[4], O[4];
@@ -267,7 +265,7 @@ struct WideBack {
   static constexpr int n = 2 * q;
   static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
   static constexpr int vec = m + kTriFrags * 3 * 1024;
-  static constexpr int bytes = vec + 768;
+  static constexpr int bytes = vec + 1024;
 };
 
 // The chunks from the last to the first (see chain_reverse_kernel).
@@ -318,9 +316,7 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     if (DELTA)
       async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds0 + W::n, w);
     async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
-    if (w < (DELTA ? 3 : 2) && (!KDA || w == 2))
-      async_copy<4>(a.ws + (w == 0 ? a.at.p : w == 1 ? a.at.f : a.at.b) + unit * kC * sizeof(float),
-                    lane_id() * 4, lds0 + W::vec + 256 * w);
+    if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
     if (KDA) {
       fill<DK, TH, 3, true>(lds, kr, fr);
       fill<DK, TH, 3, true>(lds + W::q, qr, pr);
@@ -336,7 +332,7 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     }
     async_wait();
     __syncthreads();
-    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col, H);
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
     if (!KDA && c > 0) fetch(c - 1);
 
     // dU = F (K H) + M^T dO

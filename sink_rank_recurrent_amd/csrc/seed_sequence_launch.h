@@ -18,8 +18,8 @@ struct ScanLayout {
   size_t n_pack;     // N (I + L beta)^-1 L, fragments of three bf16 terms
   size_t nt_pack;    // N^T
   size_t m_pack;     // M (forward) or M^T (backward)
-  size_t p, f;       // P, F: one float a token, d_k for KDA
-  size_t b;          // beta: one float a token, 0 behind the sequence's end
+  size_t vec;        // P, F (scalar gates) and beta, 64 floats each, 256 a unit
+  size_t p, f;       // P, F of KDA, d_k floats a token
   size_t state;      // S before each chunk (backward)
   size_t grad;       // H behind each chunk (backward)
   size_t e, y;       // E, Y: d_v floats a token (backward, delta rules)
