@@ -21,6 +21,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// 1 / (1 + 2^(-x log2 e)) by the hardware's exponential and reciprocal (one
+// ulp each; the argument's rounding is |x| 2^-24 of the exponential).  With
+// the library's expf and a division the arithmetic, not the memory, bounds
+// the kernels: 88 us instead of 52 for 32768 x 16 x 128 bf16 values.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
 template <int VW, typename T>
 __device__ __forceinline__ void load_values(const T* __restrict__ p, float (&x)[VW]) {
   if constexpr (VW == 1) {
@@ -43,29 +55,36 @@ template <int VW, typename T>
 __device__ __forceinline__ void store_values(T* __restrict__ p, const float (&x)[VW]) {
   if constexpr (VW == 1) {
     if constexpr (sizeof(T) == 4) *p = x[0];
-    else *p = (bf16_t)round_nearest16<kStoreBF16>(x[0]);
+    else *p = (bf16_t)round_pair(x[0], 0.f);
   } else if constexpr (sizeof(T) == 4) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
     uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      u[j] = round_nearest16<kStoreBF16>(x[2 * j]) | (round_nearest16<kStoreBF16>(x[2 * j + 1]) << 16);
+    for (int j = 0; j < 4; ++j) u[j] = round_pair(x[2 * j], x[2 * j + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
-__device__ __forceinline__ float act_of(int act, float x) {
-  const float s = sigmoid(x);
-  return act == kActNone ? x : act == kActSilu ? x * s : s;
-}
-// act(x) and its derivative
-__device__ __forceinline__ void act_both(int act, float x, float& y, float& d) {
-  const float s = sigmoid(x);
-  y = act == kActNone ? x : act == kActSilu ? x * s : s;
-  d = act == kActNone ? 1.f : act == kActSilu ? s * (1.f + x * (1.f - s)) : s * (1.f - s);
+// f(act) for the call's activation, one branch for all of a thread's values.
+template <int ACT>
+struct Act {
+  static __device__ __forceinline__ float of(float x) {
+    return ACT == kActNone ? x : ACT == kActSilu ? x * sigmoid(x) : sigmoid(x);
+  }
+  // act(x) and its derivative
+  static __device__ __forceinline__ void both(float x, float& y, float& d) {
+    const float s = sigmoid(x);
+    y = ACT == kActNone ? x : ACT == kActSilu ? x * s : s;
+    d = ACT == kActNone ? 1.f : ACT == kActSilu ? s + y * (1.f - s) : s * (1.f - s);
+  }
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == kActSilu) f(Act<kActSilu>{});
+  else if (act == kActSigmoid) f(Act<kActSigmoid>{});
+  else f(Act<kActNone>{});
 }
 
 // Sum over a team of LG threads, the same bits in each of them.
@@ -90,77 +109,120 @@ struct Item {
   bool live;
 };
 
-template <int LG, int NV, int VW, typename XT, typename IT>
-__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a, long long items) {
-  __shared__ float lds[kThreads / 64];
-  constexpr int TEAMS = kThreads / LG;
-  const int lane = threadIdx.x % LG;
-  const long long item = (long long)blockIdx.x * TEAMS + threadIdx.x / LG;
-  if (LG <= 64 && item >= items) return;   // a whole block shares its item otherwise
-  const size_t at = (size_t)item * a.d;
-  const XT* X = static_cast<const XT*>(a.x) + at;
-  const IT* Z = static_cast<const IT*>(a.gate) + at;
-  const size_t wat = a.weight_groups == 1 ? 0 : (size_t)(item % a.groups) * a.d;
-  const float inv = 1.f / (float)a.d;
-
-  float h[NV][VW], z[NV][VW];
+// One group's values in a thread, values past the group's end 0.
+template <int LG, int NV, int VW, typename T>
+__device__ __forceinline__ void load_group(const T* __restrict__ p, int lane, int d,
+                                           float (&x)[NV][VW]) {
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * LG + lane) * VW;
 #pragma unroll
-    for (int j = 0; j < VW; ++j) h[v][j] = z[v][j] = 0.f;
-    if (c < a.d) {
-      load_values<VW>(X + c, h[v]);
-      if (a.gate) load_values<VW>(Z + c, z[v]);
-    }
+    for (int j = 0; j < VW; ++j) x[v][j] = 0.f;
+    if (c < d) load_values<VW>(p + c, x[v]);
   }
-  if (a.gate) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        z[v][j] = act_of(a.act, z[v][j]);
-        if (a.gate_first) h[v][j] *= z[v][j];
-      }
-  }
-  float mean = 0.f;
+}
+
+// h minus its mean (if centered), in place, and 1 / sqrt(variance + eps).
+// Values past the group's end are 0 before and left out of the variance.
+template <int LG, int NV, int VW>
+__device__ __forceinline__ float normalise(float (&h)[NV][VW], int lane, const NormArgs& a,
+                                           float inv, float* lds) {
   if (a.centered) {
+    float mean = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < VW; ++j) mean += (v * LG + lane) * VW < a.d ? h[v][j] : 0.f;
+      for (int j = 0; j < VW; ++j) mean += h[v][j];
     mean = team_sum<LG>(mean, lds) * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if ((v * LG + lane) * VW < a.d) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) h[v][j] -= mean;
+      }
   }
   float var = 0.f;
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int j = 0; j < VW; ++j) {
-      h[v][j] -= mean;
-      var += (v * LG + lane) * VW < a.d ? h[v][j] * h[v][j] : 0.f;
-    }
-  var = team_sum<LG>(var, lds) * inv;
-  const float rstd = 1.f / sqrtf(var + a.eps);
+    for (int j = 0; j < VW; ++j) var += h[v][j] * h[v][j];
+  return 1.f / sqrtf(team_sum<LG>(var, lds) * inv + a.eps);
+}
 
-  IT* Yp = static_cast<IT*>(a.y) + at;
+// A block runs over every gridDim.x-th batch of items of one weight group
+// (blockIdx.y; all items where the weights are shared), weight and bias in
+// registers (read for every item they are four times the bytes of bf16
+// values).
+template <int LG, int NV, int VW, typename XT, typename IT>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a, long long items) {
+  __shared__ float lds[kThreads / 64];
+  constexpr int TEAMS = kThreads / LG;
+  const int lane = threadIdx.x % LG;
+  const bool split = a.weight_groups > 1;
+  const size_t wat = split ? (size_t)blockIdx.y * a.d : 0;
+  const size_t step = split ? (size_t)a.groups * a.d : a.d;   // from item to item
+  const float inv = 1.f / (float)a.d;
+  const XT* X = static_cast<const XT*>(a.x) + wat;
+  const IT* Z = static_cast<const IT*>(a.gate) + wat;
+  IT* Y = static_cast<IT*>(a.y) + wat;
+
+  float w[NV][VW], b[NV][VW];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * LG + lane) * VW;
-    if (c >= a.d) continue;
-    float w[VW], b[VW], y[VW];
 #pragma unroll
     for (int j = 0; j < VW; ++j) {
-      w[j] = 1.f;
-      b[j] = 0.f;
+      w[v][j] = 1.f;
+      b[v][j] = 0.f;
     }
-    if (a.weight) load_values<VW>(a.weight + wat + c, w);
-    if (a.bias) load_values<VW>(a.bias + wat + c, b);
+    if (c < a.d) {
+      if (a.weight) load_values<VW>(a.weight + wat + c, w[v]);
+      if (a.bias) load_values<VW>(a.bias + wat + c, b[v]);
+    }
+  }
+  const long long stride = (long long)gridDim.x * TEAMS;
+  for (long long item = (long long)blockIdx.x * TEAMS + threadIdx.x / LG; item < items;
+       item += stride) {   // a team's lanes leave together
+    float h[NV][VW], z[NV][VW];
+    load_group<LG>(X + item * step, lane, a.d, h);
+    if (a.gate) {
+      load_group<LG>(Z + item * step, lane, a.d, z);
+      with_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < VW; ++j) {
-      const float n = h[v][j] * rstd * w[j] + b[j];
-      y[j] = !a.gate ? act_of(a.act, n) : a.gate_first ? n : n * z[v][j];
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) z[v][j] = act.of(z[v][j]);
+      });
+      if (a.gate_first) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) h[v][j] *= z[v][j];
+      }
     }
-    store_values<VW>(Yp + c, y);
+    const float rstd = normalise<LG>(h, lane, a, inv, lds);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < VW; ++j) h[v][j] = h[v][j] * rstd * w[v][j] + b[v][j];
+    if (!a.gate) {
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) h[v][j] = act.of(h[v][j]);
+      });
+    } else if (!a.gate_first) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < VW; ++j) h[v][j] *= z[v][j];
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LG + lane) * VW;
+      if (c < a.d) store_values<VW>(Y + item * step + c, h[v]);
+    }
   }
 }
 
@@ -194,98 +256,105 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a, lon
     }
   }
 
-  for (long long first = (long long)blockIdx.x * TEAMS; first < items;
-       first += (long long)gridDim.x * TEAMS) {
-    const long long item = first + team;
-    if (LG <= 64 && item >= items) break;
-    const size_t at = (split ? (size_t)item * a.groups + blockIdx.y : (size_t)item) * a.d;
-    const XT* X = static_cast<const XT*>(a.x) + at;
-    const IT* Z = static_cast<const IT*>(a.gate) + at;
-    const IT* DY = static_cast<const IT*>(a.dy) + at;
-    float x[NV][VW], z[NV][VW], g[NV][VW];
+  const size_t step = split ? (size_t)a.groups * a.d : a.d;   // from item to item
+  const XT* X = static_cast<const XT*>(a.x) + wat;
+  const IT* Z = static_cast<const IT*>(a.gate) + wat;
+  const IT* DY = static_cast<const IT*>(a.dy) + wat;
+  const long long stride = (long long)gridDim.x * TEAMS;
+  long long item = (long long)blockIdx.x * TEAMS + team;
+  for (; item < items; item += stride) {   // a team's lanes leave together
+    float x[NV][VW], z[NV][VW], g[NV][VW], h[NV][VW];
+    load_group<LG>(X + item * step, lane, a.d, x);
+    load_group<LG>(DY + item * step, lane, a.d, g);
+    if (a.gate) load_group<LG>(Z + item * step, lane, a.d, z);
+    // gate first: x is needed again, and act's derivative in place of the gate
+    if (a.gate && a.gate_first) {
+      with_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * LG + lane) * VW;
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < VW; ++j) x[v][j] = z[v][j] = g[v][j] = 0.f;
-      if (c < a.d) {
-        load_values<VW>(X + c, x[v]);
-        load_values<VW>(DY + c, g[v]);
-        if (a.gate) load_values<VW>(Z + c, z[v]);
-      }
+          for (int j = 0; j < VW; ++j) {
+            float y, d;
+            act.both(z[v][j], y, d);
+            h[v][j] = x[v][j] * y;
+            z[v][j] = x[v][j] * d;
+            x[v][j] = y;
+          }
+      });
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < VW; ++j) h[v][j] = x[v][j];
     }
-    // h in place of x (gate first: x is needed again, with act(z) beside it)
-    float h[NV][VW], mean = 0.f;
+    const float rstd = normalise<LG>(h, lane, a, inv, lds);
+    // h becomes hat, g the gradient of n; the gate behind: z its gradient
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        h[v][j] = a.gate && a.gate_first ? x[v][j] * act_of(a.act, z[v][j]) : x[v][j];
-        mean += (v * LG + lane) * VW < a.d ? h[v][j] : 0.f;
-      }
-    mean = a.centered ? team_sum<LG>(mean, lds) * inv : 0.f;
-    float var = 0.f;
+      for (int j = 0; j < VW; ++j) h[v][j] *= rstd;
+    if (!a.gate) {
+      with_act(a.act, [&](auto act) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        h[v][j] -= mean;
-        var += (v * LG + lane) * VW < a.d ? h[v][j] * h[v][j] : 0.f;
-      }
-    const float rstd = 1.f / sqrtf(team_sum<LG>(var, lds) * inv + a.eps);
-
-    // g becomes dhat, h becomes hat
+          for (int j = 0; j < VW; ++j) {
+            float y, d;
+            act.both(h[v][j] * w[v][j] + b[v][j], y, d);
+            g[v][j] *= d;
+          }
+      });
+    } else if (!a.gate_first) {
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            float y, d;
+            act.both(z[v][j], y, d);
+            z[v][j] = g[v][j] * (h[v][j] * w[v][j] + b[v][j]) * d;
+            g[v][j] *= y;
+          }
+      });
+    }
+    // (values past the group's end: g and h are 0)
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
-        const bool in = (v * LG + lane) * VW < a.d;
-        const float hat = h[v][j] * rstd, n = hat * w[v][j] + b[v][j];
-        float dn = g[v][j], y, d;
-        if (!a.gate) {
-          act_both(a.act, n, y, d);
-          dn *= d;
-        } else if (!a.gate_first) {
-          act_both(a.act, z[v][j], y, d);
-          z[v][j] = dn * n * d;   // the gate's gradient
-          dn *= y;
-        }
-        dw[v][j] += in ? dn * hat : 0.f;
-        db[v][j] += in ? dn : 0.f;
-        const float dhat = dn * w[v][j];
-        g[v][j] = dhat;
-        h[v][j] = hat;
-        s1 += in ? dhat : 0.f;
-        s2 += in ? dhat * hat : 0.f;
+        dw[v][j] += g[v][j] * h[v][j];
+        db[v][j] += g[v][j];
+        g[v][j] *= w[v][j];
+        s1 += g[v][j];
+        s2 += g[v][j] * h[v][j];
       }
     s1 = a.centered ? team_sum<LG>(s1, lds) * inv : 0.f;
     s2 = team_sum<LG>(s2, lds) * inv;
-    XT* DX = static_cast<XT*>(a.dx) + at;
-    IT* DZ = static_cast<IT*>(a.dgate) + at;
+    XT* DX = static_cast<XT*>(a.dx) + wat + item * step;
+    IT* DZ = static_cast<IT*>(a.dgate) + wat + item * step;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * LG + lane) * VW;
       if (c >= a.d) continue;
-      float dx[VW];
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        dx[j] = rstd * (g[v][j] - s1 - h[v][j] * s2);
-        if (a.gate && a.gate_first) {
-          float y, d;
-          act_both(a.act, z[v][j], y, d);
-          z[v][j] = dx[j] * x[v][j] * d;
-          dx[j] *= y;
+      for (int j = 0; j < VW; ++j) g[v][j] = rstd * (g[v][j] - s1 - h[v][j] * s2);
+      if (a.gate && a.gate_first) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          z[v][j] *= g[v][j];
+          g[v][j] *= x[v][j];
         }
       }
-      store_values<VW>(DX + c, dx);
+      store_values<VW>(DX + c, g[v]);
       if (a.gate) store_values<VW>(DZ + c, z[v]);
     }
   }
 
   if (!sums) return;
   // the block's part: teams added in order
-  float* out = a.ws + ((size_t)blockIdx.x * a.weight_groups + (split ? blockIdx.y : 0)) * 2 * a.d;
+  const size_t columns = ((size_t)a.weight_groups * 2 * a.d + 3) & ~(size_t)3;
+  float* out = a.ws + blockIdx.x * columns + (split ? (size_t)blockIdx.y * 2 * a.d : 0);
   for (int what = 0; what < 2; ++what) {
     float(&acc)[NV][VW] = what == 0 ? dw : db;
     if constexpr (TEAMS > 1) {
@@ -311,23 +380,31 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a, lon
   }
 }
 
-// dweight and dbias: the parts summed by 16 threads a channel, then those in
-// order.
+// dweight and dbias: a block sums four neighbouring columns of the parts
+// [parts][stride], thread t the parts t, t + 256, ...; then by halves.
 __global__ __launch_bounds__(kThreads) void parts_kernel(NormArgs a) {
-  __shared__ float lds[16][17];
-  const int c = blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
-  const int total = a.weight_groups * 2 * a.d;   // [group][dw, db][d]
-  float s = 0.f;
-  if (c < total)
-    for (int p = row; p < a.parts; p += 16) s += a.ws[(size_t)p * total + c];
-  lds[row][threadIdx.x & 15] = s;
+  __shared__ float4 lds[kThreads];
+  const int total = a.weight_groups * 2 * a.d, stride = (total + 3) & ~3;   // [group][dw, db][d]
+  const int c = blockIdx.x * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = threadIdx.x; p < a.parts; p += kThreads) {
+    const float4 x = *reinterpret_cast<const float4*>(a.ws + (size_t)p * stride + c);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  lds[threadIdx.x] = s;
+  for (int half = kThreads / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < half) {
+      const float4 x = lds[threadIdx.x + half];
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+      lds[threadIdx.x] = s;
+    }
+  }
   __syncthreads();
-  if (row == 0 && c < total) {
-    s = 0.f;
-    for (int j = 0; j < 16; ++j) s += lds[j][threadIdx.x & 15];
-    const int grp = c / (2 * a.d), rest = c % (2 * a.d);
+  if (threadIdx.x < 4 && c + (int)threadIdx.x < total) {
+    const int at = c + threadIdx.x, grp = at / (2 * a.d), rest = at % (2 * a.d);
     float* to = rest < a.d ? a.dweight : a.dbias;
-    if (to) to[(size_t)grp * a.d + rest % a.d] = s;
+    if (to) to[(size_t)grp * a.d + rest % a.d] = reinterpret_cast<const float*>(lds)[threadIdx.x];
   }
 }
 
@@ -339,9 +416,8 @@ int team_of(int d, bool vectors) {
 
 template <int LG, int NV, int VW, bool BWD>
 hipError_t norm_types(const NormArgs& a, hipStream_t stream) {
-  const long long items = a.rows * (BWD && a.weight_groups > 1 ? 1 : a.groups);
-  const dim3 grid(BWD ? (unsigned)a.parts : (unsigned)((items + kThreads / LG - 1) / (kThreads / LG)),
-                  BWD ? a.weight_groups : 1);
+  const long long items = a.rows * (a.weight_groups > 1 ? 1 : a.groups);
+  const dim3 grid((unsigned)a.parts, a.weight_groups);
 #define SEED_NORM(XT, IT)                                                                      \
   do {                                                                                         \
     if (BWD)                                                                                   \
@@ -383,24 +459,36 @@ hipError_t norm(const NormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Blocks of the backward pass for each weight group: enough for 2048 in
-// all, and no more than there are batches of items.
+// Blocks of the backward pass for each weight group, no more than there are
+// batches of items: 2048 in all fill the CUs, but each writes its sums once,
+// so fewer, down to 512, where a block has less than some 40 items (8002
+// groups of 2047 values: the sums took 39 us of 109 with 2048 blocks).
 int group_norm_parts(long long rows, int groups, int d, int weight_groups) {
   const int teams = kThreads / team_of(d, d % 8 == 0);
   const long long items = rows * (weight_groups > 1 ? 1 : groups);
   const long long batches = (items + teams - 1) / teams;
-  const long long most = weight_groups > 1 ? (2048 + weight_groups - 1) / weight_groups : 2048;
+  long long all = rows * groups / 40;
+  all = all > 2048 ? 2048 : all < 512 ? 512 : all;
+  const long long most = (all + weight_groups - 1) / weight_groups;
   const long long parts = batches < most ? batches : most;
   return (int)(parts < 1 ? 1 : parts);
 }
 
-hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) { return norm<false>(a, stream); }
+hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) {
+  // 4096 blocks in all, or one for each batch of items
+  const int teams = kThreads / team_of(a.d, a.d % 8 == 0);
+  const long long items = a.rows * (a.weight_groups > 1 ? 1 : a.groups);
+  const long long batches = (items + teams - 1) / teams, most = (4096 + a.weight_groups - 1) / a.weight_groups;
+  NormArgs b = a;
+  b.parts = (int)(batches < most ? batches : most);
+  return norm<false>(b, stream);
+}
 
 hipError_t launch_group_norm_backward(const NormArgs& a, hipStream_t stream) {
   hipError_t e = norm<true>(a, stream);
   if (e != hipSuccess || !(a.dweight || a.dbias)) return e;
   const int total = a.weight_groups * 2 * a.d;
-  hipLaunchKernelGGL(parts_kernel, dim3((total + 15) / 16), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(parts_kernel, dim3((total + 3) / 4), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

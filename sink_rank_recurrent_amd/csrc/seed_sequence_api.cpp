@@ -178,6 +178,9 @@ seed_status check_norm(const char* fn, long long rows, int groups, int d, int x_
   return SEED_OK;
 }
 
+// Columns of a partial sum of dweight and dbias.
+size_t norm_columns(int weight_groups, int d) { return ((size_t)weight_groups * 2 * d + 3) & ~(size_t)3; }
+
 seed::NormArgs norm_args(long long rows, int groups, int d, const void* x, int x_dtype,
                          const void* gate, int io_dtype, const float* weight, const float* bias,
                          int weight_groups, float eps, int centered, int activation,
@@ -331,7 +334,7 @@ seed_status seed_group_norm_backward(long long rows, int groups, int d, const vo
   const bool sums = dweight != nullptr || dbias != nullptr;
   if (rows == 0 && !sums) return ok();
   const int parts = seed::group_norm_parts(rows, groups, d, weight_groups);
-  const size_t want = sums ? (size_t)parts * weight_groups * 2 * d * 4 : 0;
+  const size_t want = sums ? (size_t)parts * norm_columns(weight_groups, d) * 4 : 0;
   if (sums) {
     SEED_NEED(workspace);
     if (workspace_bytes < want)
@@ -371,7 +374,7 @@ size_t seed_group_norm_workspace_bytes(long long rows, int groups, int d, int we
                  nullptr, nullptr, weight_groups, 0.f, SEED_ACT_NONE, 0) != SEED_OK)
     return static_cast<size_t>(-1);
   ok();
-  return (size_t)seed::group_norm_parts(rows, groups, d, weight_groups) * weight_groups * 2 * d * 4;
+  return (size_t)seed::group_norm_parts(rows, groups, d, weight_groups) * norm_columns(weight_groups, d) * 4;
 }
 
 }  // extern "C"

@@ -50,7 +50,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _same_device(**tensors) -> torch.device:
-    device = None
+    first = None
     for name, t in tensors.items():
         if t is None:
             continue
@@ -58,11 +58,28 @@ def _same_device(**tensors) -> torch.device:
             raise TypeError(f"{name} must be a tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be in device memory (got {t.device})")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    return device
+        index = t.get_device()
+        if first is None:
+            first = index
+        elif index != first:
+            raise ValueError(f"{name} is on device {index}, the other tensors on {first}")
+    return torch.device("cuda", first)
+
+
+class _On:
+    """The tensors' device made current, where it is not."""
+
+    def __init__(self, device):
+        self.device = device if device.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.device is not None:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *error):
+        if self.device is not None:
+            self.guard.__exit__(*error)
 
 
 def _scan_shape(rule: str, q, v, cu_seqlens, n_seq=None):
@@ -142,7 +159,7 @@ def seed_scan(rule: str, q, k, v, g, beta, o, S, S0=None, cu_seqlens=None, works
     n_seq, tokens, lead, H, HK, d_k, d_v = _scan_inputs(rule, q, k, v, g, beta, S0, cu_seqlens)
     _need(o, "o", (*lead, H, d_v), (q.dtype,))
     _need(S, "S", (n_seq, H, d_k, d_v), _F32)
-    with torch.cuda.device(device):
+    with _On(device):
         ws = _workspace(workspace, _workspace_bytes(rule, n_seq, H, HK, d_k, d_v, tokens, False),
                         device)
         st = lib().seed_scan(RULES[rule], n_seq, H, HK, d_k, d_v, tokens, _ptr(cu_seqlens),
@@ -179,7 +196,7 @@ def seed_scan_backward(rule: str, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, S
     for name, t in (("dS", dS), ("dS0", dS0)):
         if t is not None:
             _need(t, name, (n_seq, H, d_k, d_v), _F32)
-    with torch.cuda.device(device):
+    with _On(device):
         ws = _workspace(workspace, _workspace_bytes(rule, n_seq, H, HK, d_k, d_v, tokens, True),
                         device)
         st = lib().seed_scan_backward(
@@ -228,7 +245,7 @@ def seed_group_norm(x, y, weight=None, bias=None, gate=None, eps: float = 1e-5,
     device = _same_device(x=x, y=y, weight=weight, bias=bias, gate=gate)
     shape, rows, G, d, wg = _norm_inputs(x, gate, y.dtype, weight, bias, activation)
     _need(y, "y", shape, _IN)
-    with torch.cuda.device(device):
+    with _On(device):
         st = lib().seed_group_norm(rows, G, d, _ptr(x), _code(x.dtype), _ptr(gate), _code(y.dtype),
                                    _ptr(weight), _ptr(bias), wg, eps, int(centered),
                                    ACTIVATIONS[activation], int(gate_first), _ptr(y),
@@ -271,7 +288,7 @@ def seed_group_norm_backward(dy, x, dx, dgate=None, dweight=None, dbias=None, we
                                      f"({G}, {d})")
                 wg = t.shape[0] if t.dim() == 2 else 1
             _need(t, name, tuple(like.shape), _F32)
-    with torch.cuda.device(device):
+    with _On(device):
         ws = None
         if dweight is not None or dbias is not None:
             ws = workspace
