@@ -189,21 +189,29 @@ __device__ __forceinline__ Range sequence(const ScanArgs& a, int s) {
 // in s, disjoint, and below tokens / 64 + n_seq, without a table.
 __device__ __forceinline__ int slot_base(const Range& r, int s) { return r.start / kC + s; }
 
+// The sequence of a slot, slots of `unit` tokens (start / unit + s the first
+// of sequence s): the last whose first slot is not behind it; a wave tries 64
+// at a time.
+__device__ __forceinline__ int sequence_of_slot(const ScanArgs& a, int slot, int unit) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, span = a.n_seq;
+  while (span > 1) {
+    const int step = (span + 63) >> 6;
+    const int i = lo + lane * step;
+    const bool at = lane * step < span && sequence(a, i).start / unit + i <= slot;
+    const int last = 63 - __builtin_clzll(__ballot(at) | 1);
+    lo += last * step;
+    span = min(step, span - last * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // The chunk of a slot: sequence and first token, n tokens (0: none).
 struct Chunk {
   int seq, tok, n, index;
 };
 __device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& a, int slot) {
-  // the last sequence whose base is <= slot: a wave tries 64 at a time
-  int lo = 0, span = a.n_seq;
-  while (span > 1) {
-    const int step = (span + 63) >> 6;
-    const int i = lo + lane_id() * step;
-    const bool at = lane_id() * step < span && slot_base(sequence(a, i), i) <= slot;
-    const int last = 63 - __builtin_clzll(__ballot(at) | 1);
-    lo += last * step;
-    span = min(step, span - last * step);
-  }
+  const int lo = sequence_of_slot(a, slot, kC);
   const Range r = sequence(a, lo);
   const int c = slot - slot_base(r, lo);
   if (c < 0 || c * kC >= r.len) return {lo, 0, 0, 0};

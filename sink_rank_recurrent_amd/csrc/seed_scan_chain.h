@@ -151,20 +151,59 @@ struct Piece<bf16_t> {
   }
 };
 
-// Where a workgroup's columns are: grid n_seq * heads * (d_v / (16 NW)).
+// What a workgroup walks: 16 NW columns of a head's state (of `columns` in
+// all) through chunks c0 .. c1 - 1 of a sequence: all of them, or a segment.
+// A wave whose columns are d_v and more carries columns of the unit matrix
+// instead of the state's, with V = 0.  c0 > c1: nothing.
 template <int NW>
-struct Place {
-  int seq, head, hk, col0, col;   // col0: the wave's first column
-  __device__ __forceinline__ explicit Place(const ScanArgs& a) {
-    const int blocks = a.d_v / (16 * NW);
+struct Walk {
+  int seq, head, hk, col0, col, c0, c1, chunks, base;   // col0: the wave's first column
+  size_t segment;                                       // (segment, head), for what is kept for it
+  Range rg;
+  __device__ __forceinline__ Walk(const ScanArgs& a, int columns) {
+    const int blocks = columns / (16 * NW);
     const int sh = blockIdx.x / blocks;
-    seq = sh / a.heads;
+    const int first = sh / a.heads;
     head = sh % a.heads;
+    segment = (size_t)sh;
+    seq = a.at.seg ? sequence_of_slot(a, first, kC * a.at.seg) : first;
+    rg = sequence(a, seq);
+    chunks = (rg.len + kC - 1) / kC;
+    base = slot_base(rg, seq);
+    c0 = 0;
+    c1 = chunks;
+    if (a.at.seg) {
+      const int i = first - (rg.start / (kC * a.at.seg) + seq);
+      c0 = i * a.at.seg;
+      c1 = min(chunks, c0 + a.at.seg);
+      if (i < 0 || (i > 0 && c0 >= chunks)) c0 = c1 + 1;
+    }
     hk = head / (a.heads / a.key_heads);
     col0 = (blockIdx.x % blocks) * 16 * NW + wave_id() * 16;
     col = col0 + (lane_id() & 15);
   }
 };
+inline size_t walk_grid(const ScanArgs& a, int columns, int waves) {
+  return (size_t)(a.at.seg ? a.at.segs : a.n_seq) * a.heads * (columns / (16 * waves));
+}
+
+// A kept state in the waves' order, back into them.
+template <int IT>
+__device__ __forceinline__ void load_chunk_state(const float* p, int col0, f32x4 (&x)[IT]) {
+#pragma unroll
+  for (int m = 0; m < IT; ++m)
+    x[m] = *reinterpret_cast<const f32x4*>(p + (col0 / 16 * IT + m) * 256 + lane_id() * 4);
+}
+// Columns of the unit matrix.
+template <int IT>
+__device__ __forceinline__ void unit_state(int col, f32x4 (&x)[IT]) {
+#pragma unroll
+  for (int m = 0; m < IT; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[m][r] = state_row(m) + r == col ? 1.f : 0.f;
+}
+
+enum WalkMode { kRead = 0, kSave = 1, kCarry = 2 };
 
 // Waves of a workgroup: all of a head's columns, or half of 128 where whole
 // heads would leave some of the 256 CUs idle (backward of 64 x 32 chunks of
@@ -172,7 +211,7 @@ struct Place {
 // 1024 x 8 chunks: 385 us with four, 234 us with eight).
 inline int walk_waves(const ScanArgs& a) {
   const int all = a.d_v / 16;
-  return all == 8 && (long long)a.n_seq * a.heads < 256 ? 4 : all;
+  return all == 8 && (a.at.seg || (long long)a.n_seq * a.heads < 256) ? 4 : all;
 }
 
 }  // namespace scan

@@ -54,19 +54,22 @@ struct Stage {
   }
 };
 
-// SAVE keeps each chunk's incoming state and E for the backward pass and
-// writes no read-outs.
-template <int RULE, int DK, int NW, bool SAVE>
+// kSave keeps each chunk's incoming state and E for the backward pass and
+// writes no read-outs; kCarry keeps what a segment makes of zero and of the
+// unit matrix.
+template <int RULE, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
-  constexpr bool DELTA = RULE != kMAMBA2;
-  constexpr int IT = DK / 16, NT = SAVE ? 3 : 2;   // terms of the corrections
-  using St = Stage<RULE, DK, !SAVE, NT, 2, !SAVE>;
+  constexpr bool DELTA = RULE != kMAMBA2, READ = MODE == kRead, SAVE = MODE == kSave, CARRY = MODE == kCarry;
+  constexpr int IT = DK / 16, NT = !READ ? 3 : 2;   // terms of the corrections
+  using St = Stage<RULE, DK, READ, NT, 2, READ>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
-  const Place<NW> at(a);
+  const Walk<NW> at(a, a.d_v + (CARRY && DELTA ? DK : 0));
+  if (at.c0 > at.c1 || (CARRY && at.c1 == at.chunks)) return;   // nothing is behind a last segment
   const uint32_t lds0 = lds_offset(lds), mine0 = lds0 + 2 * St::bytes + 2048 * w;
-  const Range rg = sequence(a, at.seq);
-  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const Range rg = at.rg;
+  const int c0 = at.c0, c1 = at.c1, base = at.base;
+  const bool unit_cols = CARRY && DELTA && at.col0 >= a.d_v;
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
   const uint32_t g = lane_id() >> 4;
@@ -78,28 +81,38 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
   bf16_t* out = static_cast<bf16_t*>(a.o) + vat;
 
   f32x4 S[IT];
-  load_state(a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+  if (unit_cols) unit_state(at.col - a.d_v, S);
+  else if (!CARRY && c0 > 0)
+    load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, S);
+  else load_state(!CARRY && a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+  float through = 1.f;
 
   char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of V, then of O
-  if (chunks > 0) {
-    St::template load<NW, -1>(a, lds0, K, Q, kld, (size_t)base * a.heads + at.head, min(kC, rg.len), false, w);
-    wave_load(V, vld, min(kC, rg.len), mine0);
+  auto values = [&](int c) {
+    if (!unit_cols)
+      wave_load(V + (size_t)c * kC * vld, vld, min(kC, rg.len - c * kC), mine0);
+  };
+  if (c0 < c1) {
+    St::template load<NW, -1>(a, lds0 + (c0 & 1) * St::bytes, K + (size_t)c0 * kC * kld,
+                              Q + (size_t)c0 * kC * kld, kld, (size_t)(base + c0) * a.heads + at.head,
+                              min(kC, rg.len - c0 * kC), false, w);
+    values(c0);
     async_wait();
     __syncthreads();
   }
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     const char* now = lds + (c & 1) * St::bytes;
     f32x4 u[4], R[4], O[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      u[m] = wave_tile(mine, m);
+      u[m] = unit_cols ? zero4() : wave_tile(mine, m);
       R[m] = O[m] = zero4();
     }
     drop_rows(u, n);
     auto stage = [&](auto part) {
-      if (c + 1 < chunks)
+      if (c + 1 < c1)
         St::template load<NW, decltype(part)::value>(
             a, lds0 + ((c + 1) & 1) * St::bytes, K + (size_t)(c + 1) * kC * kld,
             Q + (size_t)(c + 1) * kC * kld, kld, unit + a.heads, min(kC, rg.len - (c + 1) * kC), false, w);
@@ -108,7 +121,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     if (SAVE)
       keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
 
-    if (DELTA || !SAVE) {
+    if (DELTA || READ) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
         const Frag<NT> s = split_tiles<NT>(S[2 * ks], S[2 * ks + 1]);
@@ -118,7 +131,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
           mma_tiles<4, 1, NT, NT>(R, f, s);
         }
-        if (!SAVE) {
+        if (READ) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now + St::q, m, ks);
           mma_tiles<4, 1, NT, 2>(O, f, s);
@@ -160,7 +173,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
       for (int m = 0; m < 4; ++m) u[m] *= b[m];
     }
     stage(Part<2>{});
-    if (!SAVE) {
+    if (READ) {
       constexpr int NU = DELTA ? 2 : 1;   // V itself is one term
       const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
       Frag<2> f[4];
@@ -175,14 +188,14 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
       O[3] = z[1];
       wave_store(out + (size_t)c * kC * vld, vld, n, O, mine);
     }
-    if (c + 1 < chunks)
-      wave_load(V + (size_t)(c + 1) * kC * vld, vld, min(kC, rg.len - (c + 1) * kC), mine0);
+    if (c + 1 < c1) values(c + 1);
     // S' = P_end S + K^T (F u)
     const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
 #pragma unroll
     for (int m = 0; m < 4; ++m) u[m] *= lds_vec(now + St::vec + 256, m);
 #pragma unroll
     for (int m = 0; m < IT; ++m) S[m] *= last;
+    if (CARRY && !DELTA) through *= last;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const Frag<3> x = split_tiles<3>(u[2 * ks], u[2 * ks + 1]);
@@ -194,22 +207,30 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     async_wait();
     __syncthreads();
   }
-  if (!SAVE) keep_state(a.S + state, a.d_v, state_lane, S);
+  if (READ && c1 == at.chunks) keep_state(a.S + state, a.d_v, state_lane, S);
+  if (CARRY) {
+    float* trans = reinterpret_cast<float*>(a.ws + a.at.trans);
+    if (unit_cols) keep_chunk_state(trans + at.segment * DK * DK, at.col0 - a.d_v, S);
+    else keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.carry) + at.segment * DK * a.d_v, at.col0, S);
+    if (!DELTA && threadIdx.x == 0) trans[at.segment] = through;
+  }
 }
 
 // The chunks from the last to the first, H the gradient of the state behind
 // the chunk.  Keeps H and (delta rules) Y, writes dV and dS0.
-template <int RULE, int DK, int NW>
+// (LOCAL: from H = 0, keeps only what a segment passes back.)
+template <int RULE, int DK, int NW, bool LOCAL>
 __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   constexpr bool DELTA = RULE != kMAMBA2;
   constexpr int IT = DK / 16;
   using St = Stage<RULE, DK, true, 3, 3, true>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
-  const Place<NW> at(a);
+  const Walk<NW> at(a, a.d_v);
+  if (at.c0 > at.c1 || (LOCAL && at.c0 == 0)) return;   // nothing is before a first segment
   const uint32_t lds0 = lds_offset(lds), mine0 = lds0 + 2 * St::bytes + 2048 * w;
-  const Range rg = sequence(a, at.seq);
-  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const Range rg = at.rg;
+  const int c0 = at.c0, c1 = at.c1, base = at.base;
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
   const uint32_t g = lane_id() >> 4;
@@ -221,11 +242,14 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   bf16_t* dV = static_cast<bf16_t*>(a.dv) + vat;
 
   f32x4 H[IT];
-  load_state(a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
+  // a last segment starts from dS, in its own first pass too
+  if (c1 < at.chunks && !LOCAL)
+    load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, H);
+  else load_state(c1 == at.chunks && a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
 
   char* mine = lds + 2 * St::bytes + 2048 * w;   // the wave's columns of dO, then of dV
-  if (chunks > 0) {
-    const int c = chunks - 1, rows = rg.len - c * kC;
+  if (c0 < c1) {
+    const int c = c1 - 1, rows = min(kC, rg.len - c * kC);
     St::template load<NW, -1>(a, lds0 + (c & 1) * St::bytes, K + (size_t)c * kC * kld,
                           Q + (size_t)c * kC * kld, kld, (size_t)(base + c) * a.heads + at.head, rows,
                           true, w);
@@ -233,18 +257,19 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
     async_wait();
     __syncthreads();
   }
-  for (int c = chunks - 1; c >= 0; --c) {
+  for (int c = c1 - 1; c >= c0; --c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     const char* now = lds + (c & 1) * St::bytes;
     auto stage = [&](auto part) {
-      if (c > 0)
+      if (c > c0)
         St::template load<NW, decltype(part)::value>(
             a, lds0 + ((c - 1) & 1) * St::bytes, K + (size_t)(c - 1) * kC * kld,
             Q + (size_t)(c - 1) * kC * kld, kld, unit - a.heads, kC, true, w);
     };
     stage(Part<0>{});
-    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
+    if (!LOCAL)
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
 
     // dU = F (K H) + M^T dO
     f32x4 y[4], go[4];
@@ -300,13 +325,14 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
       y[2] -= t[2];
       y[3] -= t[3];
       drop_rows(y, n);
-      keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
+      if (!LOCAL)
+        keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= b[m];
     }
     stage(Part<2>{});
-    wave_store(dV + (size_t)c * kC * vld, vld, n, y, mine);
-    if (c > 0) wave_load(dO + (size_t)(c - 1) * kC * vld, vld, kC, mine0);
+    if (!LOCAL) wave_store(dV + (size_t)c * kC * vld, vld, n, y, mine);
+    if (c > c0) wave_load(dO + (size_t)(c - 1) * kC * vld, vld, kC, mine0);
 
     // dS = P_end H + Q^T (P dO) - K^T (P dR)
     const float last = *reinterpret_cast<const float*>(now + St::vec + 4 * (kC - 1));
@@ -335,29 +361,35 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
     async_wait();
     __syncthreads();
   }
-  if (a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
+  if (LOCAL)
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.carry) + at.segment * DK * a.d_v, at.col0, H);
+  else if (c0 == 0 && a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
 }
 
 template <typename F>
-hipError_t launch(F kernel, const ScanArgs& a, int waves, size_t lds, hipStream_t stream) {
+hipError_t launch(F kernel, const ScanArgs& a, int columns, int waves, size_t lds, hipStream_t stream) {
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const size_t grid = (size_t)a.n_seq * a.heads * (a.d_v / (16 * waves));
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * waves), lds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)walk_grid(a, columns, waves)), dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
 }
 
 template <int RULE, int DK, int NW>
 hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
-  if (what == 0)
-    return launch(chain_forward_kernel<RULE, DK, NW, false>, a, NW,
-                  2 * Stage<RULE, DK, true, 2, 2, true>::bytes + 2048 * NW, stream);
-  if (what == 1)
-    return launch(chain_forward_kernel<RULE, DK, NW, true>, a, NW,
-                  2 * Stage<RULE, DK, false, 3, 2, false>::bytes + 2048 * NW, stream);
-  return launch(chain_reverse_kernel<RULE, DK, NW>, a, NW, 2 * Stage<RULE, DK, true, 3, 3, true>::bytes + 2048 * NW,
-                stream);
+  constexpr size_t own = 2048 * NW;
+  constexpr size_t read = 2 * Stage<RULE, DK, true, 2, 2, true>::bytes + own;
+  constexpr size_t save = 2 * Stage<RULE, DK, false, 3, 2, false>::bytes + own;
+  constexpr size_t back = 2 * Stage<RULE, DK, true, 3, 3, true>::bytes + own;
+  switch (what) {
+    case 0: return launch(chain_forward_kernel<RULE, DK, NW, kRead>, a, a.d_v, NW, read, stream);
+    case 1: return launch(chain_forward_kernel<RULE, DK, NW, kSave>, a, a.d_v, NW, save, stream);
+    case 2: return launch(chain_reverse_kernel<RULE, DK, NW, false>, a, a.d_v, NW, back, stream);
+    case 3:
+      return launch(chain_forward_kernel<RULE, DK, NW, kCarry>, a,
+                    a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
+    default: return launch(chain_reverse_kernel<RULE, DK, NW, true>, a, a.d_v, NW, back, stream);
+  }
 }
 template <int RULE>
 hipError_t chain_shape(const ScanArgs& a, int what, hipStream_t stream) {

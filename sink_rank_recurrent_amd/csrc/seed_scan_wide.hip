@@ -61,6 +61,12 @@ struct Tiles {
         x[m][r] = n >= kC || 16 * m + 4 * (lane_id() >> 4) + r < n ? row[lane] : T(0);
       }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[m][r] = T(0);
+  }
   __device__ __forceinline__ f32x4 tile(int m) const {
     return f32x4{load_scalar(&x[m][0]), load_scalar(&x[m][1]), load_scalar(&x[m][2]),
                  load_scalar(&x[m][3])};
@@ -69,30 +75,33 @@ struct Tiles {
 
 // Terms: as in seed_scan_chain.hip, two for the corrections and the read-outs
 // where the read-outs are bf16, three otherwise.
-template <int RULE, int DK, typename T, bool SAVE>
+template <int RULE, int DK, typename T, bool READ>
 struct Wide {
   static constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
-  static constexpr bool OUT16 = sizeof(T) == 2 && !SAVE;
+  static constexpr bool OUT16 = sizeof(T) == 2 && READ;
   static constexpr int NC = OUT16 ? 2 : 3;                       // corrections
   static constexpr int NV = sizeof(T) == 2 ? 1 : 3;              // a value or a gradient
   static constexpr int q = 3 * kPlane<DK>;
-  static constexpr int n = q + (SAVE ? 0 : NC * kPlane<DK>);
+  static constexpr int n = q + (READ ? NC * kPlane<DK> : 0);
   static constexpr int m = n + (DELTA ? kTriFrags * NC * 1024 : 0);
-  static constexpr int vec = m + (SAVE ? 0 : kTriFrags * NC * 1024);
+  static constexpr int vec = m + (READ ? kTriFrags * NC * 1024 : 0);
   static constexpr int bytes = vec + 1024;
 };
 
-template <int RULE, int DK, int NW, typename T, bool SAVE>
+template <int RULE, int DK, int NW, typename T, int MODE>
 __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
-  using W = Wide<RULE, DK, T, SAVE>;
+  constexpr bool READ = MODE == kRead, SAVE = MODE == kSave, CARRY = MODE == kCarry;
+  using W = Wide<RULE, DK, T, READ>;
   constexpr bool KDA = W::KDA, DELTA = W::DELTA;
   constexpr int IT = DK / 16, NC = W::NC, TH = 64 * NW;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
-  const Place<NW> at(a);
+  const Walk<NW> at(a, a.d_v + (CARRY && DELTA ? DK : 0));
+  if (at.c0 > at.c1 || (CARRY && at.c1 == at.chunks)) return;   // nothing is behind a last segment
   const uint32_t lds0 = lds_offset(lds);
-  const Range rg = sequence(a, at.seq);
-  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const Range rg = at.rg;
+  const int c0 = at.c0, c1 = at.c1, base = at.base;
+  const bool unit_cols = CARRY && DELTA && at.col0 >= a.d_v;
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
   const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
@@ -104,7 +113,11 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
   T* out = static_cast<T*>(a.o) + vat;
 
   f32x4 S[IT];
-  load_state(a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+  if (unit_cols) unit_state(at.col - a.d_v, S);
+  else if (!CARRY && c0 > 0)
+    load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, S);
+  else load_state(!CARRY && a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
+  float through = 1.f;
 
   Share<DK, TH, T> kr, qr;
   Share<DK, TH, float> pr, fr;
@@ -114,30 +127,31 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     kr.load(K + (size_t)c * kC * kld, kld, n);
-    if (!SAVE) qr.load(Q + (size_t)c * kC * kld, kld, n);
+    if (READ) qr.load(Q + (size_t)c * kC * kld, kld, n);
     if (KDA) {
       pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
       fr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
     }
-    v.load(V + (size_t)c * kC * vld, vld, row_lane, n);
+    if (unit_cols) v.clear();
+    else v.load(V + (size_t)c * kC * vld, vld, row_lane, n);
   };
-  if (chunks > 0) fetch(0);
-  for (int c = 0; c < chunks; ++c) {
+  if (c0 < c1) fetch(c0);
+  for (int c = c0; c < c1; ++c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     __syncthreads();   // the chunk before is done with the planes
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
-    if (!SAVE)
+    if (READ)
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
     if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
     if (KDA) {
       if (DELTA) fill<DK, TH, NC, true>(lds, kr, pr);
-      if (!SAVE) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
+      if (READ) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
     } else {
       fill<DK, TH, 3, false>(lds, kr, pr);
-      if (!SAVE) fill<DK, TH, NC, false>(lds + W::q, qr, pr);
+      if (READ) fill<DK, TH, NC, false>(lds + W::q, qr, pr);
     }
     f32x4 u[4];
 #pragma unroll
@@ -146,12 +160,12 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     __syncthreads();
     if (SAVE)
       keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
-    if (!KDA && c + 1 < chunks) fetch(c + 1);
+    if (!KDA && c + 1 < c1) fetch(c + 1);
 
     f32x4 R[4], O[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) R[m] = O[m] = zero4();
-    if (DELTA || !SAVE) {
+    if (DELTA || READ) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
         const Frag<NC> s = split_tiles<NC>(S[2 * ks], S[2 * ks + 1]);
@@ -161,7 +175,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds, m, ks);
           mma_tiles<4, NC, NC, NC>(R, f, s);
         }
-        if (!SAVE) {
+        if (READ) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds + W::q, m, ks);
           mma_tiles<4, NC, NC, NC>(O, f, s);
@@ -175,7 +189,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
                                                   (unit * kC + kC - 1) * DK + state_row(m));
       __syncthreads();
       fill<DK, TH, 3, true>(lds, kr, fr);
-      if (c + 1 < chunks) fetch(c + 1);
+      if (c + 1 < c1) fetch(c + 1);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -210,7 +224,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) u[m] *= b[m];
     }
-    if (!SAVE) {
+    if (READ) {
       constexpr int NU = DELTA ? NC : W::NV;   // V itself is one term
       const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
       Frag<NC> f[4];
@@ -236,6 +250,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       for (int m = 0; m < 4; ++m) u[m] *= lds_vec(lds + W::vec + 256, m);
 #pragma unroll
       for (int m = 0; m < IT; ++m) S[m] *= end;
+      if (CARRY && !DELTA) through *= end;
     }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -255,7 +270,13 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       }
     }
   }
-  if (!SAVE) keep_state(a.S + state, a.d_v, state_lane, S);
+  if (READ && c1 == at.chunks) keep_state(a.S + state, a.d_v, state_lane, S);
+  if (CARRY) {
+    float* trans = reinterpret_cast<float*>(a.ws + a.at.trans);
+    if (unit_cols) keep_chunk_state(trans + at.segment * DK * DK, at.col0 - a.d_v, S);
+    else keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.carry) + at.segment * DK * a.d_v, at.col0, S);
+    if (!DELTA && threadIdx.x == 0) trans[at.segment] = through;
+  }
 }
 
 template <int DK, int RULE>
@@ -269,17 +290,18 @@ struct WideBack {
 };
 
 // The chunks from the last to the first (see chain_reverse_kernel).
-template <int RULE, int DK, int NW, typename T>
+template <int RULE, int DK, int NW, typename T, bool LOCAL>
 __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
   using W = WideBack<DK, RULE>;
   constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
   constexpr int IT = DK / 16, TH = 64 * NW, NV = sizeof(T) == 2 ? 1 : 3;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
-  const Place<NW> at(a);
+  const Walk<NW> at(a, a.d_v);
+  if (at.c0 > at.c1 || (LOCAL && at.c0 == 0)) return;   // nothing is before a first segment
   const uint32_t lds0 = lds_offset(lds);
-  const Range rg = sequence(a, at.seq);
-  const int chunks = (rg.len + kC - 1) / kC, base = slot_base(rg, at.seq);
+  const Range rg = at.rg;
+  const int c0 = at.c0, c1 = at.c1, base = at.base;
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * a.d_v;
   const size_t state = ((size_t)at.seq * a.heads + at.head) * DK * a.d_v;
   const uint32_t g = lane_id() >> 4, row_lane = 4 * g * (uint32_t)vld + at.col;
@@ -291,7 +313,10 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
   T* dV = static_cast<T*>(a.dv) + vat;
 
   f32x4 H[IT];
-  load_state(a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
+  // a last segment starts from dS, in its own first pass too
+  if (c1 < at.chunks && !LOCAL)
+    load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, H);
+  else load_state(c1 == at.chunks && a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
 
   Share<DK, TH, T> kr, qr;
   Share<DK, TH, float> pr, fr;
@@ -307,8 +332,8 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     }
     d.load(dO + (size_t)c * kC * vld, vld, row_lane, n);
   };
-  if (chunks > 0) fetch(chunks - 1);
-  for (int c = chunks - 1; c >= 0; --c) {
+  if (c0 < c1) fetch(c1 - 1);
+  for (int c = c1 - 1; c >= c0; --c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     __syncthreads();
@@ -332,8 +357,9 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     }
     async_wait();
     __syncthreads();
-    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
-    if (!KDA && c > 0) fetch(c - 1);
+    if (!LOCAL)
+      keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
+    if (!KDA && c > c0) fetch(c - 1);
 
     // dU = F (K H) + M^T dO
 #pragma unroll
@@ -352,7 +378,7 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
                                                   (unit * kC + kC - 1) * DK + state_row(m));
       __syncthreads();
       fill<DK, TH, 3, true>(lds, kr, pr);
-      if (c > 0) fetch(c - 1);
+      if (c > c0) fetch(c - 1);
     } else {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= lds_vec(lds + W::vec + 256, m);
@@ -392,11 +418,12 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
       y[2] -= t[2];
       y[3] -= t[3];
       drop_rows(y, n);
-      keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
+      if (!LOCAL)
+        keep_tiles(reinterpret_cast<float*>(a.ws + a.at.y) + unit * kC * a.d_v, a.d_v, keep_lane, y);
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= b[m];
     }
-    store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+    if (!LOCAL) store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
 
     // dS = P_end H + (P Q)^T dO - (P K)^T dR
     if (KDA) {
@@ -441,28 +468,33 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
       }
     }
   }
-  if (a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
+  if (LOCAL)
+    keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.carry) + at.segment * DK * a.d_v, at.col0, H);
+  else if (c0 == 0 && a.dS0) keep_state(a.dS0 + state, a.d_v, state_lane, H);
 }
 
 template <typename F>
-hipError_t launch(F kernel, const ScanArgs& a, int waves, size_t lds, hipStream_t stream) {
+hipError_t launch(F kernel, const ScanArgs& a, int columns, int waves, size_t lds, hipStream_t stream) {
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const size_t grid = (size_t)a.n_seq * a.heads * (a.d_v / (16 * waves));
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * waves), lds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)walk_grid(a, columns, waves)), dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
 }
 
 template <int RULE, int DK, int NW, typename T>
 hipError_t wide(const ScanArgs& a, int what, hipStream_t stream) {
-  if (what == 0)
-    return launch(wide_forward_kernel<RULE, DK, NW, T, false>, a, NW, Wide<RULE, DK, T, false>::bytes,
-                  stream);
-  if (what == 1)
-    return launch(wide_forward_kernel<RULE, DK, NW, T, true>, a, NW, Wide<RULE, DK, T, true>::bytes,
-                  stream);
-  return launch(wide_reverse_kernel<RULE, DK, NW, T>, a, NW, WideBack<DK, RULE>::bytes, stream);
+  constexpr size_t read = Wide<RULE, DK, T, true>::bytes, save = Wide<RULE, DK, T, false>::bytes;
+  constexpr size_t back = WideBack<DK, RULE>::bytes;
+  switch (what) {
+    case 0: return launch(wide_forward_kernel<RULE, DK, NW, T, kRead>, a, a.d_v, NW, read, stream);
+    case 1: return launch(wide_forward_kernel<RULE, DK, NW, T, kSave>, a, a.d_v, NW, save, stream);
+    case 2: return launch(wide_reverse_kernel<RULE, DK, NW, T, false>, a, a.d_v, NW, back, stream);
+    case 3:
+      return launch(wide_forward_kernel<RULE, DK, NW, T, kCarry>, a,
+                    a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
+    default: return launch(wide_reverse_kernel<RULE, DK, NW, T, true>, a, a.d_v, NW, back, stream);
+  }
 }
 template <int RULE, typename T>
 hipError_t wide_shape(const ScanArgs& a, int what, hipStream_t stream) {

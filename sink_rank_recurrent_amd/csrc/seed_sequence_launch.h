@@ -26,6 +26,12 @@ struct ScanLayout {
   size_t dq, dk;     // per-head gradients of keys and queries (backward: KDA, shared heads)
   size_t tp, tf;     // gradients of P and F (backward, KDA)
   size_t slow;       // 1 where a chunk's gradients go pair by pair (backward, KDA): one int
+  // a long axis in segments of `seg` chunks (0: whole sequences), for each
+  // (segment, head): the state a segment leaves behind zero (or the gradient
+  // it passes back from zero), how it carries a state through (a matrix;
+  // Mamba-2: a factor), and the state at its start (gradient at its end)
+  int seg, segs;
+  size_t carry, trans, start;
   size_t bytes;
 };
 
@@ -60,10 +66,13 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t stream);
 // Phases of the recurrence (seed_scan_*.hip).
 hipError_t launch_scan_prep(const ScanArgs& a, bool backward, hipStream_t stream);
 // From chunk to chunk: what = 0 forward, 1 forward for the backward pass
-// (keeps S and E, writes no read-outs), 2 backward.  chain: bf16 inputs and
+// (keeps S and E, writes no read-outs), 2 backward; in segments also 3 what
+// each carries, 4 what each passes back.  chain: bf16 inputs and
 // scalar gates; wide: the others.
 hipError_t launch_scan_chain(const ScanArgs& a, int what, hipStream_t stream);
 hipError_t launch_scan_wide(const ScanArgs& a, int what, hipStream_t stream);
+// The starts of all segments from their carries (seed_scan_join.hip).
+hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_scan_grads(const ScanArgs& a, hipStream_t stream);
 
 enum NormAct { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };

@@ -129,6 +129,31 @@ def test_backward(rule, dims, dtype, offsets):
 
 
 @pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("initial", [False, True])
+def test_segments(rule, dims, dtype, initial):
+    """Few heads and long sequences go in segments side by side: sequences of
+    27, 0, 1 and 7 chunks, the segments' ends inside and at a sequence's end,
+    rows outside."""
+    offsets = [70, 1770, 1770, 1830, 2240]
+    T = 2250
+    x = inputs(rule, T, 2, 1, *dims, 4, dtype, 12, initial=initial)
+    o, S = run(rule, x, offsets)
+    h = host(x)
+    wo, wS = oseq.scan(rule, **h, offsets=offsets)
+    check(o, wo, offsets, "o")
+    check(S, wS, offsets, "S")
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    do = torch.randn(x["v"].shape, device="cuda", generator=gen).to(dtype)
+    dS = torch.randn(4, 2, *dims, device="cuda", generator=gen) if initial else None
+    got = run_back(rule, x, offsets, do, dS)
+    want = oseq.scan_backward(rule, **h, offsets=offsets, do=f64(do), dS=None if dS is None else f64(dS))
+    for name in got:
+        check(got[name], want[name], offsets, name, terms=want.get(name + "_scale"))
+
+
+@pytest.mark.parametrize("rule", RULES)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_shared_keys_outside_rows_and_no_initial_state(rule, dtype):
     """Six heads on two key heads; tokens before the first sequence and
