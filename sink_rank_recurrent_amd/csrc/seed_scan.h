@@ -162,10 +162,12 @@ __device__ __forceinline__ Frag<3> load_pack(const uint16_t* __restrict__ pack, 
     f.t[n] = *reinterpret_cast<const u32x4*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8);
   return f;
 }
+// (third: the third term is read by somebody)
 __device__ __forceinline__ void store_pack(uint16_t* __restrict__ pack, int frag,
-                                           const Frag<3>& f) {
+                                           const Frag<3>& f, bool third = true) {
 #pragma unroll
   for (int n = 0; n < 3; ++n)
+    if (n < 2 || third)
     *reinterpret_cast<u32x4*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8) = f.t[n];
 }
 
@@ -192,18 +194,36 @@ __device__ __forceinline__ int slot_base(const Range& r, int s) { return r.start
 // The sequence of a slot, slots of `unit` tokens (start / unit + s the first
 // of sequence s): the last whose first slot is not behind it; a wave tries 64
 // at a time.
-__device__ __forceinline__ int sequence_of_slot(const ScanArgs& a, int slot, int unit) {
+struct Found {
+  int seq;
+  Range rg;
+};
+__device__ __forceinline__ Found sequence_of_slot(const ScanArgs& a, int slot, int unit) {
   const int lane = threadIdx.x & 63;
   int lo = 0, span = a.n_seq;
-  while (span > 1) {
+  Range r;
+  for (;;) {
     const int step = (span + 63) >> 6;
-    const int i = lo + lane * step;
-    const bool at = lane * step < span && sequence(a, i).start / unit + i <= slot;
+    const int i = min(lo + lane * step, a.n_seq - 1);
+    r = sequence(a, i);
+    const bool at = lane * step < span && r.start / unit + i <= slot;
     const int last = 63 - __builtin_clzll(__ballot(at) | 1);
     lo += last * step;
+    if (step == 1) {
+      return {__builtin_amdgcn_readfirstlane(lo),
+              {__builtin_amdgcn_readlane(r.start, last), __builtin_amdgcn_readlane(r.len, last)}};
+    }
     span = min(step, span - last * step);
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The head of number x of a token's: heads in turn over the key heads, so that
+// (with workgroups dealt to 8 XCDs in turn) heads that share keys share an
+// L2.  Kernels count heads fastest: workgroups that run together then read
+// whole rows (one head at a time, preparation of 64 x 512 tokens x 16 heads
+// took 155 us instead of 144, the KDA gradients 384 us instead of 315).
+__device__ __forceinline__ int head_of(const ScanArgs& a, int x) {
+  return x % a.key_heads * (a.heads / a.key_heads) + x / a.key_heads;
 }
 
 // The chunk of a slot: sequence and first token, n tokens (0: none).
@@ -211,8 +231,9 @@ struct Chunk {
   int seq, tok, n, index;
 };
 __device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& a, int slot) {
-  const int lo = sequence_of_slot(a, slot, kC);
-  const Range r = sequence(a, lo);
+  const Found found = sequence_of_slot(a, slot, kC);
+  const int lo = found.seq;
+  const Range r = found.rg;
   const int c = slot - slot_base(r, lo);
   if (c < 0 || c * kC >= r.len) return {lo, 0, 0, 0};
   const int left = r.len - c * kC;
@@ -367,7 +388,16 @@ __device__ __forceinline__ void load_piece(const T* __restrict__ row, int col0, 
   const int g = lane_id() >> 4;
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j] = 0.f;
-  if (live) {
+  if constexpr (sizeof(T) == 2) {
+    if (live) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(row + col0 + 8 * g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(v[j] << 16);
+        x[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+      }
+    }
+  } else if (live) {
     float a[4], b[4];
     load_vec<4>(row + col0 + 8 * g, a);
     load_vec<4>(row + col0 + 8 * g + 4, b);

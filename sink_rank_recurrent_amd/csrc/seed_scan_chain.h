@@ -164,10 +164,16 @@ struct Walk {
     const int blocks = columns / (16 * NW);
     const int sh = blockIdx.x / blocks;
     const int first = sh / a.heads;
-    head = sh % a.heads;
-    segment = (size_t)sh;
-    seq = a.at.seg ? sequence_of_slot(a, first, kC * a.at.seg) : first;
-    rg = sequence(a, seq);
+    head = head_of(a, sh % a.heads);
+    segment = (size_t)first * a.heads + head;
+    if (a.at.seg) {
+      const Found found = sequence_of_slot(a, first, kC * a.at.seg);
+      seq = found.seq;
+      rg = found.rg;
+    } else {
+      seq = first;
+      rg = sequence(a, seq);
+    }
     chunks = (rg.len + kC - 1) / kC;
     base = slot_base(rg, seq);
     c0 = 0;

@@ -57,11 +57,11 @@ __global__ __launch_bounds__(256) void grads_kernel(ScanArgs a) {
   float* dF = dP + kC;
   float* red = dF + kC;              // [4][64]
   float* hs = red + 4 * kC;          // [DK]
-  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int l16 = l & 15, g16 = l >> 4, n = ch.n;
-  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   if (KDA && !reinterpret_cast<const int*>(a.ws + a.at.slow)[unit]) return;
   const int hk = head / (a.heads / a.key_heads);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * DV;
@@ -460,11 +460,11 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
   float* red = Fv + kC;       // [4][64]
   float* dPF = red + 4 * kC;  // [half][dP, dF][64]
   float* hs = dPF + 4 * kC;   // [8]
-  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
+  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
   const int w4 = (tid >> 6) & 3, half = tid >> 8, n = ch.n;
-  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t kld = (size_t)a.key_heads * DK, vld = (size_t)a.heads * DV;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
@@ -806,11 +806,11 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   float* tot = reinterpret_cast<float*>(smem + Lds::small);   // [x, z][4][32]
   float* hs = tot + 4 * 2 * 32;                 // [wave][32]
   int* bad = reinterpret_cast<int*>(hs + 8 * 32);
-  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
+  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
   const int w4 = (tid >> 6) & 3, half = tid >> 8, n = ch.n;
-  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t kld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
@@ -1126,21 +1126,21 @@ hipError_t grads(const ScanArgs& a, hipStream_t stream) {
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_scalar_kernel<RULE, DK, DV, T>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((grads_scalar_kernel<RULE, DK, DV, T>), dim3(a.slots, a.heads), dim3(512),
+    hipLaunchKernelGGL((grads_scalar_kernel<RULE, DK, DV, T>), dim3((unsigned)((size_t)a.slots * a.heads)), dim3(512),
                        bytes, stream, a);
   } else {
   constexpr size_t bytes = KdaLds<DK, DV, T>::bytes;
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kda_kernel<DK, DV, T>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grads_kda_kernel<DK, DV, T>), dim3(a.slots, a.heads), dim3(512), bytes, stream, a);
+  hipLaunchKernelGGL((grads_kda_kernel<DK, DV, T>), dim3((unsigned)((size_t)a.slots * a.heads)), dim3(512), bytes, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t lds = ((KDA ? 2 : 4) * kC * kLd + 6 * kC + DK + (KDA ? 3 * kC * DK : 0)) * sizeof(float);
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kernel<RULE, DK, DV, T>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grads_kernel<RULE, DK, DV, T>), dim3(a.slots, a.heads), dim3(256), lds, stream, a);
+  hipLaunchKernelGGL((grads_kernel<RULE, DK, DV, T>), dim3((unsigned)((size_t)a.slots * a.heads)), dim3(256), lds, stream, a);
   }
   e = hipGetLastError();
   if (e != hipSuccess || a.key_heads == a.heads) return e;

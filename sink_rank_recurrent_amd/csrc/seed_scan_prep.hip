@@ -59,7 +59,8 @@ __device__ __forceinline__ void solve(float* L, float* X, const float* beta, int
 
 // The triangle of an LDS matrix as a pack (transposed: of its transpose).
 __device__ __forceinline__ void pack_triangle(uint16_t* __restrict__ pack, const float* mat,
-                                              bool transposed, int mt, int ks) {
+                                              bool transposed, int mt, int ks,
+                                              bool third = true) {
   const int frag = transposed ? upper_frag(mt, ks) : lower_frag(mt, ks);
   if (frag < 0) return;
   const int row = 16 * mt + (lane_id() & 15), g = lane_id() >> 4;
@@ -71,86 +72,117 @@ __device__ __forceinline__ void pack_triangle(uint16_t* __restrict__ pack, const
     tiles_to_floats(*reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 4 * g),
                     *reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 16 + 4 * g), x);
   }
-  store_pack(pack, frag, split<3>(x));
+  store_pack(pack, frag, split<3>(x), third);
 }
 
 // Half a fragment (slots 4 h .. 4 h + 3): one accumulator tile of the
 // transposed product.
 __device__ __forceinline__ void store_half(uint16_t* __restrict__ pack, int frag, int h,
-                                           const f32x4& c) {
+                                           const f32x4& c, bool third) {
   const float x[8] = {c[0], c[1], c[2], c[3], 0.f, 0.f, 0.f, 0.f};
   const Frag<3> f = split<3>(x);
 #pragma unroll
   for (int n = 0; n < 3; ++n)
-    *reinterpret_cast<uint2*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8 + 4 * h) =
+    if (n < 2 || third)
+      *reinterpret_cast<uint2*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8 + 4 * h) =
         make_uint2(f.t[n][0], f.t[n][1]);
 }
 
-// Four waves a (chunk, head); wave a has the tokens 16 a .. + 15 as rows.
+// A chunk's rows of a float32 array into three planes, rows from n on 0.
+template <int DK>
+__device__ __forceinline__ void split_rows(const float* rows, size_t ld, int n, char* planes) {
+  for (int e = threadIdx.x; e < kC * DK / 8; e += 256) {
+    const int t = e / (DK / 8), c = e % (DK / 8);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (t < n) {
+      const float* p = rows + (size_t)t * ld + 8 * c;
+      tiles_to_floats(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4), x);
+    }
+    const Frag<3> f = split<3>(x);
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+      *reinterpret_cast<u32x4*>(planes + m * kPlane<DK> + piece_at<DK>(t, c)) = f.t[m];
+  }
+}
+
+// Four waves a (chunk, head); wave w has the tokens 16 w .. + 15 as rows.  K
+// and Q lie in LDS by whole rows (256 bytes at a time: fragments straight from
+// memory, 64 bytes of a row at a time, took the preparation of 64 x 512
+// tokens x 16 heads 132 us), L then in their place.  (float32: only K, in
+// three terms; a wave takes its rows of Q from memory.)
 template <int RULE, int DK, typename T, bool BWD>
 __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   constexpr int NT = sizeof(T) == 2 ? 1 : 3;
   constexpr bool DELTA = RULE != kMAMBA2;
-  __shared__ __attribute__((aligned(16))) float L[DELTA ? kC * kRow : 4];
-  __shared__ __attribute__((aligned(16))) float X[DELTA ? 64 * 20 : 4];
+  constexpr int KQ = (NT == 1 ? 2 : 3) * kPlane<DK>, SOLVE = (kC * kRow + 64 * 20) * 4;
+  __shared__ __attribute__((aligned(1024))) char buf[DELTA && SOLVE > KQ ? SOLVE : KQ];
   __shared__ __attribute__((aligned(16))) float bt[kC];
-  __shared__ __attribute__((aligned(16))) uint16_t kl[4 * (DK / 32) * NT * kFrag];   // K's fragments
   __shared__ Decay dec;
-  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  char* Kp = buf;
+  char* Qp = buf + kPlane<DK>;
+  float* L = reinterpret_cast<float*>(buf);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, w = threadIdx.x >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
-  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const int head = head_of(a, blockIdx.x % a.heads), w = wave_id(), l = lane_id(), g16 = l >> 4, l16 = l & 15;
+  const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t ld = (size_t)a.key_heads * DK;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
+  // a forward pass with bf16 read-outs reads two terms, its segments' carries
+  // three of N
+  const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
-  // the wave's rows of K and Q
-  const int t0 = 16 * w + l16;
-  Frag<NT> kt[DK / 32], qt[DK / 32];
-#pragma unroll
-  for (int ks = 0; ks < DK / 32; ++ks) {
-    float x[8];
-    load_piece(K + (size_t)t0 * ld, 32 * ks, t0 < ch.n, x);
-    kt[ks] = split<NT>(x);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *reinterpret_cast<u32x4*>(kl + (((w * (DK / 32) + ks) * NT + n) * 64 + l) * 8) = kt[ks].t[n];
-    load_piece(Q + (size_t)t0 * ld, 32 * ks, t0 < ch.n, x);
-    qt[ks] = split<NT>(x);
+  if constexpr (NT == 1) {
+    async_rows<DK, 4>(K, Q, ld, ch.n, lds_offset(Kp), lds_offset(Qp), true, w);
+  } else {
+    split_rows<DK>(K, ld, ch.n, Kp);
   }
   if (w == 0) {
     const size_t gate = ((size_t)ch.tok + l) * a.heads + head;
     float P, F;
     float* vec = reinterpret_cast<float*>(a.ws + a.at.vec) + unit * 256;
-    decays(dec, l < ch.n ? a.g[gate] : 1.f, P, F);
-    vec[l] = P;
-    vec[64 + l] = F;
     if (DELTA) {
       bt[l] = l < ch.n ? a.beta[gate] : 0.f;
       vec[128 + l] = bt[l];
     }
+    decays(dec, l < ch.n ? a.g[gate] : 1.f, P, F);
+    vec[l] = P;
+    vec[64 + l] = F;
   }
+  async_wait();
   __syncthreads();
 
-  for (int b = 0; b < 4; ++b) {
-    // lane (t, s): its row of the right operand and four rows of the left;
-    // backward the left operand is Q, and M's tile comes out transposed
-    f32x4 ll = {0.f, 0.f, 0.f, 0.f}, mm = ll;
-    if (b <= w) {
+  // lane (t, s): its row of the right operand and four rows of the left;
+  // backward the left operand is Q, and M's tile comes out transposed
+  f32x4 lt[4], mt[4];
 #pragma unroll
-      for (int ks = 0; ks < DK / 32; ++ks) {
-        Frag<NT> kb;
+  for (int b = 0; b < 4; ++b) lt[b] = mt[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          kb.t[n] = *reinterpret_cast<const u32x4*>(kl + (((b * (DK / 32) + ks) * NT + n) * 64 + l) * 8);
-        if (DELTA) mma(ll, kb, kt[ks]);
-        if (BWD) mma(mm, qt[ks], kb);
-        else mma(mm, kb, qt[ks]);
-      }
+  for (int ks = 0; ks < DK / 32; ++ks) {
+    const Frag<NT> kt = lds_rows<DK, NT>(Kp, w, ks);
+    Frag<NT> qt;
+    if constexpr (NT == 1) {
+      qt = lds_rows<DK, NT>(Qp, w, ks);
+    } else {
+      float x[8];
+      load_piece(Q + (size_t)(16 * w + l16) * ld, 32 * ks, 16 * w + l16 < ch.n, x);
+      qt = split<NT>(x);
     }
-    f32x4 gl = {0.f, 0.f, 0.f, 0.f}, gm = gl;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b > w) continue;
+      const Frag<NT> kb = lds_rows<DK, NT>(Kp, b, ks);
+      if (DELTA) mma(lt[b], kb, kt);
+      if (BWD) mma(mt[b], qt, kb);
+      else mma(mt[b], kb, qt);
+    }
+  }
+  if (DELTA) __syncthreads();   // L takes K's place
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    f32x4 gl = {0.f, 0.f, 0.f, 0.f}, gm = gl, mm = mt[b];
     const int t = 16 * w + l16, s = 16 * b + 4 * g16;        // L, and M forward
     const int tm = 16 * w + 4 * g16, sm = 16 * b + l16;      // M backward
     if (b < w) {
@@ -162,24 +194,35 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
       gm = BWD ? inside<true>(dec.gate, tm, sm) : gl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        gm[r] = (BWD ? sm <= tm + r : s + r <= t) ? gm[r] : 0.f;
+        const bool in = BWD ? sm <= tm + r : s + r <= t;
+        gm[r] = in ? gm[r] : 0.f;
+        mm[r] = in ? mm[r] : 0.f;
         gl[r] = s + r < t ? gl[r] : 0.f;
       }
     }
-    if (DELTA) *reinterpret_cast<f32x4*>(L + (16 * w + l16) * kRow + 16 * b + 4 * g16) = ll * gl;
+    // (rows and columns past the sequence's end repeat its last token: their
+    // beta, values and read-outs are dropped, but N and M must not reach them)
+    if (ch.n < kC) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (t >= ch.n || s + r >= ch.n) gl[r] = lt[b][r] = 0.f;
+        if (BWD ? tm + r >= ch.n || sm >= ch.n : t >= ch.n || s + r >= ch.n) gm[r] = mm[r] = 0.f;
+      }
+    }
+    if (DELTA) *reinterpret_cast<f32x4*>(L + t * kRow + s) = lt[b] * gl;
     mm *= gm;
     if (BWD) {
       // rows s of tile b, tokens of tile w; a block's zero half is written too
-      if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
+      if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm, true);
     } else {
-      if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
+      if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm, m_third);
     }
   }
   if (DELTA) {
     __syncthreads();
-    solve(L, X, bt, w);
+    solve(L, L + kC * kRow, bt, w);
     uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-    for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
+    for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1, n_third);
     if (BWD) {
       uint16_t* tp =
           reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
@@ -282,10 +325,10 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   __shared__ __attribute__((aligned(16))) float bt[kC];
   __shared__ int unsafe;
   uint16_t* kl = reinterpret_cast<uint16_t*>(buf);   // K / P in fragments
-  const Chunk ch = chunk_of_slot(a, blockIdx.x);
+  const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = blockIdx.y, tid = threadIdx.x, w = tid >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
-  const size_t unit = (size_t)blockIdx.x * a.heads + head;
+  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, w = tid >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
+  const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t ld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
@@ -294,6 +337,9 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   float* P = reinterpret_cast<float*>(a.ws + a.at.p) + unit * kC * DK;
   float* F = reinterpret_cast<float*>(a.ws + a.at.f) + unit * kC * DK;
   uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
+  // a forward pass with bf16 read-outs reads two terms, its segments' carries
+  // three of N
+  const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
   if (tid < kC) {
     bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
@@ -360,7 +406,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   if (unsafe) {
     float* M = reinterpret_cast<float*>(buf);
     slow_triangles<DK>(K, Q, ld, gates, gld, ch.n, M + kC * kRow, L, M, P, F);
-    for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1);
+    for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1, m_third);
   } else {
     f32x4 lt[4], mt[4];
 #pragma unroll
@@ -392,16 +438,16 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
       }
       *reinterpret_cast<f32x4*>(L + (16 * w + l16) * kRow + 16 * b + 4 * g16) = ll;
       if (BWD) {
-        if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
+        if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm, true);
       } else {
-        if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
+        if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm, m_third);
       }
     }
     __syncthreads();
   }
   solve(L, X, bt, w);
   uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-  for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
+  for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1, n_third);
   if (BWD) {
     uint16_t* tp =
         reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
@@ -411,7 +457,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
 
 template <int DK, typename T, bool BWD>
 hipError_t prep(const ScanArgs& a, hipStream_t stream) {
-  const dim3 grid(a.slots, a.heads);
+  const dim3 grid((unsigned)((size_t)a.slots * a.heads));
   if (a.rule == kKDA) {
     hipLaunchKernelGGL((prep_kda_kernel<DK, T, BWD>), grid, dim3(256), 0, stream, a);
   } else if (a.rule == kGDN) {

@@ -79,9 +79,11 @@ seed_status check_shape(const char* fn, int rule, int n_seq, int heads, int key_
                 d_k, d_v);
   if (heads > 65535)
     return fail(SEED_E_UNSUPPORTED, "%s: %d heads exceed the grid limit of 65535", fn, heads);
-  if ((long long)n_seq * heads * (d_v / 16) > 0x7fffffffLL ||
-      (long long)tokens + 64LL * n_seq > 0x7fffffffLL)
-    return fail(SEED_E_UNSUPPORTED, "%s: n_seq * heads or tokens exceed the grid limit", fn);
+  // a workgroup for each (chunk or sequence, head, columns)
+  const long long slots = (long long)tokens / seed::kScanChunk + n_seq;
+  if ((long long)tokens + 64LL * n_seq > 0x7fffffffLL ||
+      slots > 0x7fffffffLL / ((long long)heads * ((d_k + d_v) / 16)))
+    return fail(SEED_E_UNSUPPORTED, "%s: n_seq * heads or tokens * heads exceed the grid limit", fn);
   return SEED_OK;
 }
 
