@@ -21,17 +21,38 @@ __device__ __forceinline__ f32x4 lds_vec(const char* vec, int m) {
   return *reinterpret_cast<const f32x4*>(vec + 64 * m + 16 * (lane_id() >> 4));
 }
 
-// A wave's 64 rows x 16 columns of a bf16 array, in 2 KB of LDS of its own
-// (rows of 32 bytes).  Loads repeat row n - 1 from row n on.
+// A wave's 64 rows x 16 columns of an array, in LDS of its own (bf16: 2 KB,
+// rows of 32 bytes; float32: 4 KB).  Loads repeat row n - 1 from row n on, and
+// first wait for the wave's reads of what they replace.
+__device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+template <typename T>
+constexpr int kOwn = kC * 16 * (int)sizeof(T);
+__device__ __forceinline__ void wave_load(const float* p, uint32_t ld, int n, uint32_t to) {
+  lds_done();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 16 * i + (lane_id() >> 2);
+    async_copy(p, (uint32_t)min(t, n - 1) * (4 * ld) + 16 * (lane_id() & 3), to + 1024 * i);
+  }
+}
 __device__ __forceinline__ void wave_load(const bf16_t* p, uint32_t ld, int n, uint32_t to) {
+  lds_done();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = 32 * i + (lane_id() >> 1);
     async_copy(p, (uint32_t)min(t, n - 1) * (2 * ld) + 16 * (lane_id() & 1), to + 1024 * i);
   }
 }
+template <typename T>
+__device__ __forceinline__ f32x4 wave_tile(const char* from, int m);
+template <>
+__device__ __forceinline__ f32x4 wave_tile<float>(const char* from, int m) {
+  const float* at = reinterpret_cast<const float*>(from) + (16 * m + 4 * (lane_id() >> 4)) * 16 + (lane_id() & 15);
+  return f32x4{at[0], at[16], at[32], at[48]};
+}
 // As accumulator tiles, by transposing reads.
-__device__ __forceinline__ f32x4 wave_tile(const char* from, int m) {
+template <>
+__device__ __forceinline__ f32x4 wave_tile<bf16_t>(const char* from, int m) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   const int l = lane_id(), i = l & 15, g = l >> 4;
@@ -55,6 +76,20 @@ __device__ __forceinline__ void wave_store(bf16_t* p, size_t ld, int n, const f3
     const int t = 32 * i + (l >> 1);
     const u32x4 v = *reinterpret_cast<const u32x4*>(by + 1024 * i + 16 * l);
     if (t < n) *reinterpret_cast<u32x4*>(p + (size_t)t * ld + 8 * (l & 1)) = v;
+  }
+}
+__device__ __forceinline__ void wave_store(float* p, size_t ld, int n, const f32x4 (&x)[4], char* by) {
+  const int l = lane_id();
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      reinterpret_cast<float*>(by)[(16 * m + 4 * (l >> 4) + r) * 16 + (l & 15)] = x[m][r];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 16 * i + (l >> 2);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(by + 1024 * i + 16 * l);
+    if (t < n) *reinterpret_cast<f32x4*>(p + (size_t)t * ld + 4 * (l & 3)) = v;
   }
 }
 template <typename T>

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     f32x4 u[4], R[4], O[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      u[m] = unit_cols ? zero4() : wave_tile(mine, m);
+      u[m] = unit_cols ? zero4() : wave_tile<bf16_t>(mine, m);
       R[m] = O[m] = zero4();
     }
     drop_rows(u, n);
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       y[m] = zero4();
-      go[m] = wave_tile(mine, m);
+      go[m] = wave_tile<bf16_t>(mine, m);
     }
     drop_rows(go, n);
 #pragma unroll

@@ -4,7 +4,10 @@
 // wave owns 16 columns; the operands are split into LDS planes by the whole
 // workgroup, from values loaded while the chunk before was computed.  With
 // gates per channel K serves twice, scaled by P and by F: the second fills
-// the same planes once the first is used up.
+// the same planes once the first is used up, and F is loaded once P is used
+// (held together with P it spilt, and every spilt value was waited for: 25000
+// cycles a chunk of 48000).  A barrier behind the last use of N, M and the
+// vectors lets the next chunk's be loaded while the state is brought up.
 #include "seed_scan_chain.h"
 
 namespace seed {
@@ -120,47 +123,64 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
   float through = 1.f;
 
   Share<DK, TH, T> kr, qr;
-  Share<DK, TH, float> pr, fr;
+  Share<DK, TH, float> xr;   // P, then F
+  constexpr bool OWN = sizeof(T) == 2 || NW == 4;   // room for the waves' own columns of V
+  char* mine = lds + W::bytes + kOwn<T> * w;
+  const uint32_t mine0 = lds0 + W::bytes + kOwn<T> * w;
   Tiles<T> v;
   f32x4 last[KDA ? IT : 1];
-  auto fetch = [&](int c) {
+  auto keys = [&](int c) {
     const int n = min(kC, rg.len - c * kC);
-    const size_t unit = (size_t)(base + c) * a.heads + at.head;
     kr.load(K + (size_t)c * kC * kld, kld, n);
     if (READ) qr.load(Q + (size_t)c * kC * kld, kld, n);
-    if (KDA) {
-      pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
-      fr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
-    }
-    if (unit_cols) v.clear();
+    if (KDA)
+      xr.load(reinterpret_cast<const float*>(a.ws + a.at.p) +
+                  ((size_t)(base + c) * a.heads + at.head) * kC * DK, DK, kC);
+  };
+  auto values = [&](int c) {
+    const int n = min(kC, rg.len - c * kC);
+    if (unit_cols) return;
+    if constexpr (OWN) wave_load(V + at.col0 + (size_t)c * kC * vld, vld, n, mine0);
     else v.load(V + (size_t)c * kC * vld, vld, row_lane, n);
   };
-  if (c0 < c1) fetch(c0);
-  for (int c = c0; c < c1; ++c) {
-    const int n = min(kC, rg.len - c * kC);
+  auto triangles = [&](int c) {
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
-    __syncthreads();   // the chunk before is done with the planes
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
     if (READ)
       async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
     if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
+  };
+  if (c0 < c1) {
+    keys(c0);
+    values(c0);
+    triangles(c0);
+  }
+  for (int c = c0; c < c1; ++c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    __syncthreads();   // the chunk before is done with the planes
     if (KDA) {
-      if (DELTA) fill<DK, TH, NC, true>(lds, kr, pr);
-      if (READ) fill<DK, TH, NC, true>(lds + W::q, qr, pr);
+      if (DELTA) fill<DK, TH, NC, true>(lds, kr, xr);
+      if (READ) fill<DK, TH, NC, true>(lds + W::q, qr, xr);
     } else {
-      fill<DK, TH, 3, false>(lds, kr, pr);
-      if (READ) fill<DK, TH, NC, false>(lds + W::q, qr, pr);
+      fill<DK, TH, 3, false>(lds, kr, xr);
+      if (READ) fill<DK, TH, NC, false>(lds + W::q, qr, xr);
     }
-    f32x4 u[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) u[m] = v.tile(m);
     async_wait();
     __syncthreads();
+    f32x4 u[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if constexpr (OWN) u[m] = unit_cols ? zero4() : wave_tile<T>(mine, m);
+      else u[m] = unit_cols ? zero4() : v.tile(m);
+    }
+    drop_rows(u, n);
     if (SAVE)
       keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
-    if (!KDA && c + 1 < c1) fetch(c + 1);
+    if (KDA) xr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
+    else if (c + 1 < c1) keys(c + 1);
 
     f32x4 R[4], O[4];
 #pragma unroll
@@ -188,8 +208,8 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
         last[m] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.ws + a.at.p) +
                                                   (unit * kC + kC - 1) * DK + state_row(m));
       __syncthreads();
-      fill<DK, TH, 3, true>(lds, kr, fr);
-      if (c + 1 < c1) fetch(c + 1);
+      fill<DK, TH, 3, true>(lds, kr, xr);
+      if (c + 1 < c1) keys(c + 1);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -237,11 +257,12 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       mma_tiles<2, NC, NU, NC>(z, h, x1);
       O[2] = z[0];
       O[3] = z[1];
-      store_tiles(out + (size_t)c * kC * vld, vld, row_lane, n, O);
+      if constexpr (OWN) wave_store(out + at.col0 + (size_t)c * kC * vld, vld, n, O, mine);
+      else store_tiles(out + (size_t)c * kC * vld, vld, row_lane, n, O);
     }
+    if (c + 1 < c1) values(c + 1);
     // S' = P_end S + (F K)^T u
     if (KDA) {
-      __syncthreads();   // F K is in place
 #pragma unroll
       for (int m = 0; m < IT; ++m) S[m] *= last[m];
     } else {
@@ -252,6 +273,8 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       for (int m = 0; m < IT; ++m) S[m] *= end;
       if (CARRY && !DELTA) through *= end;
     }
+    __syncthreads();   // F K is in place, N, M and the vectors are used up
+    if (c + 1 < c1) triangles(c + 1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const Frag<3> x = split_tiles<3>(u[2 * ks], u[2 * ks + 1]);
@@ -320,8 +343,11 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
 
   Share<DK, TH, T> kr, qr;
   Share<DK, TH, float> pr, fr;
+  constexpr bool OWN = sizeof(T) == 2 || NW == 4;   // room for the waves' own columns of dO
+  char* mine = lds + W::bytes + kOwn<T> * w;
+  const uint32_t mine0 = lds0 + W::bytes + kOwn<T> * w;
   Tiles<T> d;
-  auto fetch = [&](int c) {
+  auto keys = [&](int c) {
     const int n = min(kC, rg.len - c * kC);
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     kr.load(K + (size_t)c * kC * kld, kld, n);
@@ -330,18 +356,29 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
       pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
       fr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
     }
-    d.load(dO + (size_t)c * kC * vld, vld, row_lane, n);
   };
-  if (c0 < c1) fetch(c1 - 1);
-  for (int c = c1 - 1; c >= c0; --c) {
+  auto values = [&](int c) {
     const int n = min(kC, rg.len - c * kC);
+    if constexpr (OWN) wave_load(dO + at.col0 + (size_t)c * kC * vld, vld, n, mine0);
+    else d.load(dO + (size_t)c * kC * vld, vld, row_lane, n);
+  };
+  auto triangles = [&](int c) {
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
-    __syncthreads();
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
       async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds0 + W::n, w);
     async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
     if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
+  };
+  if (c0 < c1) {
+    keys(c1 - 1);
+    values(c1 - 1);
+    triangles(c1 - 1);
+  }
+  for (int c = c1 - 1; c >= c0; --c) {
+    const int n = min(kC, rg.len - c * kC);
+    const size_t unit = (size_t)(base + c) * a.heads + at.head;
+    __syncthreads();
     if (KDA) {
       fill<DK, TH, 3, true>(lds, kr, fr);
       fill<DK, TH, 3, true>(lds + W::q, qr, pr);
@@ -349,17 +386,21 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
       fill<DK, TH, 3, false>(lds, kr, pr);
       fill<DK, TH, 3, false>(lds + W::q, qr, pr);
     }
+    async_wait();
+    __syncthreads();
     f32x4 y[4], go[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       y[m] = zero4();
-      go[m] = d.tile(m);
+      if constexpr (OWN) go[m] = wave_tile<T>(mine, m);
+      else go[m] = d.tile(m);
     }
-    async_wait();
-    __syncthreads();
+    drop_rows(go, n);
     if (!LOCAL)
       keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.grad) + unit * DK * a.d_v, at.col0, H);
-    if (!KDA && c > c0) fetch(c - 1);
+    // P again for P K: not held through the product, which would spill it
+    if (KDA) pr.load(reinterpret_cast<const float*>(a.ws + a.at.p) + unit * kC * DK, DK, kC);
+    else if (c > c0) keys(c - 1);
 
     // dU = F (K H) + M^T dO
 #pragma unroll
@@ -378,7 +419,7 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
                                                   (unit * kC + kC - 1) * DK + state_row(m));
       __syncthreads();
       fill<DK, TH, 3, true>(lds, kr, pr);
-      if (c > c0) fetch(c - 1);
+      if (c > c0) keys(c - 1);
     } else {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= lds_vec(lds + W::vec + 256, m);
@@ -423,11 +464,14 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] *= b[m];
     }
-    if (!LOCAL) store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+    if (!LOCAL) {
+      if constexpr (OWN) wave_store(dV + at.col0 + (size_t)c * kC * vld, vld, n, y, mine);
+      else store_tiles(dV + (size_t)c * kC * vld, vld, row_lane, n, y);
+    }
+    if (c > c0) values(c - 1);
 
     // dS = P_end H + (P Q)^T dO - (P K)^T dR
     if (KDA) {
-      __syncthreads();   // P K is in place
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[m] = -y[m];
 #pragma unroll
@@ -443,6 +487,8 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
 #pragma unroll
       for (int m = 0; m < IT; ++m) H[m] *= end;
     }
+    __syncthreads();   // P K is in place, N, M and the vectors are used up
+    if (c > c0) triangles(c - 1);
     constexpr int NG = KDA ? NV : 3;   // dO itself, or times P
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -484,8 +530,10 @@ hipError_t launch(F kernel, const ScanArgs& a, int columns, int waves, size_t ld
 
 template <int RULE, int DK, int NW, typename T>
 hipError_t wide(const ScanArgs& a, int what, hipStream_t stream) {
-  constexpr size_t read = Wide<RULE, DK, T, true>::bytes, save = Wide<RULE, DK, T, false>::bytes;
-  constexpr size_t back = WideBack<DK, RULE>::bytes;
+  constexpr size_t own = sizeof(T) == 2 || NW == 4 ? kOwn<T> * NW : 0;
+  constexpr size_t read = Wide<RULE, DK, T, true>::bytes + own, save = Wide<RULE, DK, T, false>::bytes + own;
+  constexpr size_t back = WideBack<DK, RULE>::bytes + own;
+  static_assert(read <= 160 * 1024 && save <= 160 * 1024 && back <= 160 * 1024, "LDS of a CU");
   switch (what) {
     case 0: return launch(wide_forward_kernel<RULE, DK, NW, T, kRead>, a, a.d_v, NW, read, stream);
     case 1: return launch(wide_forward_kernel<RULE, DK, NW, T, kSave>, a, a.d_v, NW, save, stream);
