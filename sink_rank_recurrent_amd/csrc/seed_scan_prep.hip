@@ -234,7 +234,10 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
 // Gates per key channel.  With P the decay from the chunk's start,
 // G_ts = P_t / P_s channel by channel, so L and M are products of K P, Q P and
 // K / P.  That is taken where every P of the chunk lies in 2^-60 .. 2^60 (the
-// quotient then costs one rounding; a masked pair stays finite).  Chunks with
+// hardware reciprocal is good to a unit in the last place, 2^-23, and a masked
+// pair stays finite).  bf16 rows of K and Q come whole through LDS (172 us for
+// 24 ragged sequences of 7919 tokens in all, 32 heads of 128 x 128; loads of
+// the lanes' own 64-byte pieces and an IEEE division: 202).  Chunks with
 // smaller decays, zeros among them, are summed pair by pair (slow_triangles).
 
 // The product over the lanes of a row of 16 up to (and with) this one.
@@ -251,13 +254,13 @@ __device__ __forceinline__ float row_prefix(float x) {
 }
 
 // L and M [64][kRow] (M only for s <= t) and P, F of a chunk, any gates: lane
-// s runs down column s, a wave has 16 rows; 32 channels at a time through
-// `buf` (3 * 64 * 33 floats).
+// s runs down column s, a wave has 16 rows; 16 channels at a time through
+// `buf` (3 * 64 * 17 floats).
 template <int DK, typename T>
 __device__ void slow_triangles(const T* __restrict__ K, const T* __restrict__ Q, size_t ld,
                                const float* __restrict__ gates, size_t gld, int n, float* buf,
                                float* L, float* M, float* __restrict__ P, float* __restrict__ F) {
-  constexpr int LR = 33;
+  constexpr int LR = 17;
   float* gs = buf;
   float* kk = gs + kC * LR;
   float* qq = kk + kC * LR;
@@ -265,17 +268,17 @@ __device__ void slow_triangles(const T* __restrict__ K, const T* __restrict__ Q,
   float accL[16], accM[16];
 #pragma unroll
   for (int t = 0; t < 16; ++t) accL[t] = accM[t] = 0.f;
-  for (int c0 = 0; c0 < DK; c0 += 32) {
+  for (int c0 = 0; c0 < DK; c0 += 16) {
     __syncthreads();
-    for (int e = tid; e < kC * 32; e += 256) {
-      const int t = e >> 5, i = e & 31;
+    for (int e = tid; e < kC * 16; e += 256) {
+      const int t = e >> 4, i = e & 15;
       const bool live = t < n;
       gs[t * LR + i] = live ? gates[(size_t)t * gld + c0 + i] : 1.f;
       kk[t * LR + i] = live ? load_scalar(K + (size_t)t * ld + c0 + i) : 0.f;
       qq[t * LR + i] = live ? load_scalar(Q + (size_t)t * ld + c0 + i) : 0.f;
     }
     __syncthreads();
-    if (tid < 32) {
+    if (tid < 16) {
       float x = 1.f;
 #pragma unroll 1
       for (int t = 0; t < kC; ++t) {
@@ -290,7 +293,7 @@ __device__ void slow_triangles(const T* __restrict__ K, const T* __restrict__ Q,
       }
     }
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float ks = kk[l * LR + i];
       float cur = 0.f;
 #pragma unroll 1
@@ -317,17 +320,21 @@ __device__ void slow_triangles(const T* __restrict__ K, const T* __restrict__ Q,
 template <int DK, typename T, bool BWD>
 __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   constexpr int KS = DK / 32;
-  constexpr int KBAR = 4 * KS * 3 * kFrag * 2, SLOW = (kC * kRow + 3 * kC * 33) * 4;   // bytes
-  __shared__ __attribute__((aligned(16))) char buf[KBAR > SLOW ? KBAR : SLOW];
-  __shared__ __attribute__((aligned(16))) float L[kC * kRow];
-  __shared__ __attribute__((aligned(16))) float X[64 * 20];
+  // K and Q as they come (bf16), then K / P in fragments, then L and the
+  // inverses (or, pair by pair, L, M and 16 channels)
+  constexpr int KBAR = 4 * KS * 3 * kFrag * 2, MAT = kC * kRow * 4, SLOW = 2 * MAT + 3 * kC * 17 * 4;
+  __shared__ __attribute__((aligned(1024))) char buf[KBAR > SLOW ? KBAR : SLOW];
   __shared__ __attribute__((aligned(16))) float tot[4][DK];
   __shared__ __attribute__((aligned(16))) float bt[kC];
   __shared__ int unsafe;
-  uint16_t* kl = reinterpret_cast<uint16_t*>(buf);   // K / P in fragments
+  uint16_t* kl = reinterpret_cast<uint16_t*>(buf);
+  float* L = reinterpret_cast<float*>(buf);
+  float* M = L + kC * kRow;
+  float* X = M + kC * kRow;
   const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
-  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, w = tid >> 6, l = lane_id(), g16 = l >> 4, l16 = l & 15;
+  const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, w = wave_id(), l = lane_id();
+  const int g16 = l >> 4, l16 = l & 15;
   const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t ld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
@@ -341,20 +348,24 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   // three of N
   const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
-  if (tid < kC) {
-    bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
-    reinterpret_cast<float*>(a.ws + a.at.vec)[unit * 256 + 128 + tid] = bt[tid];
-  }
-  if (tid == 0) unsafe = 0;
+  if constexpr (sizeof(T) == 2)
+    async_rows<DK, 4>(K, Q, ld, ch.n, lds_offset(buf), lds_offset(buf + kPlane<DK>), true, w);
   const int t0 = 16 * w + l16;
   const bool live = t0 < ch.n;
   float p[KS][8], k[KS][8], q[KS][8];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
     load_piece(gates + (size_t)t0 * gld, 32 * ks, live, p[ks]);
-    load_piece(K + (size_t)t0 * ld, 32 * ks, live, k[ks]);
-    load_piece(Q + (size_t)t0 * ld, 32 * ks, live, q[ks]);
+    if constexpr (sizeof(T) == 4) {
+      load_piece(K + (size_t)t0 * ld, 32 * ks, live, k[ks]);
+      load_piece(Q + (size_t)t0 * ld, 32 * ks, live, q[ks]);
+    }
   }
+  if (tid < kC) {
+    bt[tid] = tid < ch.n ? a.beta[((size_t)ch.tok + tid) * a.heads + head] : 0.f;
+    reinterpret_cast<float*>(a.ws + a.at.vec)[unit * 256 + 128 + tid] = bt[tid];
+  }
+  if (tid == 0) unsafe = 0;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
@@ -365,25 +376,43 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
       *reinterpret_cast<f32x4*>(to + 4) = f32x4{p[ks][4], p[ks][5], p[ks][6], p[ks][7]};
     }
   }
+  async_wait();
   __syncthreads();
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<1> x = lds_rows<DK, 1>(buf, w, ks), y = lds_rows<DK, 1>(buf + kPlane<DK>, w, ks);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        k[ks][2 * j] = live ? __uint_as_float(x.t[0][j] << 16) : 0.f;
+        k[ks][2 * j + 1] = live ? __uint_as_float(x.t[0][j] & 0xffff0000u) : 0.f;
+        q[ks][2 * j] = live ? __uint_as_float(y.t[0][j] << 16) : 0.f;
+        q[ks][2 * j + 1] = live ? __uint_as_float(y.t[0][j] & 0xffff0000u) : 0.f;
+      }
+    }
+    __syncthreads();   // K / P takes their place
+  }
   bool fine = true;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
+    f32x4 before[2], all[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      before[h] = all[h] = f32x4{1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&tot[b][32 * ks + 8 * g16 + 4 * h]);
+        if (b < w) before[h] *= x;
+        all[h] *= x;
+      }
+    }
     float end[8], kb[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = 32 * ks + 8 * g16 + j;
-      float before = 1.f, all = 1.f;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float x = tot[b][c];
-        before *= b < w ? x : 1.f;
-        all *= x;
-      }
-      const float x = p[ks][j] * before, inv = 1.f / x;
+      const float x = p[ks][j] * before[j >> 2][j & 3], inv = __builtin_amdgcn_rcpf(x);
       fine &= x >= kSafe && inv >= kSafe;
       p[ks][j] = x;
-      end[j] = all * inv;
+      end[j] = all[j >> 2][j & 3] * inv;
       kb[j] = k[ks][j] * inv;
       fine &= fabsf(kb[j]) <= 0x1p100f;   // no overflow in a masked pair
       k[ks][j] *= x;
@@ -404,8 +433,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   __syncthreads();
 
   if (unsafe) {
-    float* M = reinterpret_cast<float*>(buf);
-    slow_triangles<DK>(K, Q, ld, gates, gld, ch.n, M + kC * kRow, L, M, P, F);
+    slow_triangles<DK>(K, Q, ld, gates, gld, ch.n, X, L, M, P, F);
     for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1, m_third);
   } else {
     f32x4 lt[4], mt[4];
@@ -426,6 +454,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
         else mma(mt[b], kb, qt);
       }
     }
+    __syncthreads();   // L takes the place of K / P
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       f32x4 ll = lt[b], mm = mt[b];
