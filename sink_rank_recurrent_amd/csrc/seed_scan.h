@@ -127,19 +127,6 @@ __device__ __forceinline__ void load_row8(const T* __restrict__ row, int col0, b
   }
 }
 
-// A column of a row-major array as a fragment: the contracted index runs
-// over rows row0 .. row0 + 31, of which `rows` are live.
-template <typename T>
-__device__ __forceinline__ void load_col8(const T* __restrict__ base, size_t ld, int row0,
-                                          int rows, float (&x)[8]) {
-  const int g = lane_id() >> 4;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int t = row0 + 16 * (j >> 2) + 4 * g + (j & 3);
-    x[j] = t < rows ? load_scalar(base + (size_t)t * ld) : 0.f;
-  }
-}
-
 __device__ __forceinline__ void store_scalar(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_scalar(bf16_t* p, float x) {
   *p = (bf16_t)round_pair(x, 0.f);
@@ -154,15 +141,8 @@ __host__ __device__ constexpr int upper_frag(int mt, int ks) {
   return mt < 2 ? 2 * mt + ks : (ks == 1 ? 2 + mt : -1);
 }
 
-// A packed fragment of three terms: [frag][term][lane][8].
-__device__ __forceinline__ Frag<3> load_pack(const uint16_t* __restrict__ pack, int frag) {
-  Frag<3> f;
-#pragma unroll
-  for (int n = 0; n < 3; ++n)
-    f.t[n] = *reinterpret_cast<const u32x4*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8);
-  return f;
-}
-// (third: the third term is read by somebody)
+// A packed fragment of three terms, [frag][term][lane][8]; the third only where
+// it is read by somebody.
 __device__ __forceinline__ void store_pack(uint16_t* __restrict__ pack, int frag,
                                            const Frag<3>& f, bool third = true) {
 #pragma unroll
