@@ -466,6 +466,20 @@ def _first_window(W: int, first_window) -> int:
     return fw
 
 
+def _prefill(state, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream) -> torch.Tensor:
+    """The dense states behind the prompts of a batch (sequence.seed_scan),
+    converted into `state`; returns the dense states."""
+    from . import sequence   # it imports this module
+
+    with torch.cuda.device(state.a.device), torch.cuda.stream(stream):
+        S = torch.empty(state.batch, state.heads, state.d_k, state.d_v, device=state.a.device,
+                        dtype=torch.float32)
+        sequence.seed_scan(state.rule, q, k, v, g, beta, o, S, S0=S0, cu_seqlens=cu_seqlens,
+                           workspace=workspace, stream=stream)
+        state.from_dense(S, stream)
+    return S
+
+
 class ShallowState:
     """Device tensors of one layer's shallow states plus the column count r.
 
@@ -504,6 +518,15 @@ class ShallowState:
             self.gam.fill_(1.0)
         self.r = self.R
         self.limit = self.R + self.first_window
+
+    def prefill(self, q, k, v, g, beta, o, S0=None, cu_seqlens=None, workspace=None,
+                stream=None) -> torch.Tensor:
+        """Run the prompts of all requests (sequence.seed_scan: their read-outs
+        to `o`) and convert the states behind them (from_dense).  The arrays
+        are [batch, length, heads, d], or packed [tokens, heads, d] with
+        cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
+        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def step(self, q, k, v, g, beta, o, stream=None) -> None:
         if self.lazy:
@@ -626,6 +649,15 @@ class ShallowState16:
         self.gam.fill_(1.0)
         self.r = R
         self.limit = R + self.first_window
+
+    def prefill(self, q, k, v, g, beta, o, S0=None, cu_seqlens=None, workspace=None,
+                stream=None) -> torch.Tensor:
+        """Run the prompts of all requests (sequence.seed_scan: their read-outs
+        to `o`) and convert the states behind them (from_dense).  The arrays
+        are [batch, length, heads, d], or packed [tokens, heads, d] with
+        cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
+        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def step(self, q, k, v, g, beta, o, stream=None) -> None:
         seed_decode_step_h16(self.rule, self.a, self.Uk, self.Vk, self.Uw, self.Vw, self.gam,
@@ -755,6 +787,15 @@ class ScheduledState:
         self.KV[0].copy_(V)
         self.gam.fill_(1.0)
         self.gam_snap.fill_(1.0)
+
+    def prefill(self, q, k, v, g, beta, o, S0=None, cu_seqlens=None, workspace=None,
+                stream=None) -> torch.Tensor:
+        """Run the prompts of all requests (sequence.seed_scan: their read-outs
+        to `o`) and convert the states behind them (from_dense).  The arrays
+        are [batch, length, heads, d], or packed [tokens, heads, d] with
+        cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
+        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def held_columns(self, b: int, t=None) -> int:
         """Columns request b holds before step t (default: the next step)."""

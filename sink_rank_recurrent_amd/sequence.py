@@ -131,9 +131,12 @@ def _workspace_bytes(rule, n_seq, H, HK, d_k, d_v, tokens, backward: bool) -> in
     return n
 
 
-def _workspace(workspace, nbytes: int, device) -> torch.Tensor:
+def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        # from the pool of the stream that uses it: that of torch's current
+        # stream may hand out memory which that stream is still using
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 vector")
     return workspace
@@ -161,20 +164,12 @@ def seed_scan(rule: str, q, k, v, g, beta, o, S, S0=None, cu_seqlens=None, works
     _need(S, "S", (n_seq, H, d_k, d_v), _F32)
     with _On(device):
         ws = _workspace(workspace, _workspace_bytes(rule, n_seq, H, HK, d_k, d_v, tokens, False),
-                        device)
+                        device, stream)
         st = lib().seed_scan(RULES[rule], n_seq, H, HK, d_k, d_v, tokens, _ptr(cu_seqlens),
                              _ptr(q), _ptr(k), _ptr(v), 1 if q.dtype == torch.bfloat16 else 0,
                              _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S), _ptr(ws),
                              ws.numel(), _stream(stream, device.index))
-        _release(ws, workspace, stream)
     _check("seed_scan", st)
-
-
-def _release(ws, given, stream) -> None:
-    """A workspace made for a call on a stream that is not torch's current
-    one must not be handed out again before that stream has passed it."""
-    if given is None and stream is not None:
-        ws.record_stream(stream)
 
 
 def seed_scan_backward(rule: str, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, S0=None, dS=None,
@@ -198,13 +193,12 @@ def seed_scan_backward(rule: str, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, S
             _need(t, name, (n_seq, H, d_k, d_v), _F32)
     with _On(device):
         ws = _workspace(workspace, _workspace_bytes(rule, n_seq, H, HK, d_k, d_v, tokens, True),
-                        device)
+                        device, stream)
         st = lib().seed_scan_backward(
             RULES[rule], n_seq, H, HK, d_k, d_v, tokens, _ptr(cu_seqlens), _ptr(q), _ptr(k),
             _ptr(v), 1 if q.dtype == torch.bfloat16 else 0, _ptr(g), _ptr(beta), _ptr(S0),
             _ptr(do), _ptr(dS), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dS0),
             _ptr(ws), ws.numel(), _stream(stream, device.index))
-        _release(ws, workspace, stream)
     _check("seed_scan_backward", st)
 
 
@@ -291,15 +285,14 @@ def seed_group_norm_backward(dy, x, dx, dgate=None, dweight=None, dbias=None, we
     with _On(device):
         ws = None
         if dweight is not None or dbias is not None:
-            ws = workspace
-            if ws is None:
-                ws = group_norm_workspace(x, like)
-            _workspace(ws, 0, device)
+            if workspace is None:
+                with torch.cuda.stream(stream):
+                    ws = group_norm_workspace(x, like)
+            else:
+                ws = _workspace(workspace, 0, device, stream)
         st = lib().seed_group_norm_backward(
             rows, G, d, _ptr(dy), _ptr(x), _code(x.dtype), _ptr(gate), _code(dy.dtype),
             _ptr(weight), _ptr(bias), wg, eps, int(centered), ACTIVATIONS[activation],
             int(gate_first), _ptr(dx), _ptr(dgate), _ptr(dweight), _ptr(dbias), _ptr(ws),
             0 if ws is None else ws.numel(), _stream(stream, device.index))
-        if ws is not None:
-            _release(ws, workspace, stream)
     _check("seed_group_norm_backward", st)

@@ -198,6 +198,11 @@ def test_binding_refuses():
         sequence.seed_group_norm(q, q)
     with pytest.raises(TypeError):
         sequence.seed_group_norm(q.numpy(), q)
+    st = binding.ShallowState("gdn", 5, 2, 128, 128, 16, 16, torch.ones(2, 128), device="cpu")
+    x = q.view(5, 2, 2, 128)
+    with pytest.raises(ValueError):
+        st.prefill(x, x, x, x[..., 0], x[..., 0], x)
+    assert st.r == 0
 
 
 @pytest.mark.skipif(HOST_ONLY or shutil.which("g++") is None or _gcc_lib("libasan.so") is None
