@@ -643,13 +643,14 @@ struct KdaLds {
   static constexpr int s = u > mats ? u : mats;
   static constexpr int k = s + 6 * plane;
   static constexpr int small = k + 9 * kplane;
-  static constexpr int bytes = small + (4 * 2 * 32 + 8 * 32 + 8) * 4;
+  static constexpr int bytes = small + (4 * 2 * 32 + 4 * 32 + 8) * 4;
 };
 
 template <int DK, int DV, typename T>
-__global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
+__global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
   using Lds = KdaLds<DK, DV, T>;
   constexpr int NT = Lds::NT, KS = DV / 32, MT = DK / 32;
+  constexpr int NS = DV / 64;                   // columns of a state a thread brings
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   float* m0 = reinterpret_cast<float*>(smem);   // u of the waves, then dL and dM
   float* m1 = m0 + kC * kRow;
@@ -657,11 +658,11 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   char* Kp = smem + Lds::k;                     // K', K~, Q~: three planes each
   float* tot = reinterpret_cast<float*>(smem + Lds::small);   // [x, z][4][32]
   float* hs = tot + 4 * 2 * 32;                 // [wave][32]
-  int* bad = reinterpret_cast<int*>(hs + 8 * 32);
+  int* bad = reinterpret_cast<int*>(hs + 4 * 32);
   const Chunk ch = chunk_of_slot(a, blockIdx.x / a.heads);
   if (ch.n == 0) return;
   const int head = head_of(a, blockIdx.x % a.heads), tid = threadIdx.x, l = lane_id(), l16 = l & 15, g = l >> 4;
-  const int w4 = (tid >> 6) & 3, half = tid >> 8, n = ch.n;
+  const int w = wave_id(), n = ch.n;
   const size_t unit = (size_t)(blockIdx.x / a.heads) * a.heads + head;
   const int hk = head / (a.heads / a.key_heads);
   const size_t kld = (size_t)a.key_heads * DK, gld = (size_t)a.heads * DK;
@@ -677,7 +678,7 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   __syncthreads();
   {
     bool fine = true;
-    for (int e = tid; e < kC * DK / 4; e += 512) {
+    for (int e = tid; e < kC * DK / 4; e += 256) {
       const int t = e / (DK / 4), i = 4 * (e % (DK / 4));
       const f32x4 p = *reinterpret_cast<const f32x4*>(P + t * DK + i);
       f32x4 q = {1.f, 1.f, 1.f, 1.f};
@@ -693,7 +694,7 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
     if (!fine) *bad = 1;
   }
   // the wave's rows of dO, dR and u
-  const int row = 16 * w4 + l16;
+  const int row = 16 * w + l16;
   Frag<NT> ado[KS];
   Frag<3> adr[KS], au[KS];
   float db = 0.f;
@@ -718,10 +719,10 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
       }
       adr[ks] = split<3>(y);
       au[ks] = split<3>(x);
-      if (w4 < 3 && half == 0) {
+      if (w < 3) {
 #pragma unroll
         for (int m = 0; m < 3; ++m)
-          *reinterpret_cast<u32x4*>(smem + (((w4 * KS + ks) * 3 + m) * 64 + l) * 16) = au[ks].t[m];
+          *reinterpret_cast<u32x4*>(smem + (((w * KS + ks) * 3 + m) * 64 + l) * 16) = au[ks].t[m];
       }
     }
     db += __shfl_xor(db, 16);
@@ -730,106 +731,120 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
   __syncthreads();
   if (tid == 0) reinterpret_cast<int*>(a.ws + a.at.slow)[unit] = *bad;
   if (*bad) return;
-  if (half == 0 && g == 0 && row < n) a.dbeta[((size_t)ch.tok + row) * a.heads + head] = db;
+  if (g == 0 && row < n) a.dbeta[((size_t)ch.tok + row) * a.heads + head] = db;
 
-  // the pairs: row tile w4, column tiles half, half + 2
-  f32x4 pl[2], pm[2];
+  // the pairs: row tile w
+  f32x4 pl[4], pm[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int b = 2 * i + half;
-    pl[i] = pm[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (b > w4) continue;
+  for (int b = 0; b < 4; ++b) {
+    pl[b] = pm[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b > w) continue;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       Frag<3> u = au[ks];
-      if (b < w4) {
+      if (b < w) {
 #pragma unroll
         for (int m = 0; m < 3; ++m)
           u.t[m] = *reinterpret_cast<const u32x4*>(smem + (((b * KS + ks) * 3 + m) * 64 + l) * 16);
       }
-      mma(pm[i], ado[ks], u);
-      mma(pl[i], adr[ks], u);
+      mma(pm[b], ado[ks], u);
+      mma(pl[b], adr[ks], u);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 4 * g + r;
-      if (b == w4 && l16 > t) pm[i][r] = 0.f;
-      pl[i][r] = b == w4 && l16 >= t ? 0.f : -pl[i][r];
+      if (b == w && l16 > t) pm[b][r] = 0.f;
+      pl[b][r] = b == w && l16 >= t ? 0.f : -pl[b][r];
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int b = 2 * i + half;
+  for (int b = 0; b < 4; ++b)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      m0[(16 * w4 + 4 * g + r) * kRow + 16 * b + l16] = pl[i][r];
-      m1[(16 * w4 + 4 * g + r) * kRow + 16 * b + l16] = pm[i][r];
+      m0[(16 * w + 4 * g + r) * kRow + 16 * b + l16] = pl[b][r];
+      m1[(16 * w + 4 * g + r) * kRow + 16 * b + l16] = pm[b][r];
+    }
+  __syncthreads();
+  // their rows and columns w as fragments
+  Frag<3> rl[2], rm[2], cl[2], cm[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    float x[8];
+    if (ks <= (w >> 1)) {
+      mat_rows(m0, row, ks, x);
+      rl[ks] = split<3>(x);
+      mat_rows(m1, row, ks, x);
+      rm[ks] = split<3>(x);
+    }
+    if (ks >= (w >> 1)) {
+      mat_cols(m0, row, ks, x);
+      cl[ks] = split<3>(x);
+      mat_cols(m1, row, ks, x);
+      cm[ks] = split<3>(x);
     }
   }
 
-  const bool stager = tid < 4 * DV;
-  float sv[8], hv[8], pv[8];
+  float sv[NS][8], hv[NS][8], pv[8];
   Piece<T> kv, qv;
   auto fetch = [&](int part) {
-    if (stager) {
-      float y[4];
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int at = chunk_state_at<DK>(2 * part + h, tid & 3, tid >> 2);
+        const int at = chunk_state_at<DK>(2 * part + h, tid & 3, 64 * i + (tid >> 2));
         load_vec<4>(Sc + at, y);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sv[4 * h + r] = y[r];
+        for (int r = 0; r < 4; ++r) sv[i][4 * h + r] = y[r];
         load_vec<4>(Hc + at, y);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) hv[4 * h + r] = y[r];
+        for (int r = 0; r < 4; ++r) hv[i][4 * h + r] = y[r];
       }
+    const int t = tid >> 2, c = 32 * part + 8 * (tid & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load_vec<4>(P + t * DK + c + 4 * h, y);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) pv[4 * h + r] = y[r];
     }
-    if (tid < 256) {
-      const int t = tid >> 2, c = 32 * part + 8 * (tid & 3);
-      float y[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load_vec<4>(P + t * DK + c + 4 * h, y);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) pv[4 * h + r] = y[r];
-      }
-      kv.clear();
-      qv.clear();
-      if (t < n) {
-        kv.load(K + (size_t)t * kld + c);
-        qv.load(Q + (size_t)t * kld + c);
-      }
+    kv.clear();
+    qv.clear();
+    if (t < n) {
+      kv.load(K + (size_t)t * kld + c);
+      qv.load(Q + (size_t)t * kld + c);
     }
   };
   const bool shared = a.key_heads != a.heads;
   fetch(0);
   for (int part = 0; part < MT; ++part) {
     __syncthreads();
-    if (stager) {
-      const int at = part_at(tid >> 2, tid & 3);
-      const Frag<3> s = split<3>(sv), h = split<3>(hv);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int at = part_at(64 * i + (tid >> 2), tid & 3);
+      const Frag<3> s = split<3>(sv[i]), h = split<3>(hv[i]);
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         *reinterpret_cast<u32x4*>(Sp + m * Lds::plane + at) = s.t[m];
         *reinterpret_cast<u32x4*>(Sp + (3 + m) * Lds::plane + at) = h.t[m];
       }
-      // <H, S> by channel: a wave's 16 rows
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float x = sv[j] * hv[j];
-#pragma unroll
-        for (int o = 4; o < 64; o *= 2) x += __shfl_xor(x, o);
-        if (l < 4) hs[(tid >> 6) * 32 + 8 * l + j] = x;
-      }
     }
-    if (tid < 256) {
+    // <H, S> by channel: a wave's 16 NS columns
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x = sv[0][j] * hv[0][j];
+      if (NS == 2) x += sv[NS - 1][j] * hv[NS - 1][j];
+#pragma unroll
+      for (int o = 4; o < 64; o *= 2) x += __shfl_xor(x, o);
+      if (l < 4) hs[w * 32 + 8 * l + j] = x;
+    }
+    {
       float x[8], y[8], z[8];
       kv.get(y);
       qv.get(z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = y[j] / pv[j];
+        x[j] = y[j] * __builtin_amdgcn_rcpf(pv[j]);
         y[j] *= pv[j];
         z[j] *= pv[j];
       }
@@ -844,101 +859,116 @@ __global__ __launch_bounds__(512) void grads_kda_kernel(ScanArgs a) {
     }
     __syncthreads();
     if (part + 1 < MT) fetch(part + 1);
-    f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1, a1 = x1, a2 = x1, a3 = x1;
+    const int t0 = 16 * w + 4 * g;
+    float q[2][4], k[2][4], pt[2][4], ft[2][4], gt[2][4], end[2];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const Frag<3> s = part_cols<Lds::plane>(Sp, half, ks);
-      const Frag<3> h = part_cols<Lds::plane>(Sp + 3 * Lds::plane, half, ks);
-      mma(x1, ado[ks], s);
-      mma(x2, adr[ks], s);
-      mma(x3, au[ks], h);
-    }
-    const int i = 32 * part + 16 * half + l16, t0 = 16 * w4 + 4 * g;
-    float q[4], k[4], pt[4], ft[4], gt[4];
+    for (int half = 0; half < 2; ++half) {
+      const int i = 32 * part + 16 * half + l16;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = t0 + r;
-      pt[r] = P[t * DK + i];
-      ft[r] = F[t * DK + i];
-      q[r] = t < n ? load_scalar(Q + (size_t)t * kld + i) : 0.f;
-      k[r] = t < n ? load_scalar(K + (size_t)t * kld + i) : 0.f;
-      gt[r] = t < n ? gates[(size_t)t * gld + i] : 1.f;
-    }
-    float end = 0.f;
-#pragma unroll
-    for (int o = 0; o < DV / 16; ++o) end += hs[o * 32 + 16 * half + l16];
-    end *= P[(kC - 1) * DK + i];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      float x[8];
-      if (ks <= (w4 >> 1)) {
-        const Frag<3> f = part_cols<Lds::kplane>(Kp, half, ks);
-        mat_rows(m1, row, ks, x);
-        mma(a1, split<3>(x), f);
-        mat_rows(m0, row, ks, x);
-        mma(a2, split<3>(x), f);
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + r;
+        pt[half][r] = P[t * DK + i];
+        ft[half][r] = F[t * DK + i];
+        q[half][r] = t < n ? load_scalar(Q + (size_t)t * kld + i) : 0.f;
+        k[half][r] = t < n ? load_scalar(K + (size_t)t * kld + i) : 0.f;
+        gt[half][r] = t < n ? gates[(size_t)t * gld + i] : 1.f;
       }
-      if (ks >= (w4 >> 1)) {
-        mat_cols(m0, row, ks, x);
-        mma(a3, split<3>(x), part_cols<Lds::kplane>(Kp + 3 * Lds::kplane, half, ks));
-        mat_cols(m1, row, ks, x);
-        mma(a3, split<3>(x), part_cols<Lds::kplane>(Kp + 6 * Lds::kplane, half, ks));
-      }
+      end[half] = P[(kC - 1) * DK + i];
     }
-    float xs[4], zs[4];
+    f32x4 x1[2], x2[2], x3[2], a1[2], a2[2], a3[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = t0 + r;
-      const float dq = pt[r] * (x1[r] + a1[r]), rk = pt[r] * (a2[r] - x2[r]);
-      const float ck = a3[r] / pt[r], fk = ft[r] * x3[r];
-      xs[r] = q[r] * dq + k[r] * (rk - ck);
-      zs[r] = k[r] * fk;
-      if (t >= n) continue;
-      if (shared) {
-        const size_t at = ((size_t)(ch.tok + t) * a.heads + head) * DK + i;
-        reinterpret_cast<float*>(a.ws + a.at.dq)[at] = dq;
-        reinterpret_cast<float*>(a.ws + a.at.dk)[at] = rk + ck + fk;
-      } else {
-        const size_t at = ((size_t)(ch.tok + t) * a.key_heads + hk) * DK + i;
-        store_scalar(static_cast<T*>(a.dq) + at, dq);
-        store_scalar(static_cast<T*>(a.dk) + at, rk + ck + fk);
-      }
-    }
-    // sums of x over t and behind, of z before t: rows, lanes, waves
-    const float sx = (xs[0] + xs[1]) + (xs[2] + xs[3]), sz = (zs[0] + zs[1]) + (zs[2] + zs[3]);
-    float bx = 0.f, bz = 0.f, allx = sx, allz = sz;
+    for (int half = 0; half < 2; ++half)
+      x1[half] = x2[half] = x3[half] = a1[half] = a2[half] = a3[half] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int o = 1; o < 4; ++o) {
-      const float x = __shfl(sx, (l16 + 16 * (g + o)) & 63), z = __shfl(sz, (l16 + 16 * (g - o)) & 63);
-      bx += g + o < 4 ? x : 0.f;
-      bz += g - o >= 0 ? z : 0.f;
-    }
-    allx += __shfl_xor(allx, 16);
-    allx += __shfl_xor(allx, 32);
-    allz += __shfl_xor(allz, 16);
-    allz += __shfl_xor(allz, 32);
-    if (g == 0) {
-      tot[w4 * 32 + 16 * half + l16] = allx;
-      tot[128 + w4 * 32 + 16 * half + l16] = allz;
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const Frag<3> s = part_cols<Lds::plane>(Sp, half, ks);
+        const Frag<3> h = part_cols<Lds::plane>(Sp + 3 * Lds::plane, half, ks);
+        mma(x1[half], ado[ks], s);
+        mma(x2[half], adr[ks], s);
+        mma(x3[half], au[ks], h);
+      }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (ks <= (w >> 1)) {
+          const Frag<3> f = part_cols<Lds::kplane>(Kp, half, ks);
+          mma(a1[half], rm[ks], f);
+          mma(a2[half], rl[ks], f);
+        }
+        if (ks >= (w >> 1)) {
+          mma(a3[half], cl[ks], part_cols<Lds::kplane>(Kp + 3 * Lds::kplane, half, ks));
+          mma(a3[half], cm[ks], part_cols<Lds::kplane>(Kp + 6 * Lds::kplane, half, ks));
+        }
+      }
+    float xs[2][4], zs[2][4], bx[2], bz[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int i = 32 * part + 16 * half + l16;
+      end[half] *= (hs[16 * half + l16] + hs[32 + 16 * half + l16]) +
+                   (hs[64 + 16 * half + l16] + hs[96 + 16 * half + l16]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + r;
+        const float p = pt[half][r], dq = p * (x1[half][r] + a1[half][r]), rk = p * (a2[half][r] - x2[half][r]);
+        const float ck = a3[half][r] * __builtin_amdgcn_rcpf(p), fk = ft[half][r] * x3[half][r];
+        xs[half][r] = q[half][r] * dq + k[half][r] * (rk - ck);
+        zs[half][r] = k[half][r] * fk;
+        if (t >= n) continue;
+        if (shared) {
+          const size_t at = ((size_t)(ch.tok + t) * a.heads + head) * DK + i;
+          reinterpret_cast<float*>(a.ws + a.at.dq)[at] = dq;
+          reinterpret_cast<float*>(a.ws + a.at.dk)[at] = rk + ck + fk;
+        } else {
+          const size_t at = ((size_t)(ch.tok + t) * a.key_heads + hk) * DK + i;
+          store_scalar(static_cast<T*>(a.dq) + at, dq);
+          store_scalar(static_cast<T*>(a.dk) + at, rk + ck + fk);
+        }
+      }
+      // sums of x over t and behind, of z before t: rows, lanes, waves
+      const float sx = (xs[half][0] + xs[half][1]) + (xs[half][2] + xs[half][3]);
+      const float sz = (zs[half][0] + zs[half][1]) + (zs[half][2] + zs[half][3]);
+      float allx = sx, allz = sz;
+      bx[half] = bz[half] = 0.f;
+#pragma unroll
+      for (int o = 1; o < 4; ++o) {
+        const float x = __shfl(sx, (l16 + 16 * (g + o)) & 63), z = __shfl(sz, (l16 + 16 * (g - o)) & 63);
+        bx[half] += g + o < 4 ? x : 0.f;
+        bz[half] += g - o >= 0 ? z : 0.f;
+      }
+      allx += __shfl_xor(allx, 16);
+      allx += __shfl_xor(allx, 32);
+      allz += __shfl_xor(allz, 16);
+      allz += __shfl_xor(allz, 32);
+      if (g == 0) {
+        tot[w * 32 + 16 * half + l16] = allx;
+        tot[128 + w * 32 + 16 * half + l16] = allz;
+      }
     }
     __syncthreads();
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      bx += o > w4 ? tot[o * 32 + 16 * half + l16] : 0.f;
-      bz += o < w4 ? tot[128 + o * 32 + 16 * half + l16] : 0.f;
-    }
-    float ax = bx;
+    for (int half = 0; half < 2; ++half) {
+      const int i = 32 * part + 16 * half + l16;
 #pragma unroll
-    for (int r = 3; r >= 0; --r) {
-      ax += xs[r];
-      xs[r] = ax;
-    }
+      for (int o = 0; o < 4; ++o) {
+        bx[half] += o > w ? tot[o * 32 + 16 * half + l16] : 0.f;
+        bz[half] += o < w ? tot[128 + o * 32 + 16 * half + l16] : 0.f;
+      }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = t0 + r;
-      if (t < n)
-        a.dg[((size_t)(ch.tok + t) * a.heads + head) * DK + i] = (xs[r] + bz + end) / gt[r];
-      bz += zs[r];
+      for (int r = 3; r >= 0; --r) {
+        bx[half] += xs[half][r];
+        xs[half][r] = bx[half];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + r;
+        if (t < n)
+          a.dg[((size_t)(ch.tok + t) * a.heads + head) * DK + i] =
+              (xs[half][r] + bz[half] + end[half]) * __builtin_amdgcn_rcpf(gt[half][r]);
+        bz[half] += zs[half][r];
+      }
     }
   }
 }
@@ -988,7 +1018,7 @@ hipError_t grads(const ScanArgs& a, hipStream_t stream) {
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(grads_kda_slow_kernel<DK, DV, T>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)slow);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((grads_kda_kernel<DK, DV, T>), grid, dim3(512), bytes, stream, a);
+    hipLaunchKernelGGL((grads_kda_kernel<DK, DV, T>), grid, dim3(256), bytes, stream, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((grads_kda_slow_kernel<DK, DV, T>), grid, dim3(256), slow, stream, a);
