@@ -3,8 +3,8 @@
 //
 // For one sequence and head, with S the state before the chunk, P_t the
 // decay from the chunk's start through token t, F_t the decay after t to the
-// chunk's end and G_ts the decay after s through t (products of the gates,
-// never quotients, so gates of 0 are exact):
+// chunk's end and G_ts the decay after s through t (products of the gates, so
+// gates of 0 are exact; per key channel G_ts = P_t / P_s where that is safe):
 //   L_ts = G_ts k_t.k_s (s < t),  M_ts = G_ts q_t.k_s (s <= t)
 //   R = V - P (K S),   E = R - N (beta R),  N = (I + L beta)^-1 L,
 //   u = beta E  (Mamba-2: u = E = V),

@@ -37,7 +37,8 @@ ScanLayout scan_layout(int rule, int n_seq, int heads, int key_heads, int d_k, i
   // start that a first pass over the others' carries gives.  The first pass
   // and the second each cost what the whole would, so segments pay where
   // whole sequences fill at most a quarter of the CUs (a workgroup has 64
-  // columns): 16 heads of 64 x 64 over 256 chunks took 1655 us whole.
+  // columns): 16 heads of 64 x 64 over 256 chunks took 1655 us whole and take
+  // 240 in segments; 128 workgroups of 32 chunks were slower in segments.
   const long long groups = (long long)n_seq * heads * (d_v / 64);
   const int chunks = tokens / kScanChunk / (n_seq > 0 ? n_seq : 1);
   if (groups <= 64 && chunks >= 8) {

@@ -6,6 +6,12 @@
 // M) are the same for all waves: they come through LDS, the next chunk's by
 // asynchronous loads while this one is computed.
 //
+// Bound by instruction issue where the chip is full: 64 sequences x 512 tokens
+// x 16 heads of 128 x 128 forward in 210 us, the matrix cores busy 38 % and
+// the VALU 41 % of the time, 500 MB at 2.4 TB/s.  With fewer than 256
+// workgroups (4 sequences x 2048 tokens: 128) by the chain itself, 4 us a
+// chunk forward and 6.5 backward (128 and 208 us for 32 chunks).
+//
 // Terms: what is added to the state takes all three terms of F u.  Forward,
 // K S and N (beta R) only correct u and take two (at most 2^-18 of an
 // operand's value is left out, its sign at random: the states stay within

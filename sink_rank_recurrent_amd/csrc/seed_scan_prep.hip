@@ -6,7 +6,6 @@ namespace seed {
 namespace scan {
 namespace {
 
-
 // A 16 x 16 x 16 product in fp32: a's rows from LDS, b an accumulator tile.
 __device__ __forceinline__ void mma_f32(f32x4& c, const f32x4& a, const f32x4& b) {
 #pragma unroll
@@ -110,6 +109,12 @@ __device__ __forceinline__ void split_rows(const float* rows, size_t ld, int n, 
 // memory, 64 bytes of a row at a time, took the preparation of 64 x 512
 // tokens x 16 heads 132 us), L then in their place.  (float32: only K, in
 // three terms; a wave takes its rows of Q from memory.)
+//
+// Bound by the steps' latency and the VALU, not by memory: for those 64 x 512
+// tokens x 16 heads 111 us, 360 MB moved at 3.2 TB/s, the VALU issuing half of
+// the time and the matrix cores 13 % of it; the decays are one wave's work and
+// the inverses of L's diagonal blocks 16 dependent steps.  Four workgroups a
+// CU hide part of it.
 template <int RULE, int DK, typename T, bool BWD>
 __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   constexpr int NT = sizeof(T) == 2 ? 1 : 3;
