@@ -195,6 +195,10 @@ struct Walk {
   int seq, head, hk, col0, col, c0, c1, chunks, base;   // col0: the wave's first column
   size_t segment;                                       // (segment, head), for what is kept for it
   Range rg;
+  // the sequence has several segments: all take their first states from the
+  // workspace, since S may be S0 (dS0 may be dS), written by one workgroup
+  // while another has yet to start
+  bool split;
   __device__ __forceinline__ Walk(const ScanArgs& a, int columns) {
     const int blocks = columns / (16 * NW);
     const int sh = blockIdx.x / blocks;
@@ -213,6 +217,7 @@ struct Walk {
     base = slot_base(rg, seq);
     c0 = 0;
     c1 = chunks;
+    split = a.at.seg > 0 && chunks > a.at.seg;
     if (a.at.seg) {
       const int i = first - (rg.start / (kC * a.at.seg) + seq);
       c0 = i * a.at.seg;

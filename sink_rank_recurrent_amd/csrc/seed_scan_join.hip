@@ -77,15 +77,16 @@ __global__ __launch_bounds__(256) void join_kernel(ScanArgs a) {
   };
   f32x4 S[IT];
   const size_t state = ((size_t)seq * a.heads + head) * size;
-  const float* from = BACK ? nullptr : a.S0;   // a last segment's carry already has dS
+  const float* from = BACK ? a.dS : a.S0;
   load_state(from ? from + state : nullptr, a.d_v, 8 * (lane_id() >> 4) * a.d_v + col, S);
   const int first = BACK ? segments - 1 : 0;
+  keep_chunk_state(start + unit(first) * size, col0, S);
   if (DELTA && !BACK) fetch(first);
   for (int n = 0; n + 1 < segments; ++n) {
     const int i = BACK ? segments - 1 - n : n;   // the segment passed through
     f32x4 x[IT];
     load_chunk_state(carry + unit(i) * size, col0, x);
-    if (BACK && n == 0) {
+    if (BACK && n == 0) {   // the last segment's carry already has dS
 #pragma unroll
       for (int m = 0; m < IT; ++m) S[m] = x[m];
     } else if (DELTA) {

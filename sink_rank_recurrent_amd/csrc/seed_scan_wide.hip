@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
 
   f32x4 S[IT];
   if (unit_cols) unit_state(at.col - a.d_v, S);
-  else if (!CARRY && c0 > 0)
+  else if (!CARRY && at.split)
     load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, S);
   else load_state(!CARRY && a.S0 ? a.S0 + state : nullptr, a.d_v, state_lane, S);
   float through = 1.f;
@@ -343,8 +343,8 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
   T* dV = static_cast<T*>(a.dv) + vat;
 
   f32x4 H[IT];
-  // a last segment starts from dS, in its own first pass too
-  if (c1 < at.chunks && !LOCAL)
+  // in the segments' own first pass the last one starts from dS
+  if (at.split && !LOCAL)
     load_chunk_state(reinterpret_cast<const float*>(a.ws + a.at.start) + at.segment * DK * a.d_v, at.col0, H);
   else load_state(c1 == at.chunks && a.dS ? a.dS + state : nullptr, a.d_v, state_lane, H);
 

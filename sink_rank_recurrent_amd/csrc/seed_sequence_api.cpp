@@ -79,10 +79,10 @@ seed_status check_shape(const char* fn, int rule, int n_seq, int heads, int key_
                 d_k, d_v);
   if (heads > 65535)
     return fail(SEED_E_UNSUPPORTED, "%s: %d heads exceed the grid limit of 65535", fn, heads);
-  // a workgroup for each (chunk or sequence, head, columns)
+  // at most 1024 threads for each (chunk or sequence, head), 2^32 in a grid
   const long long slots = (long long)tokens / seed::kScanChunk + n_seq;
   if ((long long)tokens + 64LL * n_seq > 0x7fffffffLL ||
-      slots > 0x7fffffffLL / ((long long)heads * ((d_k + d_v) / 16)))
+      slots > 0xffffffffLL / 1024 / heads)
     return fail(SEED_E_UNSUPPORTED, "%s: n_seq * heads or tokens * heads exceed the grid limit", fn);
   return SEED_OK;
 }

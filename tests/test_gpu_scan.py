@@ -313,6 +313,59 @@ def test_in_place_states_and_a_workspace_that_is_dirty():
     assert all(torch.equal(a[k], out[k]) for k in a)
 
 
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_in_place_states_in_segments(rule, dtype):
+    """S is S0 and dS0 is dS where a sequence goes in segments, one of which
+    writes them and another of which starts from them."""
+    offsets = [0, 1700, 1800]
+    x = inputs(rule, 1800, 2, 2, 128, 64, 2, dtype, 14)
+    o, S = run(rule, x, offsets)
+    cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    o2, S2 = torch.full_like(o, 7.0), x["S0"].clone()
+    sequence.seed_scan(rule, x["q"], x["k"], x["v"], x["g"], x["beta"], o2, S2, S0=S2, cu_seqlens=cu)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    do, dS = torch.randn(x["v"].shape, device="cuda").to(dtype), torch.randn_like(S)
+    want = run_back(rule, x, offsets, do, dS)
+    out = {k: torch.full_like(v, 7.0) for k, v in x.items() if v is not None}
+    out["S0"] = dS.clone()
+    sequence.seed_scan_backward(rule, x["q"], x["k"], x["v"], x["g"], x["beta"], do, out["q"],
+                                out["k"], out["v"], out["g"], out.get("beta"), S0=x["S0"],
+                                dS=out["S0"], dS0=out["S0"], cu_seqlens=cu)
+    assert all(torch.equal(want[k], out[k]) for k in want)
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_two_calls_at_once(rule):
+    """Calls on two streams at the same time, each with a workspace of its
+    own, given or made by the call: the bits of one call alone."""
+    offsets = [0, 300, 1000]
+    x = inputs(rule, 1000, 4, 2, 128, 128, 2, torch.bfloat16, 15)
+    cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    o, S = run(rule, x, offsets)
+    do, dS = torch.randn(x["v"].shape, device="cuda").to(torch.bfloat16), torch.randn_like(S)
+    want = run_back(rule, x, offsets, do, dS)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets = [({k: torch.full_like(v, 7.0) for k, v in x.items() if v is not None},
+             torch.full_like(o, 7.0), torch.full_like(S, 7.0)) for _ in streams]
+    given = sequence.scan_workspace(rule, x["q"], x["v"], 2, backward=True)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, stream in enumerate(streams):
+            ws = given if i else None
+            out, oi, Si = sets[i]
+            sequence.seed_scan(rule, x["q"], x["k"], x["v"], x["g"], x["beta"], oi, Si, S0=x["S0"],
+                               cu_seqlens=cu, workspace=ws, stream=stream)
+            sequence.seed_scan_backward(rule, x["q"], x["k"], x["v"], x["g"], x["beta"], do,
+                                        out["q"], out["k"], out["v"], out["g"], out.get("beta"),
+                                        S0=x["S0"], dS=dS, dS0=out["S0"], cu_seqlens=cu,
+                                        workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for out, oi, Si in sets:
+        assert torch.equal(o, oi) and torch.equal(S, Si)
+        assert all(torch.equal(want[k], out[k]) for k in want)
+
+
 @pytest.mark.parametrize("backward", [False, True])
 def test_no_tokens(backward):
     x = inputs("gdn", 0, 2, 2, 64, 64, 2, torch.float32, 9)
