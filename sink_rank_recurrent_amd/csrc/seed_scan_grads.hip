@@ -279,15 +279,40 @@ __device__ __forceinline__ Frag<3> part_cols(const char* planes, int half, int k
   return f;
 }
 
+// Row `row` of an array in the order of load_row8, all of it on its way at
+// once (a branch around each piece made every one wait for the one before);
+// row n - 1 instead of a row behind it, taken for 0 by `or_zero`.
+template <int KS, typename T>
+__device__ __forceinline__ void load_rows(const T* base, size_t ld, int row, int n, float (&x)[KS][8]) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) load_row8(base + (size_t)min(row, n - 1) * ld, 32 * ks, true, x[ks]);
+}
+__device__ __forceinline__ void or_zero(float (&x)[8], bool live) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = live ? x[j] : 0.f;
+}
+
+// One value of N planes.
+template <int DK, int N>
+__device__ __forceinline__ float lds_value(const char* planes, int t, int i) {
+  float x = 0.f;
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n)
+    x += __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
+             planes + n * kPlane<DK> + piece_at<DK>(t, i >> 3) + 2 * (i & 7)) << 16);
+  return x;
+}
+
 // Scalar gates.  Eight waves a (chunk, head): wave (rows 16 w4, half) has the
 // 16 tokens' rows of dO, dR and u in registers and every other 16 columns of
 // each result.  First the pairs inside the chunk (K and Q in LDS, u of the
 // other waves' rows through LDS), then 32 channels of S and H at a time.
 //
 // Bound by latency, one workgroup a CU (its rows alone are 112 registers a
-// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 265 us, 390 MB at
-// 1.5 TB/s, matrix cores 17 % and VALU 31 % busy; of a workgroup's 70000
-// cycles 19000 go to the first loads, 16000 to the states' and 10000 to dg.
+// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 243 us, 390 MB at
+// 1.6 TB/s, matrix cores 19 % and VALU 34 % busy; of a workgroup's 64000
+// cycles 19000 go to the first loads and 10000 to dg.  (K and Q again from
+// memory behind the states' loads, to wait for both: 269.)
 // Four waves with all columns, so that two workgroups share a CU, spilt 100
 // registers and took 357 us; four waves with the whole register file 482.
 template <int RULE, int DK, int DV, typename T>
@@ -297,8 +322,8 @@ struct GradLds {
   static constexpr int u = 3 * (DV / 32) * NE * 1024;
   static constexpr int mats = 2 * kC * kRow * 4;
   static constexpr int plane = 32 * DV * 2;          // 32 channels of S or H, one term
-  static constexpr int pairs = kq + (u > mats ? u : mats);
-  static constexpr int small = pairs > 6 * plane ? pairs : 6 * plane;
+  static constexpr int pairs = u > mats ? u : mats;
+  static constexpr int small = kq + (pairs > 6 * plane ? pairs : 6 * plane);
   static constexpr int bytes = small + (int)sizeof(Decay) + (2 + 4 + 4) * kC * 4 + 64;
 };
 
@@ -362,31 +387,33 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
   Frag<NE> au[KS];
   {
     const bool live = row < n;
-    const T* dO = static_cast<const T*>(a.dO) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
-    const T* V = static_cast<const T*>(a.v) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
-    const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
-    const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
+    const size_t vat = ((size_t)ch.tok * a.heads + head) * DV, vld = (size_t)a.heads * DV, eat = unit * kC * DV;
     const float b = DELTA ? reinterpret_cast<const float*>(a.ws + a.at.vec)[unit * 256 + 128 + row] : 0.f;
     float db = 0.f;
+    float o[KS][8], x[KS][8], y[DELTA ? KS : 1][8];
+    load_rows(static_cast<const T*>(a.dO) + vat, vld, row, n, o);
+    if constexpr (DELTA) {
+      load_rows(reinterpret_cast<const float*>(a.ws + a.at.e) + eat, DV, row, n, x);
+      load_rows(reinterpret_cast<const float*>(a.ws + a.at.y) + eat, DV, row, n, y);
+    } else {
+      load_rows(static_cast<const T*>(a.v) + vat, vld, row, n, x);
+    }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      float x[8], y[8];
-      load_row8(dO, 32 * ks, live, x);
-      ado[ks] = split<NT>(x);
+      or_zero(o[ks], live);
+      or_zero(x[ks], live);
+      ado[ks] = split<NT>(o[ks]);
       if constexpr (DELTA) {
-        load_row8(E, 32 * ks, live, x);
-        load_row8(Y, 32 * ks, live, y);
+        or_zero(y[ks], live);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          db += x[j] * y[j];
-          x[j] *= b;
-          y[j] *= b;
+          db += x[ks][j] * y[ks][j];
+          x[ks][j] *= b;
+          y[ks][j] *= b;
         }
-        adr[ks] = split<3>(y);
-      } else {
-        load_row8(V, 32 * ks, live, x);
+        adr[ks] = split<3>(y[ks]);
       }
-      au[ks] = split<NE>(x);
+      au[ks] = split<NE>(x[ks]);
       if (w4 < 3 && half == 0) {
 #pragma unroll
         for (int m = 0; m < NE; ++m)
@@ -554,8 +581,8 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
       const Frag<3> s = split<3>(sv), h = split<3>(hv);
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
-        *reinterpret_cast<u32x4*>(smem + m * Lds::plane + at) = s.t[m];
-        *reinterpret_cast<u32x4*>(smem + (3 + m) * Lds::plane + at) = h.t[m];
+        *reinterpret_cast<u32x4*>(Up + m * Lds::plane + at) = s.t[m];
+        *reinterpret_cast<u32x4*>(Up + (3 + m) * Lds::plane + at) = h.t[m];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) hsum += sv[j] * hv[j];
@@ -566,8 +593,8 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
     f32x4 x1 = {0.f, 0.f, 0.f, 0.f}, x2 = x1, x3 = x1;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const Frag<3> s = part_cols<Lds::plane>(smem, half, ks);
-      const Frag<3> h = part_cols<Lds::plane>(smem + 3 * Lds::plane, half, ks);
+      const Frag<3> s = part_cols<Lds::plane>(Up, half, ks);
+      const Frag<3> h = part_cols<Lds::plane>(Up + 3 * Lds::plane, half, ks);
       mma(x1, ado[ks], s);
       if constexpr (DELTA) mma(x2, adr[ks], s);
       mma(x3, au[ks], h);
@@ -579,7 +606,8 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w4 + 4 * g + r;
       if (t >= n) continue;
-      const float q = load_scalar(Q + (size_t)t * kld + i), k = load_scalar(K + (size_t)t * kld + i);
+      // (from LDS: a load would wait for the next part's states, loads arriving in order)
+      const float q = lds_value<DK, NT>(Qp, t, i), k = lds_value<DK, NT>(Kp, t, i);
       dp[r] += q * x1[r] - k * x2[r];
       df[r] += k * x3[r];
       if (shared) {
@@ -714,25 +742,26 @@ __global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
   float db = 0.f;
   {
     const bool live = row < n;
-    const T* dO = static_cast<const T*>(a.dO) + ((size_t)(ch.tok + row) * a.heads + head) * DV;
-    const float* E = reinterpret_cast<const float*>(a.ws + a.at.e) + (unit * kC + row) * DV;
-    const float* Y = reinterpret_cast<const float*>(a.ws + a.at.y) + (unit * kC + row) * DV;
+    const size_t eat = unit * kC * DV;
     const float b = reinterpret_cast<const float*>(a.ws + a.at.vec)[unit * 256 + 128 + row];
+    float o[KS][8], x[KS][8], y[KS][8];
+    load_rows(static_cast<const T*>(a.dO) + ((size_t)ch.tok * a.heads + head) * DV, (size_t)a.heads * DV, row, n, o);
+    load_rows(reinterpret_cast<const float*>(a.ws + a.at.e) + eat, DV, row, n, x);
+    load_rows(reinterpret_cast<const float*>(a.ws + a.at.y) + eat, DV, row, n, y);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      float x[8], y[8];
-      load_row8(dO, 32 * ks, live, x);
-      ado[ks] = split<NT>(x);
-      load_row8(E, 32 * ks, live, x);
-      load_row8(Y, 32 * ks, live, y);
+      or_zero(o[ks], live);
+      or_zero(x[ks], live);
+      or_zero(y[ks], live);
+      ado[ks] = split<NT>(o[ks]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        db += x[j] * y[j];
-        x[j] *= b;
-        y[j] *= b;
+        db += x[ks][j] * y[ks][j];
+        x[ks][j] *= b;
+        y[ks][j] *= b;
       }
-      adr[ks] = split<3>(y);
-      au[ks] = split<3>(x);
+      adr[ks] = split<3>(y[ks]);
+      au[ks] = split<3>(x[ks]);
       if (w < 3) {
 #pragma unroll
         for (int m = 0; m < 3; ++m)
