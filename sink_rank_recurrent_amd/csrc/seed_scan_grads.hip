@@ -292,6 +292,35 @@ __device__ __forceinline__ void or_zero(float (&x)[8], bool live) {
   for (int j = 0; j < 8; ++j) x[j] = live ? x[j] : 0.f;
 }
 
+// Rows t0 .. t0 + 3 (of n) of dQ and dK, channel i: to the gradients, or to
+// the workspace where heads share keys.  (With scalar gates the products are
+// left between these branches: behind them they spilt, 249 us instead of 232.)
+template <typename T>
+__device__ __forceinline__ void store_keys(const ScanArgs& a, int tok, int t0, int n, int head, int hk,
+                                           int i, int d_k, const f32x4& dq, const f32x4& dk) {
+  if (a.key_heads != a.heads) {
+    const size_t at = ((size_t)(tok + t0) * a.heads + head) * d_k + i;
+    float* q = reinterpret_cast<float*>(a.ws + a.at.dq) + at;
+    float* k = reinterpret_cast<float*>(a.ws + a.at.dk) + at;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (t0 + r < n) {
+        q[(size_t)r * a.heads * d_k] = dq[r];
+        k[(size_t)r * a.heads * d_k] = dk[r];
+      }
+  } else {
+    const size_t at = ((size_t)(tok + t0) * a.key_heads + hk) * d_k + i;
+    T* q = static_cast<T*>(a.dq) + at;
+    T* k = static_cast<T*>(a.dk) + at;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (t0 + r < n) {
+        store_scalar(q + (size_t)r * a.key_heads * d_k, dq[r]);
+        store_scalar(k + (size_t)r * a.key_heads * d_k, dk[r]);
+      }
+  }
+}
+
 // One value of N planes.
 template <int DK, int N>
 __device__ __forceinline__ float lds_value(const char* planes, int t, int i) {
@@ -309,10 +338,10 @@ __device__ __forceinline__ float lds_value(const char* planes, int t, int i) {
 // other waves' rows through LDS), then 32 channels of S and H at a time.
 //
 // Bound by latency, one workgroup a CU (its rows alone are 112 registers a
-// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 243 us, 390 MB at
-// 1.6 TB/s, matrix cores 19 % and VALU 34 % busy; of a workgroup's 64000
-// cycles 19000 go to the first loads and 10000 to dg.  (K and Q again from
-// memory behind the states' loads, to wait for both: 269.)
+// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 232 us, 390 MB at
+// 1.7 TB/s, matrix cores 20 % and VALU 36 % busy.  (K and Q again from memory
+// behind the states' loads, to wait for both, and the rows' pieces one after
+// the other: 269.)
 // Four waves with all columns, so that two workgroups share a CU, spilt 100
 // registers and took 357 us; four waves with the whole register file 482.
 template <int RULE, int DK, int DV, typename T>
@@ -674,8 +703,9 @@ __global__ __launch_bounds__(512) void grads_scalar_kernel(ScanArgs a) {
 // dO, dR and u and its rows and columns of dL and dM are fragments for all
 // channels (eight waves with half of the columns each spilt 97 registers and
 // split the triangles anew for every 32 channels: 312 us for 3001 tokens x 16
-// heads of 128 x 128 instead of 203).  Bound by latency: matrix cores 9 %,
-// VALU 20 % busy.
+// heads of 128 x 128 instead of 203; loads without branches, all on their way
+// at once, and one loop body, not four, made that 170).  Bound by latency:
+// matrix cores 11 %, VALU 24 % busy.
 template <int DK, int DV, typename T>
 struct KdaLds {
   static constexpr int NT = sizeof(T) == 2 ? 1 : 3;
@@ -720,19 +750,21 @@ __global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
   __syncthreads();
   {
     bool fine = true;
-    for (int e = tid; e < kC * DK / 4; e += 256) {
-      const int t = e / (DK / 4), i = 4 * (e % (DK / 4));
-      const f32x4 p = *reinterpret_cast<const f32x4*>(P + t * DK + i);
-      f32x4 q = {1.f, 1.f, 1.f, 1.f};
-      float k[4] = {0.f, 0.f, 0.f, 0.f};
-      if (t < n) {
-        q = *reinterpret_cast<const f32x4*>(gates + (size_t)t * gld + i);
-        load_vec<4>(K + (size_t)t * kld + i, k);
-      }
+    constexpr int CHECKS = kC * DK / 4 / 256;
+    f32x4 p[CHECKS], gt[CHECKS];
+    float k[CHECKS][4];
+#pragma unroll
+    for (int c = 0; c < CHECKS; ++c) {   // (rows behind the last: the last again)
+      const int e = tid + 256 * c, t = e / (DK / 4), i = 4 * (e % (DK / 4)), live = min(t, n - 1);
+      p[c] = *reinterpret_cast<const f32x4*>(P + t * DK + i);
+      gt[c] = *reinterpret_cast<const f32x4*>(gates + (size_t)live * gld + i);
+      load_vec<4>(K + (size_t)live * kld + i, k[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CHECKS; ++c)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        fine &= p[r] >= kSafe && p[r] <= 1.f / kSafe && q[r] >= 0.25f && fabsf(k[r]) <= 0x1p40f;
-    }
+        fine &= p[c][r] >= kSafe && p[c][r] <= 1.f / kSafe && gt[c][r] >= 0.25f && fabsf(k[c][r]) <= 0x1p40f;
     if (!fine) *bad = 1;
   }
   // the wave's rows of dO, dR and u
@@ -858,8 +890,8 @@ __global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
       qv.load(Q + (size_t)t * kld + c);
     }
   };
-  const bool shared = a.key_heads != a.heads;
   fetch(0);
+#pragma unroll 1
   for (int part = 0; part < MT; ++part) {
     __syncthreads();
 #pragma unroll
@@ -912,9 +944,10 @@ __global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
         const int t = t0 + r;
         pt[half][r] = P[t * DK + i];
         ft[half][r] = F[t * DK + i];
-        q[half][r] = t < n ? load_scalar(Q + (size_t)t * kld + i) : 0.f;
-        k[half][r] = t < n ? load_scalar(K + (size_t)t * kld + i) : 0.f;
-        gt[half][r] = t < n ? gates[(size_t)t * gld + i] : 1.f;
+        const size_t live = min(t, n - 1);
+        q[half][r] = load_scalar(Q + live * kld + i);
+        k[half][r] = load_scalar(K + live * kld + i);
+        gt[half][r] = gates[live * gld + i];
       }
       end[half] = P[(kC - 1) * DK + i];
     }
@@ -952,24 +985,17 @@ __global__ __launch_bounds__(256, 1) void grads_kda_kernel(ScanArgs a) {
       const int i = 32 * part + 16 * half + l16;
       end[half] *= (hs[16 * half + l16] + hs[32 + 16 * half + l16]) +
                    (hs[64 + 16 * half + l16] + hs[96 + 16 * half + l16]);
+      f32x4 dq, dk;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = t0 + r;
-        const float p = pt[half][r], dq = p * (x1[half][r] + a1[half][r]), rk = p * (a2[half][r] - x2[half][r]);
+        const float p = pt[half][r], rk = p * (a2[half][r] - x2[half][r]);
         const float ck = a3[half][r] * __builtin_amdgcn_rcpf(p), fk = ft[half][r] * x3[half][r];
-        xs[half][r] = q[half][r] * dq + k[half][r] * (rk - ck);
-        zs[half][r] = k[half][r] * fk;
-        if (t >= n) continue;
-        if (shared) {
-          const size_t at = ((size_t)(ch.tok + t) * a.heads + head) * DK + i;
-          reinterpret_cast<float*>(a.ws + a.at.dq)[at] = dq;
-          reinterpret_cast<float*>(a.ws + a.at.dk)[at] = rk + ck + fk;
-        } else {
-          const size_t at = ((size_t)(ch.tok + t) * a.key_heads + hk) * DK + i;
-          store_scalar(static_cast<T*>(a.dq) + at, dq);
-          store_scalar(static_cast<T*>(a.dk) + at, rk + ck + fk);
-        }
+        dq[r] = p * (x1[half][r] + a1[half][r]);
+        dk[r] = rk + ck + fk;
+        xs[half][r] = t0 + r < n ? q[half][r] * dq[r] + k[half][r] * (rk - ck) : 0.f;
+        zs[half][r] = t0 + r < n ? k[half][r] * fk : 0.f;
       }
+      store_keys<T>(a, ch.tok, t0, n, head, hk, i, DK, dq, dk);
       // sums of x over t and behind, of z before t: rows, lanes, waves
       const float sx = (xs[half][0] + xs[half][1]) + (xs[half][2] + xs[half][3]);
       const float sz = (zs[half][0] + zs[half][1]) + (zs[half][2] + zs[half][3]);
