@@ -87,22 +87,36 @@ __device__ __forceinline__ void store_half(uint16_t* __restrict__ pack, int frag
         make_uint2(f.t[n][0], f.t[n][1]);
 }
 
-// A chunk's rows of a float32 array into three planes, rows from n on 0.
+// A chunk's rows of a float32 array into three planes, rows from n on 0: a
+// thread's pieces, all on their way at once.
 template <int DK>
-__device__ __forceinline__ void split_rows(const float* rows, size_t ld, int n, char* planes) {
-  for (int e = threadIdx.x; e < kC * DK / 8; e += 256) {
-    const int t = e / (DK / 8), c = e % (DK / 8);
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (t < n) {
-      const float* p = rows + (size_t)t * ld + 8 * c;
-      tiles_to_floats(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4), x);
-    }
-    const Frag<3> f = split<3>(x);
+struct FloatRows {
+  static constexpr int N = kC * DK / 8 / 256;
+  f32x4 a[N], b[N];
+  __device__ __forceinline__ void load(const float* rows, size_t ld, int n) {
 #pragma unroll
-    for (int m = 0; m < 3; ++m)
-      *reinterpret_cast<u32x4*>(planes + m * kPlane<DK> + piece_at<DK>(t, c)) = f.t[m];
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + 256 * i, t = e / (DK / 8), c = e % (DK / 8);
+      const float* p = rows + (size_t)min(t, n - 1) * ld + 8 * c;
+      a[i] = *reinterpret_cast<const f32x4*>(p);
+      b[i] = *reinterpret_cast<const f32x4*>(p + 4);
+    }
   }
-}
+  __device__ __forceinline__ void split_to(int n, char* planes) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + 256 * i, t = e / (DK / 8), c = e % (DK / 8);
+      float x[8];
+      tiles_to_floats(a[i], b[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = t < n ? x[j] : 0.f;
+      const Frag<3> f = split<3>(x);
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+        *reinterpret_cast<u32x4*>(planes + m * kPlane<DK> + piece_at<DK>(t, c)) = f.t[m];
+    }
+  }
+};
 
 // Four waves a (chunk, head); wave w has the tokens 16 w .. + 15 as rows.  K
 // and Q lie in LDS by whole rows (256 bytes at a time: fragments straight from
@@ -111,7 +125,7 @@ __device__ __forceinline__ void split_rows(const float* rows, size_t ld, int n, 
 // three terms; a wave takes its rows of Q from memory.)
 //
 // Bound by the steps' latency and the VALU, not by memory: for those 64 x 512
-// tokens x 16 heads 111 us, 360 MB moved at 3.2 TB/s, the VALU issuing half of
+// tokens x 16 heads 108 us, 360 MB moved at 3.3 TB/s, the VALU issuing half of
 // the time and the matrix cores 13 % of it; the decays are one wave's work and
 // the inverses of L's diagonal blocks 16 dependent steps.  Four workgroups a
 // CU hide part of it.
@@ -139,20 +153,32 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   // three of N
   const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
+  // loads arrive in order, and the decays are the longest way: the gates first
+  const int row = 16 * w + l16;
+  float gate = 1.f, beta = 0.f;
+  if (w == 0) {
+    const size_t at = ((size_t)ch.tok + min(l, ch.n - 1)) * a.heads + head;
+    gate = a.g[at];
+    if (DELTA) beta = a.beta[at];
+  }
+  float q[NT == 1 ? 1 : DK / 32][8];   // the wave's rows of Q (float32)
   if constexpr (NT == 1) {
     async_rows<DK, 4>(K, Q, ld, ch.n, lds_offset(Kp), lds_offset(Qp), true, w);
   } else {
-    split_rows<DK>(K, ld, ch.n, Kp);
+    FloatRows<DK> k;
+    k.load(K, ld, ch.n);
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) load_piece(Q + (size_t)min(row, ch.n - 1) * ld, 32 * ks, true, q[ks]);
+    k.split_to(ch.n, Kp);
   }
   if (w == 0) {
-    const size_t gate = ((size_t)ch.tok + l) * a.heads + head;
     float P, F;
     float* vec = reinterpret_cast<float*>(a.ws + a.at.vec) + unit * 256;
     if (DELTA) {
-      bt[l] = l < ch.n ? a.beta[gate] : 0.f;
+      bt[l] = l < ch.n ? beta : 0.f;
       vec[128 + l] = bt[l];
     }
-    decays(dec, l < ch.n ? a.g[gate] : 1.f, P, F);
+    decays(dec, l < ch.n ? gate : 1.f, P, F);
     vec[l] = P;
     vec[64 + l] = F;
   }
@@ -171,9 +197,8 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
     if constexpr (NT == 1) {
       qt = lds_rows<DK, NT>(Qp, w, ks);
     } else {
-      float x[8];
-      load_piece(Q + (size_t)(16 * w + l16) * ld, 32 * ks, 16 * w + l16 < ch.n, x);
-      qt = split<NT>(x);
+      for (int j = 0; j < 8; ++j) q[ks][j] = row < ch.n ? q[ks][j] : 0.f;
+      qt = split<NT>(q[ks]);
     }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
