@@ -312,16 +312,18 @@ __device__ __forceinline__ Frag<N> lds_pack(const char* pack, int frag) {
 // same in every lane) + `off`, to 64 consecutive places from LDS offset `to`
 // (the same in every lane).  Written as asm because the compiler would make
 // every later LDS read wait for it, another buffer's too; the caller waits
-// (async_wait, then a barrier).  M0 holds the LDS side; the s_nop is the wait
-// state such a load needs after M0 is written, and M0 is put back for the
-// compiler.
+// (async_wait, then a barrier).  M0 holds the LDS side and is put back for the
+// compiler.  The compiler fills no wait states inside asm: the two moves and
+// s_nop 2 are the five that a memory instruction needs behind a vector
+// instruction that wrote its scalar base (the readfirstlanes above), and the
+// one behind the write of M0.
 __device__ __forceinline__ void async_copy(const void* from, uint32_t off, uint32_t to) {
   uint32_t kept;
   const uint64_t p = reinterpret_cast<uint64_t>(from);
   const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32 |
                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p);
   to = __builtin_amdgcn_readfirstlane(to);
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\t"
                "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                : "=&s"(kept) : "v"(off), "s"(base), "s"(to) : "memory");
 }
