@@ -47,12 +47,11 @@ extern "C" {
  * key channel as quotients of products where those of 64 tokens stay within
  * 2^-60 .. 2^60, as products otherwise.  Logarithms are never taken.
  * Sums and states are fp32; the products run on the matrix cores with an fp32
- * operand as three bf16 terms (2^-27 of it is left out).  Where the inputs
- * are bf16 and nothing goes backward, the terms that correct v by what the
- * state holds, and the read-outs, take two (2^-18): the last state is within
- * 1e-6 of its norm either way.  A NaN or infinity of a token reaches its
- * sequence's state and read-outs from the first token of its 64 on, and no
- * other sequence.
+ * operand as three bf16 terms (2^-27 of it is left out), whatever the inputs'
+ * type: the last state of 512 tokens is within 1e-6 of its norm, also with
+ * gates of 1 or keys that point one way.  A NaN or infinity of a token
+ * reaches its sequence's state and read-outs from the first token of its 64
+ * on, and no other sequence.
  * 1 <= key_heads <= heads, heads a multiple of key_heads, heads <= 65535;
  * d_k, d_v as in seed.h.
  */

@@ -77,12 +77,12 @@ __device__ __forceinline__ Frag<N> split(const float (&x)[8]) {
   return f;
 }
 
-// c += a b over the products of terms i, j with i + j < ORDER (the smallest
+// c += a b over the products of terms i, j with i + j < 3 (the smallest
 // first).
-template <int NA, int NB, int ORDER = 3>
+template <int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>& b) {
 #pragma unroll
-  for (int o = ORDER - 1; o >= 0; --o) {
+  for (int o = 2; o >= 0; --o) {
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int j = o - i;
@@ -141,13 +141,11 @@ __host__ __device__ constexpr int upper_frag(int mt, int ks) {
   return mt < 2 ? 2 * mt + ks : (ks == 1 ? 2 + mt : -1);
 }
 
-// A packed fragment of three terms, [frag][term][lane][8]; the third only where
-// it is read by somebody.
+// A packed fragment of three terms, [frag][term][lane][8].
 __device__ __forceinline__ void store_pack(uint16_t* __restrict__ pack, int frag,
-                                           const Frag<3>& f, bool third = true) {
+                                           const Frag<3>& f) {
 #pragma unroll
   for (int n = 0; n < 3; ++n)
-    if (n < 2 || third)
     *reinterpret_cast<u32x4*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8) = f.t[n];
 }
 
@@ -352,14 +350,13 @@ __device__ __forceinline__ void async_rows(const bf16_t* K, const bf16_t* Q, uin
   }
 }
 
-// The first N of the three terms of a pack's fragments.
-template <int N, int W>
+// A pack's fragments.
+template <int W>
 __device__ __forceinline__ void async_pack(const uint16_t* pack, uint32_t to, int wave) {
 #pragma unroll
-  for (int j = 0; j < (kTriFrags * N + W - 1) / W; ++j) {
+  for (int j = 0; j < (kTriFrags * 3 + W - 1) / W; ++j) {
     const int i = wave + j * W;
-    if (i < kTriFrags * N)
-      async_copy(pack + (i / N * 3 + i % N) * kFrag, lane_id() * 16, to + i * 1024);
+    if (i < kTriFrags * 3) async_copy(pack + i * kFrag, lane_id() * 16, to + i * 1024);
   }
 }
 
@@ -457,11 +454,11 @@ __device__ __forceinline__ void decays(Decay& d, float gate, float& P, float& F)
 
 // c[m] += a[m] b for MT row tiles, the tiles in turn so that consecutive
 // MFMAs do not wait for each other.
-template <int MT, int NA, int NB, int ORDER = 3>
+template <int MT, int NA, int NB>
 __device__ __forceinline__ void mma_tiles(f32x4 (&c)[MT], const Frag<NA> (&a)[MT],
                                           const Frag<NB>& b) {
 #pragma unroll
-  for (int o = ORDER - 1; o >= 0; --o) {
+  for (int o = 2; o >= 0; --o) {
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       const int j = o - i;

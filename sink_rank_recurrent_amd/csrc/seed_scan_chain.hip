@@ -12,12 +12,12 @@
 // workgroups (4 sequences x 2048 tokens: 128) by the chain itself, 4 us a
 // chunk forward and 6.5 backward (128 and 208 us for 32 chunks).
 //
-// Terms: what is added to the state takes all three terms of F u.  Forward,
-// K S and N (beta R) only correct u and take two (at most 2^-18 of an
-// operand's value is left out, its sign at random: the states stay within
-// 1e-6), as do the read-outs' products, which are rounded to 2^-9 after all.
-// The backward pass keeps three throughout: dbeta and dg are inner products
-// of these results and would lose digits (1.1e-6 instead of 3e-7).
+// Terms: three of every fp32 operand.  Two where the result only corrects u or
+// is rounded to bf16 would take 308 us instead of 361 for those 64 x 512 tokens
+// x 16 heads with their preparation, but the corrections enter the state, which
+// then is off by 7e-7 of its norm, 3e-6 with gates near 1 or keys that point one
+// way (three: 1.3e-7 and 2.4e-7, as plain fp32), and 3 in 1000 read-outs are not
+// the bf16 nearest to the exact one (three: 2 in 10000).
 #include "seed_scan_chain.h"
 
 namespace seed {
@@ -30,13 +30,13 @@ struct Part {
 };
 
 // LDS of one chunk's operands.
-template <int RULE, int DK, bool K_Q, int NT, int MT, bool HAS_M>
+template <int RULE, int DK, bool K_Q, bool HAS_M>
 struct Stage {
   static constexpr bool DELTA = RULE != kMAMBA2;
   static constexpr int q = kPlane<DK>;
   static constexpr int n = q + (K_Q ? kPlane<DK> : 0);
-  static constexpr int m = n + (DELTA ? kTriFrags * NT * 1024 : 0);
-  static constexpr int vec = m + (HAS_M ? kTriFrags * MT * 1024 : 0);   // P, F, beta
+  static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int vec = m + (HAS_M ? kTriFrags * 3 * 1024 : 0);   // P, F, beta
   static constexpr int bytes = vec + 1024;
 
   // The chunk's loads, PART 0 .. 2 of them (-1: all): spread over the chunk
@@ -49,12 +49,12 @@ struct Stage {
     if (PART <= 0) async_rows<DK, W>(K, Q, ld, rows, to, to + q, K_Q, w);
     if (PART < 0 || PART == 1) {
       if (DELTA)
-        async_pack<NT, W>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
+        async_pack<W>(reinterpret_cast<const uint16_t*>(a.ws + (transposed ? a.at.nt_pack : a.at.n_pack)) +
                               unit * pack, to + n, w);
     }
     if (PART < 0 || PART == 2) {
       if (HAS_M)
-        async_pack<MT, W>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w);
+        async_pack<W>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, to + m, w);
       if (w == W - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, to + vec);
     }
   }
@@ -66,8 +66,8 @@ struct Stage {
 template <int RULE, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
   constexpr bool DELTA = RULE != kMAMBA2, READ = MODE == kRead, SAVE = MODE == kSave, CARRY = MODE == kCarry;
-  constexpr int IT = DK / 16, NT = !READ ? 3 : 2;   // terms of the corrections
-  using St = Stage<RULE, DK, READ, NT, 2, READ>;
+  constexpr int IT = DK / 16;
+  using St = Stage<RULE, DK, READ, READ>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
   const Walk<NW> at(a, a.d_v + (CARRY && DELTA ? DK : 0));
@@ -130,17 +130,17 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     if (DELTA || READ) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        const Frag<NT> s = split_tiles<NT>(S[2 * ks], S[2 * ks + 1]);
+        const Frag<3> s = split_tiles<3>(S[2 * ks], S[2 * ks + 1]);
         Frag<1> f[4];
         if (DELTA) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now, m, ks);
-          mma_tiles<4, 1, NT, NT>(R, f, s);
+          mma_tiles(R, f, s);
         }
         if (READ) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 1>(now + St::q, m, ks);
-          mma_tiles<4, 1, NT, 2>(O, f, s);
+          mma_tiles(O, f, s);
         }
       }
     }
@@ -158,16 +158,16 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
         b[m] = lds_vec(now + St::vec + 512, m);
         y[m] = zero4();
       }
-      const Frag<NT> x0 = split_tiles<NT>(b[0] * u[0], b[1] * u[1]);
-      const Frag<NT> x1 = split_tiles<NT>(b[2] * u[2], b[3] * u[3]);
-      Frag<NT> f[4];
+      const Frag<3> x0 = split_tiles<3>(b[0] * u[0], b[1] * u[1]);
+      const Frag<3> x1 = split_tiles<3>(b[2] * u[2], b[3] * u[3]);
+      Frag<3> f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NT>(now + St::n, lower_frag(m, 0));
-      mma_tiles<4, NT, NT, NT>(y, f, x0);
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::n, lower_frag(m, 0));
+      mma_tiles(y, f, x0);
       f32x4 z[2] = {y[2], y[3]};
-      const Frag<NT> h[2] = {lds_pack<NT>(now + St::n, lower_frag(2, 1)),
-                            lds_pack<NT>(now + St::n, lower_frag(3, 1))};
-      mma_tiles<2, NT, NT, NT>(z, h, x1);
+      const Frag<3> h[2] = {lds_pack<3>(now + St::n, lower_frag(2, 1)),
+                            lds_pack<3>(now + St::n, lower_frag(3, 1))};
+      mma_tiles(z, h, x1);
       u[0] -= y[0];
       u[1] -= y[1];
       u[2] -= z[0];
@@ -180,16 +180,16 @@ __global__ __launch_bounds__(64 * NW) void chain_forward_kernel(ScanArgs a) {
     }
     stage(Part<2>{});
     if (READ) {
-      constexpr int NU = DELTA ? 2 : 1;   // V itself is one term
+      constexpr int NU = DELTA ? 3 : 1;   // V itself is one term
       const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
-      Frag<2> f[4];
+      Frag<3> f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = lds_pack<2>(now + St::m, lower_frag(m, 0));
-      mma_tiles<4, 2, NU, 2>(O, f, x0);
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(now + St::m, lower_frag(m, 0));
+      mma_tiles(O, f, x0);
       f32x4 z[2] = {O[2], O[3]};
-      const Frag<2> h[2] = {lds_pack<2>(now + St::m, lower_frag(2, 1)),
-                            lds_pack<2>(now + St::m, lower_frag(3, 1))};
-      mma_tiles<2, 2, NU, 2>(z, h, x1);
+      const Frag<3> h[2] = {lds_pack<3>(now + St::m, lower_frag(2, 1)),
+                            lds_pack<3>(now + St::m, lower_frag(3, 1))};
+      mma_tiles(z, h, x1);
       O[2] = z[0];
       O[3] = z[1];
       wave_store(out + (size_t)c * kC * vld, vld, n, O, mine);
@@ -229,7 +229,7 @@ template <int RULE, int DK, int NW, bool LOCAL>
 __global__ __launch_bounds__(64 * NW) void chain_reverse_kernel(ScanArgs a) {
   constexpr bool DELTA = RULE != kMAMBA2;
   constexpr int IT = DK / 16;
-  using St = Stage<RULE, DK, true, 3, 3, true>;
+  using St = Stage<RULE, DK, true, true>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
   const Walk<NW> at(a, a.d_v);
@@ -384,9 +384,10 @@ hipError_t launch(F kernel, const ScanArgs& a, int columns, int waves, size_t ld
 template <int RULE, int DK, int NW>
 hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
   constexpr size_t own = 2048 * NW;
-  constexpr size_t read = 2 * Stage<RULE, DK, true, 2, 2, true>::bytes + own;
-  constexpr size_t save = 2 * Stage<RULE, DK, false, 3, 2, false>::bytes + own;
-  constexpr size_t back = 2 * Stage<RULE, DK, true, 3, 3, true>::bytes + own;
+  constexpr size_t read = 2 * Stage<RULE, DK, true, true>::bytes + own;
+  constexpr size_t save = 2 * Stage<RULE, DK, false, false>::bytes + own;
+  constexpr size_t back = 2 * Stage<RULE, DK, true, true>::bytes + own;
+  static_assert(read <= 160 * 1024 && save <= 160 * 1024 && back <= 160 * 1024, "LDS of a CU");
   switch (what) {
     case 0: return launch(chain_forward_kernel<RULE, DK, NW, kRead>, a, a.d_v, NW, read, stream);
     case 1: return launch(chain_forward_kernel<RULE, DK, NW, kSave>, a, a.d_v, NW, save, stream);

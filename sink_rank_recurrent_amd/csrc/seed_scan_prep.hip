@@ -58,8 +58,7 @@ __device__ __forceinline__ void solve(float* L, float* X, const float* beta, int
 
 // The triangle of an LDS matrix as a pack (transposed: of its transpose).
 __device__ __forceinline__ void pack_triangle(uint16_t* __restrict__ pack, const float* mat,
-                                              bool transposed, int mt, int ks,
-                                              bool third = true) {
+                                              bool transposed, int mt, int ks) {
   const int frag = transposed ? upper_frag(mt, ks) : lower_frag(mt, ks);
   if (frag < 0) return;
   const int row = 16 * mt + (lane_id() & 15), g = lane_id() >> 4;
@@ -71,19 +70,18 @@ __device__ __forceinline__ void pack_triangle(uint16_t* __restrict__ pack, const
     tiles_to_floats(*reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 4 * g),
                     *reinterpret_cast<const f32x4*>(mat + row * kRow + 32 * ks + 16 + 4 * g), x);
   }
-  store_pack(pack, frag, split<3>(x), third);
+  store_pack(pack, frag, split<3>(x));
 }
 
 // Half a fragment (slots 4 h .. 4 h + 3): one accumulator tile of the
 // transposed product.
 __device__ __forceinline__ void store_half(uint16_t* __restrict__ pack, int frag, int h,
-                                           const f32x4& c, bool third) {
+                                           const f32x4& c) {
   const float x[8] = {c[0], c[1], c[2], c[3], 0.f, 0.f, 0.f, 0.f};
   const Frag<3> f = split<3>(x);
 #pragma unroll
   for (int n = 0; n < 3; ++n)
-    if (n < 2 || third)
-      *reinterpret_cast<uint2*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8 + 4 * h) =
+    *reinterpret_cast<uint2*>(pack + (size_t)(frag * 3 + n) * kFrag + lane_id() * 8 + 4 * h) =
         make_uint2(f.t[n][0], f.t[n][1]);
 }
 
@@ -149,9 +147,6 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
   const T* K = static_cast<const T*>(a.k) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   const T* Q = static_cast<const T*>(a.q) + ((size_t)ch.tok * a.key_heads + hk) * DK;
   uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
-  // a forward pass with bf16 read-outs reads two terms, its segments' carries
-  // three of N
-  const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
   // loads arrive in order, and the decays are the longest way: the gates first
   const int row = 16 * w + l16;
@@ -243,16 +238,16 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
     mm *= gm;
     if (BWD) {
       // rows s of tile b, tokens of tile w; a block's zero half is written too
-      if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm, true);
+      if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
     } else {
-      if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm, m_third);
+      if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
     }
   }
   if (DELTA) {
     __syncthreads();
     solve(L, L + kC * kRow, bt, w);
     uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-    for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1, n_third);
+    for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
     if (BWD) {
       uint16_t* tp =
           reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);
@@ -374,9 +369,6 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
   float* P = reinterpret_cast<float*>(a.ws + a.at.p) + unit * kC * DK;
   float* F = reinterpret_cast<float*>(a.ws + a.at.f) + unit * kC * DK;
   uint16_t* mp = reinterpret_cast<uint16_t*>(a.ws + a.at.m_pack) + unit * (kTriFrags * 3 * kFrag);
-  // a forward pass with bf16 read-outs reads two terms, its segments' carries
-  // three of N
-  const bool m_third = BWD || sizeof(T) == 4, n_third = m_third || a.at.seg > 0;
 
   if constexpr (sizeof(T) == 2)
     async_rows<DK, 4>(K, Q, ld, ch.n, lds_offset(buf), lds_offset(buf + kPlane<DK>), true, w);
@@ -464,7 +456,7 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
 
   if (unsafe) {
     slow_triangles<DK>(K, Q, ld, gates, gld, ch.n, X, L, M, P, F);
-    for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1, m_third);
+    for (int i = w; i < 8; i += 4) pack_triangle(mp, M, BWD, i >> 1, i & 1);
   } else {
     f32x4 lt[4], mt[4];
 #pragma unroll
@@ -497,16 +489,16 @@ __global__ __launch_bounds__(256, 2) void prep_kda_kernel(ScanArgs a) {
       }
       *reinterpret_cast<f32x4*>(L + (16 * w + l16) * kRow + 16 * b + 4 * g16) = ll;
       if (BWD) {
-        if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm, true);
+        if (upper_frag(b, w >> 1) >= 0) store_half(mp, upper_frag(b, w >> 1), w & 1, mm);
       } else {
-        if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm, m_third);
+        if (lower_frag(w, b >> 1) >= 0) store_half(mp, lower_frag(w, b >> 1), b & 1, mm);
       }
     }
     __syncthreads();
   }
   solve(L, X, bt, w);
   uint16_t* np = reinterpret_cast<uint16_t*>(a.ws + a.at.n_pack) + unit * (kTriFrags * 3 * kFrag);
-  for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1, n_third);
+  for (int i = w; i < 8; i += 4) pack_triangle(np, L, false, i >> 1, i & 1);
   if (BWD) {
     uint16_t* tp =
         reinterpret_cast<uint16_t*>(a.ws + a.at.nt_pack) + unit * (kTriFrags * 3 * kFrag);

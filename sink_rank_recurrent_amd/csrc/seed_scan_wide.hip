@@ -6,7 +6,9 @@
 // gates per channel K serves twice, scaled by P and by F: the second fills
 // the same planes once the first is used up, and F is loaded once P is used
 // (held together with P it spilt, and every spilt value was waited for: 25000
-// cycles a chunk of 48000).  A barrier behind the last use of N, M and the
+// cycles a chunk of 48000).  P_end waits in LDS for the same reason: held in
+// registers from before the corrections on, 24 sequences of 7919 tokens took
+// 514 us with their preparation, 413 so.  A barrier behind the last use of N, M and the
 // vectors lets the next chunk's be loaded while the state is brought up.
 //
 // Bound as there: 24 ragged sequences of 7919 tokens x 32 heads with gates per
@@ -83,19 +85,16 @@ struct Tiles {
   }
 };
 
-// Terms: as in seed_scan_chain.hip, two for the corrections and the read-outs
-// where the read-outs are bf16, three otherwise.
 template <int RULE, int DK, typename T, bool READ>
 struct Wide {
   static constexpr bool KDA = RULE == kKDA, DELTA = RULE != kMAMBA2;
-  static constexpr bool OUT16 = sizeof(T) == 2 && READ;
-  static constexpr int NC = OUT16 ? 2 : 3;                       // corrections
   static constexpr int NV = sizeof(T) == 2 ? 1 : 3;              // a value or a gradient
   static constexpr int q = 3 * kPlane<DK>;
-  static constexpr int n = q + (READ ? NC * kPlane<DK> : 0);
-  static constexpr int m = n + (DELTA ? kTriFrags * NC * 1024 : 0);
-  static constexpr int vec = m + (READ ? kTriFrags * NC * 1024 : 0);
-  static constexpr int bytes = vec + 1024;
+  static constexpr int n = q + (READ ? 3 * kPlane<DK> : 0);
+  static constexpr int m = n + (DELTA ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int vec = m + (READ ? kTriFrags * 3 * 1024 : 0);
+  static constexpr int end = vec + 1024;   // KDA: the last 256 values of P, P_end behind them
+  static constexpr int bytes = end + (KDA ? 1024 : 0);
 };
 
 template <int RULE, int DK, int NW, typename T, int MODE>
@@ -103,7 +102,7 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
   constexpr bool READ = MODE == kRead, SAVE = MODE == kSave, CARRY = MODE == kCarry;
   using W = Wide<RULE, DK, T, READ>;
   constexpr bool KDA = W::KDA, DELTA = W::DELTA;
-  constexpr int IT = DK / 16, NC = W::NC, TH = 64 * NW;
+  constexpr int IT = DK / 16, TH = 64 * NW;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int w = wave_id();
   const Walk<NW> at(a, a.d_v + (CARRY && DELTA ? DK : 0));
@@ -135,7 +134,6 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
   char* mine = lds + W::bytes + kOwn<T> * w;
   const uint32_t mine0 = lds0 + W::bytes + kOwn<T> * w;
   Tiles<T> v;
-  f32x4 last[KDA ? IT : 1];
   auto keys = [&](int c) {
     const int n = min(kC, rg.len - c * kC);
     kr.load(K + (size_t)c * kC * kld, kld, n);
@@ -154,10 +152,12 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
+      async_pack<NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.n_pack) + unit * pack, lds0 + W::n, w);
     if (READ)
-      async_pack<NC, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
+      async_pack<NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
     if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
+    if (KDA && w == 0)
+      async_copy(a.ws + a.at.p + (unit + 1) * (kC * DK * 4) - 1024, lane_id() * 16, lds0 + W::end);
   };
   if (c0 < c1) {
     keys(c0);
@@ -169,21 +169,14 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     __syncthreads();   // the chunk before is done with the planes
     if (KDA) {
-      if (DELTA) fill<DK, TH, NC, true>(lds, kr, xr);
-      if (READ) fill<DK, TH, NC, true>(lds + W::q, qr, xr);
+      if (DELTA) fill<DK, TH, 3, true>(lds, kr, xr);
+      if (READ) fill<DK, TH, 3, true>(lds + W::q, qr, xr);
     } else {
       fill<DK, TH, 3, false>(lds, kr, xr);
-      if (READ) fill<DK, TH, NC, false>(lds + W::q, qr, xr);
+      if (READ) fill<DK, TH, 3, false>(lds + W::q, qr, xr);
     }
     async_wait();
     __syncthreads();
-    f32x4 u[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if constexpr (OWN) u[m] = unit_cols ? zero4() : wave_tile<T>(mine, m);
-      else u[m] = unit_cols ? zero4() : v.tile(m);
-    }
-    drop_rows(u, n);
     if (SAVE)
       keep_chunk_state(reinterpret_cast<float*>(a.ws + a.at.state) + unit * DK * a.d_v, at.col0, S);
     if (KDA) xr.load(reinterpret_cast<const float*>(a.ws + a.at.f) + unit * kC * DK, DK, kC);
@@ -195,29 +188,33 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     if (DELTA || READ) {
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        const Frag<NC> s = split_tiles<NC>(S[2 * ks], S[2 * ks + 1]);
-        Frag<NC> f[4];
+        const Frag<3> s = split_tiles<3>(S[2 * ks], S[2 * ks + 1]);
         if (DELTA) {
+          Frag<3> f[4];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds, m, ks);
-          mma_tiles<4, NC, NC, NC>(R, f, s);
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 3>(lds, m, ks);
+          mma_tiles(R, f, s);
         }
         if (READ) {
+          Frag<3> f[4];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, NC>(lds + W::q, m, ks);
-          mma_tiles<4, NC, NC, NC>(O, f, s);
+          for (int m = 0; m < 4; ++m) f[m] = lds_rows<DK, 3>(lds + W::q, m, ks);
+          mma_tiles(O, f, s);
         }
       }
     }
     if (KDA) {   // K's planes are used up: F K takes their place
-#pragma unroll
-      for (int m = 0; m < IT; ++m)
-        last[m] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.ws + a.at.p) +
-                                                  (unit * kC + kC - 1) * DK + state_row(m));
       __syncthreads();
       fill<DK, TH, 3, true>(lds, kr, xr);
       if (c + 1 < c1) keys(c + 1);
     }
+    f32x4 u[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if constexpr (OWN) u[m] = unit_cols ? zero4() : wave_tile<T>(mine, m);
+      else u[m] = unit_cols ? zero4() : v.tile(m);
+    }
+    drop_rows(u, n);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const f32x4 p = KDA ? f32x4{1.f, 1.f, 1.f, 1.f} : lds_vec(lds + W::vec, m);
@@ -231,16 +228,16 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
         b[m] = lds_vec(lds + W::vec + 512, m);
         y[m] = zero4();
       }
-      const Frag<NC> x0 = split_tiles<NC>(b[0] * u[0], b[1] * u[1]);
-      const Frag<NC> x1 = split_tiles<NC>(b[2] * u[2], b[3] * u[3]);
-      Frag<NC> f[4];
+      const Frag<3> x0 = split_tiles<3>(b[0] * u[0], b[1] * u[1]);
+      const Frag<3> x1 = split_tiles<3>(b[2] * u[2], b[3] * u[3]);
+      Frag<3> f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NC>(lds + W::n, lower_frag(m, 0));
-      mma_tiles<4, NC, NC, NC>(y, f, x0);
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(lds + W::n, lower_frag(m, 0));
+      mma_tiles(y, f, x0);
       f32x4 z[2] = {y[2], y[3]};
-      const Frag<NC> h[2] = {lds_pack<NC>(lds + W::n, lower_frag(2, 1)),
-                             lds_pack<NC>(lds + W::n, lower_frag(3, 1))};
-      mma_tiles<2, NC, NC, NC>(z, h, x1);
+      const Frag<3> h[2] = {lds_pack<3>(lds + W::n, lower_frag(2, 1)),
+                             lds_pack<3>(lds + W::n, lower_frag(3, 1))};
+      mma_tiles(z, h, x1);
       u[0] -= y[0];
       u[1] -= y[1];
       u[2] -= z[0];
@@ -252,16 +249,16 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
       for (int m = 0; m < 4; ++m) u[m] *= b[m];
     }
     if (READ) {
-      constexpr int NU = DELTA ? NC : W::NV;   // V itself is one term
+      constexpr int NU = DELTA ? 3 : W::NV;   // V itself is one term
       const Frag<NU> x0 = split_tiles<NU>(u[0], u[1]), x1 = split_tiles<NU>(u[2], u[3]);
-      Frag<NC> f[4];
+      Frag<3> f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = lds_pack<NC>(lds + W::m, lower_frag(m, 0));
-      mma_tiles<4, NC, NU, NC>(O, f, x0);
+      for (int m = 0; m < 4; ++m) f[m] = lds_pack<3>(lds + W::m, lower_frag(m, 0));
+      mma_tiles(O, f, x0);
       f32x4 z[2] = {O[2], O[3]};
-      const Frag<NC> h[2] = {lds_pack<NC>(lds + W::m, lower_frag(2, 1)),
-                             lds_pack<NC>(lds + W::m, lower_frag(3, 1))};
-      mma_tiles<2, NC, NU, NC>(z, h, x1);
+      const Frag<3> h[2] = {lds_pack<3>(lds + W::m, lower_frag(2, 1)),
+                             lds_pack<3>(lds + W::m, lower_frag(3, 1))};
+      mma_tiles(z, h, x1);
       O[2] = z[0];
       O[3] = z[1];
       if constexpr (OWN) wave_store(out + at.col0 + (size_t)c * kC * vld, vld, n, O, mine);
@@ -271,7 +268,8 @@ __global__ __launch_bounds__(64 * NW) void wide_forward_kernel(ScanArgs a) {
     // S' = P_end S + (F K)^T u
     if (KDA) {
 #pragma unroll
-      for (int m = 0; m < IT; ++m) S[m] *= last[m];
+      for (int m = 0; m < IT; ++m)
+        S[m] *= *reinterpret_cast<const f32x4*>(lds + W::end + 4 * (256 - DK + state_row(m)));
     } else {
       const float end = *reinterpret_cast<const float*>(lds + W::vec + 4 * (kC - 1));
 #pragma unroll
@@ -373,8 +371,8 @@ __global__ __launch_bounds__(64 * NW) void wide_reverse_kernel(ScanArgs a) {
     const size_t unit = (size_t)(base + c) * a.heads + at.head;
     constexpr size_t pack = kTriFrags * 3 * kFrag;
     if (DELTA)
-      async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds0 + W::n, w);
-    async_pack<3, NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
+      async_pack<NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.nt_pack) + unit * pack, lds0 + W::n, w);
+    async_pack<NW>(reinterpret_cast<const uint16_t*>(a.ws + a.at.m_pack) + unit * pack, lds0 + W::m, w);
     if (w == NW - 1) async_copy(a.ws + a.at.vec + unit * 1024, lane_id() * 16, lds0 + W::vec);
   };
   if (c0 < c1) {
