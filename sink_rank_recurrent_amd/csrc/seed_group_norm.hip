@@ -397,30 +397,35 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a, lon
 }
 
 // dweight and dbias: a block sums four neighbouring columns of the parts
-// [parts][stride], thread t the parts t, t + 256, ...; then by halves.
+// [parts][stride], thread t the parts t, t + 256, ...; then by halves.  Wide
+// weights have more columns than a grid has blocks for (2^32 threads along
+// x): a block then goes on to the columns a grid further.
+constexpr int kPartsBlocks = 1 << 16;
 __global__ __launch_bounds__(kThreads) void parts_kernel(NormArgs a) {
   __shared__ float4 lds[kThreads];
   const int total = a.weight_groups * 2 * a.d, stride = (total + 3) & ~3;   // [group][dw, db][d]
-  const int c = blockIdx.x * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = threadIdx.x; p < a.parts; p += kThreads) {
-    const float4 x = *reinterpret_cast<const float4*>(a.ws + (size_t)p * stride + c);
-    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-  }
-  lds[threadIdx.x] = s;
-  for (int half = kThreads / 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if ((int)threadIdx.x < half) {
-      const float4 x = lds[threadIdx.x + half];
+  for (int c = blockIdx.x * 4; c < total; c += gridDim.x * 4) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = threadIdx.x; p < a.parts; p += kThreads) {
+      const float4 x = *reinterpret_cast<const float4*>(a.ws + (size_t)p * stride + c);
       s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-      lds[threadIdx.x] = s;
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < 4 && c + (int)threadIdx.x < total) {
-    const int at = c + threadIdx.x, grp = at / (2 * a.d), rest = at % (2 * a.d);
-    float* to = rest < a.d ? a.dweight : a.dbias;
-    if (to) to[(size_t)grp * a.d + rest % a.d] = reinterpret_cast<const float*>(lds)[threadIdx.x];
+    __syncthreads();   // the columns before are written out
+    lds[threadIdx.x] = s;
+    for (int half = kThreads / 2; half > 0; half >>= 1) {
+      __syncthreads();
+      if ((int)threadIdx.x < half) {
+        const float4 x = lds[threadIdx.x + half];
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        lds[threadIdx.x] = s;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 4 && c + (int)threadIdx.x < total) {
+      const int at = c + threadIdx.x, grp = at / (2 * a.d), rest = at % (2 * a.d);
+      float* to = rest < a.d ? a.dweight : a.dbias;
+      if (to) to[(size_t)grp * a.d + rest % a.d] = reinterpret_cast<const float*>(lds)[threadIdx.x];
+    }
   }
 }
 
@@ -503,8 +508,8 @@ hipError_t launch_group_norm(const NormArgs& a, hipStream_t stream) {
 hipError_t launch_group_norm_backward(const NormArgs& a, hipStream_t stream) {
   hipError_t e = norm<true>(a, stream);
   if (e != hipSuccess || !(a.dweight || a.dbias)) return e;
-  const int total = a.weight_groups * 2 * a.d;
-  hipLaunchKernelGGL(parts_kernel, dim3((total + 3) / 4), dim3(kThreads), 0, stream, a);
+  const int blocks = (a.weight_groups * 2 * a.d + 3) / 4;
+  hipLaunchKernelGGL(parts_kernel, dim3(blocks < kPartsBlocks ? blocks : kPartsBlocks), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
