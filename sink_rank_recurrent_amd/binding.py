@@ -476,6 +476,8 @@ def _prefill(state, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream) -> t
                         dtype=torch.float32)
         sequence.seed_scan(state.rule, q, k, v, g, beta, o, S, S0=S0, cu_seqlens=cu_seqlens,
                            workspace=workspace, stream=stream)
+        if isinstance(state, ScheduledState):
+            state._start_again()
         state.from_dense(S, stream)
     return S
 
@@ -794,8 +796,21 @@ class ScheduledState:
         to `o`) and convert the states behind them (from_dense).  The arrays
         are [batch, length, heads, d], or packed [tokens, heads, d] with
         cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
-        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        prompts.  Returns the dense states [batch, heads, d_k, d_v].  The next
+        step is step 0 of the schedule again, with every window empty."""
         return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
+
+    def _start_again(self) -> None:
+        """Back to before step 0: snapshots that wait for their compression
+        are dropped, and the current stream is ordered after those launched
+        (they write the kept buffers)."""
+        if self.pending:
+            cur = torch.cuda.current_stream(self.a.device)
+            for side in self.sides:
+                cur.wait_stream(side)
+        self.pending = {}
+        self._acc = []
+        self.t = 0
 
     def held_columns(self, b: int, t=None) -> int:
         """Columns request b holds before step t (default: the next step)."""
