@@ -52,6 +52,8 @@ extern "C" {
  * gates of 1 or keys that point one way.  A NaN or infinity of a token
  * reaches its sequence's state and read-outs from the first token of its 64
  * on, and no other sequence.
+ * Outputs and the workspace must not overlap inputs (cu_seqlens is one) or
+ * each other (S may be S0).
  * 1 <= key_heads <= heads, heads a multiple of key_heads, heads <= 65535;
  * d_k, d_v as in seed.h.
  */
@@ -67,8 +69,8 @@ seed_status seed_scan(int rule, int n_seq, int heads, int key_heads, int d_k, in
  * NULL for Mamba-2), dS0 may be NULL.  dq and dk of a shared key head are
  * the sums over its heads, in fp32, rounded once.  Nothing from seed_scan is
  * needed: the states are run again.  Rows outside every sequence are left as
- * they were.  Gradients must not overlap inputs or each other (dS0 may be
- * dS).
+ * they were.  Gradients and the workspace must not overlap inputs or each
+ * other (dS0 may be dS).
  */
 seed_status seed_scan_backward(int rule, int n_seq, int heads, int key_heads, int d_k, int d_v,
                                int tokens, const int *cu_seqlens, const void *q, const void *k,

@@ -226,8 +226,9 @@ seed_status seed_scan(int rule, int n_seq, int heads, int key_heads, int d_k, in
                      {"v", v, T * heads * d_v * e},
                      {"g", g, T * heads * (rule == SEED_RULE_KDA ? d_k : 1) * 4},
                      {"beta", beta, T * heads * 4},
-                     {"S0", S == S0 ? nullptr : S0, state}};
-  SEED_TRY(check_overlap(fn, out, 3, in, 6));
+                     {"S0", S == S0 ? nullptr : S0, state},
+                     {"cu_seqlens", cu_seqlens, ((size_t)n_seq + 1) * sizeof(int)}};
+  SEED_TRY(check_overlap(fn, out, 3, in, 7));
   seed::ScanArgs a = scan_args(rule, n_seq, heads, key_heads, d_k, d_v, tokens, cu_seqlens, q, k, v,
                                in_dtype, g, beta, S0, workspace, false);
   a.o = o;
@@ -264,8 +265,9 @@ seed_status seed_scan_backward(int rule, int n_seq, int heads, int key_heads, in
                       {"workspace", workspace, workspace_bytes}};
   const Part in[] = {{"q", q, keys}, {"k", k, keys}, {"v", v, values}, {"g", g, gates},
                      {"beta", beta, T * heads * 4}, {"S0", S0, state}, {"dO", dO, values},
-                     {"dS", dS0 == dS ? nullptr : dS, state}};
-  SEED_TRY(check_overlap(fn, out, 7, in, 8));
+                     {"dS", dS0 == dS ? nullptr : dS, state},
+                     {"cu_seqlens", cu_seqlens, ((size_t)n_seq + 1) * sizeof(int)}};
+  SEED_TRY(check_overlap(fn, out, 7, in, 9));
   seed::ScanArgs a = scan_args(rule, n_seq, heads, key_heads, d_k, d_v, tokens, cu_seqlens, q, k, v,
                                in_dtype, g, beta, S0, workspace, true);
   a.dO = dO;
