@@ -388,14 +388,17 @@ hipError_t chain(const ScanArgs& a, int what, hipStream_t stream) {
   constexpr size_t save = 2 * Stage<RULE, DK, false, false>::bytes + own;
   constexpr size_t back = 2 * Stage<RULE, DK, true, true>::bytes + own;
   static_assert(read <= 160 * 1024 && save <= 160 * 1024 && back <= 160 * 1024, "LDS of a CU");
+  // (segments are walked by four waves: walk_waves)
+  if constexpr (NW == 4) {
+    if (what == 3)
+      return launch(chain_forward_kernel<RULE, DK, NW, kCarry>, a, a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
+    if (what == 4) return launch(chain_reverse_kernel<RULE, DK, NW, true>, a, a.d_v, NW, back, stream);
+  }
   switch (what) {
     case 0: return launch(chain_forward_kernel<RULE, DK, NW, kRead>, a, a.d_v, NW, read, stream);
     case 1: return launch(chain_forward_kernel<RULE, DK, NW, kSave>, a, a.d_v, NW, save, stream);
     case 2: return launch(chain_reverse_kernel<RULE, DK, NW, false>, a, a.d_v, NW, back, stream);
-    case 3:
-      return launch(chain_forward_kernel<RULE, DK, NW, kCarry>, a,
-                    a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
-    default: return launch(chain_reverse_kernel<RULE, DK, NW, true>, a, a.d_v, NW, back, stream);
+    default: return hipErrorInvalidValue;
   }
 }
 template <int RULE>

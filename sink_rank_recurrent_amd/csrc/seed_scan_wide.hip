@@ -539,14 +539,17 @@ hipError_t wide(const ScanArgs& a, int what, hipStream_t stream) {
   constexpr size_t read = Wide<RULE, DK, T, true>::bytes + own, save = Wide<RULE, DK, T, false>::bytes + own;
   constexpr size_t back = WideBack<DK, RULE>::bytes + own;
   static_assert(read <= 160 * 1024 && save <= 160 * 1024 && back <= 160 * 1024, "LDS of a CU");
+  // (segments are walked by four waves: walk_waves)
+  if constexpr (NW == 4) {
+    if (what == 3)
+      return launch(wide_forward_kernel<RULE, DK, NW, T, kCarry>, a, a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
+    if (what == 4) return launch(wide_reverse_kernel<RULE, DK, NW, T, true>, a, a.d_v, NW, back, stream);
+  }
   switch (what) {
     case 0: return launch(wide_forward_kernel<RULE, DK, NW, T, kRead>, a, a.d_v, NW, read, stream);
     case 1: return launch(wide_forward_kernel<RULE, DK, NW, T, kSave>, a, a.d_v, NW, save, stream);
     case 2: return launch(wide_reverse_kernel<RULE, DK, NW, T, false>, a, a.d_v, NW, back, stream);
-    case 3:
-      return launch(wide_forward_kernel<RULE, DK, NW, T, kCarry>, a,
-                    a.d_v + (RULE != kMAMBA2 ? DK : 0), NW, save, stream);
-    default: return launch(wide_reverse_kernel<RULE, DK, NW, T, true>, a, a.d_v, NW, back, stream);
+    default: return hipErrorInvalidValue;
   }
 }
 template <int RULE, typename T>
