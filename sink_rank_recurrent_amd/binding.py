@@ -471,6 +471,7 @@ def _prefill(state, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream) -> t
     converted into `state`; returns the dense states."""
     from . import sequence   # it imports this module
 
+    caller = None if stream is None else torch.cuda.current_stream(state.a.device)
     with torch.cuda.device(state.a.device), torch.cuda.stream(stream):
         S = torch.empty(state.batch, state.heads, state.d_k, state.d_v, device=state.a.device,
                         dtype=torch.float32)
@@ -479,6 +480,8 @@ def _prefill(state, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream) -> t
         if isinstance(state, ScheduledState):
             state._start_again()
         state.from_dense(S, stream)
+    if stream != caller:
+        S.record_stream(caller)   # from the pool of `stream`, read by the caller
     return S
 
 
