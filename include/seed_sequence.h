@@ -51,7 +51,8 @@ extern "C" {
  * type: the last state of 512 tokens is within 1e-6 of its norm, also with
  * gates of 1 or keys that point one way.  A NaN or infinity of a token
  * reaches its sequence's state and read-outs from the first token of its 64
- * on, and no other sequence.
+ * on, and no other sequence.  A finite float32 above 3.39e38, where bf16 ends,
+ * counts as one.
  * Outputs and the workspace must not overlap inputs (cu_seqlens is one) or
  * each other (S may be S0).
  * 1 <= key_heads <= heads, heads a multiple of key_heads, heads <= 65535;

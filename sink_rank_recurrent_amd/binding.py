@@ -530,7 +530,9 @@ class ShallowState:
         to `o`) and convert the states behind them (from_dense).  The arrays
         are [batch, length, heads, d], or packed [tokens, heads, d] with
         cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
-        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        prompts.  Returns the dense states [batch, heads, d_k, d_v].  (A graph that
+        captured this call repeats its device work only: the column counts
+        are set when it is called.)"""
         return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def step(self, q, k, v, g, beta, o, stream=None) -> None:
@@ -661,7 +663,9 @@ class ShallowState16:
         to `o`) and convert the states behind them (from_dense).  The arrays
         are [batch, length, heads, d], or packed [tokens, heads, d] with
         cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
-        prompts.  Returns the dense states [batch, heads, d_k, d_v]."""
+        prompts.  Returns the dense states [batch, heads, d_k, d_v].  (A graph that
+        captured this call repeats its device work only: the column counts
+        are set when it is called.)"""
         return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def step(self, q, k, v, g, beta, o, stream=None) -> None:
@@ -800,7 +804,8 @@ class ScheduledState:
         are [batch, length, heads, d], or packed [tokens, heads, d] with
         cu_seqlens [batch + 1]; S0 [batch, heads, d_k, d_v] continues earlier
         prompts.  Returns the dense states [batch, heads, d_k, d_v].  The next
-        step is step 0 of the schedule again, with every window empty."""
+        step is step 0 of the schedule again, with every window empty.  (A
+        graph that captured this call repeats its device work only.)"""
         return _prefill(self, q, k, v, g, beta, o, S0, cu_seqlens, workspace, stream)
 
     def _start_again(self) -> None:

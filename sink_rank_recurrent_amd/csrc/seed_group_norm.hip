@@ -8,14 +8,16 @@
 //   dh = rstd (dhat - mean(dhat) [centered] - hat mean(dhat hat)).
 // Everything between the loads and the stores is fp32.
 //
-// Bound by HBM: a team of lanes keeps a group in registers, so each input is
-// read once and each output written once; the statistics are two passes over
-// the registers.  Teams are 16 to 256 threads, by the group's width, so that
+// A team of lanes keeps a group in registers, so each input is read once and
+// each output written once; the statistics are two passes over the registers.  Teams are 16 to 256 threads, by the group's width, so that
 // a thread holds one to four 16-byte vectors of 16-bit values (32 single
-// values where d is no multiple of 8).  32768 x 16 groups of 128 bf16 values
-// take 51 us (5.2 TB/s), backwards 8192 x 16 with a gate 31 us (5.5 TB/s) and
-// 7 us for the weights' gradients; 4001 x 2 groups of 2047 float32 values
-// backwards 66 us (5.0 TB/s: single values, rows off every alignment) and 12.
+// values where d is no multiple of 8).  bf16 values of 128 channels are bound by
+// the arithmetic on them as much as by memory: 32768 x 16 groups take 51 us,
+// the VALU issuing 73 % of the time (268 MB of inputs and outputs, 201 of them
+// past the memory-side cache, 4.0 TB/s), backwards 8192 x 16 with a gate 31 us,
+// the VALU 69 %, and 7 us for the weights' gradients.  4001 x 2 groups of 2047
+// float32 values backwards take 66 us, the VALU 37 % (239 MB past the cache, 3.6
+// TB/s: single values, rows off every alignment), and 12.
 // (Sums over rows of 16 lanes by moves between lanes inside the additions and
 // the hardware's root; with exchanges through LDS and an IEEE root and
 // division 52, 32 and 73.)

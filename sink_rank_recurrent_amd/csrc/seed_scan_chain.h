@@ -252,9 +252,9 @@ __device__ __forceinline__ void unit_state(int col, f32x4 (&x)[IT]) {
 enum WalkMode { kRead = 0, kSave = 1, kCarry = 2 };
 
 // Waves of a workgroup: all of a head's columns, or half of 128 where whole
-// heads would leave some of the 256 CUs idle (backward of 64 x 32 chunks of
-// 128 x 128 GDN heads: 212 us with four waves, 253 us with eight; forward of
-// 1024 x 8 chunks: 385 us with four, 234 us with eight).
+// heads would leave some of the 256 CUs idle (64 x 32 chunks of 128 x 128 GDN
+// heads: backward 207 us with four waves, 236 with eight, forward 126 and 154;
+// forward of 1024 x 8 chunks: 391 us with four, 298 with eight).
 inline int walk_waves(const ScanArgs& a) {
   const int all = a.d_v / 16;
   return all == 8 && (a.at.seg || (long long)a.n_seq * a.heads < 256) ? 4 : all;

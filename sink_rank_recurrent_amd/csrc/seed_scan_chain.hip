@@ -7,10 +7,10 @@
 // asynchronous loads while this one is computed.
 //
 // Bound by instruction issue where the chip is full: 64 sequences x 512 tokens
-// x 16 heads of 128 x 128 forward in 210 us, the matrix cores busy 38 % and
-// the VALU 41 % of the time, 500 MB at 2.4 TB/s.  With fewer than 256
+// x 16 heads of 128 x 128 forward in 289 us, the matrix cores busy 46 % and
+// the VALU 46 % of the time, 558 MB at 1.9 TB/s.  With fewer than 256
 // workgroups (4 sequences x 2048 tokens: 128) by the chain itself, 4 us a
-// chunk forward and 6.5 backward (128 and 208 us for 32 chunks).
+// chunk forward and 6.5 backward (128 and 209 us for 32 chunks).
 //
 // Terms: three of every fp32 operand.  Two where the result only corrects u or
 // is rounded to bf16 would take 308 us instead of 361 for those 64 x 512 tokens

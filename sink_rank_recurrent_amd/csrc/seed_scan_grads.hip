@@ -338,7 +338,7 @@ __device__ __forceinline__ float lds_value(const char* planes, int t, int i) {
 // other waves' rows through LDS), then 32 channels of S and H at a time.
 //
 // Bound by latency, one workgroup a CU (its rows alone are 112 registers a
-// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 232 us, 333 MB at
+// lane): 8192 tokens x 16 heads of 128 x 128 in bf16 take 235 us, 336 MB at
 // 1.4 TB/s, matrix cores 19 % and VALU 36 % busy.  (K and Q again from memory
 // behind the states' loads, to wait for both, and the rows' pieces one after
 // the other: 269.)

@@ -123,7 +123,7 @@ struct FloatRows {
 // three terms; a wave takes its rows of Q from memory.)
 //
 // Bound by the steps' latency and the VALU, not by memory: for those 64 x 512
-// tokens x 16 heads 108 us, 360 MB moved at 3.3 TB/s, the VALU issuing half of
+// tokens x 16 heads 127 us, 461 MB moved at 3.6 TB/s, the VALU issuing half of
 // the time and the matrix cores 13 % of it; the decays are one wave's work and
 // the inverses of L's diagonal blocks 16 dependent steps.  Four workgroups a
 // CU hide part of it.
@@ -260,9 +260,9 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(ScanArgs a) {
 // G_ts = P_t / P_s channel by channel, so L and M are products of K P, Q P and
 // K / P.  That is taken where every P of the chunk lies in 2^-60 .. 2^60 (the
 // hardware reciprocal is good to a unit in the last place, 2^-23, and a masked
-// pair stays finite).  bf16 rows of K and Q come whole through LDS (172 us for
+// pair stays finite).  bf16 rows of K and Q come whole through LDS (182 us for
 // 24 ragged sequences of 7919 tokens in all, 32 heads of 128 x 128; loads of
-// the lanes' own 64-byte pieces and an IEEE division: 202).  Chunks with
+// the lanes' own 64-byte pieces and an IEEE division cost 30 more).  Chunks with
 // smaller decays, zeros among them, are summed pair by pair (slow_triangles).
 
 // The product over the lanes of a row of 16 up to (and with) this one.

@@ -12,11 +12,11 @@
 // vectors lets the next chunk's be loaded while the state is brought up.
 //
 // Bound as there: 24 ragged sequences of 7919 tokens x 32 heads with gates per
-// channel take 245 us forward (matrix cores 29 %, VALU 31 % busy, 2.2 TB/s:
+// channel take 306 us forward (matrix cores 40 %, VALU 37 % busy, 1.5 TB/s:
 // the longest sequences' workgroups run on alone); 5 sequences of 3001 tokens
-// x 16 heads 140 us forward and 204 us backward in 160 workgroups, the
+// x 16 heads 137 us forward and 205 us backward in 160 workgroups, the
 // chain's latency.  float32, 16384 tokens x 16 heads of 64 x 64 in segments of
-// 16 chunks: 96 us for the segments' carries and 104 us for the read-outs.
+// 16 chunks: 99 us for the segments' carries and 105 us for the read-outs.
 #include "seed_scan_chain.h"
 
 namespace seed {
@@ -29,7 +29,7 @@ constexpr int kShare = kC * DK / 8 / THREADS;
 template <int DK, int THREADS, typename T>
 struct Share {
   Piece<T> x[kShare<DK, THREADS>];
-  // rows from n on are 0 (`pad`: hold no rows past the array)
+  // rows from n on are 0
   __device__ __forceinline__ void load(const T* base, size_t ld, int n) {
 #pragma unroll
     for (int i = 0; i < kShare<DK, THREADS>; ++i) {

@@ -6,7 +6,8 @@ pass.  As in ``binding``, every function takes torch tensors in device
 memory, checks their shapes, and passes raw pointers to the C ABI (declared
 in include/seed_sequence.h) on torch's current stream of the tensors'
 device; all arithmetic happens in the HIP kernels.  A workspace that is not
-given is allocated for the call.
+given is allocated for the call.  Nothing is recorded for autograd, whether the
+tensors require gradients or not: the backward passes are calls of their own.
 """
 from __future__ import annotations
 
@@ -82,24 +83,23 @@ class _On:
             self.guard.__exit__(*error)
 
 
-def _scan_shape(rule: str, q, v, cu_seqlens, n_seq=None):
+def _scan_shape(rule: str, q, v, cu_seqlens):
     """(n_seq, tokens, leading shape, heads, key_heads, d_k, d_v) of a call:
     [tokens, heads, d] arrays with cu_seqlens, [n_seq, length, heads, d]
     arrays without."""
     if rule not in RULES:
         raise ValueError(f"unknown rule {rule!r}")
-    want = 3 if cu_seqlens is not None or n_seq is not None else 4
+    want = 3 if cu_seqlens is not None else 4
     if v.dim() != want or q.dim() != want:
         raise ValueError(f"q and v must have {want} dimensions (packed [tokens, heads, d] with "
                          f"cu_seqlens, [sequences, length, heads, d] without)")
     lead = tuple(v.shape[:-2])
-    if n_seq is None:
-        if cu_seqlens is not None:
-            if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-                raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
-            n_seq = cu_seqlens.shape[0] - 1
-        else:
-            n_seq = lead[0]
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
+        n_seq = cu_seqlens.shape[0] - 1
+    else:
+        n_seq = lead[0]
     tokens = 1
     for x in lead:
         tokens *= x
