@@ -1,0 +1,332 @@
+// The selective state space scan over sequences (formulas in seed_select.h),
+// and its step for single tokens.
+#include "seed_select.h"
+
+namespace seed {
+namespace channels {
+namespace {
+
+constexpr int kThreads = 64 * kWaves;
+
+// B and C of every token in fp32, padded with zeros to whole sixteens.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
+  const int NP = a.at.waves * kStates;
+  float* out = reinterpret_cast<float*>(a.ws + a.at.rows);
+  const size_t total = (size_t)a.tokens * a.groups * 2 * NP, step = (size_t)gridDim.x * kThreads;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
+    const int n = (int)(i % NP), what = (int)(i / NP & 1);
+    const size_t tg = i / (2 * NP), t = tg / a.groups;
+    const int g = (int)(tg - t * a.groups);
+    float x = 0.f;
+    if (n < a.d_state) x = load_scalar(row_of<T>(what ? a.C : a.B, (long long)t) + (size_t)g * a.d_state + n);
+    out[i] = x;
+  }
+}
+
+enum Mode { kWhole = 0, kCarry = 1, kRead = 2 };
+
+// MODE kWhole: a sequence from its first state to its last; kCarry: what a
+// segment leaves of zero, and the sum of its steps; kRead: a segment's
+// read-outs from its first state.
+template <typename T, int SB, int MODE>
+__global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
+  __shared__ float part[SB > 1 ? kWaves * kTile * 64 : 1];
+  const Mine m = mine<SB>(a, blockIdx.y);
+  const int lane = (int)__lane_id(), c = m.c;
+  const Batch b = batch_of(a.cu, a.n_seq, a.tokens, MODE == kWhole ? 0 : a.at.shift);
+  int t0, t1;
+  if (MODE == kWhole) {
+    const int s = blockIdx.x;
+    t0 = first_token(b, s);
+    t1 = b.cu ? first_token(b, s + 1) : t0 + b.len;
+  } else {
+    const Run r = run_of(b, sequence_of(b, blockIdx.x), blockIdx.x);
+    t0 = r.t0;
+    t1 = r.t1;
+    if (t0 >= t1) return;
+  }
+  float A[kStates], h[kStates];
+  load_rates<SB>(a, m, A);
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
+  float* carry = reinterpret_cast<float*>(a.ws + a.at.carry);
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) {
+    const int n = m.sb * kStates + i;
+    h[i] = 0.f;
+    if (MODE == kWhole && a.S0 && n < a.d_state) h[i] = a.S0[state_at(a, blockIdx.x, c) + n];
+    // (a padding state's carry is not a first state: join leaves it as it is)
+    if (MODE == kRead && n < a.d_state) h[i] = carry[carry_at<SB>(a, blockIdx.x, n, c)];
+  }
+  float gone = 0.f;
+  const bool gate = MODE != kCarry && a.z.p != nullptr;
+  for (int t = t0; t < t1; t += kTile) {
+    T xr[kTile], dr[kTile], zr[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int at = t + j < t1 ? t + j : t1 - 1;
+      xr[j] = row_of<T>(a.x, at)[c];
+      dr[j] = row_of<T>(a.dt, at)[c];
+      if (gate) zr[j] = row_of<T>(a.z, at)[c];
+    }
+    float y[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      y[j] = 0.f;
+      if (t + j >= t1) continue;
+      const float x = load_scalar(&xr[j]);
+      const float delta = Step{load_scalar(&dr[j]) + bias}.of(a.softplus), u = delta * x;
+      const ScalarRow B = row_bc<SB>(a, m, t + j), C = B + SB * kStates;
+      if (MODE == kCarry) gone += delta;
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kStates; ++i) {
+        h[i] = exp2_fast(delta * A[i]) * h[i] + u * B[i];
+        if (MODE != kCarry) s[i & 1] += C[i] * h[i];
+      }
+      y[j] = s[0] + s[1];
+      if (m.sb == 0) y[j] += D * x;
+    }
+    if (MODE == kCarry) continue;
+    if constexpr (SB > 1) {
+      // the waves of a block of channels add up in order; the first one writes
+      const int wave = threadIdx.x >> 6;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) part[(wave * kTile + j) * 64 + lane] = y[j];
+      __syncthreads();
+      if (m.sb != 0) continue;
+#pragma unroll
+      for (int j = 0; j < kTile; ++j)
+#pragma unroll
+        for (int o = 1; o < SB; ++o) y[j] += part[((wave + o) * kTile + j) * 64 + lane];
+    }
+    if (!m.live) continue;
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      if (t + j >= t1) continue;
+      if (gate) {
+        const float z = load_scalar(&zr[j]);
+        y[j] *= z * sigmoid(z);
+      }
+      float one[1] = {y[j]};
+      Packed<1, T> out;
+      out.from(one);
+      out.store(row_of<T>(a.y, t + j) + c);
+    }
+  }
+  if (!m.live || MODE == kRead) return;
+#pragma unroll
+  for (int i = 0; i < kStates; ++i) {
+    const int n = m.sb * kStates + i;
+    if (MODE == kCarry) carry[carry_at<SB>(a, blockIdx.x, n, c)] = h[i];
+    else if (n < a.d_state) a.S[state_at(a, blockIdx.x, c) + n] = h[i];
+  }
+  if (MODE == kCarry && m.sb == 0)
+    reinterpret_cast<float*>(a.ws + a.at.gone)[(size_t)blockIdx.x * a.channels + c] = gone;
+}
+
+// The segments' first states, h' = exp(A gone) h + carry, in the carries'
+// places, and S; backwards also the gradients at the segments' ends, G' =
+// exp(A gone) G + back, in theirs, and dS0.  A thread is a state of a channel
+// of a sequence.
+template <bool BACK>
+__global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
+  const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = a.at.waves * kStates;
+  if (c >= a.channels) return;
+  const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
+  const float A = a.A[(size_t)c * a.d_state + n] * kLog2e;
+  const float* gone = reinterpret_cast<const float*>(a.ws + a.at.gone);
+  for (int s = blockIdx.z; s < a.n_seq; s += gridDim.z) {
+    const int first = first_run(b, s), lo = first_token(b, s);
+    const int end = b.cu ? first_token(b, s + 1) : lo + b.len;
+    const int len = end > lo ? end - lo : 0, runs = (len + (1 << a.at.shift) - 1) >> a.at.shift;
+    const size_t user = state_at(a, s, c) + n, step = (size_t)NP * a.channels;
+    float* carry = reinterpret_cast<float*>(a.ws + a.at.carry) + (size_t)first * step + (size_t)n * a.channels + c;
+    const float* g = gone + (size_t)first * a.channels + c;
+    float h = a.S0 ? a.S0[user] : 0.f;
+    for (int r = 0; r < runs; ++r) {
+      const float made = carry[r * step];
+      carry[r * step] = h;
+      h = exp2_fast(A * g[(size_t)r * a.channels]) * h + made;
+    }
+    if (!BACK) a.S[user] = h;
+    if (BACK) {
+      float* back = reinterpret_cast<float*>(a.ws + a.at.back) + (size_t)first * step + (size_t)n * a.channels + c;
+      float G = a.dS ? a.dS[user] : 0.f;
+      for (int r = runs - 1; r >= 0; --r) {
+        const float made = back[r * step];
+        back[r * step] = G;
+        G = exp2_fast(A * g[(size_t)r * a.channels]) * G + made;
+      }
+      if (a.dS0) a.dS0[user] = G;
+    }
+  }
+}
+
+// One token: LP lanes share a channel's states, four each.
+template <typename T, int LP>
+__global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
+  const int per = kThreads / LP, part = threadIdx.x % LP;
+  const int c = (int)blockIdx.x * per + threadIdx.x / LP;
+  const int at = c < a.channels ? c : a.channels - 1, g = at / (a.channels / a.groups);
+  const int n0 = part * 4, N = a.d_state;
+  float A[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = n0 + i < N ? a.A[(size_t)at * N + n0 + i] * kLog2e : 0.f;
+  const float bias = a.dt_bias ? a.dt_bias[at] : 0.f, D = a.D ? a.D[at] : 0.f;
+  for (int b = blockIdx.y; b < a.n_seq; b += gridDim.y) {
+    const size_t state = state_at(a, b, at) + n0;
+    float h[4], B[4], C[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool there = n0 + i < N;
+      h[i] = there ? a.S0[state + i] : 0.f;
+      B[i] = there ? load_scalar(row_of<T>(a.B, b) + (size_t)g * N + n0 + i) : 0.f;
+      C[i] = there ? load_scalar(row_of<T>(a.C, b) + (size_t)g * N + n0 + i) : 0.f;
+    }
+    const float x = load_scalar(row_of<T>(a.x, b) + at);
+    const float delta = Step{load_scalar(row_of<T>(a.dt, b) + at) + bias}.of(a.softplus), u = delta * x;
+    const float z = a.z.p ? load_scalar(row_of<T>(a.z, b) + at) : 0.f;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = exp2_fast(delta * A[i]) * h[i] + u * B[i];
+      s += C[i] * h[i];
+    }
+#pragma unroll
+    for (int o = 1; o < LP; o *= 2) s += __shfl_xor(s, o);
+    if (c >= a.channels) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + i < N) a.S[state + i] = h[i];
+    if (part != 0) continue;
+    float y[1] = {s + D * x};
+    if (a.z.p) y[0] *= z * sigmoid(z);
+    Packed<1, T> out;
+    out.from(y);
+    out.store(row_of<T>(a.y, b) + at);
+  }
+}
+
+int blocks_of(int channels, int groups, int waves) {
+  const int each = channels / groups, per = 64 * kWaves / waves;
+  return (each + per - 1) / per;
+}
+
+template <typename T, int SB>
+hipError_t scan_types(const SelectArgs& a, hipStream_t stream) {
+  const unsigned along = (unsigned)(a.groups * a.at.blocks);
+  if (a.at.shift < 0) {
+    hipLaunchKernelGGL((scan_kernel<T, SB, kWhole>), dim3(a.n_seq, along), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((scan_kernel<T, SB, kCarry>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = launch_select_join(a, false, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((scan_kernel<T, SB, kRead>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace channels
+
+using namespace channels;
+
+SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int tokens, bool backward) {
+  SelectLayout l{};
+  l.waves = d_state <= kStates ? 1 : d_state <= 2 * kStates ? 2 : 4;
+  l.blocks = blocks_of(channels, groups, l.waves);
+  const long long along = (long long)groups * l.blocks;
+  // Forward: whole sequences where they fill half the chip; segments else
+  // (the first pass computes every decay a second time).
+  if (backward) l.shift = 6;
+  else l.shift = n_seq * along * kWaves >= 512 || tokens / n_seq <= 64 ? -1 : 7;
+  const size_t NP = (size_t)l.waves * kStates, T = (size_t)tokens;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return here;
+  };
+  l.rows = take(T * groups * 2 * NP * 4);
+  if (l.shift >= 0) {
+    l.slots = (tokens >> l.shift) + n_seq;
+    l.carry = take(l.slots * NP * channels * 4);
+    l.gone = take((size_t)l.slots * channels * 4);
+  }
+  if (backward) {
+    l.back = take(l.slots * NP * channels * 4);
+    l.sums = take((size_t)l.blocks * T * groups * 2 * NP * 4);
+    const long long most = (1024 + along - 1) / along;
+    l.parts = (int)(l.slots < most ? l.slots : most);
+    l.weights = take((size_t)l.parts * (NP + 2) * channels * 4);
+  }
+  l.bytes = at;
+  return l;
+}
+
+// Grids: blocks of channels along y, sequences or segments of 64 along x with
+// 256 threads each.
+bool select_fits(int n_seq, int channels, int groups, int d_state, int tokens) {
+  const int waves = d_state <= kStates ? 1 : d_state <= 2 * kStates ? 2 : 4;
+  return (long long)groups * blocks_of(channels, groups, waves) <= 65535 &&
+         (long long)(tokens >> 6) + n_seq < (1LL << 24) && (long long)tokens + 64 <= 0x7fffffffLL;
+}
+
+hipError_t launch_select_prepare(const SelectArgs& a, hipStream_t stream) {
+  const size_t total = (size_t)a.tokens * a.groups * 2 * a.at.waves * kStates;
+  const size_t blocks = (total + kThreads - 1) / kThreads;
+  const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
+  if (a.bf16) hipLaunchKernelGGL((prepare_kernel<bf16_t>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((prepare_kernel<float>), grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_select_join(const SelectArgs& a, bool backward, hipStream_t stream) {
+  const dim3 grid((a.channels + kThreads - 1) / kThreads, a.d_state, a.n_seq < 65535 ? a.n_seq : 65535);
+  if (backward) hipLaunchKernelGGL((join_kernel<true>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((join_kernel<false>), grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_select(const SelectArgs& a, hipStream_t stream) {
+  if (a.tokens == 0) {   // S = S0
+    SelectArgs none = a;
+    none.at.shift = 0;
+    return launch_select_join(none, false, stream);
+  }
+  const hipError_t e = launch_select_prepare(a, stream);
+  if (e != hipSuccess) return e;
+#define SEED_SCAN(T)                                          \
+  (a.at.waves == 1   ? scan_types<T, 1>(a, stream)            \
+   : a.at.waves == 2 ? scan_types<T, 2>(a, stream)            \
+                     : scan_types<T, 4>(a, stream))
+  return a.bf16 ? SEED_SCAN(bf16_t) : SEED_SCAN(float);
+#undef SEED_SCAN
+}
+
+hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream) {
+  // up to 8 requests a block: the rates stay in registers
+  const int most = (a.n_seq + 7) / 8;
+#define SEED_STEP(T, LP)                                                                              \
+  hipLaunchKernelGGL((step_kernel<T, LP>),                                                            \
+                     dim3((a.channels + kThreads / LP - 1) / (kThreads / LP), most < 65535 ? most : 65535), \
+                     dim3(kThreads), 0, stream, a)
+#define SEED_STEPS(T)                       \
+  do {                                      \
+    if (a.d_state <= 4) SEED_STEP(T, 1);    \
+    else if (a.d_state <= 8) SEED_STEP(T, 2);  \
+    else if (a.d_state <= 16) SEED_STEP(T, 4); \
+    else if (a.d_state <= 32) SEED_STEP(T, 8); \
+    else SEED_STEP(T, 16);                  \
+  } while (0)
+  if (a.bf16) SEED_STEPS(bf16_t);
+  else SEED_STEPS(float);
+#undef SEED_STEPS
+#undef SEED_STEP
+  return hipGetLastError();
+}
+
+}  // namespace seed

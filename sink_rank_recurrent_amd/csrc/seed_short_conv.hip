@@ -1,0 +1,373 @@
+// Short causal convolution of each channel, its backward pass, and its step
+// for single tokens.  With K taps, inputs before a sequence from its S0:
+//   pre_t = b + sum_j w_j x_{t - (K - 1) + j},   y_t = act(pre_t)
+// and backwards, with e_t = dy_t act'(pre_t):
+//   dx_t = sum_j w_j e_{t + (K - 1) - j} (+ dS where x_t is kept in S),
+//   dw_j = sum_t e_t x_{t - (K - 1) + j},   db = sum_t e_t.
+//
+// 2 K + 5 operations a value against 4 (bf16) or 8 bytes: memory.  A thread
+// keeps VW neighbouring channels (16 bytes) and walks a run of tokens with the
+// last K - 1 inputs in registers, so that inside a run each input is read
+// once; K - 1 rows are read again at the run's start.
+#include "seed_channels.h"
+
+namespace seed {
+namespace channels {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStepRows = 4;     // tokens whose loads are on their way together
+
+// Weights of a thread's channels, tap by tap.
+template <int K, int VW>
+__device__ __forceinline__ void load_weights(const ConvArgs& a, int c, float (&w)[K][VW], float (&b)[VW]) {
+  float t[VW * K];
+  const float* p = a.weight + (size_t)c * K;
+#pragma unroll
+  for (int i = 0; i < VW * K; ++i) t[i] = p[i];
+#pragma unroll
+  for (int v = 0; v < VW; ++v) {
+    b[v] = a.bias ? a.bias[c + v] : 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][v] = t[v * K + j];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const Rows& r, long long t) {
+  return static_cast<const T*>(r.p) + t * r.stride;
+}
+template <typename T>
+__device__ __forceinline__ T* row_of(const OutRows& r, long long t) {
+  return static_cast<T*>(r.p) + t * r.stride;
+}
+
+// The K - 1 inputs before token t0 of run r: x, S0 or zero.
+template <int K, int VW, typename T>
+__device__ __forceinline__ void inputs_before(const ConvArgs& a, const Run& r, int c, Packed<VW, T> (&held)[K - 1]) {
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) {
+    const int t = r.t0 - (K - 1) + i;
+    held[i].zero();
+    if (t >= r.lo) held[i].load(row_of<T>(a.x, t) + c);
+    else if (a.S0)
+      held[i].load(static_cast<const T*>(a.S0) + ((size_t)r.seq * (K - 1) + (K - 1 + t - r.lo)) * a.channels + c);
+  }
+}
+
+// The thread's run: threads side by side along the channels (tx of them), then
+// along the runs.
+struct Place {
+  int c, run;
+  bool live;
+};
+template <int VW>
+__device__ __forceinline__ Place place(int channels, int tx, int runs) {
+  const int lane = threadIdx.x & (tx - 1), row = threadIdx.x / tx;
+  const long long run = (long long)blockIdx.x * (kThreads / tx) + row;
+  Place p;
+  p.c = ((int)blockIdx.y * tx + lane) * VW;
+  p.run = run < runs ? (int)run : runs - 1;
+  p.live = p.c < channels && run < runs;
+  return p;
+}
+// Its sequence: the wave looks for that of its first thread; runs of a wave
+// follow each other.
+__device__ __forceinline__ int sequence_near(const Batch& b, int run) {
+  int s = sequence_of(b, __builtin_amdgcn_readfirstlane(run));
+  while (s + 1 < b.n_seq && first_run(b, s + 1) <= run) ++s;
+  return s;
+}
+
+template <int K, int VW, typename T>
+__global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, int runs, int tx) {
+  const Batch b = batch_of(a.cu, a.n_seq, a.tokens, shift);
+  const Place at = place<VW>(a.channels, tx, runs);
+  const Run r = run_of(b, sequence_near(b, at.run), at.run);
+  if (!at.live || (r.t0 >= r.t1 && !r.first)) return;
+  const int c = at.c;
+  float w[K][VW], bias[VW], x[K][VW];
+  load_weights<K, VW>(a, c, w, bias);
+  Packed<VW, T> held[K - 1];
+  inputs_before<K>(a, r, c, held);
+  if (r.first && a.S) {
+    // what the sequence leaves: this thread has read S0's inputs (S may lie there)
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+      const int t = r.hi - (K - 1) + i;
+      Packed<VW, T> s;
+      s.zero();
+      if (t >= r.lo) s.load(row_of<T>(a.x, t) + c);
+      else {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+          if (k == K - 1 + t - r.lo) s = held[k];
+      }
+      s.store(static_cast<T*>(a.S) + ((size_t)r.seq * (K - 1) + i) * a.channels + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) held[i].floats(x[i]);
+  for (int t = r.t0; t < r.t1; t += kStepRows) {
+    Packed<VW, T> in[kStepRows];
+#pragma unroll
+    for (int j = 0; j < kStepRows; ++j)
+      in[j].load(row_of<T>(a.x, t + j < r.t1 ? t + j : r.t1 - 1) + c);
+#pragma unroll
+    for (int j = 0; j < kStepRows; ++j) {
+      if (t + j >= r.t1) break;
+      in[j].floats(x[K - 1]);
+      float y[VW];
+#pragma unroll
+      for (int v = 0; v < VW; ++v) {
+        y[v] = bias[v];
+#pragma unroll
+        for (int k = 0; k < K; ++k) y[v] += w[k][v] * x[k][v];
+        if (a.silu) y[v] *= sigmoid(y[v]);
+      }
+      Packed<VW, T> out;
+      out.from(y);
+      out.store(row_of<T>(a.y, t + j) + c);
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+        for (int v = 0; v < VW; ++v) x[k][v] = x[k + 1][v];
+    }
+  }
+}
+
+// A thread walks every gridDim.x-th run and keeps its part of the weights'
+// gradients; the parts are summed in a fixed order by sums_kernel.
+template <int K, int VW, typename T>
+__global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int shift, int runs, int tx, int parts) {
+  const Batch b = batch_of(a.cu, a.n_seq, a.tokens, shift);
+  const Place at = place<VW>(a.channels, tx, parts);
+  const int c = at.c;
+  float w[K][VW], bias[VW], dw[K][VW], db[VW];
+  if (at.live) load_weights<K, VW>(a, c, w, bias);
+#pragma unroll
+  for (int v = 0; v < VW; ++v) {
+    db[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) dw[k][v] = 0.f;
+  }
+  for (int base = 0; base < runs; base += parts) {   // the wave's lanes together
+    const int run = base + at.run < runs ? base + at.run : runs - 1;
+    const Run r = run_of(b, sequence_near(b, run), run);
+    if (!at.live || base + at.run >= runs || (r.t0 >= r.t1 && !r.first)) continue;
+    float x[K][VW], e[K][VW];   // e[K - 1]: token t
+    Packed<VW, T> held[K - 1];
+    inputs_before<K>(a, r, c, held);
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+      held[i].floats(x[i]);
+#pragma unroll
+      for (int v = 0; v < VW; ++v) e[i + 1][v] = 0.f;
+    }
+    const int end = r.t1 + K - 1;   // the run's last inputs reach K - 1 tokens on
+    for (int t = r.t0; t < end; t += kStepRows) {
+      Packed<VW, T> in[kStepRows], dy[kStepRows];
+#pragma unroll
+      for (int j = 0; j < kStepRows; ++j) {
+        in[j].zero();
+        dy[j].zero();
+        if (t + j < r.hi && t + j < end) {
+          in[j].load(row_of<T>(a.x, t + j) + c);
+          dy[j].load(row_of<T>(a.dy, t + j) + c);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kStepRows; ++j) {
+        if (t + j >= end) break;
+        const int now = t + j, back = now - (K - 1);
+        in[j].floats(x[K - 1]);
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+          for (int v = 0; v < VW; ++v) e[k][v] = e[k + 1][v];
+        float d[VW], dx[VW];
+        dy[j].floats(d);
+#pragma unroll
+        for (int v = 0; v < VW; ++v) {
+          if (a.silu) {
+            float pre = bias[v];
+#pragma unroll
+            for (int k = 0; k < K; ++k) pre += w[k][v] * x[k][v];
+            const float s = sigmoid(pre);
+            d[v] *= s + pre * s * (1.f - s);
+          }
+          e[K - 1][v] = now < r.hi ? d[v] : 0.f;
+          dx[v] = 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dx[v] += w[k][v] * e[K - 1 - k][v];
+        }
+        if (now < r.t1) {
+#pragma unroll
+          for (int v = 0; v < VW; ++v) {
+            db[v] += e[K - 1][v];
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k][v] += e[K - 1][v] * x[k][v];
+          }
+        }
+        // the gradient of the input K - 1 tokens back: of the run, or of S0
+        if (back >= r.t0 || r.first) {
+          const int kept = back - (r.hi - (K - 1));   // its place in S
+          if (a.dS && kept >= 0) {
+            Packed<VW, T> p;
+            float s[VW];
+            p.load(static_cast<const T*>(a.dS) + ((size_t)r.seq * (K - 1) + kept) * a.channels + c);
+            p.floats(s);
+#pragma unroll
+            for (int v = 0; v < VW; ++v) dx[v] += s[v];
+          }
+          Packed<VW, T> p;
+          p.from(dx);
+          if (back >= r.lo) p.store(row_of<T>(a.dx, back) + c);
+          else if (a.dS0)
+            p.store(static_cast<T*>(a.dS0) + ((size_t)r.seq * (K - 1) + (K - 1 + back - r.lo)) * a.channels + c);
+        }
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+          for (int v = 0; v < VW; ++v) x[k][v] = x[k + 1][v];
+      }
+    }
+  }
+  if (!at.live || !(a.dweight || a.dbias)) return;
+  float* out = a.ws + (size_t)at.run * (K + 1) * a.channels + c;
+#pragma unroll
+  for (int v = 0; v < VW; ++v) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) out[(size_t)k * a.channels + v] = dw[k][v];
+    out[(size_t)K * a.channels + v] = db[v];
+  }
+}
+
+// dweight and dbias from the parts [parts][K + 1][channels]: a block sums 64
+// channels of one of the K + 1, each of its waves every fourth part, then the
+// waves in order.
+__global__ __launch_bounds__(kThreads) void sums_kernel(ConvArgs a, int parts) {
+  __shared__ float lds[kThreads];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k = blockIdx.y;
+  const int c = (int)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < a.channels)
+    for (int p = wave; p < parts; p += 4) s += a.ws[((size_t)p * (a.width + 1) + k) * a.channels + c];
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (wave != 0 || c >= a.channels) return;
+  s = lds[lane] + lds[64 + lane] + lds[128 + lane] + lds[192 + lane];
+  if (k < a.width) {
+    if (a.dweight) a.dweight[(size_t)c * a.width + k] = s;
+  } else if (a.dbias) {
+    a.dbias[c] = s;
+  }
+}
+
+template <int K, int VW, typename T>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, int tx) {
+  const Place at = place<VW>(a.channels, tx, a.n_seq);
+  if (!at.live) return;
+  const int c = at.c;
+  float w[K][VW], bias[VW], x[K][VW], y[VW];
+  Packed<VW, T> held[K];
+  const size_t state = (size_t)at.run * (K - 1) * a.channels + c;
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) held[i].load(static_cast<const T*>(a.S0) + state + (size_t)i * a.channels);
+  held[K - 1].load(row_of<T>(a.x, at.run) + c);
+  load_weights<K, VW>(a, c, w, bias);
+#pragma unroll
+  for (int i = 0; i < K; ++i) held[i].floats(x[i]);
+#pragma unroll
+  for (int v = 0; v < VW; ++v) {
+    y[v] = bias[v];
+#pragma unroll
+    for (int k = 0; k < K; ++k) y[v] += w[k][v] * x[k][v];
+    if (a.silu) y[v] *= sigmoid(y[v]);
+  }
+  Packed<VW, T> out;
+  out.from(y);
+  out.store(row_of<T>(a.y, at.run) + c);
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) held[i + 1].store(static_cast<T*>(a.S) + state + (size_t)i * a.channels);
+}
+
+// Threads along the channels: a power of two, at most a block's.
+int threads_along(int channels, int vw) {
+  const int lanes = (channels + vw - 1) / vw;
+  int tx = 1;
+  while (tx < lanes && tx < kThreads) tx *= 2;
+  return tx;
+}
+constexpr int kRun = 5;   // log2 of a run's tokens
+int runs_of(int n_seq, int tokens) { return (tokens >> kRun) + n_seq; }
+
+template <typename F>
+hipError_t with_form(const ConvArgs& a, F f) {
+#define SEED_FORM(K)                                                        \
+  do {                                                                      \
+    if (a.bf16) {                                                           \
+      if (a.vectors) f(std::integral_constant<int, K>{}, std::integral_constant<int, 8>{}, bf16_t{}); \
+      else f(std::integral_constant<int, K>{}, std::integral_constant<int, 1>{}, bf16_t{}); \
+    } else {                                                                \
+      if (a.vectors) f(std::integral_constant<int, K>{}, std::integral_constant<int, 4>{}, float{}); \
+      else f(std::integral_constant<int, K>{}, std::integral_constant<int, 1>{}, float{}); \
+    }                                                                       \
+  } while (0)
+  if (a.width == 2) SEED_FORM(2);
+  else if (a.width == 3) SEED_FORM(3);
+  else SEED_FORM(4);
+#undef SEED_FORM
+  return hipGetLastError();
+}
+
+dim3 grid_of(int runs, int channels, int vw, int tx) {
+  const int rows = kThreads / tx, lanes = (channels + vw - 1) / vw;
+  return dim3((runs + rows - 1) / rows, (lanes + tx - 1) / tx);
+}
+
+}  // namespace
+}  // namespace channels
+
+using namespace channels;
+
+int short_conv_parts(int n_seq, int channels, int tokens) {
+  // 128 to a run each: more would add to the bytes of the sums
+  const int runs = runs_of(n_seq, tokens);
+  return runs < 128 ? runs : 128;
+}
+
+// At most 256 threads for each run and 256 channels, 2^32 in a grid's row.
+bool short_conv_fits(int n_seq, int channels, int tokens) {
+  return (long long)(tokens >> kRun) + n_seq < (1LL << 24) - 1 && (long long)tokens + 4LL < 0x7fffffffLL;
+}
+
+hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream) {
+  return with_form(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw), runs = runs_of(a.n_seq, a.tokens);
+    hipLaunchKernelGGL((conv_kernel<k, vw, decltype(t)>), grid_of(runs, a.channels, vw, tx), dim3(kThreads), 0,
+                       stream, a, kRun, runs, tx);
+  });
+}
+
+hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream) {
+  const int parts = short_conv_parts(a.n_seq, a.channels, a.tokens);
+  const hipError_t e = with_form(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw), runs = runs_of(a.n_seq, a.tokens);
+    hipLaunchKernelGGL((conv_backward_kernel<k, vw, decltype(t)>), grid_of(parts, a.channels, vw, tx),
+                       dim3(kThreads), 0, stream, a, kRun, runs, tx, parts);
+  });
+  if (e != hipSuccess || !(a.dweight || a.dbias)) return e;
+  hipLaunchKernelGGL(sums_kernel, dim3((a.channels + 63) / 64, a.width + 1), dim3(kThreads), 0, stream, a, parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_short_conv_step(const ConvArgs& a, hipStream_t stream) {
+  return with_form(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw);
+    hipLaunchKernelGGL((conv_step_kernel<k, vw, decltype(t)>), grid_of(a.n_seq, a.channels, vw, tx),
+                       dim3(kThreads), 0, stream, a, tx);
+  });
+}
+
+}  // namespace seed
