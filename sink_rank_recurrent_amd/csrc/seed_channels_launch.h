@@ -48,19 +48,24 @@ int short_conv_parts(int n_seq, int channels, int tokens);
 // Whether the grids for these sizes can be launched.
 bool short_conv_fits(int n_seq, int channels, int tokens);
 
-// Parts of the scan's workspace, in bytes from its start.
+// Parts of the scan's workspace, in bytes from its start.  A workgroup's four
+// waves share a block of 64 channels, `quarter` states of each a wave; a
+// channel's states are padded to 4 quarters.
 struct SelectLayout {
-  int waves;        // waves that share a block of 64 channels, 16 states each: 1, 2 or 4
-  int blocks;       // workgroups over a group's channels
+  int quarter;      // 2, 4, 8 or 16
+  int blocks;       // blocks of 64 channels of a group
+  int sets;         // sets of four blocks, a workgroup's (backward)
   int shift;        // log2 of a segment's tokens; -1: whole sequences (forward)
   int slots;        // segments: tokens / 2^shift + n_seq
   int parts;        // workgroups over the segments (backward)
-  size_t rows;      // B and C of each token and group in fp32, 2 x 16 waves floats
+  size_t rows;      // [token][group][wave]: B and C of its states in fp32
   size_t carry;     // [slot][state][channel]: what a segment makes of zero, then its first state
   size_t back;      // the same for the gradient: what it passes back from zero, then that at its end
   size_t gone;      // [slot][channel]: sum of the steps
-  size_t sums;      // [block][token][group][2][state]: parts of dB and dC
-  size_t weights;   // [part][state + 2][channel]: parts of dA, dD and ddt_bias
+  size_t kept;      // [8 tokens][state][channel]: what a segment makes of zero before them (backward)
+  size_t before;    // [8 tokens][channel]: sum of the steps before them
+  size_t sums;      // [set][token][group][wave]: parts of dB and dC
+  size_t weights;   // [part][state, dD, ddt_bias][channel]
   size_t bytes;
 };
 

@@ -9,11 +9,12 @@
 //   ddelta_t = x_t du_t + A.r_t,  dx_t = delta_t du_t + D ds_t
 //   ddt_t = ddelta_t softplus'(v_t),  dz_t = dy_t s_t silu'(z_t).
 //
-// A lane is a channel and keeps 16 of its states in registers, so that the
-// sums over states stay in the lane, and B and C of a token, the same for a
-// wave's channels, are scalar operands: they are read through the scalar cache
-// from fp32 rows, padded to whole sixteens (prepare_kernel).  For d_state
-// above 16, 2 or 4 waves of a workgroup share a block of channels.
+// A lane is a channel; the four waves of a workgroup have the same 64
+// channels and a quarter of the states each, in registers.  What a token needs
+// once per channel (softplus, gate, the gradients of x, dt and z) is shared
+// out among the waves, two of every eight tokens each, and goes through LDS.
+// B and C of a token are the same for a wave's lanes: they are scalar operands,
+// read through the scalar cache from fp32 rows (prepare_kernel).
 #pragma once
 
 #include "seed_channels.h"
@@ -21,9 +22,10 @@
 namespace seed {
 namespace channels {
 
-constexpr int kStates = 16;     // a lane's
 constexpr int kWaves = 4;       // of a workgroup
-constexpr int kTile = 8;        // tokens whose inputs are on their way together
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 8;        // tokens that go through LDS together
+constexpr int kOwn = kTile / kWaves;   // of them prepared by one wave
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 typedef const __attribute__((address_space(4))) float* ScalarRow;   // read by scalar loads
@@ -53,50 +55,41 @@ struct Step {
   }
 };
 
-// Which channels and states a wave of a workgroup has.
+// A wave's channels and states.
 struct Mine {
-  int group, c, sb;     // c: clamped to the group's channels
-  int block;            // the workgroup's among the group's
+  int group, c, wave;   // c: clamped to the group's channels
   bool live;
 };
-template <int SB>
-__device__ __forceinline__ Mine mine(const SelectArgs& a, int block) {
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), each = a.channels / a.groups;
-  Mine m;
-  m.group = block / a.at.blocks;
-  m.block = block - m.group * a.at.blocks;
-  m.sb = wave % SB;
-  const int in = (m.block * (kWaves / SB) + wave / SB) * 64 + (int)__lane_id();
-  m.live = in < each;
-  m.c = m.group * each + (in < each ? in : each - 1);
-  return m;
+__device__ __forceinline__ Mine mine(const SelectArgs& a, int group, int block) {
+  const int each = a.channels / a.groups, in = block * 64 + (int)__lane_id();
+  return {group, group * each + (in < each ? in : each - 1),
+          __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), in < each};
 }
 
 // Index of a state of channel c among the user's [.][channels][d_state].
 __device__ __forceinline__ size_t state_at(const SelectArgs& a, int of, int c) {
   return ((size_t)of * a.channels + c) * a.d_state;
 }
-// ... and among the workspace's [slot][16 waves states][channels].
-template <int SB>
-__device__ __forceinline__ size_t carry_at(const SelectArgs& a, int slot, int n, int c) {
-  return ((size_t)slot * (SB * kStates) + n) * a.channels + c;
+// ... and among the workspace's [.][4 Q states][channels].
+template <int Q>
+__device__ __forceinline__ size_t carry_at(const SelectArgs& a, int of, int n, int c) {
+  return ((size_t)of * (4 * Q) + n) * a.channels + c;
 }
 
 // A in powers of two: exp(delta A) = 2^(delta A log2 e).
-template <int SB>
-__device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, float (&A)[kStates]) {
+template <int Q>
+__device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, float (&A)[Q]) {
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
-    const int n = m.sb * kStates + i;
+  for (int i = 0; i < Q; ++i) {
+    const int n = m.wave * Q + i;
     A[i] = n < a.d_state ? a.A[(size_t)m.c * a.d_state + n] * kLog2e : 0.f;
   }
 }
 
-// B (and, 16 SB floats on, C) of a token for a wave's states.
-template <int SB>
+// B and, Q floats on, C of a token for a wave's states.
+template <int Q>
 __device__ __forceinline__ ScalarRow row_bc(const SelectArgs& a, const Mine& m, int t) {
-  return (ScalarRow)(uintptr_t)(a.ws + a.at.rows) +
-         ((size_t)t * a.groups + m.group) * (2 * SB * kStates) + m.sb * kStates;
+  return (ScalarRow)(uintptr_t)(a.ws + a.at.rows) + (((size_t)t * a.groups + m.group) * 4 + m.wave) * (2 * Q);
 }
 
 template <typename T>

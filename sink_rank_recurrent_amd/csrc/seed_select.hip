@@ -6,17 +6,16 @@ namespace seed {
 namespace channels {
 namespace {
 
-constexpr int kThreads = 64 * kWaves;
-
-// B and C of every token in fp32, padded with zeros to whole sixteens.
+// B and C of every token in fp32, [token][group][wave][B, C of its Q states],
+// padded with zeros.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
-  const int NP = a.at.waves * kStates;
+  const int Q = a.at.quarter;
   float* out = reinterpret_cast<float*>(a.ws + a.at.rows);
-  const size_t total = (size_t)a.tokens * a.groups * 2 * NP, step = (size_t)gridDim.x * kThreads;
+  const size_t total = (size_t)a.tokens * a.groups * 8 * Q, step = (size_t)gridDim.x * kThreads;
   for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
-    const int n = (int)(i % NP), what = (int)(i / NP & 1);
-    const size_t tg = i / (2 * NP), t = tg / a.groups;
+    const int in = (int)(i % (8 * Q)), n = in / (2 * Q) * Q + in % Q, what = in / Q & 1;
+    const size_t tg = i / (8 * Q), t = tg / a.groups;
     const int g = (int)(tg - t * a.groups);
     float x = 0.f;
     if (n < a.d_state) x = load_scalar(row_of<T>(what ? a.C : a.B, (long long)t) + (size_t)g * a.d_state + n);
@@ -26,13 +25,30 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
 
 enum Mode { kWhole = 0, kCarry = 1, kRead = 2 };
 
+// The inputs of a wave's tokens of a tile as they lie in memory.
+template <typename T>
+struct Raw {
+  T x[kOwn], dt[kOwn], z[kOwn];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int t, int t1, bool gate, Raw<T>& r) {
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const int at = t + m.wave * kOwn + o, in = at < t1 ? at : t1 - 1;
+    r.x[o] = row_of<T>(a.x, in)[m.c];
+    r.dt[o] = row_of<T>(a.dt, in)[m.c];
+    if (gate) r.z[o] = row_of<T>(a.z, in)[m.c];
+  }
+}
+
 // MODE kWhole: a sequence from its first state to its last; kCarry: what a
 // segment leaves of zero, and the sum of its steps; kRead: a segment's
 // read-outs from its first state.
-template <typename T, int SB, int MODE>
+template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
-  __shared__ float part[SB > 1 ? kWaves * kTile * 64 : 1];
-  const Mine m = mine<SB>(a, blockIdx.y);
+  __shared__ float2 prep[2][kTile][64];                           // delta, delta x
+  __shared__ float part[MODE == kCarry ? 1 : 2][kWaves][kTile][64];
+  const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
   const int lane = (int)__lane_id(), c = m.c;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, MODE == kWhole ? 0 : a.at.shift);
   int t0, t1;
@@ -46,84 +62,94 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
     t1 = r.t1;
     if (t0 >= t1) return;
   }
-  float A[kStates], h[kStates];
-  load_rates<SB>(a, m, A);
+  float A[Q], h[Q];
+  load_rates<Q>(a, m, A);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
   float* carry = reinterpret_cast<float*>(a.ws + a.at.carry);
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
-    const int n = m.sb * kStates + i;
+  for (int i = 0; i < Q; ++i) {
+    const int n = m.wave * Q + i;
     h[i] = 0.f;
     if (MODE == kWhole && a.S0 && n < a.d_state) h[i] = a.S0[state_at(a, blockIdx.x, c) + n];
     // (a padding state's carry is not a first state: join leaves it as it is)
-    if (MODE == kRead && n < a.d_state) h[i] = carry[carry_at<SB>(a, blockIdx.x, n, c)];
+    if (MODE == kRead && n < a.d_state) h[i] = carry[carry_at<Q>(a, blockIdx.x, n, c)];
   }
   float gone = 0.f;
   const bool gate = MODE != kCarry && a.z.p != nullptr;
-  for (int t = t0; t < t1; t += kTile) {
-    T xr[kTile], dr[kTile], zr[kTile];
+  Raw<T> raw, next;
+  float x[kOwn], z[kOwn];
+  // the tile's steps into LDS; tokens behind the last: steps of zero
+  auto prepare = [&](int t, float2 (&to)[kTile][64]) {
 #pragma unroll
-    for (int j = 0; j < kTile; ++j) {
-      const int at = t + j < t1 ? t + j : t1 - 1;
-      xr[j] = row_of<T>(a.x, at)[c];
-      dr[j] = row_of<T>(a.dt, at)[c];
-      if (gate) zr[j] = row_of<T>(a.z, at)[c];
+    for (int o = 0; o < kOwn; ++o) {
+      const int j = m.wave * kOwn + o;
+      const bool there = t + j < t1;
+      x[o] = load_scalar(&raw.x[o]);
+      if (gate) z[o] = load_scalar(&raw.z[o]);
+      const float delta = Step{load_scalar(&raw.dt[o]) + bias}.of(a.softplus);
+      to[j][lane] = there ? make_float2(delta, delta * x[o]) : make_float2(0.f, 0.f);
+      if (MODE == kCarry && there) gone += delta;
     }
-    float y[kTile];
+  };
+  if (t0 < t1) {
+    load_raw(a, m, t0, t1, gate, raw);
+    prepare(t0, prep[0]);
+    load_raw(a, m, t0 + kTile, t1, gate, raw);
+    __syncthreads();
+  }
+  int turn = 0;
+  for (int t = t0; t < t1; t += kTile, turn ^= 1) {
+    load_raw(a, m, t + 2 * kTile, t1, gate, next);
+    float xs[kOwn], zs[kOwn];
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      xs[o] = x[o];
+      zs[o] = z[o];
+    }
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
-      y[j] = 0.f;
-      if (t + j >= t1) continue;
-      const float x = load_scalar(&xr[j]);
-      const float delta = Step{load_scalar(&dr[j]) + bias}.of(a.softplus), u = delta * x;
-      const ScalarRow B = row_bc<SB>(a, m, t + j), C = B + SB * kStates;
-      if (MODE == kCarry) gone += delta;
-      float s[2] = {0.f, 0.f};
+      const float2 k = prep[turn][j][lane];
+      const ScalarRow B = row_bc<Q>(a, m, t + j < t1 ? t + j : t1 - 1), C = B + Q;
+      float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kStates; ++i) {
-        h[i] = exp2_fast(delta * A[i]) * h[i] + u * B[i];
-        if (MODE != kCarry) s[i & 1] += C[i] * h[i];
+      for (int i = 0; i < Q; ++i) {
+        h[i] = exp2_fast(k.x * A[i]) * h[i] + k.y * B[i];
+        if (MODE != kCarry) s += C[i] * h[i];
       }
-      y[j] = s[0] + s[1];
-      if (m.sb == 0) y[j] += D * x;
+      if (MODE != kCarry) part[turn][m.wave][j][lane] = s;
     }
-    if (MODE == kCarry) continue;
-    if constexpr (SB > 1) {
-      // the waves of a block of channels add up in order; the first one writes
-      const int wave = threadIdx.x >> 6;
-      __syncthreads();
+    prepare(t + kTile, prep[turn ^ 1]);
+    raw = next;
+    __syncthreads();
+    if (MODE == kCarry || !m.live) continue;
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) part[(wave * kTile + j) * 64 + lane] = y[j];
-      __syncthreads();
-      if (m.sb != 0) continue;
-#pragma unroll
-      for (int j = 0; j < kTile; ++j)
-#pragma unroll
-        for (int o = 1; o < SB; ++o) y[j] += part[((wave + o) * kTile + j) * 64 + lane];
-    }
-    if (!m.live) continue;
-#pragma unroll
-    for (int j = 0; j < kTile; ++j) {
+    for (int o = 0; o < kOwn; ++o) {
+      const int j = m.wave * kOwn + o;
       if (t + j >= t1) continue;
-      if (gate) {
-        const float z = load_scalar(&zr[j]);
-        y[j] *= z * sigmoid(z);
-      }
-      float one[1] = {y[j]};
+      float y[1] = {D * xs[o]};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) y[0] += part[turn][w][j][lane];
+      if (gate) y[0] *= zs[o] * sigmoid(zs[o]);
       Packed<1, T> out;
-      out.from(one);
+      out.from(y);
       out.store(row_of<T>(a.y, t + j) + c);
     }
   }
+  if (MODE == kCarry) {
+    // the sum of the steps: each wave has that of its tokens
+    prep[0][m.wave][lane].x = gone;   // (every wave is through with it)
+    __syncthreads();
+    if (m.wave == 0 && m.live)
+      reinterpret_cast<float*>(a.ws + a.at.gone)[(size_t)blockIdx.x * a.channels + c] =
+          (prep[0][0][lane].x + prep[0][1][lane].x) + (prep[0][2][lane].x + prep[0][3][lane].x);
+  }
   if (!m.live || MODE == kRead) return;
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
-    const int n = m.sb * kStates + i;
-    if (MODE == kCarry) carry[carry_at<SB>(a, blockIdx.x, n, c)] = h[i];
+  for (int i = 0; i < Q; ++i) {
+    const int n = m.wave * Q + i;
+    if (MODE == kCarry) carry[carry_at<Q>(a, blockIdx.x, n, c)] = h[i];
     else if (n < a.d_state) a.S[state_at(a, blockIdx.x, c) + n] = h[i];
   }
-  if (MODE == kCarry && m.sb == 0)
-    reinterpret_cast<float*>(a.ws + a.at.gone)[(size_t)blockIdx.x * a.channels + c] = gone;
 }
 
 // The segments' first states, h' = exp(A gone) h + carry, in the carries'
@@ -132,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
 // of a sequence.
 template <bool BACK>
 __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
-  const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = a.at.waves * kStates;
+  const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
   const float A = a.A[(size_t)c * a.d_state + n] * kLog2e;
@@ -209,23 +235,21 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   }
 }
 
-int blocks_of(int channels, int groups, int waves) {
-  const int each = channels / groups, per = 64 * kWaves / waves;
-  return (each + per - 1) / per;
-}
+int quarter_of(int d_state) { return d_state <= 8 ? 2 : d_state <= 16 ? 4 : d_state <= 32 ? 8 : 16; }
+int blocks_of(int channels, int groups) { return (channels / groups + 63) / 64; }
 
-template <typename T, int SB>
+template <typename T, int Q>
 hipError_t scan_types(const SelectArgs& a, hipStream_t stream) {
   const unsigned along = (unsigned)(a.groups * a.at.blocks);
   if (a.at.shift < 0) {
-    hipLaunchKernelGGL((scan_kernel<T, SB, kWhole>), dim3(a.n_seq, along), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((scan_kernel<T, Q, kWhole>), dim3(a.n_seq, along), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((scan_kernel<T, SB, kCarry>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((scan_kernel<T, Q, kCarry>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = launch_select_join(a, false, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_kernel<T, SB, kRead>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((scan_kernel<T, Q, kRead>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -236,14 +260,15 @@ using namespace channels;
 
 SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int tokens, bool backward) {
   SelectLayout l{};
-  l.waves = d_state <= kStates ? 1 : d_state <= 2 * kStates ? 2 : 4;
-  l.blocks = blocks_of(channels, groups, l.waves);
+  l.quarter = quarter_of(d_state);
+  l.blocks = blocks_of(channels, groups);
+  l.sets = (l.blocks + 3) / 4;
   const long long along = (long long)groups * l.blocks;
   // Forward: whole sequences where they fill half the chip; segments else
   // (the first pass computes every decay a second time).
   if (backward) l.shift = 6;
-  else l.shift = n_seq * along * kWaves >= 512 || tokens / n_seq <= 64 ? -1 : 7;
-  const size_t NP = (size_t)l.waves * kStates, T = (size_t)tokens;
+  else l.shift = n_seq * along >= 256 || tokens / n_seq <= 64 ? -1 : 7;
+  const size_t NP = (size_t)l.quarter * 4, T = (size_t)tokens, C = (size_t)channels;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -253,15 +278,18 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   l.rows = take(T * groups * 2 * NP * 4);
   if (l.shift >= 0) {
     l.slots = (tokens >> l.shift) + n_seq;
-    l.carry = take(l.slots * NP * channels * 4);
-    l.gone = take((size_t)l.slots * channels * 4);
+    l.carry = take(l.slots * NP * C * 4);
+    l.gone = take(l.slots * C * 4);
   }
   if (backward) {
-    l.back = take(l.slots * NP * channels * 4);
-    l.sums = take((size_t)l.blocks * T * groups * 2 * NP * 4);
-    const long long most = (1024 + along - 1) / along;
-    l.parts = (int)(l.slots < most ? l.slots : most);
-    l.weights = take((size_t)l.parts * (NP + 2) * channels * 4);
+    const size_t tiles = (size_t)(tokens >> 3) + n_seq;
+    l.back = take(l.slots * NP * C * 4);
+    l.kept = take(tiles * NP * C * 4);
+    l.before = take(tiles * C * 4);
+    l.sums = take(l.sets * T * groups * 2 * NP * 4);
+    // a workgroup goes on to further segments where there are many
+    l.parts = l.slots < 512 ? l.slots : 512;
+    l.weights = take(l.parts * (NP + 2) * C * 4);
   }
   l.bytes = at;
   return l;
@@ -270,13 +298,12 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
 // Grids: blocks of channels along y, sequences or segments of 64 along x with
 // 256 threads each.
 bool select_fits(int n_seq, int channels, int groups, int d_state, int tokens) {
-  const int waves = d_state <= kStates ? 1 : d_state <= 2 * kStates ? 2 : 4;
-  return (long long)groups * blocks_of(channels, groups, waves) <= 65535 &&
+  return (long long)groups * blocks_of(channels, groups) <= 65535 &&
          (long long)(tokens >> 6) + n_seq < (1LL << 24) && (long long)tokens + 64 <= 0x7fffffffLL;
 }
 
 hipError_t launch_select_prepare(const SelectArgs& a, hipStream_t stream) {
-  const size_t total = (size_t)a.tokens * a.groups * 2 * a.at.waves * kStates;
+  const size_t total = (size_t)a.tokens * a.groups * 8 * a.at.quarter;
   const size_t blocks = (total + kThreads - 1) / kThreads;
   const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
   if (a.bf16) hipLaunchKernelGGL((prepare_kernel<bf16_t>), grid, dim3(kThreads), 0, stream, a);
@@ -300,9 +327,10 @@ hipError_t launch_select(const SelectArgs& a, hipStream_t stream) {
   const hipError_t e = launch_select_prepare(a, stream);
   if (e != hipSuccess) return e;
 #define SEED_SCAN(T)                                          \
-  (a.at.waves == 1   ? scan_types<T, 1>(a, stream)            \
-   : a.at.waves == 2 ? scan_types<T, 2>(a, stream)            \
-                     : scan_types<T, 4>(a, stream))
+  (a.at.quarter == 2   ? scan_types<T, 2>(a, stream)          \
+   : a.at.quarter == 4 ? scan_types<T, 4>(a, stream)          \
+   : a.at.quarter == 8 ? scan_types<T, 8>(a, stream)          \
+                       : scan_types<T, 16>(a, stream))
   return a.bf16 ? SEED_SCAN(bf16_t) : SEED_SCAN(float);
 #undef SEED_SCAN
 }

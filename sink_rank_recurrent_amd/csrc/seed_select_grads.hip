@@ -2,77 +2,133 @@
 // seed_select.h), in segments of 64 tokens:
 //   ends_kernel   what a segment leaves of zero, h, and what it passes back to
 //                 its first state from its own read-outs, sum over t of
-//                 (a_1 .. a_t) ds_t C_t, in one walk that makes each decay once
+//                 (a_1 .. a_t) ds_t C_t, in one walk that makes each decay
+//                 once; the state it has come to before every 8th token
 //   join          the segments' first states and the gradients at their ends
-//   grads_kernel  each segment forward, keeping the state before every 8th
-//                 token in LDS, then 8 tokens at a time backward: their states
-//                 and decays again into registers, and the chain rule
-//   sums          dB and dC over blocks of channels, dA, dD and ddt_bias over
-//                 segments, in a fixed order.
+//   grads_kernel  8 tokens at a time, the last first: the states and decays
+//                 from the state before them (what the segment had made of
+//                 zero, and the decayed first state), and the chain rule
+//   sums          dB and dC over sets of four blocks of channels, dA, dD and
+//                 ddt_bias over segments, in a fixed order.
 #include "seed_select.h"
 
 namespace seed {
 namespace channels {
 namespace {
 
-constexpr int kThreads = 64 * kWaves;
-constexpr int kShift = 6, kLen = 1 << kShift, kK = kTile, kParts = kLen / kK;
+constexpr int kShift = 6, kLen = 1 << kShift, kTiles = kLen / kTile;
+constexpr int kSet = 4;     // blocks of channels that a workgroup takes one after the other
 
-// A token's inputs for a lane: delta, u = delta x, and the gradient of s.
-struct Token {
-  float x, v, delta, u, z, dy, ds;
+// The inputs of a wave's tokens of a tile as they lie in memory.
+template <typename T>
+struct Raw {
+  T x[kOwn], dt[kOwn], z[kOwn], dy[kOwn];
 };
 template <typename T>
-__device__ __forceinline__ Token token_of(const SelectArgs& a, int t, int c, float bias, bool live) {
-  Token k;
-  k.x = load_scalar(row_of<T>(a.x, t) + c);
-  k.v = load_scalar(row_of<T>(a.dt, t) + c) + bias;
-  k.dy = load_scalar(row_of<T>(a.dy, t) + c);
-  k.z = a.z.p ? load_scalar(row_of<T>(a.z, t) + c) : 0.f;
-  k.delta = live ? Step{k.v}.of(a.softplus) : 0.f;
-  k.u = live ? k.delta * k.x : 0.f;
-  k.ds = !live ? 0.f : a.z.p ? k.dy * k.z * sigmoid(k.z) : k.dy;
-  return k;
+__device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int t, int t1, Raw<T>& r) {
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const int at = t + m.wave * kOwn + o, in = at < t1 ? at : t1 - 1;
+    r.x[o] = row_of<T>(a.x, in)[m.c];
+    r.dt[o] = row_of<T>(a.dt, in)[m.c];
+    r.dy[o] = row_of<T>(a.dy, in)[m.c];
+    if (a.z.p) r.z[o] = row_of<T>(a.z, in)[m.c];
+  }
 }
 
-template <typename T, int SB>
+// A token's values for a lane; behind the last token steps and gradients of
+// zero.
+struct Token {
+  float x, v, delta, z, dy, ds;
+};
+template <typename T>
+__device__ __forceinline__ Token token_of(const SelectArgs& a, const Raw<T>& r, int o, float bias, bool there) {
+  Token k;
+  k.x = load_scalar(&r.x[o]);
+  k.v = load_scalar(&r.dt[o]) + bias;
+  k.dy = load_scalar(&r.dy[o]);
+  k.z = a.z.p ? load_scalar(&r.z[o]) : 0.f;
+  k.delta = there ? Step{k.v}.of(a.softplus) : 0.f;
+  k.ds = !there ? 0.f : a.z.p ? k.dy * (k.z * sigmoid(k.z)) : k.dy;
+  return k;
+}
+// delta, delta x, ds and x as the waves share them.
+__device__ __forceinline__ float4 shared_of(const Token& k, bool there) {
+  return there ? make_float4(k.delta, k.delta * k.x, k.ds, k.x) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// Number of the 8 tokens from t on among the batch's tiles: like that of a run.
+__device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (size_t)(r.lo >> 3) + r.seq + ((t - r.lo) >> 3); }
+
+template <typename T, int Q>
 __global__ __launch_bounds__(kThreads) void ends_kernel(SelectArgs a) {
-  const Mine m = mine<SB>(a, blockIdx.y);
+  __shared__ float4 prep[2][kTile][64];
+  const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
-  const int slot = blockIdx.x, c = m.c;
+  const int slot = blockIdx.x, c = m.c, lane = (int)__lane_id();
   const Run r = run_of(b, sequence_of(b, slot), slot);
   if (r.t0 >= r.t1) return;
-  float A[kStates], h[kStates], P[kStates], G[kStates];
-  load_rates<SB>(a, m, A);
+  float A[Q], h[Q], P[Q], G[Q];
+  load_rates<Q>(a, m, A);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
+  for (int i = 0; i < Q; ++i) {
     h[i] = G[i] = 0.f;
     P[i] = 1.f;
   }
-  float gone = 0.f;
-  for (int t = r.t0; t < r.t1; ++t) {
-    const Token k = token_of<T>(a, t, c, bias, true);
-    const ScalarRow B = row_bc<SB>(a, m, t), C = B + SB * kStates;
-    gone += k.delta;
+  Raw<T> raw;
+  auto prepare = [&](int t, float4 (&to)[kTile][64]) {
 #pragma unroll
-    for (int i = 0; i < kStates; ++i) {
-      const float d = exp2_fast(k.delta * A[i]);
-      h[i] = d * h[i] + k.u * B[i];
-      P[i] *= d;
-      G[i] += P[i] * (k.ds * C[i]);
+    for (int o = 0; o < kOwn; ++o) {
+      const int j = m.wave * kOwn + o;
+      const bool there = t + j < r.t1;
+      to[j][lane] = shared_of(token_of(a, raw, o, bias, there), there);
     }
+  };
+  load_raw(a, m, r.t0, r.t1, raw);
+  prepare(r.t0, prep[0]);
+  load_raw(a, m, r.t0 + kTile, r.t1, raw);
+  __syncthreads();
+  float gone = 0.f;
+  float* kept = reinterpret_cast<float*>(a.ws + a.at.kept);
+  float* before = reinterpret_cast<float*>(a.ws + a.at.before);
+  int turn = 0;
+  for (int t = r.t0; t < r.t1; t += kTile, turn ^= 1) {
+    Raw<T> next;
+    load_raw(a, m, t + 2 * kTile, r.t1, next);
+    const size_t tile = tile_number(r, t);
+    if (m.live) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) kept[(tile * (4 * Q) + m.wave * Q + i) * a.channels + c] = h[i];
+      if (m.wave == 0) before[tile * a.channels + c] = gone;
+    }
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const float4 k = prep[turn][j][lane];
+      const ScalarRow B = row_bc<Q>(a, m, t + j < r.t1 ? t + j : r.t1 - 1), C = B + Q;
+      gone += k.x;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const float d = exp2_fast(k.x * A[i]);
+        h[i] = d * h[i] + k.y * B[i];
+        P[i] *= d;
+        G[i] += P[i] * (k.z * C[i]);
+      }
+    }
+    prepare(t + kTile, prep[turn ^ 1]);
+    raw = next;
+    __syncthreads();
   }
   if (!m.live) return;
   float* carry = reinterpret_cast<float*>(a.ws + a.at.carry);
   float* back = reinterpret_cast<float*>(a.ws + a.at.back);
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) {
-    const size_t at = carry_at<SB>(a, slot, m.sb * kStates + i, c);
+  for (int i = 0; i < Q; ++i) {
+    const size_t at = carry_at<Q>(a, slot, m.wave * Q + i, c);
     carry[at] = h[i];
     back[at] = G[i];
   }
-  if (m.sb == 0) reinterpret_cast<float*>(a.ws + a.at.gone)[(size_t)slot * a.channels + c] = gone;
+  if (m.wave == 0) reinterpret_cast<float*>(a.ws + a.at.gone)[(size_t)slot * a.channels + c] = gone;
 }
 
 // p + q where the lane's bit is 0: p of both halves of the lanes, where it is
@@ -91,208 +147,214 @@ __device__ __forceinline__ float fold(float p, float q) {
     return keep + dpp_mov<ctrl>(give);
   }
 }
-// Sums over the 64 lanes of 64 values: lane l gets that of value l.
-__device__ __forceinline__ float fold64(float (&v)[64]) {
+// Sums over the 64 lanes of N values, 32 or 64: lane l gets that of value l
+// (of value l / 2).
+template <int N>
+__device__ __forceinline__ float fold_all(float (&v)[N]) {
+  static_assert(N == 32 || N == 64, "a wave's lanes, or half of them");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = fold<5>(v[i], v[i + 32]);
+  for (int i = 0; i < N / 2; ++i) v[i] = fold<5>(v[i], v[i + N / 2]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = fold<4>(v[i], v[i + 16]);
+  for (int i = 0; i < N / 4; ++i) v[i] = fold<4>(v[i], v[i + N / 4]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fold<3>(v[i], v[i + 8]);
+  for (int i = 0; i < N / 8; ++i) v[i] = fold<3>(v[i], v[i + N / 8]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = fold<2>(v[i], v[i + 4]);
+  for (int i = 0; i < N / 16; ++i) v[i] = fold<2>(v[i], v[i + N / 16]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) v[i] = fold<1>(v[i], v[i + 2]);
-  return fold<0>(v[0], v[1]);
+  for (int i = 0; i < N / 32; ++i) v[i] = fold<1>(v[i], v[i + N / 32]);
+  if constexpr (N == 64) return fold<0>(v[0], v[1]);
+  else return v[0] + dpp_mov<0xB1>(v[0]);
 }
 
-template <typename T, int SB>
+// A set of four blocks of channels of one group (blockIdx.y) over every
+// gridDim.x-th segment.
+template <typename T, int Q>
 __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
-  __shared__ float kept[kWaves][kParts - 1][kStates][64];   // states before each part but the first
-  __shared__ float sums[2][kWaves][kK * 2 * kStates];       // dB and dC of 8 tokens, by wave
-  __shared__ float part[SB > 1 ? kWaves * 3 * kK * 64 : 1];
-  const Mine m = mine<SB>(a, blockIdx.y);
+  constexpr int kValues = kTile * 2 * Q;                  // dB and dC of 8 tokens, a wave's states
+  constexpr int kFold = kValues < 64 ? kValues : 64, kFolds = kValues / kFold;
+  constexpr int kFoldTile = kTile / kFolds;               // tokens of a fold
+  __shared__ float4 prep[kTile][64];
+  __shared__ float4 part[kWaves][kTile][64];
+  __shared__ float sums[kTiles][kWaves][kFolds][64];
+  const int lane = (int)__lane_id();
+  const int group = blockIdx.y / a.at.sets, set = blockIdx.y % a.at.sets;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
-  const int lane = (int)__lane_id(), wave = threadIdx.x >> 6, c = m.c;
-  float A[kStates], dA[kStates];
-  load_rates<SB>(a, m, A);
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
-  float dD = 0.f, dbias = 0.f;
-#pragma unroll
-  for (int i = 0; i < kStates; ++i) dA[i] = 0.f;
   const float* starts = reinterpret_cast<const float*>(a.ws + a.at.carry);
   const float* ends = reinterpret_cast<const float*>(a.ws + a.at.back);
-  int turn = 0;
+  const float* kept = reinterpret_cast<const float*>(a.ws + a.at.kept);
+  const float* before = reinterpret_cast<const float*>(a.ws + a.at.before);
 
   for (int slot = blockIdx.x; slot < a.at.slots; slot += gridDim.x) {
     const Run r = run_of(b, sequence_of(b, slot), slot);
-    if (r.t0 >= r.t1) continue;   // the whole workgroup
-    const int parts = (r.t1 - r.t0 + kK - 1) / kK;
-    float h[kStates], G[kStates];
+    const bool none = r.t0 >= r.t1;   // the whole workgroup
+    const int tiles = none ? 0 : (r.t1 - r.t0 + kTile - 1) / kTile;
+    for (int block = set * kSet; block < (set + 1) * kSet && block < a.at.blocks; ++block) {
+      const Mine m = mine(a, group, block);
+      const int c = m.c;
+      float A[Q], dA[Q], H[Q], G[Q];
+      load_rates<Q>(a, m, A);
+      const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
+      float dD = 0.f, dbias = 0.f;
 #pragma unroll
-    for (int i = 0; i < kStates; ++i) {
-      const int n = m.sb * kStates + i;
-      const size_t at = carry_at<SB>(a, slot, n, c);
-      // (join leaves the padding states' carries as they are)
-      h[i] = n < a.d_state ? starts[at] : 0.f;
-      G[i] = n < a.d_state ? ends[at] : 0.f;
-    }
-    for (int p = 0; p + 1 < parts; ++p) {
-      for (int j = 0; j < kK; ++j) {
-        const int t = r.t0 + p * kK + j;
-        const Token k = token_of<T>(a, t, c, bias, true);
-        const ScalarRow B = row_bc<SB>(a, m, t);
-#pragma unroll
-        for (int i = 0; i < kStates; ++i) h[i] = exp2_fast(k.delta * A[i]) * h[i] + k.u * B[i];
-      }
-#pragma unroll
-      for (int i = 0; i < kStates; ++i) kept[wave][p][i][lane] = h[i];
-    }
-    for (int p = parts - 1; p >= 0; --p) {
-      const int t0 = r.t0 + p * kK;
-      float first[kStates], hs[kK][kStates], d[kK][kStates];
-      Token k[kK];
-#pragma unroll
-      for (int i = 0; i < kStates; ++i) {
-        const int n = m.sb * kStates + i;
-        first[i] = p > 0 ? kept[wave][p - 1][i][lane] : n < a.d_state ? starts[carry_at<SB>(a, slot, n, c)] : 0.f;
-      }
-      // tokens behind the segment's last: steps and gradients of zero
-#pragma unroll
-      for (int j = 0; j < kK; ++j) {
-        const int t = t0 + j < r.t1 ? t0 + j : r.t1 - 1;
-        k[j] = token_of<T>(a, t, c, bias, t0 + j < r.t1);
-        const ScalarRow B = row_bc<SB>(a, m, t);
-#pragma unroll
-        for (int i = 0; i < kStates; ++i) {
-          d[j][i] = exp2_fast(k[j].delta * A[i]);
-          hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]) + k[j].u * B[i];
+      for (int i = 0; i < Q; ++i) {
+        const int n = m.wave * Q + i;
+        dA[i] = H[i] = G[i] = 0.f;
+        if (!none && n < a.d_state) {   // (join leaves the padding states' carries as they are)
+          H[i] = starts[carry_at<Q>(a, slot, n, c)];
+          G[i] = ends[carry_at<Q>(a, slot, n, c)];
         }
       }
-      float s[kK], du[kK], rate[kK], total[kK / 2];
+      Raw<T> raw;
+      if (!none) load_raw(a, m, r.t0 + (tiles - 1) * kTile, r.t1, raw);
+      for (int p = tiles - 1; p >= 0; --p) {
+        const int t0 = r.t0 + p * kTile;
+        const size_t tile = tile_number(r, t0);
+        float first[Q], hs[kTile][Q], d[kTile][Q];
+        const float gone = before[tile * a.channels + c];
 #pragma unroll
-      for (int jj = kK / 2 - 1; jj >= 0; --jj) {
-        float v[64];   // of two tokens: dB, dC
+        for (int i = 0; i < Q; ++i)
+          first[i] = exp2_fast(gone * A[i]) * H[i] + kept[(tile * (4 * Q) + m.wave * Q + i) * a.channels + c];
+        Token own[kOwn];
 #pragma unroll
-        for (int jo = 1; jo >= 0; --jo) {
-          const int j = 2 * jj + jo, t = t0 + j < r.t1 ? t0 + j : r.t1 - 1;
-          const ScalarRow B = row_bc<SB>(a, m, t), C = B + SB * kStates;
-          s[j] = du[j] = rate[j] = 0.f;
+        for (int o = 0; o < kOwn; ++o) {
+          const int j = m.wave * kOwn + o;
+          const bool there = t0 + j < r.t1;
+          own[o] = token_of(a, raw, o, bias, there);
+          prep[j][lane] = shared_of(own[o], there);
+        }
+        if (p > 0) load_raw(a, m, t0 - kTile, r.t1, raw);
+        __syncthreads();
 #pragma unroll
-          for (int i = 0; i < kStates; ++i) {
-            G[i] += k[j].ds * C[i];
-            v[jo * 32 + i] = m.live ? G[i] * k[j].u : 0.f;
-            v[jo * 32 + 16 + i] = m.live ? k[j].ds * hs[j][i] : 0.f;
-            s[j] += C[i] * hs[j][i];
-            du[j] += G[i] * B[i];
-            G[i] *= d[j][i];
-            const float q = G[i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
-            rate[j] += A[i] * q;
-            dA[i] += k[j].delta * q;
+        for (int j = 0; j < kTile; ++j) {
+          const float4 k = prep[j][lane];
+          const ScalarRow B = row_bc<Q>(a, m, t0 + j < r.t1 ? t0 + j : r.t1 - 1);
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            d[j][i] = exp2_fast(k.x * A[i]);
+            hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]) + k.y * B[i];
           }
         }
-        total[jj] = fold64(v);
-      }
-      if constexpr (SB > 1) {
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kK; ++j) {
-          part[((wave * kK + j) * 3 + 0) * 64 + lane] = s[j];
-          part[((wave * kK + j) * 3 + 1) * 64 + lane] = du[j];
-          part[((wave * kK + j) * 3 + 2) * 64 + lane] = rate[j];
-        }
-        __syncthreads();
-        if (m.sb == 0) {
+        for (int f = kFolds - 1; f >= 0; --f) {
+          float v[kFold];
 #pragma unroll
-          for (int j = 0; j < kK; ++j)
+          for (int jj = kFoldTile - 1; jj >= 0; --jj) {
+            const int j = f * kFoldTile + jj;
+            const float4 k = prep[j][lane];
+            const ScalarRow B = row_bc<Q>(a, m, t0 + j < r.t1 ? t0 + j : r.t1 - 1), C = B + Q;
+            float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
-            for (int o = 1; o < SB; ++o) {
-              s[j] += part[(((wave + o) * kK + j) * 3 + 0) * 64 + lane];
-              du[j] += part[(((wave + o) * kK + j) * 3 + 1) * 64 + lane];
-              rate[j] += part[(((wave + o) * kK + j) * 3 + 2) * 64 + lane];
+            for (int i = 0; i < Q; ++i) {
+              G[i] += k.z * C[i];
+              v[jj * 2 * Q + i] = m.live ? G[i] * k.y : 0.f;
+              v[jj * 2 * Q + Q + i] = m.live ? k.z * hs[j][i] : 0.f;
+              s += C[i] * hs[j][i];
+              du += G[i] * B[i];
+              G[i] *= d[j][i];
+              const float q = G[i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
+              rate += A[i] * q;
+              dA[i] += k.x * q;
             }
+            part[m.wave][j][lane] = make_float4(s, du, rate, 0.f);
+          }
+          const float total = fold_all(v);
+          float& to = sums[p][m.wave][f][lane];
+          to = block == set * kSet ? total : to + total;
         }
-      }
-      if (m.sb == 0 && m.live) {
+        __syncthreads();
+        if (!m.live) continue;
 #pragma unroll
-        for (int j = 0; j < kK; ++j) {
-          const int t = t0 + j;
+        for (int o = 0; o < kOwn; ++o) {
+          const int j = m.wave * kOwn + o, t = t0 + j;
           if (t >= r.t1) continue;
-          const float ddelta = k[j].x * du[j] + rate[j] * kLn2;
-          const float dv = ddelta * Step{k[j].v}.slope(a.softplus);
+          const Token& k = own[o];
+          float s = 0.f, du = 0.f, rate = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float4 q = part[w][j][lane];
+            s += q.x;
+            du += q.y;
+            rate += q.z;
+          }
+          const float dv = (k.x * du + rate * kLn2) * Step{k.v}.slope(a.softplus);
           dbias += dv;
-          dD += k[j].ds * k[j].x;
+          dD += k.ds * k.x;
           Packed<1, T> out;
-          float one[1] = {k[j].delta * du[j] + D * k[j].ds};
+          float one[1] = {k.delta * du + D * k.ds};
           out.from(one);
           out.store(row_of<T>(a.dx, t) + c);
           one[0] = dv;
           out.from(one);
           out.store(row_of<T>(a.ddt, t) + c);
           if (a.z.p) {
-            const float g = sigmoid(k[j].z), sy = s[j] + D * k[j].x;
-            one[0] = k[j].dy * sy * (g + k[j].z * g * (1.f - g));
+            const float g = sigmoid(k.z);
+            one[0] = k.dy * (s + D * k.x) * (g + k.z * g * (1.f - g));
             out.from(one);
             out.store(row_of<T>(a.dz, t) + c);
           }
         }
       }
-      // dB and dC of the part: the waves of the same states add up in order
-      float(&mine_sums)[kWaves][kK * 2 * kStates] = sums[turn];
-      turn ^= 1;
-#pragma unroll
-      for (int jj = 0; jj < kK / 2; ++jj) mine_sums[wave][jj * 64 + lane] = total[jj];
+      // the block's part of the weights' gradients: that of the workgroup's
+      // segments before, and this one's
       __syncthreads();
-      const int j = threadIdx.x / 32, what = threadIdx.x / 16 & 1, n = threadIdx.x & 15;
-      if (t0 + j < r.t1) {
-        float* out = reinterpret_cast<float*>(a.ws + a.at.sums) +
-                     ((((size_t)m.block * a.tokens + t0 + j) * a.groups + m.group) * 2 + what) * (SB * kStates) + n;
+      part[m.wave][0][lane] = make_float4(dD, dbias, 0.f, 0.f);
+      __syncthreads();
+      if (m.live) {
+        float* out = reinterpret_cast<float*>(a.ws + a.at.weights) + (size_t)blockIdx.x * (4 * Q + 2) * a.channels + c;
+        const bool more = slot >= (int)gridDim.x;
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
+        for (int i = 0; i < Q; ++i) {
+          float& to = out[(size_t)(m.wave * Q + i) * a.channels];
+          to = more ? to + dA[i] : dA[i];
+        }
+        if (m.wave < 2) {
           float x = 0.f;
 #pragma unroll
-          for (int w = sb; w < kWaves; w += SB) x += mine_sums[w][threadIdx.x];
-          out[sb * kStates] = x;
+          for (int w = 0; w < kWaves; ++w) x += m.wave == 0 ? part[w][0][lane].x : part[w][0][lane].y;
+          float& to = out[(size_t)(4 * Q + m.wave) * a.channels];
+          to = more ? to + x : x;
         }
       }
     }
-  }
-  if (!m.live) return;
-  float* out = reinterpret_cast<float*>(a.ws + a.at.weights) + (size_t)blockIdx.x * (SB * kStates + 2) * a.channels + c;
+    // dB and dC of the set
+    const int wave = (int)threadIdx.x >> 6, share = kFold < 64 ? 2 : 1, value = lane / share;
+    for (int p = 0; p < tiles; ++p)
 #pragma unroll
-  for (int i = 0; i < kStates; ++i) out[(size_t)(m.sb * kStates + i) * a.channels] = dA[i];
-  if (m.sb == 0) {
-    out[(size_t)(SB * kStates) * a.channels] = dD;
-    out[(size_t)(SB * kStates + 1) * a.channels] = dbias;
+      for (int f = 0; f < kFolds; ++f) {
+        const int at = f * kFold + value, t = r.t0 + p * kTile + at / (2 * Q);
+        if (t < r.t1 && lane % share == 0)
+          reinterpret_cast<float*>(a.ws + a.at.sums)[((((size_t)set * a.tokens + t) * a.groups + group) * 4 + wave) * (2 * Q) +
+                                                     at % (2 * Q)] = sums[p][wave][f][lane];
+      }
   }
 }
 
-// dB and dC: the parts of the blocks of channels, in order.
+// dB and dC: the parts of the sets of channels, in order.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void rows_kernel(SelectArgs a) {
-  const int NP = a.at.waves * kStates;
+  const int Q = a.at.quarter;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, 0);
   const float* sums = reinterpret_cast<const float*>(a.ws + a.at.sums);
   const int first = first_token(b, 0), end = b.cu ? first_token(b, a.n_seq) : a.tokens;
-  const size_t row = (size_t)a.groups * 2 * NP, step = (size_t)gridDim.x * kThreads;
+  const size_t row = (size_t)a.groups * 8 * Q, step = (size_t)gridDim.x * kThreads;
   for (size_t i = first * row + (size_t)blockIdx.x * kThreads + threadIdx.x; i < end * row; i += step) {
-    const int n = (int)(i % NP), what = (int)(i / NP & 1);
+    const int in = (int)(i % (8 * Q)), n = in / (2 * Q) * Q + in % Q, what = in / Q & 1;
     if (n >= a.d_state) continue;
-    const size_t tg = i / (2 * NP), t = tg / a.groups;
+    const size_t tg = i / (8 * Q), t = tg / a.groups;
     const int g = (int)(tg - t * a.groups);
     float x[1] = {0.f};
-    for (int k = 0; k < a.at.blocks; ++k) x[0] += sums[(size_t)k * a.tokens * row + i];
+    for (int k = 0; k < a.at.sets; ++k) x[0] += sums[(size_t)k * a.tokens * row + i];
     Packed<1, T> out;
     out.from(x);
     out.store(row_of<T>(what ? a.dC : a.dB, (long long)t) + (size_t)g * a.d_state + n);
   }
 }
 
-// dA, dD and ddt_bias: the parts [part][state + 2][channel], a wave every
-// fourth, then the waves in order.
+// dA, dD and ddt_bias: the parts [part][states, dD, ddt_bias][channel], a wave
+// every fourth, then the waves in order.
 __global__ __launch_bounds__(kThreads) void weights_kernel(SelectArgs a, int parts) {
   __shared__ float lds[kThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, NP = a.at.waves * kStates;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, NP = 4 * a.at.quarter;
   const int c = (int)blockIdx.x * 64 + lane, n = blockIdx.y, row = n < a.d_state ? n : NP + (n - a.d_state);
   const float* w = reinterpret_cast<const float*>(a.ws + a.at.weights);
   float s = 0.f;
@@ -310,17 +372,16 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(SelectArgs a, int par
   }
 }
 
-template <typename T, int SB>
+template <typename T, int Q>
 hipError_t grads_types(const SelectArgs& a, hipStream_t stream) {
-  const unsigned along = (unsigned)(a.groups * a.at.blocks);
-  hipLaunchKernelGGL((ends_kernel<T, SB>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((ends_kernel<T, Q>), dim3(a.at.slots, a.groups * a.at.blocks), dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = launch_select_join(a, true, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grads_kernel<T, SB>), dim3(a.at.parts, along), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((grads_kernel<T, Q>), dim3(a.at.parts, a.groups * a.at.sets), dim3(kThreads), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t values = (size_t)a.tokens * a.groups * 2 * SB * kStates, blocks = (values + kThreads - 1) / kThreads;
+  const size_t values = (size_t)a.tokens * a.groups * 8 * Q, blocks = (values + kThreads - 1) / kThreads;
   hipLaunchKernelGGL((rows_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
@@ -336,9 +397,10 @@ hipError_t launch_select_backward(const SelectArgs& a, hipStream_t stream) {
     e = launch_select_prepare(a, stream);
     if (e != hipSuccess) return e;
 #define SEED_GRADS(T)                                          \
-  (a.at.waves == 1   ? grads_types<T, 1>(a, stream)            \
-   : a.at.waves == 2 ? grads_types<T, 2>(a, stream)            \
-                     : grads_types<T, 4>(a, stream))
+  (a.at.quarter == 2   ? grads_types<T, 2>(a, stream)          \
+   : a.at.quarter == 4 ? grads_types<T, 4>(a, stream)          \
+   : a.at.quarter == 8 ? grads_types<T, 8>(a, stream)          \
+                       : grads_types<T, 16>(a, stream))
     e = a.bf16 ? SEED_GRADS(bf16_t) : SEED_GRADS(float);
 #undef SEED_GRADS
   } else {
