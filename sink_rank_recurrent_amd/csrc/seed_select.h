@@ -86,10 +86,59 @@ __device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, f
   }
 }
 
-// B and, Q floats on, C of a token for a wave's states.
+// B and C of the tokens of a tile for a wave's states.  `last`: the last token
+// of the sequence or segment, counted from the tile's first; tokens behind it
+// take its row (their steps are zero, but a row of another sequence may hold
+// an infinity).
 template <int Q>
-__device__ __forceinline__ ScalarRow row_bc(const SelectArgs& a, const Mine& m, int t) {
-  return (ScalarRow)(uintptr_t)(a.ws + a.at.rows) + (((size_t)t * a.groups + m.group) * 4 + m.wave) * (2 * Q);
+struct TileRows {
+  uintptr_t base;
+  uint32_t step;
+  int last;
+  __device__ __forceinline__ TileRows(const SelectArgs& a, const Mine& m, int t, int t1)
+      : base((uintptr_t)(a.ws + a.at.rows) + (((size_t)t * a.groups + m.group) * 4 + m.wave) * (8 * Q)),
+        step((uint32_t)a.groups * (32 * Q)), last(t1 - 1 - t) {}
+  __device__ __forceinline__ ScalarRow operator[](int j) const {
+    return (ScalarRow)(base + (uint32_t)(j < last ? j : last) * step);
+  }
+};
+// The tile's rows in scalar registers where those suffice (Q <= 4: 64 of them,
+// on their way while the steps are made); else each token's when it is used.
+template <int Q>
+struct Scalars {
+  float v[Q <= 4 ? kTile : 1][2 * Q];
+  TileRows<Q> rows;
+  __device__ __forceinline__ explicit Scalars(const TileRows<Q>& r) : rows(r) {
+    if constexpr (Q <= 4) {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * Q; ++i) v[j][i] = rows[j][i];
+    }
+  }
+  // B and, Q floats on, C of token j
+  __device__ __forceinline__ const float* of(int j) {
+    if constexpr (Q <= 4) {
+      return v[j];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * Q; ++i) v[0][i] = rows[j][i];
+      return v[0];
+    }
+  }
+};
+// Nothing is moved over this point: what a token needs, in registers or on its
+// way, does not pile up with the other tokens'.
+__device__ __forceinline__ void next_token() { __builtin_amdgcn_sched_barrier(0); }
+
+// The call's arguments, read again from where the launch put them: pointers and
+// strides of a dozen arrays, each used once a tile, would take the scalar
+// registers that the rows of B and C need.
+typedef const __attribute__((address_space(4))) SelectArgs* ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+  auto p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
 }
 
 template <typename T>

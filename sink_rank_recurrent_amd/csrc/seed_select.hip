@@ -41,6 +41,21 @@ __device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int
   }
 }
 
+// The sequence with the rank-th most tokens, of at most 64.  Workgroups start
+// in their numbers' order and go round the CUs, so that each CU gets long and
+// short ones alike (24 ragged sequences, REPLACE).
+__device__ __forceinline__ int ranked(const Batch& b, int rank) {
+  const int lane = (int)__lane_id();
+  const int len = lane < b.n_seq ? first_token(b, lane + 1) - first_token(b, lane) : 0;
+  int longer = 0;
+  for (int s = 0; s < b.n_seq; ++s) {
+    const int other = __builtin_amdgcn_readlane(len, s);
+    longer += other > len || (other == len && s < lane);
+  }
+  const uint64_t mine = __ballot(lane < b.n_seq && longer == rank);
+  return mine ? __builtin_ctzll(mine) : rank;
+}
+
 // MODE kWhole: a sequence from its first state to its last; kCarry: what a
 // segment leaves of zero, and the sum of its steps; kRead: a segment's
 // read-outs from its first state.
@@ -48,12 +63,15 @@ template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
   __shared__ float2 prep[2][kTile][64];                           // delta, delta x
   __shared__ float part[MODE == kCarry ? 1 : 2][kWaves][kTile][64];
-  const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
+  const int block = MODE == kWhole ? blockIdx.x : blockIdx.y;
+  const Mine m = mine(a, block / a.at.blocks, block % a.at.blocks);
   const int lane = (int)__lane_id(), c = m.c;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, MODE == kWhole ? 0 : a.at.shift);
-  int t0, t1;
+  int t0, t1, s = 0;
   if (MODE == kWhole) {
-    const int s = blockIdx.x;
+    s = blockIdx.z * gridDim.y + blockIdx.y;
+    if (s >= a.n_seq) return;
+    if (a.cu && a.n_seq <= 64) s = ranked(b, s);
     t0 = first_token(b, s);
     t1 = b.cu ? first_token(b, s + 1) : t0 + b.len;
   } else {
@@ -70,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
   for (int i = 0; i < Q; ++i) {
     const int n = m.wave * Q + i;
     h[i] = 0.f;
-    if (MODE == kWhole && a.S0 && n < a.d_state) h[i] = a.S0[state_at(a, blockIdx.x, c) + n];
+    if (MODE == kWhole && a.S0 && n < a.d_state) h[i] = a.S0[state_at(a, s, c) + n];
     // (a padding state's carry is not a first state: join leaves it as it is)
     if (MODE == kRead && n < a.d_state) h[i] = carry[carry_at<Q>(a, blockIdx.x, n, c)];
   }
@@ -100,6 +118,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
   int turn = 0;
   for (int t = t0; t < t1; t += kTile, turn ^= 1) {
     load_raw(a, m, t + 2 * kTile, t1, gate, next);
+    const TileRows<Q> rows(a, m, t, t1);
     float xs[kOwn], zs[kOwn];
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
@@ -109,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       const float2 k = prep[turn][j][lane];
-      const ScalarRow B = row_bc<Q>(a, m, t + j < t1 ? t + j : t1 - 1), C = B + Q;
+      const ScalarRow B = rows[j], C = B + Q;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
@@ -148,44 +167,53 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
   for (int i = 0; i < Q; ++i) {
     const int n = m.wave * Q + i;
     if (MODE == kCarry) carry[carry_at<Q>(a, blockIdx.x, n, c)] = h[i];
-    else if (n < a.d_state) a.S[state_at(a, blockIdx.x, c) + n] = h[i];
+    else if (n < a.d_state) a.S[state_at(a, s, c) + n] = h[i];
   }
 }
 
 // The segments' first states, h' = exp(A gone) h + carry, in the carries'
-// places, and S; backwards also the gradients at the segments' ends, G' =
-// exp(A gone) G + back, in theirs, and dS0.  A thread is a state of a channel
-// of a sequence.
+// places, and S; backwards also (blockIdx.z's upper half) the gradients at the
+// segments' ends, G' = exp(A gone) G + back, in theirs, and dS0.  A thread is a
+// state of a channel of a sequence; the values of kAhead segments are on their
+// way together.
+constexpr int kAhead = 8;
 template <bool BACK>
 __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
   const float A = a.A[(size_t)c * a.d_state + n] * kLog2e;
-  const float* gone = reinterpret_cast<const float*>(a.ws + a.at.gone);
-  for (int s = blockIdx.z; s < a.n_seq; s += gridDim.z) {
+  const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
+  const size_t row = (size_t)NP * a.channels;
+  for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
     const int first = first_run(b, s), lo = first_token(b, s);
     const int end = b.cu ? first_token(b, s + 1) : lo + b.len;
     const int len = end > lo ? end - lo : 0, runs = (len + (1 << a.at.shift) - 1) >> a.at.shift;
-    const size_t user = state_at(a, s, c) + n, step = (size_t)NP * a.channels;
-    float* carry = reinterpret_cast<float*>(a.ws + a.at.carry) + (size_t)first * step + (size_t)n * a.channels + c;
-    const float* g = gone + (size_t)first * a.channels + c;
-    float h = a.S0 ? a.S0[user] : 0.f;
-    for (int r = 0; r < runs; ++r) {
-      const float made = carry[r * step];
-      carry[r * step] = h;
-      h = exp2_fast(A * g[(size_t)r * a.channels]) * h + made;
-    }
-    if (!BACK) a.S[user] = h;
-    if (BACK) {
-      float* back = reinterpret_cast<float*>(a.ws + a.at.back) + (size_t)first * step + (size_t)n * a.channels + c;
-      float G = a.dS ? a.dS[user] : 0.f;
-      for (int r = runs - 1; r >= 0; --r) {
-        const float made = back[r * step];
-        back[r * step] = G;
-        G = exp2_fast(A * g[(size_t)r * a.channels]) * G + made;
+    const size_t user = state_at(a, s, c) + n;
+    const int from = reverse ? first + runs - 1 : first, way = reverse ? -1 : 1;
+    float* made = reinterpret_cast<float*>(a.ws + (reverse ? a.at.back : a.at.carry)) + (size_t)n * a.channels + c;
+    const float* gone = reinterpret_cast<const float*>(a.ws + a.at.gone) + c;
+    const float* given = reverse ? a.dS : a.S0;
+    float h = given ? given[user] : 0.f;
+    for (int r = 0; r < runs; r += kAhead) {
+      float g[kAhead], x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int at = from + way * (r + j < runs ? r + j : runs - 1);
+        g[j] = gone[(size_t)at * a.channels];
+        x[j] = made[(size_t)at * row];
       }
-      if (a.dS0) a.dS0[user] = G;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (r + j >= runs) break;
+        made[(size_t)(from + way * (r + j)) * row] = h;
+        h = exp2_fast(A * g[j]) * h + x[j];
+      }
+    }
+    if (reverse) {
+      if (a.dS0) a.dS0[user] = h;
+    } else if (!BACK) {
+      a.S[user] = h;
     }
   }
 }
@@ -242,7 +270,9 @@ template <typename T, int Q>
 hipError_t scan_types(const SelectArgs& a, hipStream_t stream) {
   const unsigned along = (unsigned)(a.groups * a.at.blocks);
   if (a.at.shift < 0) {
-    hipLaunchKernelGGL((scan_kernel<T, Q, kWhole>), dim3(a.n_seq, along), dim3(kThreads), 0, stream, a);
+    // sequences along y and z, 2^16 - 1 at most along each
+    const unsigned y = a.n_seq < 65535 ? a.n_seq : 65535, z = (a.n_seq + y - 1) / y;
+    hipLaunchKernelGGL((scan_kernel<T, Q, kWhole>), dim3(along, y, z), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((scan_kernel<T, Q, kCarry>), dim3(a.at.slots, along), dim3(kThreads), 0, stream, a);
@@ -312,7 +342,8 @@ hipError_t launch_select_prepare(const SelectArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_select_join(const SelectArgs& a, bool backward, hipStream_t stream) {
-  const dim3 grid((a.channels + kThreads - 1) / kThreads, a.d_state, a.n_seq < 65535 ? a.n_seq : 65535);
+  const int along = a.n_seq < 32767 ? a.n_seq : 32767;
+  const dim3 grid((a.channels + kThreads - 1) / kThreads, a.d_state, backward ? 2 * along : along);
   if (backward) hipLaunchKernelGGL((join_kernel<true>), grid, dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL((join_kernel<false>), grid, dim3(kThreads), 0, stream, a);
   return hipGetLastError();

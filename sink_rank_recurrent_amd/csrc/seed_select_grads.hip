@@ -20,19 +20,21 @@ constexpr int kShift = 6, kLen = 1 << kShift, kTiles = kLen / kTile;
 constexpr int kSet = 4;     // blocks of channels that a workgroup takes one after the other
 
 // The inputs of a wave's tokens of a tile as they lie in memory.
-template <typename T>
+template <typename T, bool GATE>
 struct Raw {
-  T x[kOwn], dt[kOwn], z[kOwn], dy[kOwn];
+  T x[kOwn], dt[kOwn], z[GATE ? kOwn : 1], dy[kOwn];
 };
-template <typename T>
-__device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int t, int t1, Raw<T>& r) {
+template <typename T, bool GATE>
+__device__ __forceinline__ void load_raw(const Mine& m, int t, int t1, Raw<T, GATE>& r) {
+  const ArgsAgain a = args_again();
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
-    const int at = t + m.wave * kOwn + o, in = at < t1 ? at : t1 - 1;
-    r.x[o] = row_of<T>(a.x, in)[m.c];
-    r.dt[o] = row_of<T>(a.dt, in)[m.c];
-    r.dy[o] = row_of<T>(a.dy, in)[m.c];
-    if (a.z.p) r.z[o] = row_of<T>(a.z, in)[m.c];
+    const int at = t + m.wave * kOwn + o;
+    const long long in = at < t1 ? at : t1 - 1;
+    r.x[o] = (static_cast<const T*>(a->x.p) + in * a->x.stride)[m.c];
+    r.dt[o] = (static_cast<const T*>(a->dt.p) + in * a->dt.stride)[m.c];
+    r.dy[o] = (static_cast<const T*>(a->dy.p) + in * a->dy.stride)[m.c];
+    if (GATE) r.z[o] = (static_cast<const T*>(a->z.p) + in * a->z.stride)[m.c];
   }
 }
 
@@ -41,28 +43,43 @@ __device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int
 struct Token {
   float x, v, delta, z, dy, ds;
 };
-template <typename T>
-__device__ __forceinline__ Token token_of(const SelectArgs& a, const Raw<T>& r, int o, float bias, bool there) {
-  Token k;
-  k.x = load_scalar(&r.x[o]);
-  k.v = load_scalar(&r.dt[o]) + bias;
-  k.dy = load_scalar(&r.dy[o]);
-  k.z = a.z.p ? load_scalar(&r.z[o]) : 0.f;
-  k.delta = there ? Step{k.v}.of(a.softplus) : 0.f;
-  k.ds = !there ? 0.f : a.z.p ? k.dy * (k.z * sigmoid(k.z)) : k.dy;
-  return k;
+template <typename T, bool GATE>
+__device__ __forceinline__ void tokens_of(const Raw<T, GATE>& r, float bias, bool softplus, int there,
+                                          Token (&k)[kOwn]) {
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    k[o].x = load_scalar(&r.x[o]);
+    k[o].delta = k[o].v = load_scalar(&r.dt[o]) + bias;
+    k[o].dy = k[o].ds = load_scalar(&r.dy[o]);
+    if (GATE) {
+      k[o].z = load_scalar(&r.z[o]);
+      k[o].ds = k[o].dy * (k[o].z * sigmoid(k[o].z));
+    }
+  }
+  if (softplus) {
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) k[o].delta = Step{k[o].v}.of(true);
+  }
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o)
+    if (o >= there) k[o].delta = k[o].ds = 0.f;
 }
-// delta, delta x, ds and x as the waves share them.
-__device__ __forceinline__ float4 shared_of(const Token& k, bool there) {
-  return there ? make_float4(k.delta, k.delta * k.x, k.ds, k.x) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
+// delta, delta x and ds as the waves share them.
+struct Shared {
+  float2 step[kTile][64];
+  float ds[kTile][64];
+  __device__ __forceinline__ void put(int j, int lane, const Token& k, bool there) {
+    step[j][lane] = there ? make_float2(k.delta, k.delta * k.x) : make_float2(0.f, 0.f);
+    ds[j][lane] = there ? k.ds : 0.f;
+  }
+};
 
 // Number of the 8 tokens from t on among the batch's tiles: like that of a run.
 __device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (size_t)(r.lo >> 3) + r.seq + ((t - r.lo) >> 3); }
 
-template <typename T, int Q>
+template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads) void ends_kernel(SelectArgs a) {
-  __shared__ float4 prep[2][kTile][64];
+  __shared__ Shared prep[2];
   const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
   const int slot = blockIdx.x, c = m.c, lane = (int)__lane_id();
@@ -71,48 +88,50 @@ __global__ __launch_bounds__(kThreads) void ends_kernel(SelectArgs a) {
   float A[Q], h[Q], P[Q], G[Q];
   load_rates<Q>(a, m, A);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+  const bool softplus = a.softplus;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     h[i] = G[i] = 0.f;
     P[i] = 1.f;
   }
-  Raw<T> raw;
-  auto prepare = [&](int t, float4 (&to)[kTile][64]) {
+  Raw<T, GATE> raw;
+  auto prepare = [&](int t, Shared& to) {
+    Token k[kOwn];
+    const int at = t + m.wave * kOwn;
+    tokens_of(raw, bias, softplus, r.t1 - at, k);
 #pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-      const int j = m.wave * kOwn + o;
-      const bool there = t + j < r.t1;
-      to[j][lane] = shared_of(token_of(a, raw, o, bias, there), there);
-    }
+    for (int o = 0; o < kOwn; ++o) to.put(m.wave * kOwn + o, lane, k[o], at + o < r.t1);
   };
-  load_raw(a, m, r.t0, r.t1, raw);
+  load_raw(m, r.t0, r.t1, raw);
   prepare(r.t0, prep[0]);
-  load_raw(a, m, r.t0 + kTile, r.t1, raw);
+  load_raw(m, r.t0 + kTile, r.t1, raw);
   __syncthreads();
   float gone = 0.f;
-  float* kept = reinterpret_cast<float*>(a.ws + a.at.kept);
-  float* before = reinterpret_cast<float*>(a.ws + a.at.before);
+  float* kept = reinterpret_cast<float*>(a.ws + a.at.kept) + (size_t)(m.wave * Q) * a.channels + c;
+  float* before = reinterpret_cast<float*>(a.ws + a.at.before) + c;
   int turn = 0;
   for (int t = r.t0; t < r.t1; t += kTile, turn ^= 1) {
-    Raw<T> next;
-    load_raw(a, m, t + 2 * kTile, r.t1, next);
+    Scalars<Q> scalars(TileRows<Q>(a, m, t, r.t1));
+    Raw<T, GATE> next;
+    load_raw(m, t + 2 * kTile, r.t1, next);
     const size_t tile = tile_number(r, t);
     if (m.live) {
 #pragma unroll
-      for (int i = 0; i < Q; ++i) kept[(tile * (4 * Q) + m.wave * Q + i) * a.channels + c] = h[i];
-      if (m.wave == 0) before[tile * a.channels + c] = gone;
+      for (int i = 0; i < Q; ++i) kept[(tile * (4 * Q) + i) * a.channels] = h[i];
+      if (m.wave == 0) before[tile * a.channels] = gone;
     }
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
-      const float4 k = prep[turn][j][lane];
-      const ScalarRow B = row_bc<Q>(a, m, t + j < r.t1 ? t + j : r.t1 - 1), C = B + Q;
+      const float2 k = prep[turn].step[j][lane];
+      const float ds = prep[turn].ds[j][lane];
+      const float *B = scalars.of(j), *C = B + Q;
       gone += k.x;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
         const float d = exp2_fast(k.x * A[i]);
         h[i] = d * h[i] + k.y * B[i];
         P[i] *= d;
-        G[i] += P[i] * (k.z * C[i]);
+        G[i] += P[i] * (ds * C[i]);
       }
     }
     prepare(t + kTile, prep[turn ^ 1]);
@@ -147,42 +166,32 @@ __device__ __forceinline__ float fold(float p, float q) {
     return keep + dpp_mov<ctrl>(give);
   }
 }
-// Sums over the 64 lanes of N values, 32 or 64: lane l gets that of value l
-// (of value l / 2).
-template <int N>
-__device__ __forceinline__ float fold_all(float (&v)[N]) {
-  static_assert(N == 32 || N == 64, "a wave's lanes, or half of them");
+// Sums over every fourth of the 64 lanes of 16 values: lane l gets that of
+// value l / 4 over the lanes l % 4, l % 4 + 4, ...
+__device__ __forceinline__ float fold16(float (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) v[i] = fold<5>(v[i], v[i + N / 2]);
+  for (int i = 0; i < 8; ++i) v[i] = fold<5>(v[i], v[i + 8]);
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) v[i] = fold<4>(v[i], v[i + N / 4]);
+  for (int i = 0; i < 4; ++i) v[i] = fold<4>(v[i], v[i + 4]);
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) v[i] = fold<3>(v[i], v[i + N / 8]);
-#pragma unroll
-  for (int i = 0; i < N / 16; ++i) v[i] = fold<2>(v[i], v[i + N / 16]);
-#pragma unroll
-  for (int i = 0; i < N / 32; ++i) v[i] = fold<1>(v[i], v[i + N / 32]);
-  if constexpr (N == 64) return fold<0>(v[0], v[1]);
-  else return v[0] + dpp_mov<0xB1>(v[0]);
+  for (int i = 0; i < 2; ++i) v[i] = fold<3>(v[i], v[i + 2]);
+  return fold<2>(v[0], v[1]);
 }
 
 // A set of four blocks of channels of one group (blockIdx.y) over every
 // gridDim.x-th segment.
-template <typename T, int Q>
+template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
-  constexpr int kValues = kTile * 2 * Q;                  // dB and dC of 8 tokens, a wave's states
-  constexpr int kFold = kValues < 64 ? kValues : 64, kFolds = kValues / kFold;
-  constexpr int kFoldTile = kTile / kFolds;               // tokens of a fold
-  __shared__ float4 prep[kTile][64];
+  // dB and dC of 8 tokens and a wave's states are summed over the lanes 16
+  // values at a time, those of kFoldTile tokens and kFoldStates states each
+  constexpr int kFoldTile = Q < 8 ? kTile / Q : 1, kFoldStates = Q < 8 ? Q : 8;
+  constexpr int kFolds = Q < 4 ? 1 : Q / 4;               // values a lane has at last
+  __shared__ Shared prep;
   __shared__ float4 part[kWaves][kTile][64];
   __shared__ float sums[kTiles][kWaves][kFolds][64];
   const int lane = (int)__lane_id();
   const int group = blockIdx.y / a.at.sets, set = blockIdx.y % a.at.sets;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
-  const float* starts = reinterpret_cast<const float*>(a.ws + a.at.carry);
-  const float* ends = reinterpret_cast<const float*>(a.ws + a.at.back);
-  const float* kept = reinterpret_cast<const float*>(a.ws + a.at.kept);
-  const float* before = reinterpret_cast<const float*>(a.ws + a.at.before);
 
   for (int slot = blockIdx.x; slot < a.at.slots; slot += gridDim.x) {
     const Run r = run_of(b, sequence_of(b, slot), slot);
@@ -200,97 +209,130 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
         const int n = m.wave * Q + i;
         dA[i] = H[i] = G[i] = 0.f;
         if (!none && n < a.d_state) {   // (join leaves the padding states' carries as they are)
-          H[i] = starts[carry_at<Q>(a, slot, n, c)];
-          G[i] = ends[carry_at<Q>(a, slot, n, c)];
+          H[i] = reinterpret_cast<const float*>(a.ws + a.at.carry)[carry_at<Q>(a, slot, n, c)];
+          G[i] = reinterpret_cast<const float*>(a.ws + a.at.back)[carry_at<Q>(a, slot, n, c)];
         }
       }
-      Raw<T> raw;
-      if (!none) load_raw(a, m, r.t0 + (tiles - 1) * kTile, r.t1, raw);
+      Raw<T, GATE> raw;
+      float made[Q], gone;              // before the tile: the segment's own state, its steps
+      auto load_tile = [&](int t0) {
+        load_raw(m, t0, r.t1, raw);
+        const ArgsAgain q = args_again();
+        const size_t tile = tile_number(r, t0), channels = q->channels;
+        const float* kept = reinterpret_cast<const float*>(q->ws + q->at.kept) + (tile * (4 * Q) + m.wave * Q) * channels;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) made[i] = kept[i * channels + c];
+        gone = (reinterpret_cast<const float*>(q->ws + q->at.before) + tile * channels)[c];
+      };
+      if (!none) load_tile(r.t0 + (tiles - 1) * kTile);
       for (int p = tiles - 1; p >= 0; --p) {
         const int t0 = r.t0 + p * kTile;
-        const size_t tile = tile_number(r, t0);
+        Scalars<Q> scalars(TileRows<Q>(a, m, t0, r.t1));
         float first[Q], hs[kTile][Q], d[kTile][Q];
-        const float gone = before[tile * a.channels + c];
 #pragma unroll
-        for (int i = 0; i < Q; ++i)
-          first[i] = exp2_fast(gone * A[i]) * H[i] + kept[(tile * (4 * Q) + m.wave * Q + i) * a.channels + c];
+        for (int i = 0; i < Q; ++i) first[i] = exp2_fast(gone * A[i]) * H[i] + made[i];
         Token own[kOwn];
+        const int at = t0 + m.wave * kOwn;
+        tokens_of(raw, bias, args_again()->softplus, r.t1 - at, own);
 #pragma unroll
-        for (int o = 0; o < kOwn; ++o) {
-          const int j = m.wave * kOwn + o;
-          const bool there = t0 + j < r.t1;
-          own[o] = token_of(a, raw, o, bias, there);
-          prep[j][lane] = shared_of(own[o], there);
-        }
-        if (p > 0) load_raw(a, m, t0 - kTile, r.t1, raw);
+        for (int o = 0; o < kOwn; ++o)   // lanes without a channel add nothing to dB and dC
+          prep.put(m.wave * kOwn + o, lane, own[o], at + o < r.t1 && m.live);
+        if (p > 0) load_tile(t0 - kTile);
         __syncthreads();
+        float2 k[kTile];
+        float ds[kTile];
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
-          const float4 k = prep[j][lane];
-          const ScalarRow B = row_bc<Q>(a, m, t0 + j < r.t1 ? t0 + j : r.t1 - 1);
-#pragma unroll
-          for (int i = 0; i < Q; ++i) {
-            d[j][i] = exp2_fast(k.x * A[i]);
-            hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]) + k.y * B[i];
-          }
+          k[j] = prep.step[j][lane];
+          ds[j] = prep.ds[j][lane];
         }
 #pragma unroll
-        for (int f = kFolds - 1; f >= 0; --f) {
-          float v[kFold];
+        for (int j = 0; j < kTile; ++j) {
+          const float* B = scalars.of(j);
+          if (Q > 4) next_token();
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            d[j][i] = exp2_fast(k[j].x * A[i]);
+            hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]) + k[j].y * B[i];
+          }
+        }
+        float sum[Q];     // of 16 values each: the last fold's groups of lanes
+#pragma unroll
+        for (int f = Q - 1; f >= 0; --f) {
+          float v[16];    // dB and dC of 8 / Q tokens, or of half a token's states
+          next_token();
 #pragma unroll
           for (int jj = kFoldTile - 1; jj >= 0; --jj) {
-            const int j = f * kFoldTile + jj;
-            const float4 k = prep[j][lane];
-            const ScalarRow B = row_bc<Q>(a, m, t0 + j < r.t1 ? t0 + j : r.t1 - 1), C = B + Q;
+            const int j = f * kTile / Q + jj, i0 = Q > 8 ? (f & 1) * 8 : 0;
+            const float *B = scalars.of(j), *C = B + Q;
             float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-              G[i] += k.z * C[i];
-              v[jj * 2 * Q + i] = m.live ? G[i] * k.y : 0.f;
-              v[jj * 2 * Q + Q + i] = m.live ? k.z * hs[j][i] : 0.f;
-              s += C[i] * hs[j][i];
+            for (int ii = 0; ii < kFoldStates; ++ii) {
+              const int i = i0 + ii;
+              G[i] += ds[j] * C[i];
+              v[(jj * 2 + 0) * kFoldStates + ii] = G[i] * k[j].y;
+              v[(jj * 2 + 1) * kFoldStates + ii] = ds[j] * hs[j][i];
+              if (GATE) s += C[i] * hs[j][i];
               du += G[i] * B[i];
               G[i] *= d[j][i];
               const float q = G[i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
               rate += A[i] * q;
-              dA[i] += k.x * q;
+              dA[i] += k[j].x * q;
             }
-            part[m.wave][j][lane] = make_float4(s, du, rate, 0.f);
+            float4& to = part[m.wave][j][lane];
+            if (Q > 8 && i0 == 0) {   // the upper half of the token's states came first
+              const float4 o = to;
+              s += o.x;
+              du += o.y;
+              rate += o.z;
+            }
+            to = make_float4(s, du, rate, 0.f);
           }
-          const float total = fold_all(v);
+          sum[f] = fold16(v);
+        }
+#pragma unroll
+        for (int f = 0; f < kFolds; ++f) {
+          float total;
+          if constexpr (Q > 2) total = fold<0>(fold<1>(sum[4 * f], sum[4 * f + 2]), fold<1>(sum[4 * f + 1], sum[4 * f + 3]));
+          else {
+            total = fold<1>(sum[0], sum[1]);
+            total += dpp_mov<0xB1>(total);
+          }
           float& to = sums[p][m.wave][f][lane];
           to = block == set * kSet ? total : to + total;
         }
         __syncthreads();
         if (!m.live) continue;
+        const ArgsAgain q = args_again();
 #pragma unroll
         for (int o = 0; o < kOwn; ++o) {
-          const int j = m.wave * kOwn + o, t = t0 + j;
+          const int j = m.wave * kOwn + o;
+          const long long t = t0 + j;
           if (t >= r.t1) continue;
           const Token& k = own[o];
           float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) {
-            const float4 q = part[w][j][lane];
-            s += q.x;
-            du += q.y;
-            rate += q.z;
+            const float4 v = part[w][j][lane];
+            if (GATE) s += v.x;
+            du += v.y;
+            rate += v.z;
           }
-          const float dv = (k.x * du + rate * kLn2) * Step{k.v}.slope(a.softplus);
+          const float dv = (k.x * du + rate * kLn2) * Step{k.v}.slope(q->softplus);
           dbias += dv;
           dD += k.ds * k.x;
           Packed<1, T> out;
           float one[1] = {k.delta * du + D * k.ds};
           out.from(one);
-          out.store(row_of<T>(a.dx, t) + c);
+          out.store(static_cast<T*>(q->dx.p) + t * q->dx.stride + c);
           one[0] = dv;
           out.from(one);
-          out.store(row_of<T>(a.ddt, t) + c);
-          if (a.z.p) {
+          out.store(static_cast<T*>(q->ddt.p) + t * q->ddt.stride + c);
+          if (GATE) {
             const float g = sigmoid(k.z);
             one[0] = k.dy * (s + D * k.x) * (g + k.z * g * (1.f - g));
             out.from(one);
-            out.store(row_of<T>(a.dz, t) + c);
+            out.store(static_cast<T*>(q->dz.p) + t * q->dz.stride + c);
           }
         }
       }
@@ -316,15 +358,19 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
         }
       }
     }
-    // dB and dC of the set
-    const int wave = (int)threadIdx.x >> 6, share = kFold < 64 ? 2 : 1, value = lane / share;
+    // dB and dC of the set: lane l has value l / 4 of fold 4 f + l % 4 (Q = 2:
+    // of fold l / 2 % 2)
+    const int wave = (int)threadIdx.x >> 6;
     for (int p = 0; p < tiles; ++p)
 #pragma unroll
       for (int f = 0; f < kFolds; ++f) {
-        const int at = f * kFold + value, t = r.t0 + p * kTile + at / (2 * Q);
-        if (t < r.t1 && lane % share == 0)
+        const int fold = Q > 2 ? 4 * f + (lane & 3) : lane >> 1 & 1, value = lane >> 2;
+        const int jj = value / (2 * kFoldStates), what = value / kFoldStates & 1;
+        const int j = fold * kTile / Q + jj, i = (Q > 8 ? (fold & 1) * 8 : 0) + value % kFoldStates;
+        const int t = r.t0 + p * kTile + j;
+        if (t < r.t1 && (Q > 2 || (lane & 1) == 0))
           reinterpret_cast<float*>(a.ws + a.at.sums)[((((size_t)set * a.tokens + t) * a.groups + group) * 4 + wave) * (2 * Q) +
-                                                     at % (2 * Q)] = sums[p][wave][f][lane];
+                                                     what * Q + i] = sums[p][wave][f][lane];
       }
   }
 }
@@ -374,11 +420,14 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(SelectArgs a, int par
 
 template <typename T, int Q>
 hipError_t grads_types(const SelectArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((ends_kernel<T, Q>), dim3(a.at.slots, a.groups * a.at.blocks), dim3(kThreads), 0, stream, a);
+  const dim3 ends(a.at.slots, a.groups * a.at.blocks), grads(a.at.parts, a.groups * a.at.sets);
+  if (a.z.p) hipLaunchKernelGGL((ends_kernel<T, Q, true>), ends, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((ends_kernel<T, Q, false>), ends, dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = launch_select_join(a, true, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((grads_kernel<T, Q>), dim3(a.at.parts, a.groups * a.at.sets), dim3(kThreads), 0, stream, a);
+  if (a.z.p) hipLaunchKernelGGL((grads_kernel<T, Q, true>), grads, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((grads_kernel<T, Q, false>), grads, dim3(kThreads), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t values = (size_t)a.tokens * a.groups * 8 * Q, blocks = (values + kThreads - 1) / kThreads;
