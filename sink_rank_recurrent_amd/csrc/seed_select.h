@@ -13,8 +13,13 @@
 // channels and a quarter of the states each, in registers.  What a token needs
 // once per channel (softplus, gate, the gradients of x, dt and z) is shared
 // out among the waves, two of every eight tokens each, and goes through LDS.
-// B and C of a token are the same for a wave's lanes: they are scalar operands,
-// read through the scalar cache from fp32 rows (prepare_kernel).
+// B and C of a token are the same for a wave's lanes.  Where they multiply a
+// state each (C.h, G.B) they are scalar operands, read through the scalar cache
+// from fp32 rows (prepare_kernel).  Where they make an outer product with the
+// channels (h += B u, G += C ds) a matrix instruction of 4 x 4 blocks adds four
+// states of 64 channels at once: 4 x 1 values of a token's row, the same in
+// every block, times 1 x 4 channels, onto accumulators that lie as the states
+// do.
 #pragma once
 
 #include "seed_channels.h"
@@ -86,18 +91,31 @@ __device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, f
   }
 }
 
-// B and C of the tokens of a tile for a wave's states.  `last`: the last token
-// of the sequence or segment, counted from the tile's first; tokens behind it
-// take its row (their steps are zero, but a row of another sequence may hold
-// an infinity).
+// The call's arguments, read again from where the launch put them: pointers and
+// strides of a dozen arrays, each used once a tile, would take the scalar
+// registers that the rows of B and C need.
+typedef const __attribute__((address_space(4))) SelectArgs* ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+  auto p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// The rows of B and C: [token][group][wave][its Q states][B, C].
+// Those of the tokens of a tile for a wave's states, by scalar loads.  `last`:
+// the last token of the sequence or segment, counted from the tile's first;
+// tokens behind it take its row (their steps are zero, but a row of another
+// sequence may hold an infinity).
 template <int Q>
 struct TileRows {
   uintptr_t base;
   uint32_t step;
   int last;
-  __device__ __forceinline__ TileRows(const SelectArgs& a, const Mine& m, int t, int t1)
-      : base((uintptr_t)(a.ws + a.at.rows) + (((size_t)t * a.groups + m.group) * 4 + m.wave) * (8 * Q)),
-        step((uint32_t)a.groups * (32 * Q)), last(t1 - 1 - t) {}
+  __device__ __forceinline__ TileRows(const Mine& m, int t, int t1) : last(t1 - 1 - t) {
+    const ArgsAgain a = args_again();
+    base = (uintptr_t)(a->ws + a->at.rows) + (((size_t)t * a->groups + m.group) * 4 + m.wave) * (8 * Q);
+    step = (uint32_t)a->groups * (32 * Q);
+  }
   __device__ __forceinline__ ScalarRow operator[](int j) const {
     return (ScalarRow)(base + (uint32_t)(j < last ? j : last) * step);
   }
@@ -116,7 +134,7 @@ struct Scalars {
         for (int i = 0; i < 2 * Q; ++i) v[j][i] = rows[j][i];
     }
   }
-  // B and, Q floats on, C of token j
+  // B of state i at 2 i, C at 2 i + 1
   __device__ __forceinline__ const float* of(int j) {
     if constexpr (Q <= 4) {
       return v[j];
@@ -127,18 +145,70 @@ struct Scalars {
     }
   }
 };
+
+// The tile's rows for the outer products (Q >= 4): through LDS, Q / 4 values a
+// thread.
+template <int Q>
+struct RowTile {
+  static constexpr int kFloats = kTile * 8 * Q;
+  float v[Q >= 4 ? Q / 4 : 1];
+  __device__ __forceinline__ void load(int group, int t, int t1) {
+    if constexpr (Q >= 4) {
+      const ArgsAgain a = args_again();
+      const float* rows = reinterpret_cast<const float*>(a->ws + a->at.rows);
+#pragma unroll
+      for (int q = 0; q < Q / 4; ++q) {
+        const int at = q * kThreads + (int)threadIdx.x, j = at / (8 * Q), in = at % (8 * Q);
+        const size_t row = t + j < t1 ? t + j : t1 - 1;
+        v[q] = rows[(row * a->groups + group) * (8 * Q) + in];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* lds) const {
+    if constexpr (Q >= 4) {
+#pragma unroll
+      for (int q = 0; q < Q / 4; ++q) lds[q * kThreads + (int)threadIdx.x] = v[q];
+    }
+  }
+};
+// A lane's values of token j's row: B and C of state l % 4 of every four.
+template <int Q>
+struct Outer {
+  float2 v[Q >= 4 ? Q / 4 : 1];
+  __device__ __forceinline__ void load(const float* lds, const Mine& m, int j) {
+    if constexpr (Q >= 4) {
+#pragma unroll
+      for (int q = 0; q < Q / 4; ++q)
+        v[q] = reinterpret_cast<const float2*>(lds + (j * 4 + m.wave) * (2 * Q))[4 * q + (int)(__lane_id() & 3)];
+    }
+  }
+};
+// s + row x, for B (WHAT 0) or C (1) of a token: four states an instruction.
+// (Q = 2: multiply-adds with the scalars.)
+template <int Q, int WHAT>
+__device__ __forceinline__ void add_outer(float (&s)[Q], const Outer<Q>& o, const float* scalars, float x) {
+  if constexpr (Q >= 4) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int q = 0; q < Q / 4; ++q) {
+      f32x4 acc = {s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]};
+      acc = __builtin_amdgcn_mfma_f32_4x4x1f32(WHAT ? o.v[q].y : o.v[q].x, x, acc, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[4 * q + i] = acc[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < Q; ++i) s[i] += x * scalars[2 * i + WHAT];
+  }
+}
 // Nothing is moved over this point: what a token needs, in registers or on its
 // way, does not pile up with the other tokens'.
 __device__ __forceinline__ void next_token() { __builtin_amdgcn_sched_barrier(0); }
-
-// The call's arguments, read again from where the launch put them: pointers and
-// strides of a dozen arrays, each used once a tile, would take the scalar
-// registers that the rows of B and C need.
-typedef const __attribute__((address_space(4))) SelectArgs* ArgsAgain;
-__device__ __forceinline__ ArgsAgain args_again() {
-  auto p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return p;
+// ... and what these have come to is worked out here, not where it is used.
+template <int Q>
+__device__ __forceinline__ void settle(float (&x)[Q]) {
+#pragma unroll
+  for (int i = 0; i < Q; ++i) asm volatile("" : "+v"(x[i]));
 }
 
 template <typename T>

@@ -6,7 +6,7 @@ namespace seed {
 namespace channels {
 namespace {
 
-// B and C of every token in fp32, [token][group][wave][B, C of its Q states],
+// B and C of every token in fp32, [token][group][wave][its Q states][B, C],
 // padded with zeros.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
@@ -14,7 +14,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
   float* out = reinterpret_cast<float*>(a.ws + a.at.rows);
   const size_t total = (size_t)a.tokens * a.groups * 8 * Q, step = (size_t)gridDim.x * kThreads;
   for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
-    const int in = (int)(i % (8 * Q)), n = in / (2 * Q) * Q + in % Q, what = in / Q & 1;
+    const int n = (int)(i % (8 * Q)) / 2, what = (int)i & 1;
     const size_t tg = i / (8 * Q), t = tg / a.groups;
     const int g = (int)(tg - t * a.groups);
     float x = 0.f;
@@ -60,9 +60,10 @@ __device__ __forceinline__ int ranked(const Batch& b, int rank) {
 // segment leaves of zero, and the sum of its steps; kRead: a segment's
 // read-outs from its first state.
 template <typename T, int Q, int MODE>
-__global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   __shared__ float2 prep[2][kTile][64];                           // delta, delta x
   __shared__ float part[MODE == kCarry ? 1 : 2][kWaves][kTile][64];
+  __shared__ float rows[2][RowTile<Q>::kFloats];
   const int block = MODE == kWhole ? blockIdx.x : blockIdx.y;
   const Mine m = mine(a, block / a.at.blocks, block % a.at.blocks);
   const int lane = (int)__lane_id(), c = m.c;
@@ -109,16 +110,22 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
       if (MODE == kCarry && there) gone += delta;
     }
   };
+  RowTile<Q> row;
   if (t0 < t1) {
     load_raw(a, m, t0, t1, gate, raw);
+    row.load(m.group, t0, t1);
     prepare(t0, prep[0]);
+    row.store(rows[0]);
     load_raw(a, m, t0 + kTile, t1, gate, raw);
+    row.load(m.group, t0 + kTile, t1);
     __syncthreads();
   }
   int turn = 0;
   for (int t = t0; t < t1; t += kTile, turn ^= 1) {
     load_raw(a, m, t + 2 * kTile, t1, gate, next);
-    const TileRows<Q> rows(a, m, t, t1);
+    RowTile<Q> next_row;
+    next_row.load(m.group, t + 2 * kTile, t1);
+    Scalars<Q> scalars(TileRows<Q>(m, t, t1));
     float xs[kOwn], zs[kOwn];
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
@@ -128,17 +135,23 @@ __global__ __launch_bounds__(kThreads) void scan_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       const float2 k = prep[turn][j][lane];
-      const ScalarRow B = rows[j], C = B + Q;
+      Outer<Q> outer;
+      outer.load(rows[turn], m, j);
+      const float* BC = scalars.of(j);
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        h[i] = exp2_fast(k.x * A[i]) * h[i] + k.y * B[i];
-        if (MODE != kCarry) s += C[i] * h[i];
+      for (int i = 0; i < Q; ++i) h[i] *= exp2_fast(k.x * A[i]);
+      add_outer<Q, 0>(h, outer, BC, k.y);
+      if (MODE != kCarry) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i) s += BC[2 * i + 1] * h[i];
+        part[turn][m.wave][j][lane] = s;
       }
-      if (MODE != kCarry) part[turn][m.wave][j][lane] = s;
     }
     prepare(t + kTile, prep[turn ^ 1]);
+    row.store(rows[turn ^ 1]);
     raw = next;
+    row = next_row;
     __syncthreads();
     if (MODE == kCarry || !m.live) continue;
 #pragma unroll

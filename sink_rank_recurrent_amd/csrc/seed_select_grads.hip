@@ -78,8 +78,9 @@ struct Shared {
 __device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (size_t)(r.lo >> 3) + r.seq + ((t - r.lo) >> 3); }
 
 template <typename T, int Q, bool GATE>
-__global__ __launch_bounds__(kThreads) void ends_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_kernel(SelectArgs a) {
   __shared__ Shared prep[2];
+  __shared__ float rows[2][RowTile<Q>::kFloats];
   const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
   const int slot = blockIdx.x, c = m.c, lane = (int)__lane_id();
@@ -102,40 +103,63 @@ __global__ __launch_bounds__(kThreads) void ends_kernel(SelectArgs a) {
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) to.put(m.wave * kOwn + o, lane, k[o], at + o < r.t1);
   };
+  RowTile<Q> row;
   load_raw(m, r.t0, r.t1, raw);
+  row.load(m.group, r.t0, r.t1);
   prepare(r.t0, prep[0]);
+  row.store(rows[0]);
   load_raw(m, r.t0 + kTile, r.t1, raw);
+  row.load(m.group, r.t0 + kTile, r.t1);
   __syncthreads();
   float gone = 0.f;
   float* kept = reinterpret_cast<float*>(a.ws + a.at.kept) + (size_t)(m.wave * Q) * a.channels + c;
   float* before = reinterpret_cast<float*>(a.ws + a.at.before) + c;
   int turn = 0;
   for (int t = r.t0; t < r.t1; t += kTile, turn ^= 1) {
-    Scalars<Q> scalars(TileRows<Q>(a, m, t, r.t1));
     Raw<T, GATE> next;
+    RowTile<Q> next_row;
     load_raw(m, t + 2 * kTile, r.t1, next);
+    next_row.load(m.group, t + 2 * kTile, r.t1);
     const size_t tile = tile_number(r, t);
     if (m.live) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) kept[(tile * (4 * Q) + i) * a.channels] = h[i];
       if (m.wave == 0) before[tile * a.channels] = gone;
     }
+    const TileRows<Q> tile_rows(m, t, r.t1);
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
+      if (j > 0 && j % 2 == 0) {
+        settle(P);
+        settle(G);
+        next_token();
+      }
       const float2 k = prep[turn].step[j][lane];
       const float ds = prep[turn].ds[j][lane];
-      const float *B = scalars.of(j), *C = B + Q;
+      Outer<Q> outer;
+      outer.load(rows[turn], m, j);
+      float BC[2 * Q], dsC[Q];
+      if (Q < 4) {
+#pragma unroll
+        for (int i = 0; i < 2 * Q; ++i) BC[i] = tile_rows[j][i];
+      }
       gone += k.x;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
         const float d = exp2_fast(k.x * A[i]);
-        h[i] = d * h[i] + k.y * B[i];
+        h[i] *= d;
         P[i] *= d;
-        G[i] += P[i] * (ds * C[i]);
+        dsC[i] = 0.f;
       }
+      add_outer<Q, 0>(h, outer, BC, k.y);
+      add_outer<Q, 1>(dsC, outer, BC, ds);
+#pragma unroll
+      for (int i = 0; i < Q; ++i) G[i] += P[i] * dsC[i];
     }
     prepare(t + kTile, prep[turn ^ 1]);
+    row.store(rows[turn ^ 1]);
     raw = next;
+    row = next_row;
     __syncthreads();
   }
   if (!m.live) return;
@@ -181,12 +205,13 @@ __device__ __forceinline__ float fold16(float (&v)[16]) {
 // A set of four blocks of channels of one group (blockIdx.y) over every
 // gridDim.x-th segment.
 template <typename T, int Q, bool GATE>
-__global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_kernel(SelectArgs a) {
   // dB and dC of 8 tokens and a wave's states are summed over the lanes 16
   // values at a time, those of kFoldTile tokens and kFoldStates states each
   constexpr int kFoldTile = Q < 8 ? kTile / Q : 1, kFoldStates = Q < 8 ? Q : 8;
   constexpr int kFolds = Q < 4 ? 1 : Q / 4;               // values a lane has at last
   __shared__ Shared prep;
+  __shared__ float rows[RowTile<Q>::kFloats];
   __shared__ float4 part[kWaves][kTile][64];
   __shared__ float sums[kTiles][kWaves][kFolds][64];
   const int lane = (int)__lane_id();
@@ -214,9 +239,11 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
         }
       }
       Raw<T, GATE> raw;
+      RowTile<Q> row;
       float made[Q], gone;              // before the tile: the segment's own state, its steps
       auto load_tile = [&](int t0) {
         load_raw(m, t0, r.t1, raw);
+        row.load(group, t0, r.t1);
         const ArgsAgain q = args_again();
         const size_t tile = tile_number(r, t0), channels = q->channels;
         const float* kept = reinterpret_cast<const float*>(q->ws + q->at.kept) + (tile * (4 * Q) + m.wave * Q) * channels;
@@ -227,7 +254,7 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
       if (!none) load_tile(r.t0 + (tiles - 1) * kTile);
       for (int p = tiles - 1; p >= 0; --p) {
         const int t0 = r.t0 + p * kTile;
-        Scalars<Q> scalars(TileRows<Q>(a, m, t0, r.t1));
+        Scalars<Q> scalars(TileRows<Q>(m, t0, r.t1));
         float first[Q], hs[kTile][Q], d[kTile][Q];
 #pragma unroll
         for (int i = 0; i < Q; ++i) first[i] = exp2_fast(gone * A[i]) * H[i] + made[i];
@@ -237,25 +264,25 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
 #pragma unroll
         for (int o = 0; o < kOwn; ++o)   // lanes without a channel add nothing to dB and dC
           prep.put(m.wave * kOwn + o, lane, own[o], at + o < r.t1 && m.live);
+        row.store(rows);
         if (p > 0) load_tile(t0 - kTile);
         __syncthreads();
-        float2 k[kTile];
-        float ds[kTile];
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
-          k[j] = prep.step[j][lane];
-          ds[j] = prep.ds[j][lane];
-        }
-#pragma unroll
-        for (int j = 0; j < kTile; ++j) {
-          const float* B = scalars.of(j);
-          if (Q > 4) next_token();
+          const float* BC = Q < 4 ? scalars.of(j) : nullptr;
+          if (j % 2 == 0) next_token();
+          const float2 k = prep.step[j][lane];
+          Outer<Q> outer;
+          outer.load(rows, m, j);
 #pragma unroll
           for (int i = 0; i < Q; ++i) {
-            d[j][i] = exp2_fast(k[j].x * A[i]);
-            hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]) + k[j].y * B[i];
+            d[j][i] = exp2_fast(k.x * A[i]);
+            hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
           }
+          add_outer<Q, 0>(hs[j], outer, BC, k.y);
         }
+        int again = lane;   // the steps are read a second time: 24 registers less
+        asm volatile("" : "+v"(again));
         float sum[Q];     // of 16 values each: the last fold's groups of lanes
 #pragma unroll
         for (int f = Q - 1; f >= 0; --f) {
@@ -264,20 +291,26 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
 #pragma unroll
           for (int jj = kFoldTile - 1; jj >= 0; --jj) {
             const int j = f * kTile / Q + jj, i0 = Q > 8 ? (f & 1) * 8 : 0;
-            const float *B = scalars.of(j), *C = B + Q;
+            const float* BC = scalars.of(j);
+            const float2 k = prep.step[j][again];
+            const float ds = prep.ds[j][again];
+            if (Q <= 8 || i0 > 0) {
+              Outer<Q> outer;
+              outer.load(rows, m, j);
+              add_outer<Q, 1>(G, outer, BC, ds);
+            }
             float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
             for (int ii = 0; ii < kFoldStates; ++ii) {
               const int i = i0 + ii;
-              G[i] += ds[j] * C[i];
-              v[(jj * 2 + 0) * kFoldStates + ii] = G[i] * k[j].y;
-              v[(jj * 2 + 1) * kFoldStates + ii] = ds[j] * hs[j][i];
-              if (GATE) s += C[i] * hs[j][i];
-              du += G[i] * B[i];
+              v[(jj * 2 + 0) * kFoldStates + ii] = G[i] * k.y;
+              v[(jj * 2 + 1) * kFoldStates + ii] = ds * hs[j][i];
+              if (GATE) s += BC[2 * i + 1] * hs[j][i];
+              du += G[i] * BC[2 * i];
               G[i] *= d[j][i];
               const float q = G[i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
               rate += A[i] * q;
-              dA[i] += k[j].x * q;
+              dA[i] += k.x * q;
             }
             float4& to = part[m.wave][j][lane];
             if (Q > 8 && i0 == 0) {   // the upper half of the token's states came first
@@ -289,6 +322,8 @@ __global__ __launch_bounds__(kThreads) void grads_kernel(SelectArgs a) {
             to = make_float4(s, du, rate, 0.f);
           }
           sum[f] = fold16(v);
+          settle(G);
+          settle(dA);
         }
 #pragma unroll
         for (int f = 0; f < kFolds; ++f) {
