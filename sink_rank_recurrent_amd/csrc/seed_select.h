@@ -146,31 +146,37 @@ struct Scalars {
   }
 };
 
-// The tile's rows for the outer products (Q >= 4): through LDS, Q / 4 values a
-// thread.
+// The tile's rows in LDS: Q / 4 values a thread (Q = 2: one of every second).
 template <int Q>
 struct RowTile {
   static constexpr int kFloats = kTile * 8 * Q;
   float v[Q >= 4 ? Q / 4 : 1];
   __device__ __forceinline__ void load(int group, int t, int t1) {
-    if constexpr (Q >= 4) {
-      const ArgsAgain a = args_again();
-      const float* rows = reinterpret_cast<const float*>(a->ws + a->at.rows);
+    const ArgsAgain a = args_again();
+    const float* rows = reinterpret_cast<const float*>(a->ws + a->at.rows);
 #pragma unroll
-      for (int q = 0; q < Q / 4; ++q) {
-        const int at = q * kThreads + (int)threadIdx.x, j = at / (8 * Q), in = at % (8 * Q);
-        const size_t row = t + j < t1 ? t + j : t1 - 1;
-        v[q] = rows[(row * a->groups + group) * (8 * Q) + in];
-      }
+    for (int q = 0; q < (kFloats + kThreads - 1) / kThreads; ++q) {
+      const int at = (q * kThreads + (int)threadIdx.x) % kFloats, j = at / (8 * Q), in = at % (8 * Q);
+      const size_t row = t + j < t1 ? t + j : t1 - 1;
+      v[q] = rows[(row * a->groups + group) * (8 * Q) + in];
     }
   }
   __device__ __forceinline__ void store(float* lds) const {
-    if constexpr (Q >= 4) {
 #pragma unroll
-      for (int q = 0; q < Q / 4; ++q) lds[q * kThreads + (int)threadIdx.x] = v[q];
-    }
+    for (int q = 0; q < (kFloats + kThreads - 1) / kThreads; ++q)
+      lds[(q * kThreads + (int)threadIdx.x) % kFloats] = v[q];
   }
 };
+// Token j's row for a wave's states, the same in every lane: B of state i at
+// 2 i, C at 2 i + 1.
+template <int Q>
+__device__ __forceinline__ void row_values(const float* lds, const Mine& m, int j, float (&v)[2 * Q]) {
+#pragma unroll
+  for (int q = 0; q < Q / 2; ++q) {
+    const float4 x = reinterpret_cast<const float4*>(lds + (j * 4 + m.wave) * (2 * Q))[q];
+    v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+  }
+}
 // A lane's values of token j's row: B and C of state l % 4 of every four.
 template <int Q>
 struct Outer {
@@ -201,6 +207,17 @@ __device__ __forceinline__ void add_outer(float (&s)[Q], const Outer<Q>& o, cons
     for (int i = 0; i < Q; ++i) s[i] += x * scalars[2 * i + WHAT];
   }
 }
+// A lane's value in row t of an array over tokens: the row's address is
+// scalar, `at` the lane's bytes into it (channels are at most 2^20).
+template <typename T>
+__device__ __forceinline__ const T* in_row(const void* p, long long stride, int t, uint32_t at) {
+  return reinterpret_cast<const T*>(static_cast<const char*>(p) + (long long)t * stride * (long long)sizeof(T) + at);
+}
+template <typename T>
+__device__ __forceinline__ T* in_row(void* p, long long stride, int t, uint32_t at) {
+  return reinterpret_cast<T*>(static_cast<char*>(p) + (long long)t * stride * (long long)sizeof(T) + at);
+}
+
 // Nothing is moved over this point: what a token needs, in registers or on its
 // way, does not pile up with the other tokens'.
 __device__ __forceinline__ void next_token() { __builtin_amdgcn_sched_barrier(0); }

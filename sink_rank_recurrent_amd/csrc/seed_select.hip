@@ -34,10 +34,11 @@ template <typename T>
 __device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int t, int t1, bool gate, Raw<T>& r) {
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
-    const int at = t + m.wave * kOwn + o, in = at < t1 ? at : t1 - 1;
-    r.x[o] = row_of<T>(a.x, in)[m.c];
-    r.dt[o] = row_of<T>(a.dt, in)[m.c];
-    if (gate) r.z[o] = row_of<T>(a.z, in)[m.c];
+    const int at = t + m.wave * kOwn + o, row = at < t1 ? at : t1 - 1;
+    const uint32_t in = (uint32_t)m.c * sizeof(T);
+    r.x[o] = *in_row<T>(a.x.p, a.x.stride, row, in);
+    r.dt[o] = *in_row<T>(a.dt.p, a.dt.stride, row, in);
+    if (gate) r.z[o] = *in_row<T>(a.z.p, a.z.stride, row, in);
   }
 }
 
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
       if (gate) y[0] *= zs[o] * sigmoid(zs[o]);
       Packed<1, T> out;
       out.from(y);
-      out.store(row_of<T>(a.y, t + j) + c);
+      out.store(in_row<T>(a.y.p, a.y.stride, t + j, (uint32_t)c * sizeof(T)));
     }
   }
   if (MODE == kCarry) {

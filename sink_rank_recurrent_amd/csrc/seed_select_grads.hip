@@ -29,12 +29,12 @@ __device__ __forceinline__ void load_raw(const Mine& m, int t, int t1, Raw<T, GA
   const ArgsAgain a = args_again();
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
-    const int at = t + m.wave * kOwn + o;
-    const long long in = at < t1 ? at : t1 - 1;
-    r.x[o] = (static_cast<const T*>(a->x.p) + in * a->x.stride)[m.c];
-    r.dt[o] = (static_cast<const T*>(a->dt.p) + in * a->dt.stride)[m.c];
-    r.dy[o] = (static_cast<const T*>(a->dy.p) + in * a->dy.stride)[m.c];
-    if (GATE) r.z[o] = (static_cast<const T*>(a->z.p) + in * a->z.stride)[m.c];
+    const int at = t + m.wave * kOwn + o, row = at < t1 ? at : t1 - 1;
+    const uint32_t in = (uint32_t)m.c * sizeof(T);
+    r.x[o] = *in_row<T>(a->x.p, a->x.stride, row, in);
+    r.dt[o] = *in_row<T>(a->dt.p, a->dt.stride, row, in);
+    r.dy[o] = *in_row<T>(a->dy.p, a->dy.stride, row, in);
+    if (GATE) r.z[o] = *in_row<T>(a->z.p, a->z.stride, row, in);
   }
 }
 
@@ -112,8 +112,6 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
   row.load(m.group, r.t0 + kTile, r.t1);
   __syncthreads();
   float gone = 0.f;
-  float* kept = reinterpret_cast<float*>(a.ws + a.at.kept) + (size_t)(m.wave * Q) * a.channels + c;
-  float* before = reinterpret_cast<float*>(a.ws + a.at.before) + c;
   int turn = 0;
   for (int t = r.t0; t < r.t1; t += kTile, turn ^= 1) {
     Raw<T, GATE> next;
@@ -122,11 +120,15 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
     next_row.load(m.group, t + 2 * kTile, r.t1);
     const size_t tile = tile_number(r, t);
     if (m.live) {
+      const ArgsAgain q = args_again();
+      const size_t channels = q->channels;
+      float* kept = reinterpret_cast<float*>(q->ws + q->at.kept) + (tile * (4 * Q) + m.wave * Q) * channels;
+      const uint32_t in = (uint32_t)c * sizeof(float);
 #pragma unroll
-      for (int i = 0; i < Q; ++i) kept[(tile * (4 * Q) + i) * a.channels] = h[i];
-      if (m.wave == 0) before[tile * a.channels] = gone;
+      for (int i = 0; i < Q; ++i) *in_row<float>(kept, channels, i, in) = h[i];
+      if (m.wave == 0)
+        *in_row<float>(reinterpret_cast<float*>(q->ws + q->at.before) + tile * channels, 0, 0, in) = gone;
     }
-    const TileRows<Q> tile_rows(m, t, r.t1);
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       if (j > 0 && j % 2 == 0) {
@@ -139,10 +141,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
       Outer<Q> outer;
       outer.load(rows[turn], m, j);
       float BC[2 * Q], dsC[Q];
-      if (Q < 4) {
-#pragma unroll
-        for (int i = 0; i < 2 * Q; ++i) BC[i] = tile_rows[j][i];
-      }
+      if (Q < 4) row_values<Q>(rows[turn], m, j, BC);
       gone += k.x;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
@@ -187,7 +186,7 @@ __device__ __forceinline__ float fold(float p, float q) {
     const bool high = (__lane_id() >> BIT) & 1;
     const float keep = high ? q : p, give = high ? p : q;
     constexpr int ctrl = BIT == 3 ? 0x128 : BIT == 2 ? 0x141 : BIT == 1 ? 0x4E : 0xB1;
-    return keep + dpp_mov<ctrl>(give);
+    return keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), ctrl, 0xf, 0xf, true));
   }
 }
 // Sums over every fourth of the 64 lanes of 16 values: lane l gets that of
@@ -247,14 +246,14 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
         const ArgsAgain q = args_again();
         const size_t tile = tile_number(r, t0), channels = q->channels;
         const float* kept = reinterpret_cast<const float*>(q->ws + q->at.kept) + (tile * (4 * Q) + m.wave * Q) * channels;
+        const uint32_t in = (uint32_t)c * sizeof(float);
 #pragma unroll
-        for (int i = 0; i < Q; ++i) made[i] = kept[i * channels + c];
-        gone = (reinterpret_cast<const float*>(q->ws + q->at.before) + tile * channels)[c];
+        for (int i = 0; i < Q; ++i) made[i] = *in_row<float>(kept, channels, i, in);
+        gone = *in_row<float>(reinterpret_cast<const float*>(q->ws + q->at.before) + tile * channels, 0, 0, in);
       };
       if (!none) load_tile(r.t0 + (tiles - 1) * kTile);
       for (int p = tiles - 1; p >= 0; --p) {
         const int t0 = r.t0 + p * kTile;
-        Scalars<Q> scalars(TileRows<Q>(m, t0, r.t1));
         float first[Q], hs[kTile][Q], d[kTile][Q];
 #pragma unroll
         for (int i = 0; i < Q; ++i) first[i] = exp2_fast(gone * A[i]) * H[i] + made[i];
@@ -269,8 +268,9 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
-          const float* BC = Q < 4 ? scalars.of(j) : nullptr;
-          if (j % 2 == 0) next_token();
+          if (Q >= 4 && j % 2 == 0) next_token();
+          float BC[2 * Q];
+          if (Q < 4) row_values<Q>(rows, m, j, BC);
           const float2 k = prep.step[j][lane];
           Outer<Q> outer;
           outer.load(rows, m, j);
@@ -291,7 +291,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
 #pragma unroll
           for (int jj = kFoldTile - 1; jj >= 0; --jj) {
             const int j = f * kTile / Q + jj, i0 = Q > 8 ? (f & 1) * 8 : 0;
-            const float* BC = scalars.of(j);
+            float BC[2 * Q];
+            row_values<Q>(rows, m, j, BC);
             const float2 k = prep.step[j][again];
             const float ds = prep.ds[j][again];
             if (Q <= 8 || i0 > 0) {
@@ -342,7 +343,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
 #pragma unroll
         for (int o = 0; o < kOwn; ++o) {
           const int j = m.wave * kOwn + o;
-          const long long t = t0 + j;
+          const int t = t0 + j;
+          const uint32_t in = (uint32_t)c * sizeof(T);
           if (t >= r.t1) continue;
           const Token& k = own[o];
           float s = 0.f, du = 0.f, rate = 0.f;
@@ -359,15 +361,15 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           Packed<1, T> out;
           float one[1] = {k.delta * du + D * k.ds};
           out.from(one);
-          out.store(static_cast<T*>(q->dx.p) + t * q->dx.stride + c);
+          out.store(in_row<T>(q->dx.p, q->dx.stride, t, in));
           one[0] = dv;
           out.from(one);
-          out.store(static_cast<T*>(q->ddt.p) + t * q->ddt.stride + c);
+          out.store(in_row<T>(q->ddt.p, q->ddt.stride, t, in));
           if (GATE) {
             const float g = sigmoid(k.z);
             one[0] = k.dy * (s + D * k.x) * (g + k.z * g * (1.f - g));
             out.from(one);
-            out.store(static_cast<T*>(q->dz.p) + t * q->dz.stride + c);
+            out.store(in_row<T>(q->dz.p, q->dz.stride, t, in));
           }
         }
       }
