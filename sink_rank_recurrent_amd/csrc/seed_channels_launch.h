@@ -54,7 +54,7 @@ bool short_conv_fits(int n_seq, int channels, int tokens);
 struct SelectLayout {
   int quarter;      // 2, 4, 8 or 16
   int blocks;       // blocks of 64 channels of a group
-  int sets;         // sets of four blocks, a workgroup's (backward)
+  int set, sets;    // blocks that a workgroup takes one after the other, and how many such sets (backward)
   int shift;        // log2 of a segment's tokens; -1: whole sequences (forward)
   int slots;        // segments: tokens / 2^shift + n_seq
   int parts;        // workgroups over the segments (backward)

@@ -31,6 +31,7 @@ constexpr int kWaves = 4;       // of a workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 8;        // tokens that go through LDS together
 constexpr int kOwn = kTile / kWaves;   // of them prepared by one wave
+constexpr int kBackShift = 7;   // log2 of the tokens of a segment of the backward pass
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 typedef const __attribute__((address_space(4))) float* ScalarRow;   // read by scalar loads

@@ -1,5 +1,5 @@
 // The backward pass of the selective state space scan (formulas in
-// seed_select.h), in segments of 64 tokens:
+// seed_select.h), in segments of 128 tokens:
 //   ends_kernel   what a segment leaves of zero, h, and what it passes back to
 //                 its first state from its own read-outs, sum over t of
 //                 (a_1 .. a_t) ds_t C_t, in one walk that makes each decay
@@ -8,7 +8,7 @@
 //   grads_kernel  8 tokens at a time, the last first: the states and decays
 //                 from the state before them (what the segment had made of
 //                 zero, and the decayed first state), and the chain rule
-//   sums          dB and dC over sets of four blocks of channels, dA, dD and
+//   sums          dB and dC over sets of blocks of channels, dA, dD and
 //                 ddt_bias over segments, in a fixed order.
 #include "seed_select.h"
 
@@ -16,8 +16,7 @@ namespace seed {
 namespace channels {
 namespace {
 
-constexpr int kShift = 6, kLen = 1 << kShift, kTiles = kLen / kTile;
-constexpr int kSet = 4;     // blocks of channels that a workgroup takes one after the other
+constexpr int kShift = kBackShift, kTiles = (1 << kShift) / kTile;
 
 // The inputs of a wave's tokens of a tile as they lie in memory.
 template <typename T, bool GATE>
@@ -201,7 +200,7 @@ __device__ __forceinline__ float fold16(float (&v)[16]) {
   return fold<2>(v[0], v[1]);
 }
 
-// A set of four blocks of channels of one group (blockIdx.y) over every
+// A set of blocks of channels of one group (blockIdx.y) over every
 // gridDim.x-th segment.
 template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_kernel(SelectArgs a) {
@@ -211,7 +210,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
   constexpr int kFolds = Q < 4 ? 1 : Q / 4;               // values a lane has at last
   __shared__ Shared prep;
   __shared__ float rows[RowTile<Q>::kFloats];
-  __shared__ float4 part[kWaves][kTile][64];
+  __shared__ float2 part[kWaves][kTile][64];                        // du and the rates' part of ddelta
+  __shared__ float part_s[GATE ? kWaves : 1][kTile][64];            // C.h
   __shared__ float sums[kTiles][kWaves][kFolds][64];
   const int lane = (int)__lane_id();
   const int group = blockIdx.y / a.at.sets, set = blockIdx.y % a.at.sets;
@@ -221,7 +221,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
     const Run r = run_of(b, sequence_of(b, slot), slot);
     const bool none = r.t0 >= r.t1;   // the whole workgroup
     const int tiles = none ? 0 : (r.t1 - r.t0 + kTile - 1) / kTile;
-    for (int block = set * kSet; block < (set + 1) * kSet && block < a.at.blocks; ++block) {
+    const int first_block = set * a.at.set;
+    for (int block = first_block; block < (set + 1) * a.at.set && block < a.at.blocks; ++block) {
       const Mine m = mine(a, group, block);
       const int c = m.c;
       float A[Q], dA[Q], H[Q], G[Q];
@@ -313,14 +314,13 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
               rate += A[i] * q;
               dA[i] += k.x * q;
             }
-            float4& to = part[m.wave][j][lane];
             if (Q > 8 && i0 == 0) {   // the upper half of the token's states came first
-              const float4 o = to;
-              s += o.x;
-              du += o.y;
-              rate += o.z;
+              if (GATE) s += part_s[m.wave][j][lane];
+              du += part[m.wave][j][lane].x;
+              rate += part[m.wave][j][lane].y;
             }
-            to = make_float4(s, du, rate, 0.f);
+            part[m.wave][j][lane] = make_float2(du, rate);
+            if (GATE) part_s[m.wave][j][lane] = s;
           }
           sum[f] = fold16(v);
           settle(G);
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
             total += dpp_mov<0xB1>(total);
           }
           float& to = sums[p][m.wave][f][lane];
-          to = block == set * kSet ? total : to + total;
+          to = block == first_block ? total : to + total;
         }
         __syncthreads();
         if (!m.live) continue;
@@ -350,10 +350,10 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) {
-            const float4 v = part[w][j][lane];
-            if (GATE) s += v.x;
-            du += v.y;
-            rate += v.z;
+            const float2 v = part[w][j][lane];
+            if (GATE) s += part_s[w][j][lane];
+            du += v.x;
+            rate += v.y;
           }
           const float dv = (k.x * du + rate * kLn2) * Step{k.v}.slope(q->softplus);
           dbias += dv;
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
       // the block's part of the weights' gradients: that of the workgroup's
       // segments before, and this one's
       __syncthreads();
-      part[m.wave][0][lane] = make_float4(dD, dbias, 0.f, 0.f);
+      part[m.wave][0][lane] = make_float2(dD, dbias);
       __syncthreads();
       if (m.live) {
         float* out = reinterpret_cast<float*>(a.ws + a.at.weights) + (size_t)blockIdx.x * (4 * Q + 2) * a.channels + c;
@@ -426,6 +426,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(SelectArgs a) {
     const size_t tg = i / (8 * Q), t = tg / a.groups;
     const int g = (int)(tg - t * a.groups);
     float x[1] = {0.f};
+#pragma unroll 8
     for (int k = 0; k < a.at.sets; ++k) x[0] += sums[(size_t)k * a.tokens * row + i];
     Packed<1, T> out;
     out.from(x);
@@ -441,8 +442,10 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(SelectArgs a, int par
   const int c = (int)blockIdx.x * 64 + lane, n = blockIdx.y, row = n < a.d_state ? n : NP + (n - a.d_state);
   const float* w = reinterpret_cast<const float*>(a.ws + a.at.weights);
   float s = 0.f;
-  if (c < a.channels)
+  if (c < a.channels) {
+#pragma unroll 8
     for (int p = wave; p < parts; p += 4) s += w[((size_t)p * (NP + 2) + row) * a.channels + c];
+  }
   lds[threadIdx.x] = s;
   __syncthreads();
   if (wave != 0 || c >= a.channels) return;

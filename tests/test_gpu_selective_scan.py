@@ -62,11 +62,11 @@ def backward(p, out, softplus, cu=None, **more):
 
 
 def depth(offsets, W, G, T):
-    """Additions in a row of the sums over tokens (a segment of 64 after the
-    other, then a quarter of the parts and the waves) and over channels (six
-    folds of a wave's lanes, the waves, the blocks)."""
-    segments = T // 64 + len(offsets) - 1
-    return max(64 * segments, 64) + 8, 6 + 4 + W // G // 64 + 1
+    """Additions in a row of the sums over tokens (a segment of at most 128
+    after the other, then the parts) and over channels (six folds of a wave's
+    lanes, the blocks)."""
+    segments = T // 128 + len(offsets) - 1
+    return 128 * segments + 8, 6 + W // G // 64 + 8
 
 
 def run_all(p, offsets, softplus, cu=None, lead=None):
@@ -95,7 +95,7 @@ def run_all(p, offsets, softplus, cu=None, lead=None):
 
 
 CASES = [
-    # offsets, channels, groups, d_state: lengths of 0 and 1, around the tiles of 8 and the segments of 64 and 128
+    # offsets, channels, groups, d_state: lengths of 0 and 1, around the tiles of 8 and the segments of 128
     ([0, 1], 1, 1, 1), ([0, 0, 2], 3, 3, 16), ([0, 7, 8, 17], 64, 1, 16), ([0, 63, 127, 192], 70, 2, 5),
     ([0, 64, 129], 130, 1, 16), ([0, 300], 24, 4, 16), ([0, 128, 128, 257], 260, 1, 8), ([0, 65, 70], 66, 1, 32),
     ([0, 40], 40, 2, 64), ([0, 3, 90], 129, 1, 33), ([0, 9], 513, 1, 16), ([0, 130], 10, 2, 17),
