@@ -20,7 +20,7 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// VW (1 or 8) neighbouring values as they lie in memory, and as floats.
+// VW (1, 4 or 8) neighbouring values as they lie in memory, and as floats.
 template <int VW, typename T>
 struct Packed;
 template <>
@@ -59,6 +59,22 @@ struct Packed<8, bf16_t> {
                    round_pair(x[6], x[7]));
   }
   __device__ __forceinline__ void store(bf16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+};
+template <>
+struct Packed<4, bf16_t> {
+  uint2 v;
+  __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void floats(float (&x)[4]) const {
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+  __device__ __forceinline__ void from(const float (&x)[4]) {
+    v = make_uint2(round_pair(x[0], x[1]), round_pair(x[2], x[3]));
+  }
+  __device__ __forceinline__ void store(bf16_t* p) const { *reinterpret_cast<uint2*>(p) = v; }
 };
 // (float32: four values, 16 bytes)
 template <>

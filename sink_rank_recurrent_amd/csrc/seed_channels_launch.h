@@ -42,8 +42,8 @@ struct ConvArgs {
 hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_short_conv_step(const ConvArgs& a, hipStream_t stream);
-// Partial sums of the weights' gradients that the backward pass keeps, each
-// width + 1 floats a channel, for either form of its rows.
+// Partial sums of the weights' gradients that the backward pass keeps at most,
+// each width + 1 floats a channel, for either form of its rows.
 int short_conv_parts(int n_seq, int channels, int tokens);
 // Whether the grids for these sizes can be launched.
 bool short_conv_fits(int n_seq, int channels, int tokens);

@@ -6,9 +6,9 @@
 //   dw_j = sum_t e_t x_{t - (K - 1) + j},   db = sum_t e_t.
 //
 // 2 K + 5 operations a value against 4 (bf16) or 8 bytes: memory.  A thread
-// keeps VW neighbouring channels (16 bytes) and walks a run of tokens with the
-// last K - 1 inputs in registers, so that inside a run each input is read
-// once; K - 1 rows are read again at the run's start.
+// keeps VW neighbouring channels and walks a run of tokens with the last K - 1
+// inputs in registers, so that inside a run each input is read once; K - 1 rows
+// are read again at the run's start (backward also behind its end).
 #include "seed_channels.h"
 
 namespace seed {
@@ -16,7 +16,7 @@ namespace channels {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStepRows = 4;     // tokens whose loads are on their way together
+constexpr int kRows = 8, kBackRows = 4;     // tokens whose loads are on their way together
 
 // Weights of a thread's channels, tap by tap.
 template <int K, int VW>
@@ -108,13 +108,13 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, i
   }
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) held[i].floats(x[i]);
-  for (int t = r.t0; t < r.t1; t += kStepRows) {
-    Packed<VW, T> in[kStepRows];
+  for (int t = r.t0; t < r.t1; t += kRows) {
+    Packed<VW, T> in[kRows];
 #pragma unroll
-    for (int j = 0; j < kStepRows; ++j)
+    for (int j = 0; j < kRows; ++j)
       in[j].load(row_of<T>(a.x, t + j < r.t1 ? t + j : r.t1 - 1) + c);
 #pragma unroll
-    for (int j = 0; j < kStepRows; ++j) {
+    for (int j = 0; j < kRows; ++j) {
       if (t + j >= r.t1) break;
       in[j].floats(x[K - 1]);
       float y[VW];
@@ -136,12 +136,15 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, i
   }
 }
 
-// A thread walks every gridDim.x-th run and keeps its part of the weights'
-// gradients; the parts are summed in a fixed order by sums_kernel.
+// A block's threads take kThreads / tx runs at a time and keep their parts of
+// the weights' gradients in registers; the block adds them up in order through
+// LDS, and sums_kernel the blocks' parts.
 template <int K, int VW, typename T>
-__global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int shift, int runs, int tx, int parts) {
+__global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int shift, int runs, int tx) {
+  __shared__ float lds[(K + 1) * VW * kThreads];
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, shift);
-  const Place at = place<VW>(a.channels, tx, parts);
+  const int side = kThreads / tx, step = (int)gridDim.x * side;
+  const Place at = place<VW>(a.channels, tx, step);
   const int c = at.c;
   float w[K][VW], bias[VW], dw[K][VW], db[VW];
   if (at.live) load_weights<K, VW>(a, c, w, bias);
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int
 #pragma unroll
     for (int k = 0; k < K; ++k) dw[k][v] = 0.f;
   }
-  for (int base = 0; base < runs; base += parts) {   // the wave's lanes together
+  for (int base = 0; base < runs; base += step) {   // the wave's lanes together
     const int run = base + at.run < runs ? base + at.run : runs - 1;
     const Run r = run_of(b, sequence_near(b, run), run);
     if (!at.live || base + at.run >= runs || (r.t0 >= r.t1 && !r.first)) continue;
@@ -165,10 +168,10 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int
       for (int v = 0; v < VW; ++v) e[i + 1][v] = 0.f;
     }
     const int end = r.t1 + K - 1;   // the run's last inputs reach K - 1 tokens on
-    for (int t = r.t0; t < end; t += kStepRows) {
-      Packed<VW, T> in[kStepRows], dy[kStepRows];
+    for (int t = r.t0; t < end; t += kBackRows) {
+      Packed<VW, T> in[kBackRows], dy[kBackRows];
 #pragma unroll
-      for (int j = 0; j < kStepRows; ++j) {
+      for (int j = 0; j < kBackRows; ++j) {
         in[j].zero();
         dy[j].zero();
         if (t + j < r.hi && t + j < end) {
@@ -177,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int
         }
       }
 #pragma unroll
-      for (int j = 0; j < kStepRows; ++j) {
+      for (int j = 0; j < kBackRows; ++j) {
         if (t + j >= end) break;
         const int now = t + j, back = now - (K - 1);
         in[j].floats(x[K - 1]);
@@ -233,13 +236,23 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int
       }
     }
   }
-  if (!at.live || !(a.dweight || a.dbias)) return;
-  float* out = a.ws + (size_t)at.run * (K + 1) * a.channels + c;
+  if (!(a.dweight || a.dbias)) return;
 #pragma unroll
   for (int v = 0; v < VW; ++v) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) out[(size_t)k * a.channels + v] = dw[k][v];
-    out[(size_t)K * a.channels + v] = db[v];
+    for (int k = 0; k < K; ++k) lds[(k * VW + v) * kThreads + threadIdx.x] = dw[k][v];
+    lds[(K * VW + v) * kThreads + threadIdx.x] = db[v];
+  }
+  __syncthreads();
+  // the block's [K + 1][VW tx] sums, neighbouring channels by neighbouring threads
+  const int first = (int)blockIdx.y * tx * VW;
+  float* out = a.ws + (size_t)blockIdx.x * (K + 1) * a.channels + first;
+  for (int i = threadIdx.x; i < (K + 1) * VW * tx; i += kThreads) {
+    const int k = i / (VW * tx), in = i % (VW * tx), lane = in / VW, v = in % VW;
+    if (first + in >= a.channels) continue;
+    float s = 0.f;
+    for (int r = 0; r < side; ++r) s += lds[(k * VW + v) * kThreads + r * tx + lane];
+    out[(size_t)k * a.channels + in] = s;
   }
 }
 
@@ -251,8 +264,10 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(ConvArgs a, int parts) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, k = blockIdx.y;
   const int c = (int)blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < a.channels)
+  if (c < a.channels) {
+#pragma unroll 8
     for (int p = wave; p < parts; p += 4) s += a.ws[((size_t)p * (a.width + 1) + k) * a.channels + c];
+  }
   lds[threadIdx.x] = s;
   __syncthreads();
   if (wave != 0 || c >= a.channels) return;
@@ -292,22 +307,30 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs a, int tx)
   for (int i = 0; i < K - 1; ++i) held[i + 1].store(static_cast<T*>(a.S) + state + (size_t)i * a.channels);
 }
 
-// Threads along the channels: a power of two, at most a block's.
-int threads_along(int channels, int vw) {
+// Threads along the channels: a power of two, at most `most`.
+int threads_along(int channels, int vw, int most) {
   const int lanes = (channels + vw - 1) / vw;
   int tx = 1;
-  while (tx < lanes && tx < kThreads) tx *= 2;
+  while (tx < lanes && tx < most) tx *= 2;
   return tx;
 }
-constexpr int kRun = 5;   // log2 of a run's tokens
-int runs_of(int n_seq, int tokens) { return (tokens >> kRun) + n_seq; }
+// log2 of a run's tokens: 32, and fewer down to 8 where the runs of four
+// channels a thread are fewer than 4096 waves.
+constexpr int kLongRun = 5, kShortRun = 3;
+int run_shift(int n_seq, int channels, int tokens) {
+  const long long waves = ((long long)channels + 255) / 256;
+  int shift = kLongRun;
+  while (shift > kShortRun && ((long long)(tokens >> shift) + n_seq) * waves < 4096) --shift;
+  return shift;
+}
+int runs_of(int n_seq, int tokens, int shift) { return (tokens >> shift) + n_seq; }
 
-template <typename F>
+template <int BF16_VECTOR, typename F>
 hipError_t with_form(const ConvArgs& a, F f) {
 #define SEED_FORM(K)                                                        \
   do {                                                                      \
     if (a.bf16) {                                                           \
-      if (a.vectors) f(std::integral_constant<int, K>{}, std::integral_constant<int, 8>{}, bf16_t{}); \
+      if (a.vectors) f(std::integral_constant<int, K>{}, std::integral_constant<int, BF16_VECTOR>{}, bf16_t{}); \
       else f(std::integral_constant<int, K>{}, std::integral_constant<int, 1>{}, bf16_t{}); \
     } else {                                                                \
       if (a.vectors) f(std::integral_constant<int, K>{}, std::integral_constant<int, 4>{}, float{}); \
@@ -331,31 +354,41 @@ dim3 grid_of(int runs, int channels, int vw, int tx) {
 
 using namespace channels;
 
+// Blocks of the backward pass along the runs: one to a set of runs, 128 at
+// most (their sums are read once more).
+constexpr int kMostParts = 128;
+int parts_of(int runs, int tx) {
+  const int sets = (runs + kThreads / tx - 1) / (kThreads / tx);
+  return sets < kMostParts ? sets : kMostParts;
+}
+
 int short_conv_parts(int n_seq, int channels, int tokens) {
-  // 128 to a run each: more would add to the bytes of the sums
-  const int runs = runs_of(n_seq, tokens);
-  return runs < 128 ? runs : 128;
+  // single channels take the most threads along the channels, so the fewest runs a block
+  return parts_of(runs_of(n_seq, tokens, run_shift(n_seq, channels, tokens)), threads_along(channels, 1, 64));
 }
 
 // At most 256 threads for each run and 256 channels, 2^32 in a grid's row.
 bool short_conv_fits(int n_seq, int channels, int tokens) {
-  return (long long)(tokens >> kRun) + n_seq < (1LL << 24) - 1 && (long long)tokens + 4LL < 0x7fffffffLL;
+  return (long long)(tokens >> kLongRun) + n_seq < (1LL << 24) - 1 && (long long)tokens + 64LL < 0x7fffffffLL;
 }
 
 hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream) {
-  return with_form(a, [&](auto k, auto vw, auto t) {
-    const int tx = threads_along(a.channels, vw), runs = runs_of(a.n_seq, a.tokens);
+  const int shift = run_shift(a.n_seq, a.channels, a.tokens), runs = runs_of(a.n_seq, a.tokens, shift);
+  return with_form<8>(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw, kThreads);
     hipLaunchKernelGGL((conv_kernel<k, vw, decltype(t)>), grid_of(runs, a.channels, vw, tx), dim3(kThreads), 0,
-                       stream, a, kRun, runs, tx);
+                       stream, a, shift, runs, tx);
   });
 }
 
 hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream) {
-  const int parts = short_conv_parts(a.n_seq, a.channels, a.tokens);
-  const hipError_t e = with_form(a, [&](auto k, auto vw, auto t) {
-    const int tx = threads_along(a.channels, vw), runs = runs_of(a.n_seq, a.tokens);
-    hipLaunchKernelGGL((conv_backward_kernel<k, vw, decltype(t)>), grid_of(parts, a.channels, vw, tx),
-                       dim3(kThreads), 0, stream, a, kRun, runs, tx, parts);
+  const int shift = run_shift(a.n_seq, a.channels, a.tokens), runs = runs_of(a.n_seq, a.tokens, shift);
+  int parts = 0;
+  const hipError_t e = with_form<4>(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw, 64), lanes = (a.channels + vw - 1) / vw;
+    parts = parts_of(runs, tx);
+    hipLaunchKernelGGL((conv_backward_kernel<k, vw, decltype(t)>), dim3(parts, (lanes + tx - 1) / tx),
+                       dim3(kThreads), 0, stream, a, shift, runs, tx);
   });
   if (e != hipSuccess || !(a.dweight || a.dbias)) return e;
   hipLaunchKernelGGL(sums_kernel, dim3((a.channels + 63) / 64, a.width + 1), dim3(kThreads), 0, stream, a, parts);
@@ -363,8 +396,8 @@ hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_short_conv_step(const ConvArgs& a, hipStream_t stream) {
-  return with_form(a, [&](auto k, auto vw, auto t) {
-    const int tx = threads_along(a.channels, vw);
+  return with_form<8>(a, [&](auto k, auto vw, auto t) {
+    const int tx = threads_along(a.channels, vw, kThreads);
     hipLaunchKernelGGL((conv_step_kernel<k, vw, decltype(t)>), grid_of(a.n_seq, a.channels, vw, tx),
                        dim3(kThreads), 0, stream, a, tx);
   });

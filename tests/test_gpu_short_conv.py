@@ -42,10 +42,11 @@ def check(got, want, off, name):
 
 
 def depth(offsets, T):
-    """Additions in a row of the weights' sums: a run of 32 tokens, every
-    128th run, then a quarter of the parts and the four waves."""
-    runs = T // 32 + len(offsets) - 1
-    return 32 * -(-runs // 128) + -(-min(runs, 128) // 4) + 4
+    """Additions in a row of the weights' sums: runs of at most 32 tokens,
+    every 128th at most, then a block's runs (256 at most), a quarter of the
+    128 blocks and the four waves."""
+    runs = T // 8 + len(offsets) - 1
+    return 32 * -(-runs // 128) + min(runs, 256) + -(-min(runs, 128) // 4) + 4
 
 
 def run_all(p, offsets, silu, bias, T, C, K, dtype, cu=None, lead=None):
