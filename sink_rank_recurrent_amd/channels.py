@@ -23,7 +23,7 @@ import torch
 
 from . import binding
 from .binding import _F32, _IN, _check, _need, _ptr, _stream
-from .sequence import ACTIVATIONS, _code, _On, _same_device, _workspace
+from .sequence import ACTIVATIONS, _code, _same_device, _workspace
 
 HEADER_PATH = os.path.join(os.path.dirname(binding.HEADER_PATH), "seed_channels.h")
 
@@ -71,16 +71,23 @@ def _rows(t, name: str, lead: tuple, tail: tuple, dtypes) -> tuple:
         return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if tuple(t.shape) != (*lead, *tail):
+    if len(tail) == 1 and len(lead) == 1 and t.dtype in dtypes and t.shape == (*lead, *tail):
+        step, one = t.stride()     # the common case first
+        if one == 1 and step >= tail[0] and lead[0] > 1:
+            return t.data_ptr(), step
+    if t.shape != (*lead, *tail):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, *tail)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    width = 1
+    width = tail[0] if len(tail) == 1 else tail[0] * tail[1]
+    if t.is_contiguous():
+        return t.data_ptr(), width
     strides = t.stride()
+    inner = 1
     for size, stride in zip(reversed(tail), reversed(strides[len(lead):])):
-        if size > 1 and stride != width:
+        if size > 1 and stride != inner:
             raise ValueError(f"{name}: the values of a row must lie behind each other")
-        width *= size
+        inner *= size
     if len(lead) == 1:
         step = strides[0] if lead[0] > 1 else width
     elif lead[1] > 1:
@@ -92,6 +99,39 @@ def _rows(t, name: str, lead: tuple, tail: tuple, dtypes) -> tuple:
     if step < width and t.numel() > 0:
         raise ValueError(f"{name}: rows of {width} values lie {step} apart")
     return t.data_ptr(), max(step, width)
+
+
+def _device(first, names: str, *others) -> int:
+    """The index of the one device that all tensors are on."""
+    try:
+        index = first.get_device()
+        if index >= 0 and all(t is None or t.get_device() == index for t in others):
+            return index
+    except AttributeError:
+        pass
+    _same_device(**dict(zip(names.split(), (first, *others))))     # says which is not
+    raise ValueError("the tensors are not on one device")
+
+
+def _call(name: str, index: int, stream, *args) -> None:
+    """Call the library on torch's current stream of device `index`, or on
+    `stream`, with that device made current."""
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, _stream(stream, index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(stream, index))
+    if st != 0:
+        _check(name, st)
+
+
+def _space(workspace, nbytes, index: int, stream) -> torch.Tensor:
+    """The caller's workspace, or one of nbytes() bytes made for the call."""
+    if workspace is not None:
+        return _workspace(workspace, 0, None, stream)
+    with torch.cuda.device(index):
+        return _workspace(None, nbytes(), torch.device("cuda", index), stream)
 
 
 def _lead(x, dims: int, cu_seqlens):
@@ -135,18 +175,15 @@ def seed_short_conv(x, weight, y, bias=None, activation="silu", S0=None, S=None,
     weight [channels, width] into y (see include/seed_channels.h).  S0 and S
     [n_seq, width - 1, channels] of x's type are the inputs before and behind
     each sequence."""
-    device = _same_device(x=x, weight=weight, y=y, bias=bias, S0=S0, S=S, cu_seqlens=cu_seqlens)
+    index = _device(x, "x weight y bias S0 S cu_seqlens", weight, y, bias, S0, S, cu_seqlens)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
     channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
     yr = _rows(y, "y", lead, (channels,), (x.dtype,))
     for name, t in (("S0", S0), ("S", S)):
         if t is not None:
             _need(t, name, (n_seq, width - 1, channels), (x.dtype,))
-    with _On(device):
-        st = lib().seed_short_conv(n_seq, channels, width, tokens, _ptr(cu_seqlens), *xr, _code(x.dtype),
-                                   _ptr(weight), _ptr(bias), _ptr(S0), ACTIVATIONS[activation], *yr,
-                                   _ptr(S), _stream(stream, device.index))
-    _check("seed_short_conv", st)
+    _call("seed_short_conv", index, stream, n_seq, channels, width, tokens, _ptr(cu_seqlens), *xr,
+          _code(x.dtype), _ptr(weight), _ptr(bias), _ptr(S0), ACTIVATIONS[activation], *yr, _ptr(S))
 
 
 def short_conv_workspace(x, weight, n_seq: int) -> torch.Tensor:
@@ -163,8 +200,8 @@ def seed_short_conv_backward(dy, x, weight, dx, dweight=None, dbias=None, bias=N
                              stream=None) -> None:
     """Gradients of seed_short_conv from dy (and dS, that of S) into dx and,
     where given, dweight, dbias and dS0 (see include/seed_channels.h)."""
-    device = _same_device(dy=dy, x=x, weight=weight, dx=dx, dweight=dweight, dbias=dbias, bias=bias,
-                          S0=S0, dS=dS, dS0=dS0, cu_seqlens=cu_seqlens, workspace=workspace)
+    index = _device(x, "x dy weight dx dweight dbias bias S0 dS dS0 cu_seqlens workspace", dy, weight, dx,
+                    dweight, dbias, bias, S0, dS, dS0, cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
     channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
     dyr = _rows(dy, "dy", lead, (channels,), (x.dtype,))
@@ -176,38 +213,30 @@ def seed_short_conv_backward(dy, x, weight, dx, dweight=None, dbias=None, bias=N
         _need(dweight, "dweight", (channels, width), _F32)
     if dbias is not None:
         _need(dbias, "dbias", (channels,), _F32)
-    with _On(device):
-        ws = None
-        if dweight is not None or dbias is not None:
-            ws = _workspace(workspace, 0 if workspace is not None else
-                            _bytes(lib().seed_short_conv_workspace_bytes(n_seq, channels, width, tokens)),
-                            device, stream)
-        st = lib().seed_short_conv_backward(
-            n_seq, channels, width, tokens, _ptr(cu_seqlens), *xr, _code(x.dtype), _ptr(weight),
-            _ptr(bias), _ptr(S0), ACTIVATIONS[activation], *dyr, _ptr(dS), *dxr, _ptr(dweight),
-            _ptr(dbias), _ptr(dS0), _ptr(ws), 0 if ws is None else ws.numel(),
-            _stream(stream, device.index))
-    _check("seed_short_conv_backward", st)
+    ws = None
+    if dweight is not None or dbias is not None:
+        ws = _space(workspace, lambda: _bytes(lib().seed_short_conv_workspace_bytes(n_seq, channels, width,
+                                                                                    tokens)), index, stream)
+    _call("seed_short_conv_backward", index, stream, n_seq, channels, width, tokens, _ptr(cu_seqlens), *xr,
+          _code(x.dtype), _ptr(weight), _ptr(bias), _ptr(S0), ACTIVATIONS[activation], *dyr, _ptr(dS), *dxr,
+          _ptr(dweight), _ptr(dbias), _ptr(dS0), _ptr(ws), 0 if ws is None else ws.numel())
 
 
 def seed_short_conv_step(x, weight, y, S, bias=None, activation="silu", S0=None, stream=None) -> None:
     """One token of every sequence: row b of x [batch, channels] behind the
     inputs in S0[b] (None: S[b], the step in place) into y, the inputs behind
     it into S [batch, width - 1, channels] (see include/seed_channels.h)."""
-    device = _same_device(x=x, weight=weight, y=y, S=S, bias=bias, S0=S0)
+    index = _device(x, "x weight y S bias S0", weight, y, S, bias, S0)
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
     channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
     yr = _rows(y, "y", lead, (channels,), (x.dtype,))
-    S0 = S if S0 is None else S0
-    for name, t in (("S", S), ("S0", S0)):
-        _need(t, name, (lead[0], width - 1, channels), (x.dtype,))
-    with _On(device):
-        st = lib().seed_short_conv_step(lead[0], channels, width, *xr, _code(x.dtype), _ptr(weight),
-                                        _ptr(bias), _ptr(S0), ACTIVATIONS[activation], *yr, _ptr(S),
-                                        _stream(stream, device.index))
-    _check("seed_short_conv_step", st)
+    _need(S, "S", (lead[0], width - 1, channels), (x.dtype,))
+    if S0 is not None:
+        _need(S0, "S0", (lead[0], width - 1, channels), (x.dtype,))
+    _call("seed_short_conv_step", index, stream, lead[0], channels, width, *xr, _code(x.dtype), _ptr(weight),
+          _ptr(bias), _ptr(S if S0 is None else S0), ACTIVATIONS[activation], *yr, _ptr(S))
 
 
 def _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead):
@@ -246,21 +275,17 @@ def seed_selective_scan(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, soft
     [channels, d_state], inputs and read-outs B, C [..., groups, d_state] into
     y and the last states S [n_seq, channels, d_state] (see
     include/seed_channels.h)."""
-    device = _same_device(x=x, dt=dt, A=A, B=B, C=C, y=y, S=S, D=D, z=z, dt_bias=dt_bias, S0=S0,
-                          cu_seqlens=cu_seqlens, workspace=workspace)
+    index = _device(x, "x dt A B C y S D z dt_bias S0 cu_seqlens workspace", dt, A, B, C, y, S, D, z, dt_bias,
+                    S0, cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
     channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
     yr = _rows(y, "y", lead, (channels,), (x.dtype,))
     for name, t in (("S", S), ("S0", S0)):
         if t is not None:
             _need(t, name, (n_seq, channels, d_state), _F32)
-    with _On(device):
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        _select_bytes(n_seq, channels, groups, d_state, tokens, False), device, stream)
-        st = lib().seed_selective_scan(n_seq, channels, groups, d_state, tokens, _ptr(cu_seqlens), *args,
-                                       _ptr(S0), *yr, _ptr(S), _ptr(ws), ws.numel(),
-                                       _stream(stream, device.index))
-    _check("seed_selective_scan", st)
+    ws = _space(workspace, lambda: _select_bytes(n_seq, channels, groups, d_state, tokens, False), index, stream)
+    _call("seed_selective_scan", index, stream, n_seq, channels, groups, d_state, tokens, _ptr(cu_seqlens),
+          *args, _ptr(S0), *yr, _ptr(S), _ptr(ws), ws.numel())
 
 
 def seed_selective_scan_backward(dy, x, dt, A, B, C, dx, ddt, dA, dB, dC, D=None, z=None, dt_bias=None,
@@ -270,9 +295,9 @@ def seed_selective_scan_backward(dy, x, dt, A, B, C, dx, ddt, dA, dB, dC, D=None
     """Gradients of seed_selective_scan's inputs from dy (and dS, that of S)
     into dx, ddt, dA, dB, dC, dz (with z) and, where given, dD, ddt_bias and
     dS0 (see include/seed_channels.h).  Shapes and types are the inputs'."""
-    device = _same_device(dy=dy, x=x, dt=dt, A=A, B=B, C=C, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, D=D,
-                          z=z, dt_bias=dt_bias, dD=dD, dz=dz, ddt_bias=ddt_bias, S0=S0, dS=dS, dS0=dS0,
-                          cu_seqlens=cu_seqlens, workspace=workspace)
+    index = _device(x, "x dy dt A B C dx ddt dA dB dC D z dt_bias dD dz ddt_bias S0 dS dS0 cu_seqlens workspace",
+                    dy, dt, A, B, C, dx, ddt, dA, dB, dC, D, z, dt_bias, dD, dz, ddt_bias, S0, dS, dS0,
+                    cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
     channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
     io = (x.dtype,)
@@ -286,14 +311,10 @@ def seed_selective_scan_backward(dy, x, dt, A, B, C, dx, ddt, dA, dB, dC, D=None
     for name, t in (("S0", S0), ("dS", dS), ("dS0", dS0)):
         if t is not None:
             _need(t, name, (n_seq, channels, d_state), _F32)
-    with _On(device):
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        _select_bytes(n_seq, channels, groups, d_state, tokens, True), device, stream)
-        st = lib().seed_selective_scan_backward(
-            n_seq, channels, groups, d_state, tokens, _ptr(cu_seqlens), *args, _ptr(S0), *dyr, _ptr(dS),
-            *dxr, *ddtr, _ptr(dA), *dBr, *dCr, _ptr(dD), *dzr, _ptr(ddt_bias), _ptr(dS0), _ptr(ws),
-            ws.numel(), _stream(stream, device.index))
-    _check("seed_selective_scan_backward", st)
+    ws = _space(workspace, lambda: _select_bytes(n_seq, channels, groups, d_state, tokens, True), index, stream)
+    _call("seed_selective_scan_backward", index, stream, n_seq, channels, groups, d_state, tokens,
+          _ptr(cu_seqlens), *args, _ptr(S0), *dyr, _ptr(dS), *dxr, *ddtr, _ptr(dA), *dBr, *dCr, _ptr(dD), *dzr,
+          _ptr(ddt_bias), _ptr(dS0), _ptr(ws), ws.numel())
 
 
 def seed_selective_step(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, softplus: bool = True,
@@ -301,16 +322,14 @@ def seed_selective_step(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, soft
     """One token of every sequence: seed_selective_scan of row b of x [batch,
     channels] from S0[b] (None: S[b], the step in place) into y and S [batch,
     channels, d_state] (see include/seed_channels.h)."""
-    device = _same_device(x=x, dt=dt, A=A, B=B, C=C, y=y, S=S, D=D, z=z, dt_bias=dt_bias, S0=S0)
+    index = _device(x, "x dt A B C y S D z dt_bias S0", dt, A, B, C, y, S, D, z, dt_bias, S0)
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
     channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
     yr = _rows(y, "y", lead, (channels,), (x.dtype,))
-    S0 = S if S0 is None else S0
-    for name, t in (("S", S), ("S0", S0)):
-        _need(t, name, (lead[0], channels, d_state), _F32)
-    with _On(device):
-        st = lib().seed_selective_step(lead[0], channels, groups, d_state, *args, _ptr(S0), *yr, _ptr(S),
-                                       _stream(stream, device.index))
-    _check("seed_selective_step", st)
+    _need(S, "S", (lead[0], channels, d_state), _F32)
+    if S0 is not None:
+        _need(S0, "S0", (lead[0], channels, d_state), _F32)
+    _call("seed_selective_step", index, stream, lead[0], channels, groups, d_state, *args,
+          _ptr(S if S0 is None else S0), *yr, _ptr(S))

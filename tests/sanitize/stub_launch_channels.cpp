@@ -12,13 +12,12 @@ int short_conv_parts(int n_seq, int, int tokens) { return tokens / 32 + n_seq < 
 bool short_conv_fits(int n_seq, int, int tokens) { return (long long)(tokens >> 5) + n_seq < (1LL << 24) - 1; }
 SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int tokens, bool backward) {
   SelectLayout l{};
-  l.waves = d_state <= 16 ? 1 : d_state <= 32 ? 2 : 4;
-  l.bytes = (size_t)tokens * groups * 128 * l.waves + (backward ? (size_t)n_seq * channels * 64 : 0);
+  const int states = d_state <= 16 ? 16 : d_state <= 32 ? 32 : 64;
+  l.bytes = (size_t)tokens * groups * 8 * states + (backward ? (size_t)n_seq * channels * 64 : 0);
   return l;
 }
 bool select_fits(int n_seq, int channels, int groups, int d_state, int tokens) {
-  const int per = d_state <= 16 ? 256 : d_state <= 32 ? 128 : 64;
-  return (long long)groups * ((channels / groups + per - 1) / per) <= 65535 &&
+  return d_state <= 64 && (long long)groups * ((channels / groups + 63) / 64) <= 65535 &&
          (long long)(tokens >> 6) + n_seq < (1LL << 24) && (long long)tokens + 64 <= 0x7fffffffLL;
 }
 hipError_t launch_select(const SelectArgs&, hipStream_t) { return hipSuccess; }
