@@ -9,6 +9,8 @@
 // keeps VW neighbouring channels and walks a run of tokens with the last K - 1
 // inputs in registers, so that inside a run each input is read once; K - 1 rows
 // are read again at the run's start (backward also behind its end).
+#include <type_traits>
+
 #include "seed_channels.h"
 
 namespace seed {
@@ -16,7 +18,12 @@ namespace channels {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 8, kBackRows = 4;     // tokens whose loads are on their way together
+// Tokens whose loads are on their way together: whole turns of the window of K
+// inputs, so that an input stays in its registers until it has left.
+template <int K>
+constexpr int kRows = K == 3 ? 6 : 8;
+template <int K>
+constexpr int kBackRows = K == 3 ? 6 : 4;
 
 // Weights of a thread's channels, tap by tap.
 template <int K, int VW>
@@ -71,22 +78,27 @@ __device__ __forceinline__ Place place(int channels, int tx, int runs) {
   p.live = p.c < channels && run < runs;
   return p;
 }
-// Its sequence: the wave looks for that of its first thread; runs of a wave
-// follow each other.
-__device__ __forceinline__ int sequence_near(const Batch& b, int run) {
-  int s = sequence_of(b, __builtin_amdgcn_readfirstlane(run));
+// Its tokens: the wave looks for the sequence of its first thread's run; runs
+// of a wave follow each other.  ONE: the wave has one run (64 threads or more
+// along the channels), so that what depends on it is scalar.
+template <bool ONE>
+__device__ __forceinline__ Run tokens_of(const Batch& b, int run) {
+  const int first = __builtin_amdgcn_readfirstlane(run);
+  int s = sequence_of(b, first);
+  if constexpr (ONE) return run_of(b, s, first);
   while (s + 1 < b.n_seq && first_run(b, s + 1) <= run) ++s;
-  return s;
+  return run_of(b, s, run);
 }
 
-template <int K, int VW, typename T>
+template <int K, int VW, bool ONE, typename T>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, int runs, int tx) {
+  constexpr int R = kRows<K>;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, shift);
   const Place at = place<VW>(a.channels, tx, runs);
-  const Run r = run_of(b, sequence_near(b, at.run), at.run);
+  const Run r = tokens_of<ONE>(b, at.run);
   if (!at.live || (r.t0 >= r.t1 && !r.first)) return;
   const int c = at.c;
-  float w[K][VW], bias[VW], x[K][VW];
+  float w[K][VW], bias[VW], x[K][VW];   // token t0 + i of the run: x[(K - 1 + i) % K]
   load_weights<K, VW>(a, c, w, bias);
   Packed<VW, T> held[K - 1];
   inputs_before<K>(a, r, c, held);
@@ -108,30 +120,28 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, i
   }
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) held[i].floats(x[i]);
-  for (int t = r.t0; t < r.t1; t += kRows) {
-    Packed<VW, T> in[kRows];
+  for (int t = r.t0; t < r.t1; t += R) {
+    Packed<VW, T> in[R];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
-      in[j].load(row_of<T>(a.x, t + j < r.t1 ? t + j : r.t1 - 1) + c);
+    for (int j = 0; j < R; ++j) in[j].load(row_of<T>(a.x, t + j < r.t1 ? t + j : r.t1 - 1) + c);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    for (int j = 0; j < R; ++j) {
       if (t + j >= r.t1) break;
-      in[j].floats(x[K - 1]);
+      in[j].floats(x[(K - 1 + j) % K]);
       float y[VW];
 #pragma unroll
       for (int v = 0; v < VW; ++v) {
         y[v] = bias[v];
 #pragma unroll
-        for (int k = 0; k < K; ++k) y[v] += w[k][v] * x[k][v];
-        if (a.silu) y[v] *= sigmoid(y[v]);
+        for (int k = 0; k < K; ++k) y[v] += w[k][v] * x[(k + j) % K][v];
+      }
+      if (a.silu) {
+#pragma unroll
+        for (int v = 0; v < VW; ++v) y[v] *= sigmoid(y[v]);
       }
       Packed<VW, T> out;
       out.from(y);
       out.store(row_of<T>(a.y, t + j) + c);
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-        for (int v = 0; v < VW; ++v) x[k][v] = x[k + 1][v];
     }
   }
 }
@@ -139,8 +149,9 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, i
 // A block's threads take kThreads / tx runs at a time and keep their parts of
 // the weights' gradients in registers; the block adds them up in order through
 // LDS, and sums_kernel the blocks' parts.
-template <int K, int VW, typename T>
+template <int K, int VW, bool ONE, typename T>
 __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int shift, int runs, int tx) {
+  constexpr int R = kBackRows<K>;
   __shared__ float lds[(K + 1) * VW * kThreads];
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, shift);
   const int side = kThreads / tx, step = (int)gridDim.x * side;
@@ -156,84 +167,97 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int
   }
   for (int base = 0; base < runs; base += step) {   // the wave's lanes together
     const int run = base + at.run < runs ? base + at.run : runs - 1;
-    const Run r = run_of(b, sequence_near(b, run), run);
+    const Run r = tokens_of<ONE>(b, run);
     if (!at.live || base + at.run >= runs || (r.t0 >= r.t1 && !r.first)) continue;
-    float x[K][VW], e[K][VW];   // e[K - 1]: token t
+    // token t0 + i of the run: x[(K - 1 + i) % K], and its e likewise
+    float x[K][VW], e[K][VW];
     Packed<VW, T> held[K - 1];
     inputs_before<K>(a, r, c, held);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       held[i].floats(x[i]);
 #pragma unroll
-      for (int v = 0; v < VW; ++v) e[i + 1][v] = 0.f;
+      for (int v = 0; v < VW; ++v) e[i][v] = 0.f;
     }
     const int end = r.t1 + K - 1;   // the run's last inputs reach K - 1 tokens on
-    for (int t = r.t0; t < end; t += kBackRows) {
-      Packed<VW, T> in[kBackRows], dy[kBackRows];
+    // R tokens from t on.  PLAIN: all of them in the run, and the K - 1 before
+    // them too, so that every one adds to the weights' gradients and has the
+    // gradient of an input of the run K - 1 tokens back.
+    auto walk = [&](auto plain, int t) {
+      constexpr bool PLAIN = decltype(plain)::value;
+      Packed<VW, T> in[R], dy[R];
 #pragma unroll
-      for (int j = 0; j < kBackRows; ++j) {
-        in[j].zero();
-        dy[j].zero();
-        if (t + j < r.hi && t + j < end) {
+      for (int j = 0; j < R; ++j) {
+        if (!PLAIN) {
+          in[j].zero();
+          dy[j].zero();
+        }
+        if (PLAIN || (t + j < r.hi && t + j < end)) {
           in[j].load(row_of<T>(a.x, t + j) + c);
           dy[j].load(row_of<T>(a.dy, t + j) + c);
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBackRows; ++j) {
-        if (t + j >= end) break;
+      for (int j = 0; j < R; ++j) {
         const int now = t + j, back = now - (K - 1);
-        in[j].floats(x[K - 1]);
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-          for (int v = 0; v < VW; ++v) e[k][v] = e[k + 1][v];
-        float d[VW], dx[VW];
-        dy[j].floats(d);
-#pragma unroll
-        for (int v = 0; v < VW; ++v) {
-          if (a.silu) {
-            float pre = bias[v];
-#pragma unroll
-            for (int k = 0; k < K; ++k) pre += w[k][v] * x[k][v];
-            const float s = sigmoid(pre);
-            d[v] *= s + pre * s * (1.f - s);
-          }
-          e[K - 1][v] = now < r.hi ? d[v] : 0.f;
-          dx[v] = 0.f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) dx[v] += w[k][v] * e[K - 1 - k][v];
-        }
-        if (now < r.t1) {
+        if (!PLAIN && now >= end) break;
+        float(&xt)[VW] = x[(K - 1 + j) % K];
+        float(&et)[VW] = e[(K - 1 + j) % K];
+        float dx[VW];
+        in[j].floats(xt);
+        dy[j].floats(et);
+        if (a.silu) {
 #pragma unroll
           for (int v = 0; v < VW; ++v) {
-            db[v] += e[K - 1][v];
+            float pre = bias[v];
 #pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][v] += e[K - 1][v] * x[k][v];
+            for (int k = 0; k < K; ++k) pre += w[k][v] * x[(k + j) % K][v];
+            const float s = sigmoid(pre);
+            et[v] *= s + pre * s * (1.f - s);
           }
         }
-        // the gradient of the input K - 1 tokens back: of the run, or of S0
-        if (back >= r.t0 || r.first) {
+        if (!PLAIN && now >= r.hi) {   // (no token: a NaN of the window would stay in it)
+#pragma unroll
+          for (int v = 0; v < VW; ++v) et[v] = 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < VW; ++v) {
+          dx[v] = 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dx[v] += w[k][v] * e[(K - 1 - k + j) % K][v];
+        }
+        if (PLAIN || now < r.t1) {
+#pragma unroll
+          for (int v = 0; v < VW; ++v) {
+            db[v] += et[v];
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k][v] += et[v] * x[(k + j) % K][v];
+          }
+        }
+        Packed<VW, T> p;
+        if constexpr (PLAIN) {
+          p.from(dx);
+          p.store(row_of<T>(a.dx, back) + c);
+        } else if (back >= r.t0 || r.first) {
+          // the gradient of the input K - 1 tokens back: of the run, or of S0
           const int kept = back - (r.hi - (K - 1));   // its place in S
           if (a.dS && kept >= 0) {
-            Packed<VW, T> p;
             float s[VW];
             p.load(static_cast<const T*>(a.dS) + ((size_t)r.seq * (K - 1) + kept) * a.channels + c);
             p.floats(s);
 #pragma unroll
             for (int v = 0; v < VW; ++v) dx[v] += s[v];
           }
-          Packed<VW, T> p;
           p.from(dx);
           if (back >= r.lo) p.store(row_of<T>(a.dx, back) + c);
           else if (a.dS0)
             p.store(static_cast<T*>(a.dS0) + ((size_t)r.seq * (K - 1) + (K - 1 + back - r.lo)) * a.channels + c);
         }
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-          for (int v = 0; v < VW; ++v) x[k][v] = x[k + 1][v];
       }
+    };
+    for (int t = r.t0; t < end; t += R) {
+      if (t - (K - 1) >= r.t0 && t + R <= r.t1) walk(std::true_type{}, t);
+      else walk(std::false_type{}, t);
     }
   }
   if (!(a.dweight || a.dbias)) return;
@@ -376,8 +400,9 @@ hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream) {
   const int shift = run_shift(a.n_seq, a.channels, a.tokens), runs = runs_of(a.n_seq, a.tokens, shift);
   return with_form<8>(a, [&](auto k, auto vw, auto t) {
     const int tx = threads_along(a.channels, vw, kThreads);
-    hipLaunchKernelGGL((conv_kernel<k, vw, decltype(t)>), grid_of(runs, a.channels, vw, tx), dim3(kThreads), 0,
-                       stream, a, shift, runs, tx);
+    const dim3 grid = grid_of(runs, a.channels, vw, tx);
+    if (tx >= 64) hipLaunchKernelGGL((conv_kernel<k, vw, true, decltype(t)>), grid, dim3(kThreads), 0, stream, a, shift, runs, tx);
+    else hipLaunchKernelGGL((conv_kernel<k, vw, false, decltype(t)>), grid, dim3(kThreads), 0, stream, a, shift, runs, tx);
   });
 }
 
@@ -387,8 +412,9 @@ hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream) {
   const hipError_t e = with_form<4>(a, [&](auto k, auto vw, auto t) {
     const int tx = threads_along(a.channels, vw, 64), lanes = (a.channels + vw - 1) / vw;
     parts = parts_of(runs, tx);
-    hipLaunchKernelGGL((conv_backward_kernel<k, vw, decltype(t)>), dim3(parts, (lanes + tx - 1) / tx),
-                       dim3(kThreads), 0, stream, a, shift, runs, tx);
+    const dim3 grid(parts, (lanes + tx - 1) / tx);
+    if (tx >= 64) hipLaunchKernelGGL((conv_backward_kernel<k, vw, true, decltype(t)>), grid, dim3(kThreads), 0, stream, a, shift, runs, tx);
+    else hipLaunchKernelGGL((conv_backward_kernel<k, vw, false, decltype(t)>), grid, dim3(kThreads), 0, stream, a, shift, runs, tx);
   });
   if (e != hipSuccess || !(a.dweight || a.dbias)) return e;
   hipLaunchKernelGGL(sums_kernel, dim3((a.channels + 63) / 64, a.width + 1), dim3(kThreads), 0, stream, a, parts);
