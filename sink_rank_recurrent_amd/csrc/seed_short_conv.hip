@@ -338,13 +338,13 @@ int threads_along(int channels, int vw, int most) {
   while (tx < lanes && tx < most) tx *= 2;
   return tx;
 }
-// log2 of a run's tokens: 32, and fewer down to 8 where the runs of four
-// channels a thread are fewer than 4096 waves.
+// log2 of a run's tokens: 32, and fewer down to 8 where the runs have fewer
+// than 2048 waves, two a SIMD, for `vw` channels a thread.
 constexpr int kLongRun = 5, kShortRun = 3;
-int run_shift(int n_seq, int channels, int tokens) {
-  const long long waves = ((long long)channels + 255) / 256;
+int run_shift(int n_seq, int channels, int tokens, int vw) {
+  const long long waves = ((long long)channels + 64 * vw - 1) / (64 * vw);
   int shift = kLongRun;
-  while (shift > kShortRun && ((long long)(tokens >> shift) + n_seq) * waves < 4096) --shift;
+  while (shift > kShortRun && ((long long)(tokens >> shift) + n_seq) * waves < 2048) --shift;
   return shift;
 }
 int runs_of(int n_seq, int tokens, int shift) { return (tokens >> shift) + n_seq; }
@@ -387,8 +387,14 @@ int parts_of(int runs, int tx) {
 }
 
 int short_conv_parts(int n_seq, int channels, int tokens) {
-  // single channels take the most threads along the channels, so the fewest runs a block
-  return parts_of(runs_of(n_seq, tokens, run_shift(n_seq, channels, tokens)), threads_along(channels, 1, 64));
+  // whichever form the rows' alignment allows
+  int most = 0;
+  for (int vw = 1; vw <= 4; vw += 3) {
+    const int runs = runs_of(n_seq, tokens, run_shift(n_seq, channels, tokens, vw));
+    const int parts = parts_of(runs, threads_along(channels, vw, 64));
+    most = parts > most ? parts : most;
+  }
+  return most;
 }
 
 // At most 256 threads for each run and 256 channels, 2^32 in a grid's row.
@@ -397,8 +403,8 @@ bool short_conv_fits(int n_seq, int channels, int tokens) {
 }
 
 hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream) {
-  const int shift = run_shift(a.n_seq, a.channels, a.tokens), runs = runs_of(a.n_seq, a.tokens, shift);
   return with_form<8>(a, [&](auto k, auto vw, auto t) {
+    const int shift = run_shift(a.n_seq, a.channels, a.tokens, vw), runs = runs_of(a.n_seq, a.tokens, shift);
     const int tx = threads_along(a.channels, vw, kThreads);
     const dim3 grid = grid_of(runs, a.channels, vw, tx);
     if (tx >= 64) hipLaunchKernelGGL((conv_kernel<k, vw, true, decltype(t)>), grid, dim3(kThreads), 0, stream, a, shift, runs, tx);
@@ -407,9 +413,9 @@ hipError_t launch_short_conv(const ConvArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_short_conv_backward(const ConvArgs& a, hipStream_t stream) {
-  const int shift = run_shift(a.n_seq, a.channels, a.tokens), runs = runs_of(a.n_seq, a.tokens, shift);
   int parts = 0;
   const hipError_t e = with_form<4>(a, [&](auto k, auto vw, auto t) {
+    const int shift = run_shift(a.n_seq, a.channels, a.tokens, vw), runs = runs_of(a.n_seq, a.tokens, shift);
     const int tx = threads_along(a.channels, vw, 64), lanes = (a.channels + vw - 1) / vw;
     parts = parts_of(runs, tx);
     const dim3 grid(parts, (lanes + tx - 1) / tx);
