@@ -339,12 +339,14 @@ int threads_along(int channels, int vw, int most) {
   return tx;
 }
 // log2 of a run's tokens: 32, and fewer down to 8 where the runs have fewer
-// than 2048 waves, two a SIMD, for `vw` channels a thread.
+// than 4096 waves, four a SIMD, for `vw` channels a thread (a run of eight
+// alone costs nearly what one of sixteen does: 3001 x 2047 single channels
+// backward 24 us with runs of 8 or 32, 18 with 16).
 constexpr int kLongRun = 5, kShortRun = 3;
 int run_shift(int n_seq, int channels, int tokens, int vw) {
   const long long waves = ((long long)channels + 64 * vw - 1) / (64 * vw);
   int shift = kLongRun;
-  while (shift > kShortRun && ((long long)(tokens >> shift) + n_seq) * waves < 2048) --shift;
+  while (shift > kShortRun && ((long long)(tokens >> shift) + n_seq) * waves < 4096) --shift;
   return shift;
 }
 int runs_of(int n_seq, int tokens, int shift) { return (tokens >> shift) + n_seq; }
