@@ -56,7 +56,7 @@ SCANB = ("n_seq", "channels", "groups", "d_state", "tokens", "cu", *SCAN_IN, "dy
          "dx_stride", "ddt", "ddt_stride", "dA", "dB", "dB_stride", "dC", "dC_stride", "dD", "dz", "dz_stride",
          "ddt_bias", "dS0", "ws", "ws_bytes", "stream")
 STEP = ("batch", "channels", "groups", "d_state", *SCAN_IN, "y", "y_stride", "S", "stream")
-SIZES = {"n_seq": 2, "batch": 5, "channels": 96, "width": 4, "tokens": 100, "dtype": 1, "activation": 1,
+SIZES = {"n_seq": 2, "batch": 5, "channels": 96, "width": 4, "tokens": 1000, "dtype": 1, "activation": 1,
          "groups": 2, "d_state": 16, "softplus": 1, "ws_bytes": BIG >> 5, "stream": None}
 STRIDES = {"B_stride": 32, "C_stride": 32, "dB_stride": 40, "dC_stride": 32}
 
@@ -78,7 +78,7 @@ def at(name, offset=0):
 
 SEQ_BAD = [
     (dict(n_seq=0), 2, "positive"), (dict(tokens=-1), 2, "at least 0"), (dict(channels=0), 2, "positive"),
-    (dict(channels=(1 << 20) + 2), 3, "2^20"), (dict(tokens=101, cu=None), 2, "equal"),
+    (dict(channels=(1 << 20) + 2), 3, "2^20"), (dict(tokens=1001, cu=None), 2, "equal"),
     (dict(n_seq=1 << 25), 3, "grid"), (dict(cu=ctypes.c_void_p(0x10002)), 1, "cu_seqlens is not"),
     (dict(tokens=0x7fffffff), 3, "grid"),
 ]
@@ -175,12 +175,12 @@ def test_step_refuses(over, status, text):
 
 def test_workspace_queries():
     reject = ctypes.c_size_t(-1).value
-    one = L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 100, 0)
-    assert 0 < one < L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 1000, 0)
-    assert one <= L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 100, 1)
+    one = L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 1000, 0)
+    assert 0 < one < L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 10000, 0)
+    assert one <= L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 1000, 1)
     assert L.seed_selective_scan_workspace_bytes(2, 96, 2, 16, 0, 1) == 0
     assert L.seed_selective_scan_workspace_bytes(2, 96, 5, 16, 100, 0) == reject
-    assert 0 < L.seed_short_conv_workspace_bytes(2, 96, 4, 100) < 1 << 20
+    assert 0 < L.seed_short_conv_workspace_bytes(2, 96, 4, 1000) < 1 << 20
     assert L.seed_short_conv_workspace_bytes(2, 96, 5, 100) == reject
 
 
