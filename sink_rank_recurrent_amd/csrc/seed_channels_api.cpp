@@ -278,7 +278,8 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void*
                                  long long y_stride, void* S, void* stream) {
   const char* fn = "seed_short_conv_step";
   if (batch < 0) return fail(SEED_E_SHAPE, "%s: batch must be at least 0 (got %d)", fn, batch);
-  SEED_TRY(check_conv(fn, 1, channels, width, batch, nullptr, io_dtype, activation));
+  // (a block or more for each sequence)
+  SEED_TRY(check_conv(fn, batch == 0 ? 1 : batch, channels, width, batch, nullptr, io_dtype, activation));
   if (batch == 0) return ok();
   const size_t e = io_dtype == SEED_BF16 ? 2 : 4, T = (size_t)batch, C = (size_t)channels;
   const size_t state = T * (width - 1) * C;

@@ -334,10 +334,17 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   l.quarter = quarter_of(d_state);
   l.blocks = blocks_of(channels, groups);
   const long long along = (long long)groups * l.blocks;
-  // Forward: whole sequences where they fill half the chip; segments else
-  // (the first pass computes every decay a second time).
+  // Forward: whole sequences where these are workgroups enough, or short;
+  // segments else (the first pass makes every decay a second time).  us, bf16,
+  // 4096 channels: 8 x 1024 tokens 224 whole, 267 in segments; 6 x 1024 214 and
+  // 210; 4 x 2048 364 and 274; 1 x 128 31 and 32; 1 x 512 96 and 45.
+  // Segments of 256 tokens, and shorter ones where that leaves fewer than 2048
+  // workgroups: 16384 x 2048 284 (128 tokens 297, 512 341), 4096 x 4096 185 (128
+  // tokens 156, 64 162), 512 x 4096 81 (128 tokens 58, 64 45).
   if (backward) l.shift = kBackShift;
-  else l.shift = n_seq * along >= 256 || tokens / n_seq <= 64 ? -1 : 7;
+  else if (n_seq * along >= 384 || tokens / n_seq <= 128) l.shift = -1;
+  else
+    for (l.shift = 8; l.shift > 6 && (tokens >> l.shift) * along < 2048;) --l.shift;
   const size_t NP = (size_t)l.quarter * 4, T = (size_t)tokens, C = (size_t)channels;
   size_t at = 0;
   auto take = [&](size_t bytes) {

@@ -95,9 +95,11 @@ def run_all(p, offsets, softplus, cu=None, lead=None):
 
 
 CASES = [
-    # offsets, channels, groups, d_state: lengths of 0 and 1, around the tiles of 8 and the segments of 128
+    # offsets, channels, groups, d_state: lengths of 0 and 1, around the tiles of 8 and the segments of 64
+    # (forward, from 129 tokens a sequence on) and 128 (backward)
     ([0, 1], 1, 1, 1), ([0, 0, 2], 3, 3, 16), ([0, 7, 8, 17], 64, 1, 16), ([0, 63, 127, 192], 70, 2, 5),
-    ([0, 64, 129], 130, 1, 16), ([0, 300], 24, 4, 16), ([0, 128, 128, 257], 260, 1, 8), ([0, 65, 70], 66, 1, 32),
+    ([0, 64, 129], 130, 1, 16), ([0, 300], 24, 4, 16),
+    ([0, 192], 40, 1, 8), ([0, 1, 257, 400], 70, 1, 16), ([0, 385], 3, 1, 40), ([0, 512, 513], 33, 3, 4), ([0, 128, 128, 257], 260, 1, 8), ([0, 65, 70], 66, 1, 32),
     ([0, 40], 40, 2, 64), ([0, 3, 90], 129, 1, 33), ([0, 9], 513, 1, 16), ([0, 130], 10, 2, 17),
 ]
 
@@ -116,9 +118,10 @@ def test_parts_of_the_formula(have):
 
 
 def test_enough_sequences_to_run_whole():
-    """40 sequences of three blocks of channels go from end to end."""
+    """50 sequences of eleven blocks of channels go from end to end, the
+    longest first."""
     n, W = 50, 700
-    lens = [(7 * i) % 13 for i in range(n)]
+    lens = [(70 * i) % 130 for i in range(n)]
     offsets = [0, *np.cumsum(lens).tolist()]
     p = make(offsets[-1], W, 1, 16, n, torch.float32, 4)
     run_all(p, offsets, True, torch.tensor(offsets, dtype=torch.int32, device="cuda"))
@@ -128,7 +131,7 @@ def test_enough_sequences_to_run_whole():
 def test_many_sequences(n_seq):
     rng = np.random.default_rng(n_seq)
     lens = rng.integers(0, 3, n_seq)
-    lens[rng.integers(0, n_seq, 2)] = 140
+    lens[rng.integers(0, n_seq, 2)] = 140      # (whole: 129 tokens a sequence would go in segments)
     offsets = [0, *np.cumsum(lens).tolist()]
     p = make(offsets[-1], 5, 1, 3, n_seq, torch.bfloat16, 5)
     run_all(p, offsets, True, torch.tensor(offsets, dtype=torch.int32, device="cuda"))
@@ -146,8 +149,8 @@ def test_extreme_steps_and_rates():
 
 
 def test_nan_and_infinity_stay_in_their_channel():
-    W, T = 70, 200
-    offsets = [0, 90, 200]
+    W, T = 70, 400
+    offsets = [0, 90, 400]
     cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
     p = make(T, W, 1, 5, 2, torch.float32, 7)
     clean = outputs(p, 2, back=False)
@@ -156,7 +159,7 @@ def test_nan_and_infinity_stay_in_their_channel():
     out = outputs(p, 2, back=False)
     forward(p, out, True, cu)
     touched = torch.zeros(T, W, dtype=torch.bool, device="cuda")
-    touched[40:90, 3], touched[100:200, 64], touched[10, 8] = True, True, True
+    touched[40:90, 3], touched[100:400, 64], touched[10, 8] = True, True, True
     assert not torch.isfinite(out["y"][touched]).any()
     assert torch.equal(out["y"][~touched], clean["y"][~touched])
     ok = torch.ones(2, W, dtype=torch.bool, device="cuda")
@@ -167,7 +170,7 @@ def test_nan_and_infinity_stay_in_their_channel():
 def test_prompt_in_parts_and_in_place():
     """A prompt in two parts, its state in place, within the sum of the bounds
     of the whole."""
-    p = make(300, 33, 1, 16, 1, torch.float32, 8)
+    p = make(300, 33, 1, 16, 1, torch.float32, 8)   # in segments; its parts, 140 and 160 tokens, too
     whole = outputs(p, 1, back=False)
     cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
     forward(p, whole, True, cu)
@@ -259,8 +262,8 @@ def test_no_tokens():
 def test_graph_stream_and_workspace(W, N):
     """On another stream with shared workspaces, and captured and replayed
     with eager calls between: the same bits."""
-    offsets = [0, 100, 164, 164, 500]
-    p = make(500, W, 1, N, 4, torch.bfloat16, 14)
+    offsets = [0, 100, 164, 164, 1200]
+    p = make(1200, W, 1, N, 4, torch.bfloat16, 14)
     cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
     ws = [channels.selective_scan_workspace(p["x"], p["B"], 4, backward=b) for b in (False, True)]
 
