@@ -38,28 +38,29 @@ typedef const __attribute__((address_space(4))) float* ScalarRow;   // read by s
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), and its slope
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), and its slope,
 // 1 / (1 + exp(-v)).  log(1 + e) = 2 atanh(e / (2 + e)): with s = e / (2 + e)
 // at most 1/3, atanh(s) / s is a polynomial in s^2, here of degree 4 (fitted
 // on Chebyshev points; 4e-9 of the value), so that small values keep their
 // relative accuracy.
-struct Step {
-  float v;
-  __device__ __forceinline__ float of(bool softplus) const {
-    if (!softplus) return v;
-    const float e = exp2_fast(fabsf(v) * -kLog2e);
-    const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-    float p = 0.14087337f;
-    p = p * q + 0.139807165f;
-    p = p * q + 0.20012425f;
-    p = p * q + 0.333331585f;
-    p = p * q + 1.f;
-    return fmaxf(v, 0.f) + 2.f * s * p;
-  }
-  __device__ __forceinline__ float slope(bool softplus) const {
-    return softplus ? sigmoid(v) : 1.f;
-  }
-};
+__device__ __forceinline__ float softplus_of(float v, float& e) {
+  e = exp2_fast(fabsf(v) * -kLog2e);
+  const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+  float p = 0.14087337f;
+  p = p * q + 0.139807165f;
+  p = p * q + 0.20012425f;
+  p = p * q + 0.333331585f;
+  p = p * q + 1.f;
+  return fmaxf(v, 0.f) + 2.f * s * p;
+}
+__device__ __forceinline__ float softplus_slope(float v, float e) {
+  const float r = __builtin_amdgcn_rcpf(1.f + e);
+  return v < 0.f ? e * r : r;
+}
+__device__ __forceinline__ float step_of(float v, bool softplus) {
+  float e;
+  return softplus ? softplus_of(v, e) : v;
+}
 
 // A wave's channels and states.
 struct Mine {

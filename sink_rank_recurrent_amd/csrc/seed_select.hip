@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
       const bool there = t + j < t1;
       x[o] = load_scalar(&raw.x[o]);
       if (gate) z[o] = load_scalar(&raw.z[o]);
-      const float delta = Step{load_scalar(&raw.dt[o]) + bias}.of(a.softplus);
+      const float delta = step_of(load_scalar(&raw.dt[o]) + bias, a.softplus);
       to[j][lane] = there ? make_float2(delta, delta * x[o]) : make_float2(0.f, 0.f);
       if (MODE == kCarry && there) gone += delta;
     }
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
     for (int r = 0; r < kRequests; ++r) {
       const int b = b0 + r;
       if (b >= a.n_seq) break;
-      const float delta = Step{dt[r] + bias}.of(a.softplus), u = delta * x[r];
+      const float delta = step_of(dt[r] + bias, a.softplus), u = delta * x[r];
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -38,26 +38,35 @@ __device__ __forceinline__ void load_raw(const Mine& m, int t, int t1, Raw<T, GA
 }
 
 // A token's values for a lane; behind the last token steps and gradients of
-// zero.
+// zero.  BACK: with what the gradients need behind the walk, softplus' slope
+// and dy silu'(z).
 struct Token {
-  float x, v, delta, z, dy, ds;
+  float x, delta, ds, slope, dys;
 };
-template <typename T, bool GATE>
+template <bool BACK, typename T, bool GATE>
 __device__ __forceinline__ void tokens_of(const Raw<T, GATE>& r, float bias, bool softplus, int there,
                                           Token (&k)[kOwn]) {
 #pragma unroll
   for (int o = 0; o < kOwn; ++o) {
     k[o].x = load_scalar(&r.x[o]);
-    k[o].delta = k[o].v = load_scalar(&r.dt[o]) + bias;
-    k[o].dy = k[o].ds = load_scalar(&r.dy[o]);
+    k[o].delta = load_scalar(&r.dt[o]) + bias;
+    k[o].slope = 1.f;
+    const float dy = load_scalar(&r.dy[o]);
+    k[o].ds = dy;
     if (GATE) {
-      k[o].z = load_scalar(&r.z[o]);
-      k[o].ds = k[o].dy * (k[o].z * sigmoid(k[o].z));
+      const float z = load_scalar(&r.z[o]), g = sigmoid(z), zg = z * g;
+      k[o].ds = dy * zg;
+      if (BACK) k[o].dys = dy * (g + zg * (1.f - g));
     }
   }
   if (softplus) {
 #pragma unroll
-    for (int o = 0; o < kOwn; ++o) k[o].delta = Step{k[o].v}.of(true);
+    for (int o = 0; o < kOwn; ++o) {
+      float e;
+      const float v = k[o].delta;
+      k[o].delta = softplus_of(v, e);
+      if (BACK) k[o].slope = softplus_slope(v, e);
+    }
   }
 #pragma unroll
   for (int o = 0; o < kOwn; ++o)
@@ -98,7 +107,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
   auto prepare = [&](int t, Shared& to) {
     Token k[kOwn];
     const int at = t + m.wave * kOwn;
-    tokens_of(raw, bias, softplus, r.t1 - at, k);
+    tokens_of<false>(raw, bias, softplus, r.t1 - at, k);
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) to.put(m.wave * kOwn + o, lane, k[o], at + o < r.t1);
   };
@@ -260,7 +269,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
         for (int i = 0; i < Q; ++i) first[i] = exp2_fast(gone * A[i]) * H[i] + made[i];
         Token own[kOwn];
         const int at = t0 + m.wave * kOwn;
-        tokens_of(raw, bias, args_again()->softplus, r.t1 - at, own);
+        tokens_of<true>(raw, bias, args_again()->softplus, r.t1 - at, own);
 #pragma unroll
         for (int o = 0; o < kOwn; ++o)   // lanes without a channel add nothing to dB and dC
           prep.put(m.wave * kOwn + o, lane, own[o], at + o < r.t1 && m.live);
@@ -355,7 +364,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
             du += v.x;
             rate += v.y;
           }
-          const float dv = (k.x * du + rate * kLn2) * Step{k.v}.slope(q->softplus);
+          const float dv = (k.x * du + rate * kLn2) * k.slope;
           dbias += dv;
           dD += k.ds * k.x;
           Packed<1, T> out;
@@ -366,8 +375,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           out.from(one);
           out.store(in_row<T>(q->ddt.p, q->ddt.stride, t, in));
           if (GATE) {
-            const float g = sigmoid(k.z);
-            one[0] = k.dy * (s + D * k.x) * (g + k.z * g * (1.f - g));
+            one[0] = (s + D * k.x) * k.dys;
             out.from(one);
             out.store(in_row<T>(q->dz.p, q->dz.stride, t, in));
           }
