@@ -42,19 +42,23 @@ __device__ __forceinline__ void load_raw(const SelectArgs& a, const Mine& m, int
   }
 }
 
-// The sequence with the rank-th most tokens, of at most 64.  Workgroups start
-// in their numbers' order and go round the CUs, so that each CU gets long and
-// short ones alike (24 ragged sequences of 7919 tokens x 4096: 228 us, 243 in their own order).
-__device__ __forceinline__ int ranked(const Batch& b, int rank) {
-  const int lane = (int)__lane_id();
-  const int len = lane < b.n_seq ? first_token(b, lane + 1) - first_token(b, lane) : 0;
+// The sequence that a workgroup's number stands for, long ones first.
+// Workgroups start in their numbers' order and go round the CUs, so that each
+// CU gets long and short ones alike (24 ragged sequences of 7919 tokens x 4096:
+// 149 us, 183 in their own order).  The sequences are ranked among every
+// `sets`-th of them, at most 64, by the whole wave.
+__device__ __forceinline__ int ranked(const Batch& b, int number) {
+  const int sets = (b.n_seq + 63) >> 6, set = number % sets, rank = number / sets;
+  const int count = (b.n_seq - set + sets - 1) / sets, lane = (int)__lane_id();
+  const int at = set + lane * sets;
+  const int len = lane < count ? first_token(b, at + 1) - first_token(b, at) : 0;
   int longer = 0;
-  for (int s = 0; s < b.n_seq; ++s) {
+  for (int s = 0; s < count; ++s) {
     const int other = __builtin_amdgcn_readlane(len, s);
     longer += other > len || (other == len && s < lane);
   }
-  const uint64_t mine = __ballot(lane < b.n_seq && longer == rank);
-  return mine ? __builtin_ctzll(mine) : rank;
+  const uint64_t found = __ballot(lane < count && longer == rank);   // one: ranks differ
+  return found ? set + __builtin_ctzll(found) * sets : number;
 }
 
 // MODE kWhole: a sequence from its first state to its last; kCarry: what a
@@ -73,7 +77,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   if (MODE == kWhole) {
     s = blockIdx.z * gridDim.y + blockIdx.y;
     if (s >= a.n_seq) return;
-    if (a.cu && a.n_seq <= 64) s = ranked(b, s);
+    if (a.cu) s = ranked(b, s);
     t0 = first_token(b, s);
     t1 = b.cu ? first_token(b, s + 1) : t0 + b.len;
   } else {
@@ -361,9 +365,9 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   if (backward) {
     const size_t tiles = (size_t)(tokens >> 3) + n_seq;
     // Blocks of channels that follow each other in a workgroup add up dB and dC
-    // before they are written: as many as leave sixteen workgroups a CU, five rounds of
-    // those that fit at once (4 x 2048 x 4096: 545 us with one block, 557 with
-    // two, 625 with four and less than two rounds, of kernel and sums).
+    // before they are written: as many as leave sixteen workgroups a CU, five
+    // rounds of those that fit at once (4 x 2048 x 4096: 639 us with one block,
+    // 653 with two, 723 with four and less than two rounds).
     l.set = 4;
     while (l.set > 1 && (long long)l.slots * groups * ((l.blocks + l.set - 1) / l.set) < 4096) l.set /= 2;
     l.sets = (l.blocks + l.set - 1) / l.set;
