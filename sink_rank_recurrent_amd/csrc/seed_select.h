@@ -13,13 +13,13 @@
 // channels and a quarter of the states each, in registers.  What a token needs
 // once per channel (softplus, gate, the gradients of x, dt and z) is shared
 // out among the waves, two of every eight tokens each, and goes through LDS.
-// B and C of a token are the same for a wave's lanes.  Where they multiply a
-// state each (C.h, G.B) they are scalar operands, read through the scalar cache
-// from fp32 rows (prepare_kernel).  Where they make an outer product with the
-// channels (h += B u, G += C ds) a matrix instruction of 4 x 4 blocks adds four
-// states of 64 channels at once: 4 x 1 values of a token's row, the same in
-// every block, times 1 x 4 channels, onto accumulators that lie as the states
-// do.
+// B and C of a token are the same for a wave's lanes; they come from fp32 rows
+// (prepare_kernel), a tile's through LDS.  Where they multiply a state each (C.h,
+// G.B) they are scalar operands or read from LDS, the same in every lane.  Where
+// they make an outer product with the channels (h += B u, G += C ds) a matrix
+// instruction of 4 x 4 blocks adds four states of 64 channels at once: 4 x 1
+// values of a token's row, the same in every block, times 1 x 4 channels, onto
+// accumulators that lie as the states do.
 #pragma once
 
 #include "seed_channels.h"
@@ -33,8 +33,6 @@ constexpr int kTile = 8;        // tokens that go through LDS together
 constexpr int kOwn = kTile / kWaves;   // of them prepared by one wave
 constexpr int kBackShift = 7;   // log2 of the tokens of a segment of the backward pass
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
-
-typedef const __attribute__((address_space(4))) float* ScalarRow;   // read by scalar loads
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -103,48 +101,23 @@ __device__ __forceinline__ ArgsAgain args_again() {
   return p;
 }
 
-// The rows of B and C: [token][group][wave][its Q states][B, C].
-// Those of the tokens of a tile for a wave's states, by scalar loads.  `last`:
-// the last token of the sequence or segment, counted from the tile's first;
-// tokens behind it take its row (their steps are zero, but a row of another
-// sequence may hold an infinity).
+// The rows of B and C: [token][group][wave][B of its Q states, C].
+// C of the tokens of a tile for a wave's states, by scalar loads.  Tokens behind
+// the last one of the sequence or segment take its row (their steps are zero,
+// but a row of another sequence may hold an infinity).
+typedef const __attribute__((address_space(4))) float* ScalarRow;
 template <int Q>
-struct TileRows {
+struct ReadOuts {
   uintptr_t base;
   uint32_t step;
-  int last;
-  __device__ __forceinline__ TileRows(const Mine& m, int t, int t1) : last(t1 - 1 - t) {
+  int last;      // counted from the tile's first token
+  __device__ __forceinline__ ReadOuts(const Mine& m, int t, int t1) : last(t1 - 1 - t) {
     const ArgsAgain a = args_again();
-    base = (uintptr_t)(a->ws + a->at.rows) + (((size_t)t * a->groups + m.group) * 4 + m.wave) * (8 * Q);
+    base = (uintptr_t)(a->ws + a->at.rows) + (((size_t)t * a->groups + m.group) * 4 + m.wave) * (8 * Q) + 4 * Q;
     step = (uint32_t)a->groups * (32 * Q);
   }
   __device__ __forceinline__ ScalarRow operator[](int j) const {
     return (ScalarRow)(base + (uint32_t)(j < last ? j : last) * step);
-  }
-};
-// The tile's rows in scalar registers where those suffice (Q <= 4: 64 of them,
-// on their way while the steps are made); else each token's when it is used.
-template <int Q>
-struct Scalars {
-  float v[Q <= 4 ? kTile : 1][2 * Q];
-  TileRows<Q> rows;
-  __device__ __forceinline__ explicit Scalars(const TileRows<Q>& r) : rows(r) {
-    if constexpr (Q <= 4) {
-#pragma unroll
-      for (int j = 0; j < kTile; ++j)
-#pragma unroll
-        for (int i = 0; i < 2 * Q; ++i) v[j][i] = rows[j][i];
-    }
-  }
-  // B of state i at 2 i, C at 2 i + 1
-  __device__ __forceinline__ const float* of(int j) {
-    if constexpr (Q <= 4) {
-      return v[j];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2 * Q; ++i) v[0][i] = rows[j][i];
-      return v[0];
-    }
   }
 };
 
@@ -169,44 +142,50 @@ struct RowTile {
       lds[(q * kThreads + (int)threadIdx.x) % kFloats] = v[q];
   }
 };
-// Token j's row for a wave's states, the same in every lane: B of state i at
-// 2 i, C at 2 i + 1.
-template <int Q>
-__device__ __forceinline__ void row_values(const float* lds, const Mine& m, int j, float (&v)[2 * Q]) {
+// B (WHAT 0) or C (1) of token j for a wave's states, the same in every lane.
+template <int Q, int WHAT>
+__device__ __forceinline__ void row_values(const float* lds, const Mine& m, int j, float (&v)[Q]) {
+  const float* p = lds + (j * kWaves + m.wave) * (2 * Q) + WHAT * Q;
+  if constexpr (Q == 2) {
+    load_vec<2>(p, v);
+  } else {
 #pragma unroll
-  for (int q = 0; q < Q / 2; ++q) {
-    const float4 x = reinterpret_cast<const float4*>(lds + (j * 4 + m.wave) * (2 * Q))[q];
-    v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+    for (int q = 0; q < Q / 4; ++q) {
+      const float4 x = reinterpret_cast<const float4*>(p)[q];
+      v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+    }
   }
 }
-// A lane's values of token j's row: B and C of state l % 4 of every four.
-template <int Q>
+// The same for outer products: a lane has those of state l % 4 of every four
+// (Q = 2: all, for multiply-adds).
+template <int Q, int WHAT>
 struct Outer {
-  float2 v[Q >= 4 ? Q / 4 : 1];
+  float v[Q >= 4 ? Q / 4 : Q];
   __device__ __forceinline__ void load(const float* lds, const Mine& m, int j) {
     if constexpr (Q >= 4) {
+      const float* p = lds + (j * kWaves + m.wave) * (2 * Q) + WHAT * Q + (__lane_id() & 3);
 #pragma unroll
-      for (int q = 0; q < Q / 4; ++q)
-        v[q] = reinterpret_cast<const float2*>(lds + (j * 4 + m.wave) * (2 * Q))[4 * q + (int)(__lane_id() & 3)];
+      for (int q = 0; q < Q / 4; ++q) v[q] = p[4 * q];
+    } else {
+      row_values<Q, WHAT>(lds, m, j, v);
     }
   }
 };
-// s + row x, for B (WHAT 0) or C (1) of a token: four states an instruction.
-// (Q = 2: multiply-adds with the scalars.)
+// s + row x of a token: four states an instruction.
 template <int Q, int WHAT>
-__device__ __forceinline__ void add_outer(float (&s)[Q], const Outer<Q>& o, const float* scalars, float x) {
+__device__ __forceinline__ void add_outer(float (&s)[Q], const Outer<Q, WHAT>& o, float x) {
   if constexpr (Q >= 4) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int q = 0; q < Q / 4; ++q) {
       f32x4 acc = {s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]};
-      acc = __builtin_amdgcn_mfma_f32_4x4x1f32(WHAT ? o.v[q].y : o.v[q].x, x, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_4x4x1f32(o.v[q], x, acc, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[4 * q + i] = acc[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < Q; ++i) s[i] += x * scalars[2 * i + WHAT];
+    for (int i = 0; i < Q; ++i) s[i] += x * o.v[i];
   }
 }
 // A lane's value in row t of an array over tokens: the row's address is

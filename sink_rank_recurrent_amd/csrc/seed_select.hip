@@ -6,7 +6,7 @@ namespace seed {
 namespace channels {
 namespace {
 
-// B and C of every token in fp32, [token][group][wave][its Q states][B, C],
+// B and C of every token in fp32, [token][group][wave][B of its Q states, C],
 // padded with zeros.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
@@ -14,7 +14,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
   float* out = reinterpret_cast<float*>(a.ws + a.at.rows);
   const size_t total = (size_t)a.tokens * a.groups * 8 * Q, step = (size_t)gridDim.x * kThreads;
   for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
-    const int n = (int)(i % (8 * Q)) / 2, what = (int)i & 1;
+    const int in = (int)(i % (8 * Q)), n = in / (2 * Q) * Q + in % Q, what = in / Q & 1;
     const size_t tg = i / (8 * Q), t = tg / a.groups;
     const int g = (int)(tg - t * a.groups);
     float x = 0.f;
@@ -68,7 +68,7 @@ template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   __shared__ float2 prep[2][kTile][64];                           // delta, delta x
   __shared__ float part[MODE == kCarry ? 1 : 2][kWaves][kTile][64];
-  __shared__ float rows[2][RowTile<Q>::kFloats];
+  __shared__ __attribute__((aligned(16))) float rows[2][RowTile<Q>::kFloats];
   const int block = MODE == kWhole ? blockIdx.x : blockIdx.y;
   const Mine m = mine(a, block / a.at.blocks, block % a.at.blocks);
   const int lane = (int)__lane_id(), c = m.c;
@@ -130,7 +130,16 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
     load_raw(a, m, t + 2 * kTile, t1, gate, next);
     RowTile<Q> next_row;
     next_row.load(m.group, t + 2 * kTile, t1);
-    Scalars<Q> scalars(TileRows<Q>(m, t, t1));
+    const ReadOuts<Q> read_outs(m, t, t1);
+    // on their way while the steps come from LDS (Q = 16: when they are used)
+    float C[Q <= 8 ? kTile : 1][Q];
+    if constexpr (MODE != kCarry && Q <= 8) {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j)
+#pragma unroll
+        for (int i = 0; i < Q; ++i) C[j][i] = read_outs[j][i];
+      next_token();
+    }
     float xs[kOwn], zs[kOwn];
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
@@ -140,16 +149,16 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       const float2 k = prep[turn][j][lane];
-      Outer<Q> outer;
-      outer.load(rows[turn], m, j);
-      const float* BC = scalars.of(j);
-      float s = 0.f;
+      Outer<Q, 0> B;
+      B.load(rows[turn], m, j);
 #pragma unroll
       for (int i = 0; i < Q; ++i) h[i] *= exp2_fast(k.x * A[i]);
-      add_outer<Q, 0>(h, outer, BC, k.y);
+      add_outer(h, B, k.y);
       if (MODE != kCarry) {
+        const ScalarRow late = read_outs[j];
+        float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < Q; ++i) s += BC[2 * i + 1] * h[i];
+        for (int i = 0; i < Q; ++i) s += (Q <= 8 ? C[Q <= 8 ? j : 0][i] : late[i]) * h[i];
         part[turn][m.wave][j][lane] = s;
       }
     }

@@ -88,7 +88,7 @@ __device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (siz
 template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_kernel(SelectArgs a) {
   __shared__ Shared prep[2];
-  __shared__ float rows[2][RowTile<Q>::kFloats];
+  __shared__ __attribute__((aligned(16))) float rows[2][RowTile<Q>::kFloats];
   const Mine m = mine(a, blockIdx.y / a.at.blocks, blockIdx.y % a.at.blocks);
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, kShift);
   const int slot = blockIdx.x, c = m.c, lane = (int)__lane_id();
@@ -146,10 +146,11 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
       }
       const float2 k = prep[turn].step[j][lane];
       const float ds = prep[turn].ds[j][lane];
-      Outer<Q> outer;
-      outer.load(rows[turn], m, j);
-      float BC[2 * Q], dsC[Q];
-      if (Q < 4) row_values<Q>(rows[turn], m, j, BC);
+      Outer<Q, 0> B;
+      Outer<Q, 1> C;
+      B.load(rows[turn], m, j);
+      C.load(rows[turn], m, j);
+      float dsC[Q];
       gone += k.x;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
@@ -158,8 +159,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
         P[i] *= d;
         dsC[i] = 0.f;
       }
-      add_outer<Q, 0>(h, outer, BC, k.y);
-      add_outer<Q, 1>(dsC, outer, BC, ds);
+      add_outer(h, B, k.y);
+      add_outer(dsC, C, ds);
 #pragma unroll
       for (int i = 0; i < Q; ++i) G[i] += P[i] * dsC[i];
     }
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
   constexpr int kFoldTile = Q < 8 ? kTile / Q : 1, kFoldStates = Q < 8 ? Q : 8;
   constexpr int kFolds = Q < 4 ? 1 : Q / 4;               // values a lane has at last
   __shared__ Shared prep;
-  __shared__ float rows[RowTile<Q>::kFloats];
+  __shared__ __attribute__((aligned(16))) float rows[RowTile<Q>::kFloats];
   __shared__ float2 part[kWaves][kTile][64];                        // du and the rates' part of ddelta
   __shared__ float part_s[GATE ? kWaves : 1][kTile][64];            // C.h
   __shared__ float sums[kTiles][kWaves][kFolds][64];
@@ -279,17 +280,15 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
           if (Q >= 4 && j % 2 == 0) next_token();
-          float BC[2 * Q];
-          if (Q < 4) row_values<Q>(rows, m, j, BC);
           const float2 k = prep.step[j][lane];
-          Outer<Q> outer;
-          outer.load(rows, m, j);
+          Outer<Q, 0> B;
+          B.load(rows, m, j);
 #pragma unroll
           for (int i = 0; i < Q; ++i) {
             d[j][i] = exp2_fast(k.x * A[i]);
             hs[j][i] = d[j][i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
           }
-          add_outer<Q, 0>(hs[j], outer, BC, k.y);
+          add_outer(hs[j], B, k.y);
         }
         int again = lane;   // the steps are read a second time: 24 registers less
         asm volatile("" : "+v"(again));
@@ -301,14 +300,15 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
 #pragma unroll
           for (int jj = kFoldTile - 1; jj >= 0; --jj) {
             const int j = f * kTile / Q + jj, i0 = Q > 8 ? (f & 1) * 8 : 0;
-            float BC[2 * Q];
-            row_values<Q>(rows, m, j, BC);
+            float B[Q], C[Q];
+            row_values<Q, 0>(rows, m, j, B);
+            if (GATE) row_values<Q, 1>(rows, m, j, C);
             const float2 k = prep.step[j][again];
             const float ds = prep.ds[j][again];
             if (Q <= 8 || i0 > 0) {
-              Outer<Q> outer;
+              Outer<Q, 1> outer;
               outer.load(rows, m, j);
-              add_outer<Q, 1>(G, outer, BC, ds);
+              add_outer(G, outer, ds);
             }
             float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
@@ -316,8 +316,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
               const int i = i0 + ii;
               v[(jj * 2 + 0) * kFoldStates + ii] = G[i] * k.y;
               v[(jj * 2 + 1) * kFoldStates + ii] = ds * hs[j][i];
-              if (GATE) s += BC[2 * i + 1] * hs[j][i];
-              du += G[i] * BC[2 * i];
+              if (GATE) s += C[i] * hs[j][i];
+              du += G[i] * B[i];
               G[i] *= d[j][i];
               const float q = G[i] * (j ? hs[j ? j - 1 : 0][i] : first[i]);
               rate += A[i] * q;
