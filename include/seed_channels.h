@@ -102,9 +102,10 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void 
  *
  * Steps, states and sums are fp32, y is rounded once.  Where a batch has few
  * sequences, they are run in segments that are joined through the workspace;
- * a segment's decay is exp(A sum(delta)).  A NaN or infinity of a token's x,
- * dt or z stays in its channel (of B or C: in its group) and in its sequence;
- * an infinity may come out as NaN.
+ * a segment's decay is exp(A sum(delta)).  An exponential is off by about
+ * (1 + |delta A|) 2^-23 of its value; decays below 2^-126 are zero.  A NaN or
+ * infinity of a token's x, dt or z stays in its channel (of B or C: in its
+ * group) and in its sequence; an infinity may come out as NaN.
  * channels a multiple of groups and <= 2^20, d_state 1 .. 64.
  */
 seed_status seed_selective_scan(int n_seq, int channels, int groups, int d_state, int tokens,

@@ -7,7 +7,9 @@ namespace channels {
 namespace {
 
 // B and C of every token in fp32, [token][group][wave][B of its Q states, C],
-// padded with zeros.
+// padded with zeros: every block of channels reads them, with aligned vector
+// and scalar loads whatever the rows' own strides and type.  Bound by its
+// launch: 8192 rows of 2 x 16 in 5 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(SelectArgs a) {
   const int Q = a.at.quarter;
@@ -64,6 +66,14 @@ __device__ __forceinline__ int ranked(const Batch& b, int number) {
 // MODE kWhole: a sequence from its first state to its last; kCarry: what a
 // segment leaves of zero, and the sum of its steps; kRead: a segment's
 // read-outs from its first state.
+//
+// Tiles of 8 tokens: each wave makes the steps of two, all read all eight from
+// LDS, and each adds up the four waves' read-outs of its two; the loads of two
+// tiles are on their way.  One barrier a tile.  Bound by the vector unit's
+// issue slots: kWhole, 24 ragged sequences of 7919 tokens x 4096 channels of 16
+// states, bf16: 145 us with all launches, the unit busy 85 % of the cycles with
+// four-cycle instructions and 99 % with all (1.9 TB/s).  In segments, 16384 x
+// 2048, fp32: kCarry 120 us (76 and 92 %), kRead 155 (76 and 89 %), 264 in all.
 template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   __shared__ float2 prep[2][kTile][64];                           // delta, delta x
@@ -202,7 +212,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
 // places, and S; backwards also (blockIdx.z's upper half) the gradients at the
 // segments' ends, G' = exp(A gone) G + back, in theirs, and dS0.  A thread is a
 // state of a channel of a sequence; the values of kAhead segments are on their
-// way together.
+// way together.  Bound by latency, its sequence's segments in turn: 64 of one
+// sequence of 2048 channels of 16 states in 11 us, 4 x 16 of 4096 backward in 17.
 constexpr int kAhead = 8;
 template <bool BACK>
 __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
@@ -248,8 +259,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
 // One token of several sequences: LP lanes share a channel's states, four each
 // (VEC: read and written as one vector), and take kRequests of them with all
 // loads on their way together, the channel's rates in registers.  Bound by the
-// states' bytes: 256 x 8192 channels of 16 in 52 us, 5.4 TB/s.
-constexpr int kRequests = 4;
+// states' bytes: 256 x 8192 channels of 16 in a call of 55 us, 5.2 TB/s (four
+// requests 56, eight 63); 64 x 4096 in 12, of which the kernel 10.
+constexpr int kRequests = 2;
 template <typename T, int LP, bool VEC>
 __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   const int per = kThreads / LP, part = threadIdx.x % LP;
@@ -348,7 +360,7 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   l.blocks = blocks_of(channels, groups);
   const long long along = (long long)groups * l.blocks;
   // Forward: whole sequences where these are workgroups enough, or short;
-  // segments else (the first pass makes every decay a second time).  us, bf16,
+  // segments else (two passes, each making every decay).  us, bf16,
   // 4096 channels: 8 x 1024 tokens 224 whole, 267 in segments; 6 x 1024 214 and
   // 210; 4 x 2048 364 and 274; 1 x 128 31 and 32; 1 x 512 96 and 45.
   // Segments of 256 tokens, and shorter ones where that leaves fewer than 2048
@@ -392,8 +404,8 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   return l;
 }
 
-// Grids: blocks of channels along y, sequences or segments of 64 along x with
-// 256 threads each.
+// Grids: blocks of channels along y, segments of 64 tokens or more along x with
+// 256 threads each, 2^32 threads at most; row numbers of a tile ahead are ints.
 bool select_fits(int n_seq, int channels, int groups, int d_state, int tokens) {
   return (long long)groups * blocks_of(channels, groups) <= 65535 &&
          (long long)(tokens >> 6) + n_seq < (1LL << 24) && (long long)tokens + 64 <= 0x7fffffffLL;
