@@ -71,10 +71,6 @@ def _rows(t, name: str, lead: tuple, tail: tuple, dtypes) -> tuple:
         return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if len(tail) == 1 and len(lead) == 1 and t.dtype in dtypes and t.shape == (*lead, *tail):
-        step, one = t.stride()     # the common case first
-        if one == 1 and step >= tail[0] and lead[0] > 1:
-            return t.data_ptr(), step
     if t.shape != (*lead, *tail):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, *tail)}")
     if t.dtype not in dtypes:
@@ -101,12 +97,30 @@ def _rows(t, name: str, lead: tuple, tail: tuple, dtypes) -> tuple:
     return t.data_ptr(), max(step, width)
 
 
+def _row(t, name: str, shape: tuple, dims: int, dtypes) -> tuple:
+    """_rows of a shape whose last `dims` dimensions make a row: packed arrays
+    of two rows or more, the common case, on a shorter way."""
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and len(shape) == dims + 1 and t.shape == shape and t.dtype in dtypes:
+        strides = t.stride()
+        width = shape[1] if dims == 1 else shape[1] * shape[2]
+        if (strides[-1] == 1 and strides[0] >= width and shape[0] > 1
+                and (dims == 1 or strides[1] == shape[2])):
+            return t.data_ptr(), strides[0]
+    return _rows(t, name, shape[:-dims], shape[-dims:], dtypes)
+
+
 def _device(first, names: str, *others) -> int:
     """The index of the one device that all tensors are on."""
     try:
         index = first.get_device()
-        if index >= 0 and all(t is None or t.get_device() == index for t in others):
-            return index
+        if index >= 0:
+            for t in others:
+                if t is not None and t.get_device() != index:
+                    break
+            else:
+                return index
     except AttributeError:
         pass
     _same_device(**dict(zip(names.split(), (first, *others))))     # says which is not
@@ -116,7 +130,7 @@ def _device(first, names: str, *others) -> int:
 def _call(name: str, index: int, stream, *args) -> None:
     """Call the library on torch's current stream of device `index`, or on
     `stream`, with that device made current."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, _stream(stream, index))
     else:
@@ -166,7 +180,8 @@ def _conv_inputs(x, lead, weight, bias, activation):
         _need(bias, "bias", (channels,), _F32)
     if activation not in (None, "silu"):
         raise ValueError(f"unknown activation {activation!r} (use None or 'silu')")
-    return channels, width, _rows(x, "x", lead, (channels,), _IN)
+    shape = (*lead, channels)
+    return channels, width, shape, _row(x, "x", shape, 1, _IN)
 
 
 def seed_short_conv(x, weight, y, bias=None, activation="silu", S0=None, S=None, cu_seqlens=None,
@@ -177,8 +192,8 @@ def seed_short_conv(x, weight, y, bias=None, activation="silu", S0=None, S=None,
     each sequence."""
     index = _device(x, "x weight y bias S0 S cu_seqlens", weight, y, bias, S0, S, cu_seqlens)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
-    channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
-    yr = _rows(y, "y", lead, (channels,), (x.dtype,))
+    channels, width, shape, xr = _conv_inputs(x, lead, weight, bias, activation)
+    yr = _row(y, "y", shape, 1, (x.dtype,))
     for name, t in (("S0", S0), ("S", S)):
         if t is not None:
             _need(t, name, (n_seq, width - 1, channels), (x.dtype,))
@@ -203,9 +218,9 @@ def seed_short_conv_backward(dy, x, weight, dx, dweight=None, dbias=None, bias=N
     index = _device(x, "x dy weight dx dweight dbias bias S0 dS dS0 cu_seqlens workspace", dy, weight, dx,
                     dweight, dbias, bias, S0, dS, dS0, cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
-    channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
-    dyr = _rows(dy, "dy", lead, (channels,), (x.dtype,))
-    dxr = _rows(dx, "dx", lead, (channels,), (x.dtype,))
+    channels, width, shape, xr = _conv_inputs(x, lead, weight, bias, activation)
+    dyr = _row(dy, "dy", shape, 1, (x.dtype,))
+    dxr = _row(dx, "dx", shape, 1, (x.dtype,))
     for name, t in (("S0", S0), ("dS", dS), ("dS0", dS0)):
         if t is not None:
             _need(t, name, (n_seq, width - 1, channels), (x.dtype,))
@@ -230,8 +245,8 @@ def seed_short_conv_step(x, weight, y, S, bias=None, activation="silu", S0=None,
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
-    channels, width, xr = _conv_inputs(x, lead, weight, bias, activation)
-    yr = _rows(y, "y", lead, (channels,), (x.dtype,))
+    channels, width, shape, xr = _conv_inputs(x, lead, weight, bias, activation)
+    yr = _row(y, "y", shape, 1, (x.dtype,))
     _need(S, "S", (lead[0], width - 1, channels), (x.dtype,))
     if S0 is not None:
         _need(S0, "S0", (lead[0], width - 1, channels), (x.dtype,))
@@ -240,21 +255,24 @@ def seed_short_conv_step(x, weight, y, S, bias=None, activation="silu", S0=None,
 
 
 def _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead):
-    """(channels, groups, d_state, arguments from x to softplus)."""
+    """(channels, groups, d_state, shapes of x and B, arguments from x to
+    softplus)."""
     if A.dim() != 2 or B.dim() != len(lead) + 2:
         raise ValueError("A must be [channels, d_state], B and C [..., groups, d_state]")
     channels, d_state = A.shape
     groups = B.shape[-2]
     _need(A, "A", (channels, d_state), _F32)
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _need(t, name, (channels,), _F32)
-    xr = _rows(x, "x", lead, (channels,), _IN)
+    if D is not None:
+        _need(D, "D", (channels,), _F32)
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", (channels,), _F32)
+    shape, rows = (*lead, channels), (*lead, groups, d_state)
+    xr = _row(x, "x", shape, 1, _IN)
     io = (x.dtype,)
-    return channels, groups, d_state, (
-        *xr, *_rows(dt, "dt", lead, (channels,), io), _ptr(A), *_rows(B, "B", lead, (groups, d_state), io),
-        *_rows(C, "C", lead, (groups, d_state), io), _code(x.dtype), _ptr(D),
-        *_rows(z, "z", lead, (channels,), io), _ptr(dt_bias), int(softplus))
+    return channels, groups, d_state, shape, rows, (
+        *xr, *_row(dt, "dt", shape, 1, io), A.data_ptr(), *_row(B, "B", rows, 2, io),
+        *_row(C, "C", rows, 2, io), _code(x.dtype), _ptr(D), *_row(z, "z", shape, 1, io), _ptr(dt_bias),
+        1 if softplus else 0)
 
 
 def _select_bytes(n_seq, channels, groups, d_state, tokens, backward: bool) -> int:
@@ -278,8 +296,8 @@ def seed_selective_scan(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, soft
     index = _device(x, "x dt A B C y S D z dt_bias S0 cu_seqlens workspace", dt, A, B, C, y, S, D, z, dt_bias,
                     S0, cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
-    channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
-    yr = _rows(y, "y", lead, (channels,), (x.dtype,))
+    channels, groups, d_state, shape, rows, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
+    yr = _row(y, "y", shape, 1, (x.dtype,))
     for name, t in (("S", S), ("S0", S0)):
         if t is not None:
             _need(t, name, (n_seq, channels, d_state), _F32)
@@ -299,11 +317,11 @@ def seed_selective_scan_backward(dy, x, dt, A, B, C, dx, ddt, dA, dB, dC, D=None
                     dy, dt, A, B, C, dx, ddt, dA, dB, dC, D, z, dt_bias, dD, dz, ddt_bias, S0, dS, dS0,
                     cu_seqlens, workspace)
     n_seq, tokens, lead = _lead(x, 1, cu_seqlens)
-    channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
+    channels, groups, d_state, shape, rows, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
     io = (x.dtype,)
-    dyr, dxr, ddtr, dzr = (_rows(t, name, lead, (channels,), io) for name, t in
+    dyr, dxr, ddtr, dzr = (_row(t, name, shape, 1, io) for name, t in
                            (("dy", dy), ("dx", dx), ("ddt", ddt), ("dz", dz)))
-    dBr, dCr = (_rows(t, name, lead, (groups, d_state), io) for name, t in (("dB", dB), ("dC", dC)))
+    dBr, dCr = (_row(t, name, rows, 2, io) for name, t in (("dB", dB), ("dC", dC)))
     _need(dA, "dA", (channels, d_state), _F32)
     for name, t in (("dD", dD), ("ddt_bias", ddt_bias)):
         if t is not None:
@@ -326,8 +344,8 @@ def seed_selective_step(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, soft
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
-    channels, groups, d_state, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
-    yr = _rows(y, "y", lead, (channels,), (x.dtype,))
+    channels, groups, d_state, shape, rows, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
+    yr = _row(y, "y", shape, 1, (x.dtype,))
     _need(S, "S", (lead[0], channels, d_state), _F32)
     if S0 is not None:
         _need(S0, "S0", (lead[0], channels, d_state), _F32)

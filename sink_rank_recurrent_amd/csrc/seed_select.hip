@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
 // (VEC: read and written as one vector), and take kRequests of them with all
 // loads on their way together, the channel's rates in registers.  Bound by the
 // states' bytes: 256 x 8192 channels of 16 in a call of 55 us, 5.2 TB/s (four
-// requests 56, eight 63); 64 x 4096 in 12, of which the kernel 10.
+// requests 56, eight 63); 64 x 4096 in 11, the kernel 10.
 constexpr int kRequests = 2;
 template <typename T, int LP, bool VEC>
 __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {

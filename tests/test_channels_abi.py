@@ -237,6 +237,32 @@ def test_rows_of_tensors():
         rows(t, "t", (4, 6), (10,), (torch.float32,))
 
 
+def test_rows_on_the_shorter_way():
+    """The calls' shorter way takes and refuses the same rows."""
+    io = (torch.bfloat16,)
+    t = torch.zeros(24, 10, dtype=torch.bfloat16)
+    wide = torch.zeros(24, 3, 10, dtype=torch.bfloat16)
+    for a, dims in ((t, 1), (t[:, 2:7], 1), (t[:1, :3], 1), (t[:0], 1), (t[::2], 1), (t[:, :1], 1),
+                    (t.view(4, 6, 10), 1), (t.view(4, 6, 10)[:1, :, :3], 1), (t.view(24, 2, 5), 2),
+                    (t[:, 2:6].view(24, 2, 2), 2), (t[:, :5].unsqueeze(1), 2), (wide[:, :2], 2),
+                    (wide[:, 1:2], 2), (wide[:, :, :1], 1), (t.view(4, 6, 2, 5), 2), (None, 1)):
+        shape = (24, 10) if a is None else tuple(a.shape)
+        assert channels._row(a, "t", shape, dims, io) == channels._rows(a, "t", shape[:-dims], shape[-dims:], io), shape
+    for a, dims in ((t.view(4, 6, 10)[:, :3], 1), (t[:, ::2], 1), (wide[:, :, :4], 2), (t.t(), 1),
+                    (t[:1].expand(5, 10), 1), (wide.transpose(0, 1), 2)):
+        shape = tuple(a.shape)
+        for f in (lambda: channels._row(a, "t", shape, dims, io),
+                  lambda: channels._rows(a, "t", shape[:-dims], shape[-dims:], io)):
+            with pytest.raises(ValueError):
+                f()
+    with pytest.raises(ValueError, match="dtype"):
+        channels._row(t, "t", (24, 10), 1, (torch.float32,))
+    with pytest.raises(ValueError, match="shape"):
+        channels._row(t, "t", (24, 11), 1, io)
+    with pytest.raises(TypeError):
+        channels._row(3, "t", (24, 10), 1, io)
+
+
 def test_binding_refuses():
     x = torch.zeros(10, 32)
     with pytest.raises(ValueError, match="device memory"):
