@@ -366,7 +366,9 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           const int t = t0 + j;
           const uint32_t in = (uint32_t)c * sizeof(T);
           if (t >= r.t1) continue;
+          // step and gradient of the read-out from LDS again (the wave's own)
           const Token& k = own[o];
+          const float delta = prep.step[j][lane].x, ds = prep.ds[j][lane];
           float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) {
@@ -377,9 +379,9 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           }
           const float dv = (k.x * du + rate * kLn2) * k.slope;
           dbias += dv;
-          dD += k.ds * k.x;
+          dD += ds * k.x;
           Packed<1, T> out;
-          float one[1] = {k.delta * du + D * k.ds};
+          float one[1] = {delta * du + D * ds};
           out.from(one);
           out.store(in_row<T>(q->dx.p, q->dx.stride, t, in));
           one[0] = dv;
