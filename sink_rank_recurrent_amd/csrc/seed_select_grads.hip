@@ -8,7 +8,7 @@
 //   grads_kernel  8 tokens at a time, the last first: the states and decays
 //                 from the state before them (what the segment had made of
 //                 zero, and the decayed first state), and the chain rule
-//   sums          dB and dC over sets of blocks of channels, dA, dD and
+//   sums_kernel   dB and dC over sets of blocks of channels, dA, dD and
 //                 ddt_bias over segments, in a fixed order.
 #include "seed_select.h"
 
@@ -433,16 +433,43 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
   }
 }
 
-// dB and dC: the parts of the sets of channels, in order.  8192 tokens of 2 x 16
-// from 64 parts (67 MB) in 14 us, 4.9 TB/s.
+// Sums of the workgroups' parts, two kinds of blocks in one launch.  The first
+// `weights` blocks: dA, dD and ddt_bias from the parts [part][states, dD,
+// ddt_bias][channel], 64 channels of one of them a block, each of its waves every
+// fourth part, then the waves in order.  The others: dB and dC from the parts of
+// the sets of channels, in order.  8192 tokens of 2 x 16 from 64 sets (67 MB) and
+// 18 x 4096 weights from 68 parts (20 MB) in 18 us, 4.9 TB/s.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void rows_kernel(SelectArgs a) {
-  const int Q = a.at.quarter;
+__global__ __launch_bounds__(kThreads) void sums_kernel(SelectArgs a, int parts, int weights) {
+  const int Q = a.at.quarter, NP = 4 * Q;
+  if ((int)blockIdx.x < weights) {   // the whole block
+    __shared__ float lds[kThreads];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rows = a.d_state + 2;
+    const int c = (int)blockIdx.x / rows * 64 + lane, n = (int)blockIdx.x % rows;
+    const int row = n < a.d_state ? n : NP + (n - a.d_state);
+    const float* w = reinterpret_cast<const float*>(a.ws + a.at.weights);
+    float s = 0.f;
+    if (c < a.channels) {
+#pragma unroll 8
+      for (int p = wave; p < parts; p += 4) s += w[((size_t)p * (NP + 2) + row) * a.channels + c];
+    }
+    lds[threadIdx.x] = s;
+    __syncthreads();
+    if (wave != 0 || c >= a.channels) return;
+    s = lds[lane] + lds[64 + lane] + lds[128 + lane] + lds[192 + lane];
+    if (n < a.d_state) a.dA[(size_t)c * a.d_state + n] = s;
+    else if (n == a.d_state) {
+      if (a.dD) a.dD[c] = s;
+    } else if (a.ddt_bias) {
+      a.ddt_bias[c] = s;
+    }
+    return;
+  }
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, 0);
   const float* sums = reinterpret_cast<const float*>(a.ws + a.at.sums);
   const int first = first_token(b, 0), end = b.cu ? first_token(b, a.n_seq) : a.tokens;
-  const size_t row = (size_t)a.groups * 8 * Q, step = (size_t)gridDim.x * kThreads;
-  for (size_t i = first * row + (size_t)blockIdx.x * kThreads + threadIdx.x; i < end * row; i += step) {
+  const size_t row = (size_t)a.groups * 8 * Q, step = (size_t)(gridDim.x - weights) * kThreads;
+  for (size_t i = first * row + (size_t)(blockIdx.x - weights) * kThreads + threadIdx.x; i < end * row; i += step) {
     const int in = (int)(i % (8 * Q)), n = in / (2 * Q) * Q + in % Q, what = in / Q & 1;
     if (n >= a.d_state) continue;
     const size_t tg = i / (8 * Q), t = tg / a.groups;
@@ -456,29 +483,14 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(SelectArgs a) {
   }
 }
 
-// dA, dD and ddt_bias: the parts [part][states, dD, ddt_bias][channel], a wave
-// every fourth, then the waves in order.  68 parts of 18 x 4096 (20 MB) in 6 us,
-// with the launch.
-__global__ __launch_bounds__(kThreads) void weights_kernel(SelectArgs a, int parts) {
-  __shared__ float lds[kThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, NP = 4 * a.at.quarter;
-  const int c = (int)blockIdx.x * 64 + lane, n = blockIdx.y, row = n < a.d_state ? n : NP + (n - a.d_state);
-  const float* w = reinterpret_cast<const float*>(a.ws + a.at.weights);
-  float s = 0.f;
-  if (c < a.channels) {
-#pragma unroll 8
-    for (int p = wave; p < parts; p += 4) s += w[((size_t)p * (NP + 2) + row) * a.channels + c];
-  }
-  lds[threadIdx.x] = s;
-  __syncthreads();
-  if (wave != 0 || c >= a.channels) return;
-  s = lds[lane] + lds[64 + lane] + lds[128 + lane] + lds[192 + lane];
-  if (n < a.d_state) a.dA[(size_t)c * a.d_state + n] = s;
-  else if (n == a.d_state) {
-    if (a.dD) a.dD[c] = s;
-  } else if (a.ddt_bias) {
-    a.ddt_bias[c] = s;
-  }
+// At most 2^14 blocks of channels by 66.  Without tokens there are no parts: zero.
+template <typename T>
+hipError_t launch_sums(const SelectArgs& a, hipStream_t stream) {
+  const int weights = (a.channels + 63) / 64 * (a.d_state + 2);
+  const size_t values = (size_t)a.tokens * a.groups * 8 * a.at.quarter, blocks = (values + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((sums_kernel<T>), dim3((unsigned)(weights + (blocks < 4096 ? blocks : 4096))), dim3(kThreads), 0,
+                     stream, a, a.tokens > 0 ? a.at.parts : 0, weights);
+  return hipGetLastError();
 }
 
 template <typename T, int Q>
@@ -491,10 +503,6 @@ hipError_t grads_types(const SelectArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   if (a.z.p) hipLaunchKernelGGL((grads_kernel<T, Q, true>), grads, dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL((grads_kernel<T, Q, false>), grads, dim3(kThreads), 0, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const size_t values = (size_t)a.tokens * a.groups * 8 * Q, blocks = (values + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL((rows_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -519,10 +527,7 @@ hipError_t launch_select_backward(const SelectArgs& a, hipStream_t stream) {
     e = launch_select_join(a, true, stream);   // dS0 = dS
   }
   if (e != hipSuccess) return e;
-  // without tokens there are no parts: zero
-  hipLaunchKernelGGL(weights_kernel, dim3((a.channels + 63) / 64, a.d_state + 2), dim3(kThreads), 0, stream, a,
-                     a.tokens > 0 ? a.at.parts : 0);
-  return hipGetLastError();
+  return a.bf16 ? launch_sums<bf16_t>(a, stream) : launch_sums<float>(a, stream);
 }
 
 }  // namespace seed
