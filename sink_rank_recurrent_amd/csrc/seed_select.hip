@@ -259,8 +259,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
 // One token of several sequences: LP lanes share a channel's states, four each
 // (VEC: read and written as one vector), and take kRequests of them with all
 // loads on their way together, the channel's rates in registers.  Bound by the
-// states' bytes: 256 x 8192 channels of 16 in a call of 55 us, 5.2 TB/s (four
-// requests 56, eight 63); 64 x 4096 in 11, the kernel 10.
+// states' bytes: 256 x 8192 channels of 16 in a call of 51 us, 5.6 TB/s (with
+// states through the caches 55, and then four requests 56, eight 63); 64 x 4096
+// in 11, the kernel 10.
 constexpr int kRequests = 2;
 template <typename T, int LP, bool VEC>
 __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
@@ -268,6 +269,11 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * per + threadIdx.x / LP;
   const int at = c < a.channels ? c : a.channels - 1, g = at / (a.channels / a.groups);
   const int n0 = part * 4, N = a.d_state;
+  // States of 32 MB or more go past the caches: until they are read again, at the
+  // next token, a model's other layers have filled these.  us for each of 24
+  // layers, states to another array: 33.6 MB 15.8 (through the caches 16.5), 134 MB
+  // 48.9 (51.4), but 16.8 MB 9.5 (9.5) and 1 MB 3.8 (3.6); in place equal.
+  const bool past = (size_t)a.n_seq * a.channels * N * sizeof(float) >= (size_t)32 << 20;
   auto four = [&](const float* p, float (&v)[4]) {
     if constexpr (VEC) {
       load_vec<4>(p, v);
@@ -313,7 +319,9 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
       if (c >= a.channels) continue;
       float* S = a.S + state_at(a, b, at) + n0;
       if constexpr (VEC) {
-        store_vec<4>(S, h[r]);
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        if (past) __builtin_nontemporal_store(f32x4{h[r][0], h[r][1], h[r][2], h[r][3]}, reinterpret_cast<f32x4*>(S));
+        else store_vec<4>(S, h[r]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -94,3 +94,28 @@ def test_states_beyond_32_bits():
     channels.seed_short_conv_step(p["x"].contiguous(), w, out, held)
     for b in (0, 7999):
         assert torch.equal(many[b], held[0]) and torch.equal(y[b], out[0])
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_step_of_many_requests(in_place):
+    """States of 32 MB and more are stored past the caches: the same values as
+    from calls of a few requests each, two steps running."""
+    batch, channels_, d_state = 131, 4096, 16     # 34 MB, an odd batch
+    gen = torch.Generator("cuda").manual_seed(7)
+
+    def normal(*s):
+        return torch.randn(*s, device="cuda", generator=gen)
+
+    A = -torch.exp(normal(channels_, d_state))
+    S = normal(batch, channels_, d_state)
+    want = S.clone()
+    for _ in range(2):
+        x, dt, z = (normal(batch, channels_).bfloat16() for _ in range(3))
+        B, C = (normal(batch, 1, d_state).bfloat16() for _ in range(2))
+        y, y_want = torch.empty_like(x), torch.empty_like(x)
+        S0, S = S, S if in_place else torch.empty_like(S)
+        channels.seed_selective_step(x, dt, A, B, C, y, S, z=z, S0=S0)
+        for lo in range(0, batch, 50):
+            p = slice(lo, min(lo + 50, batch))
+            channels.seed_selective_step(x[p], dt[p], A, B[p], C[p], y_want[p], want[p], z=z[p])
+        assert torch.equal(y, y_want) and torch.equal(S, want)
