@@ -137,6 +137,19 @@ def test_many_sequences(n_seq):
     run_all(p, offsets, True, torch.tensor(offsets, dtype=torch.int32, device="cuda"))
 
 
+@pytest.mark.parametrize("n_seq,W,G,N", [(2100, 330, 1, 6), (4200, 150, 1, 16), (2100, 300, 2, 20), (4200, 130, 1, 50)])
+def test_blocks_of_channels_one_after_the_other(n_seq, W, G, N):
+    """Segments enough for a workgroup to take several blocks of 64 channels in
+    turn, the last one fewer, and to go on to further segments (backward)."""
+    rng = np.random.default_rng(N)
+    lens = rng.integers(0, 2, n_seq)
+    lens[:2], lens[rng.integers(2, n_seq, 3)] = (9, 140), 17
+    offsets = [0, *np.cumsum(lens).tolist()]
+    dtype = torch.float32 if N == 20 else torch.bfloat16
+    p = make(offsets[-1], W, G, N, n_seq, dtype, N, {"D", "z", "dt_bias", "softplus"} if N != 16 else {"softplus"})
+    run_all(p, offsets, True, torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+
+
 def test_extreme_steps_and_rates():
     """Steps and rates whose decays vanish or stay at one, softplus far out on
     both sides, and rows of zeros."""
