@@ -40,9 +40,10 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 8;        // tokens that go through LDS together
 constexpr int kOwn = kTile / kWaves;   // of them prepared by one wave
 // log2 of the tokens of a segment of the backward pass: 4 x 2048 tokens x 4096,
-// bf16, 640 us (64 tokens 661, 256 tokens 797); 3001 x 2050, fp32, 115 (120, 204).
+// bf16, 640 us then (64 tokens 661, 256 tokens 797), now 623; 3001 x 2050, fp32,
+// 115 then (120, 204), now 110.
 constexpr int kBackShift = 7;
-constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -52,7 +53,8 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // on Chebyshev points; 4e-9 of the value), so that small values keep their
 // relative accuracy.
 __device__ __forceinline__ float softplus_of(float v, float& e) {
-  e = exp2_fast(fabsf(v) * -kLog2e);
+  // (the constant in two parts: the first alone is 1.3e-8 short in every step)
+  e = exp2_fast(-fmaf(fabsf(v), kLog2e, fabsf(v) * kLog2eRest));
   const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
   float p = 0.14087337f;
   p = p * q + 0.139807165f;
@@ -91,13 +93,16 @@ __device__ __forceinline__ size_t carry_at(const SelectArgs& a, int of, int n, i
   return ((size_t)of * (4 * Q) + n) * a.channels + c;
 }
 
-// A in powers of two: exp(delta A) = 2^(delta A log2 e).
+// exp(delta A) = 2^(delta log2 e A): the steps are scaled, each with a rounding
+// of its own, and not the rates, whose rounding would be the same in every
+// factor of a product of decays.
+__device__ __forceinline__ float in_powers_of_two(float delta) { return delta * kLog2e; }
 template <int Q>
 __device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, float (&A)[Q]) {
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int n = m.wave * Q + i;
-    A[i] = n < a.d_state ? a.A[(size_t)m.c * a.d_state + n] * kLog2e : 0.f;
+    A[i] = n < a.d_state ? a.A[(size_t)m.c * a.d_state + n] : 0.f;
   }
 }
 

@@ -73,10 +73,10 @@ __device__ __forceinline__ int ranked(const Batch& b, int number) {
 // issue slots: kWhole, 24 ragged sequences of 7919 tokens x 4096 channels of 16
 // states, bf16: 145 us with all launches, the unit busy 85 % of the cycles with
 // four-cycle instructions and 99 % with all (1.9 TB/s).  In segments, 16384 x
-// 2048, fp32: kCarry 120 us (76 and 92 %), kRead 155 (76 and 89 %), 264 in all.
+// 2048, fp32: kCarry 120 us (76 and 92 %), kRead 155 (76 and 89 %), 262 in all.
 template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
-  __shared__ float2 prep[2][kTile][64];                           // delta, delta x
+  __shared__ float2 prep[2][kTile][64];                           // the power of two of delta, delta x
   __shared__ float part[MODE == kCarry ? 1 : 2][kWaves][kTile][64];
   __shared__ __attribute__((aligned(16))) float rows[2][RowTile<Q>::kFloats];
   const int block = MODE == kWhole ? blockIdx.x : blockIdx.y;
@@ -120,9 +120,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
       const bool there = t + j < t1;
       x[o] = load_scalar(&raw.x[o]);
       if (gate) z[o] = load_scalar(&raw.z[o]);
-      const float delta = step_of(load_scalar(&raw.dt[o]) + bias, a.softplus);
-      to[j][lane] = there ? make_float2(delta, delta * x[o]) : make_float2(0.f, 0.f);
-      if (MODE == kCarry && there) gone += delta;
+      const float delta = step_of(load_scalar(&raw.dt[o]) + bias, a.softplus), power = in_powers_of_two(delta);
+      to[j][lane] = there ? make_float2(power, delta * x[o]) : make_float2(0.f, 0.f);
+      if (MODE == kCarry && there) gone += power;
     }
   };
   RowTile<Q> row;
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
-  const float A = a.A[(size_t)c * a.d_state + n] * kLog2e;
+  const float A = a.A[(size_t)c * a.d_state + n];
   const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
   const size_t row = (size_t)NP * a.channels;
   for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
@@ -259,8 +259,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
 // One token of several sequences: LP lanes share a channel's states, four each
 // (VEC: read and written as one vector), and take kRequests of them with all
 // loads on their way together, the channel's rates in registers.  Bound by the
-// states' bytes: 256 x 8192 channels of 16 in a call of 51 us, 5.6 TB/s (with
-// states through the caches 55, and then four requests 56, eight 63); 64 x 4096
+// states' bytes: 256 x 8192 channels of 16 in a call of 49 us, 5.8 TB/s (with
+// states through the caches 4 us more; four requests 1 more, eight 8); 64 x 4096
 // in 11, the kernel 10.
 constexpr int kRequests = 2;
 template <typename T, int LP, bool VEC>
@@ -284,8 +284,6 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   };
   float A[4];
   four(a.A + (size_t)at * N + n0, A);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
   const float bias = a.dt_bias ? a.dt_bias[at] : 0.f, D = a.D ? a.D[at] : 0.f;
   for (int b0 = (int)blockIdx.y * kRequests; b0 < a.n_seq; b0 += gridDim.y * kRequests) {
     float h[kRequests][4], x[kRequests], dt[kRequests], z[kRequests], B[kRequests][4], C[kRequests][4];
@@ -307,11 +305,11 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
     for (int r = 0; r < kRequests; ++r) {
       const int b = b0 + r;
       if (b >= a.n_seq) break;
-      const float delta = step_of(dt[r] + bias, a.softplus), u = delta * x[r];
+      const float delta = step_of(dt[r] + bias, a.softplus), u = delta * x[r], power = in_powers_of_two(delta);
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        h[r][i] = exp2_fast(delta * A[i]) * h[r][i] + u * B[r][i];
+        h[r][i] = exp2_fast(power * A[i]) * h[r][i] + u * B[r][i];
         s += C[r][i] * h[r][i];
       }
 #pragma unroll

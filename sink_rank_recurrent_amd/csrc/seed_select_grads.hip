@@ -72,12 +72,12 @@ __device__ __forceinline__ void tokens_of(const Raw<T, GATE>& r, float bias, boo
   for (int o = 0; o < kOwn; ++o)
     if (o >= there) k[o].delta = k[o].ds = 0.f;
 }
-// delta, delta x and ds as the waves share them.
+// The power of two of delta, delta x and ds as the waves share them.
 struct Shared {
   float2 step[kTile][64];
   float ds[kTile][64];
   __device__ __forceinline__ void put(int j, int lane, const Token& k, bool there) {
-    step[j][lane] = there ? make_float2(k.delta, k.delta * k.x) : make_float2(0.f, 0.f);
+    step[j][lane] = there ? make_float2(in_powers_of_two(k.delta), k.delta * k.x) : make_float2(0.f, 0.f);
     ds[j][lane] = there ? k.ds : 0.f;
   }
 };
@@ -366,9 +366,9 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
           const int t = t0 + j;
           const uint32_t in = (uint32_t)c * sizeof(T);
           if (t >= r.t1) continue;
-          // step and gradient of the read-out from LDS again (the wave's own)
+          // the read-out's gradient from LDS again (the wave's own)
           const Token& k = own[o];
-          const float delta = prep.step[j][lane].x, ds = prep.ds[j][lane];
+          const float ds = prep.ds[j][lane];
           float s = 0.f, du = 0.f, rate = 0.f;
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) {
@@ -377,11 +377,11 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
             du += v.x;
             rate += v.y;
           }
-          const float dv = (k.x * du + rate * kLn2) * k.slope;
+          const float dv = (k.x * du + rate) * k.slope;
           dbias += dv;
           dD += ds * k.x;
           Packed<1, T> out;
-          float one[1] = {delta * du + D * ds};
+          float one[1] = {k.delta * du + D * ds};
           out.from(one);
           out.store(in_row<T>(q->dx.p, q->dx.stride, t, in));
           one[0] = dv;
@@ -405,7 +405,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
           float& to = out[(size_t)(m.wave * Q + i) * a.channels];
-          to = more ? to + dA[i] : dA[i];
+          const float x = dA[i] * kLn2;
+          to = more ? to + x : x;
         }
         if (m.wave < 2) {
           float x = 0.f;
