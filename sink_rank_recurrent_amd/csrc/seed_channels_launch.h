@@ -61,9 +61,9 @@ struct SelectLayout {
   size_t rows;      // [token][group][wave]: B and C of its states in fp32
   size_t carry;     // [slot][state][channel]: what a segment makes of zero, then its first state
   size_t back;      // the same for the gradient: what it passes back from zero, then that at its end
-  size_t gone;      // [slot][channel]: sum of the steps
+  size_t gone;      // [slot][channel]: sum of the scaled steps
   size_t kept;      // [8 tokens][state][channel]: what a segment makes of zero before them (backward)
-  size_t before;    // [8 tokens][channel]: sum of the steps before them
+  size_t before;    // [8 tokens][channel]: sum of the scaled steps before them
   size_t sums;      // [set][token][group][wave]: parts of dB and dC
   size_t weights;   // [part][state, dD, ddt_bias][channel]
   size_t bytes;
