@@ -58,6 +58,12 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _ints(*sizes) -> None:
+    """Refuse sizes that a C int does not hold (ctypes would cut them off)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("a size of more than 2^31 - 1 (tokens, sequences, channels, taps, groups or states)")
+
+
 def _bytes(n: int) -> int:
     if n == ctypes.c_size_t(-1).value:
         raise ValueError(binding.lib().seed_last_error().decode())
@@ -166,8 +172,7 @@ def _lead(x, dims: int, cu_seqlens):
     tokens = 1
     for size in lead:
         tokens *= size
-    if tokens > 0x7fffffff:
-        raise ValueError("more than 2^31 - 1 tokens")
+    _ints(tokens, n_seq)
     return n_seq, tokens, lead
 
 
@@ -175,6 +180,7 @@ def _conv_inputs(x, lead, weight, bias, activation):
     if weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
     channels, width = weight.shape
+    _ints(channels, width)
     _need(weight, "weight", (channels, width), _F32)
     if bias is not None:
         _need(bias, "bias", (channels,), _F32)
@@ -205,8 +211,9 @@ def short_conv_workspace(x, weight, n_seq: int) -> torch.Tensor:
     """A workspace for seed_short_conv_backward calls on x [..., channels] in
     n_seq sequences."""
     channels, width = weight.shape
-    return torch.empty(_bytes(lib().seed_short_conv_workspace_bytes(n_seq, channels, width,
-                                                                    x.shape[:-1].numel())),
+    tokens = x.shape[:-1].numel()
+    _ints(n_seq, channels, width, tokens)
+    return torch.empty(_bytes(lib().seed_short_conv_workspace_bytes(n_seq, channels, width, tokens)),
                        dtype=torch.uint8, device=x.device)
 
 
@@ -245,6 +252,7 @@ def seed_short_conv_step(x, weight, y, S, bias=None, activation="silu", S0=None,
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
+    _ints(lead[0], 0)
     channels, width, shape, xr = _conv_inputs(x, lead, weight, bias, activation)
     yr = _row(y, "y", shape, 1, (x.dtype,))
     _need(S, "S", (lead[0], width - 1, channels), (x.dtype,))
@@ -261,6 +269,7 @@ def _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead):
         raise ValueError("A must be [channels, d_state], B and C [..., groups, d_state]")
     channels, d_state = A.shape
     groups = B.shape[-2]
+    _ints(channels, groups, d_state)
     _need(A, "A", (channels, d_state), _F32)
     if D is not None:
         _need(D, "D", (channels,), _F32)
@@ -283,8 +292,9 @@ def _select_bytes(n_seq, channels, groups, d_state, tokens, backward: bool) -> i
 def selective_scan_workspace(x, B, n_seq: int, backward: bool = False) -> torch.Tensor:
     """A workspace for seed_selective_scan (or seed_selective_scan_backward)
     calls on x [..., channels] and B [..., groups, d_state] in n_seq sequences."""
-    return torch.empty(_select_bytes(n_seq, x.shape[-1], B.shape[-2], B.shape[-1], x.shape[:-1].numel(),
-                                     backward), dtype=torch.uint8, device=x.device)
+    sizes = (n_seq, x.shape[-1], B.shape[-2], B.shape[-1], x.shape[:-1].numel())
+    _ints(*sizes)
+    return torch.empty(_select_bytes(*sizes, backward), dtype=torch.uint8, device=x.device)
 
 
 def seed_selective_scan(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, softplus: bool = True,
@@ -344,6 +354,7 @@ def seed_selective_step(x, dt, A, B, C, y, S, D=None, z=None, dt_bias=None, soft
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
     lead = tuple(x.shape[:1])
+    _ints(lead[0], 0)
     channels, groups, d_state, shape, rows, args = _select_inputs(x, dt, A, B, C, D, z, dt_bias, softplus, lead)
     yr = _row(y, "y", shape, 1, (x.dtype,))
     _need(S, "S", (lead[0], channels, d_state), _F32)
