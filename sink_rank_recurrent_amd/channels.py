@@ -23,7 +23,7 @@ import torch
 
 from . import binding
 from .binding import _F32, _IN, _check, _need, _ptr, _stream
-from .sequence import ACTIVATIONS, _code, _same_device, _workspace
+from .sequence import ACTIVATIONS, _code, _ints, _same_device, _workspace
 
 HEADER_PATH = os.path.join(os.path.dirname(binding.HEADER_PATH), "seed_channels.h")
 
@@ -56,12 +56,6 @@ def lib() -> ctypes.CDLL:
             getattr(L, fn).restype = n
         _lib = L
     return _lib
-
-
-def _ints(*sizes) -> None:
-    """Refuse sizes that a C int does not hold (ctypes would cut them off)."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError("a size of more than 2^31 - 1 (tokens, sequences, channels, taps, groups or states)")
 
 
 def _bytes(n: int) -> int:

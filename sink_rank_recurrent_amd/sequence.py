@@ -67,6 +67,12 @@ def _same_device(**tensors) -> torch.device:
     return torch.device("cuda", first)
 
 
+def _ints(*sizes) -> None:
+    """Refuse sizes that a C int does not hold (ctypes would cut them off)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("a size of more than 2^31 - 1")
+
+
 class _On:
     """The tensors' device made current, where it is not."""
 
@@ -103,8 +109,7 @@ def _scan_shape(rule: str, q, v, cu_seqlens):
     tokens = 1
     for x in lead:
         tokens *= x
-    if tokens > 0x7fffffff:
-        raise ValueError("more than 2^31 - 1 tokens")
+    _ints(tokens, n_seq, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1])
     return n_seq, tokens, lead, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1]
 
 
@@ -146,6 +151,7 @@ def scan_workspace(rule: str, q, v, n_seq: int, backward: bool = False) -> torch
     """A workspace for seed_scan (or seed_scan_backward) calls of these
     shapes: q [..., key_heads, d_k], v [..., heads, d_v] in n_seq sequences."""
     lead = v.shape[:-2].numel()
+    _ints(lead, n_seq, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1])
     return torch.empty(_workspace_bytes(rule, n_seq, v.shape[-2], q.shape[-2], q.shape[-1],
                                         v.shape[-1], lead, backward),
                        dtype=torch.uint8, device=v.device)
@@ -209,6 +215,7 @@ def _norm_inputs(x, gate, io, weight, bias, activation):
         raise ValueError(f"unknown activation {activation!r}")
     shape = tuple(x.shape)
     G, d = shape[-2:]
+    _ints(G, d)
     rows = x.shape[:-2].numel()
     _need(x, "x", shape, _IN)
     if gate is not None:
@@ -251,6 +258,7 @@ def group_norm_workspace(x, weight=None) -> torch.Tensor:
     """A workspace for seed_group_norm_backward calls on x with weights of
     weight's shape (None: shared)."""
     G, d = x.shape[-2:]
+    _ints(G, d)
     n = int(lib().seed_group_norm_workspace_bytes(x.shape[:-2].numel(), G, d,
                                                   weight.shape[0] if weight is not None
                                                   and weight.dim() == 2 else 1))
