@@ -105,7 +105,9 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void 
  * a segment's decay is exp(A sum(delta)).  An exponential is off by about
  * (1 + |delta A|) 2^-23 of its value; decays below 2^-126 are zero.  A NaN or
  * infinity of a token's x, dt or z stays in its channel (of B or C: in its
- * group) and in its sequence; an infinity may come out as NaN.
+ * group) and in its sequence; an infinity may come out as NaN.  A rate of
+ * -infinity is taken as the lowest fp32 number: its states keep nothing over a
+ * step (above 2^-120) but are left by a step of zero; gradients the same.
  * channels a multiple of groups and <= 2^20, d_state 1 .. 64.
  */
 seed_status seed_selective_scan(int n_seq, int channels, int groups, int d_state, int tokens,

@@ -30,6 +30,8 @@
 // states in quarters, 147 with the outer products on the matrix cores, 145 now.
 #pragma once
 
+#include <float.h>
+
 #include "seed_channels.h"
 
 namespace seed {
@@ -93,10 +95,29 @@ __device__ __forceinline__ size_t carry_at(const SelectArgs& a, int of, int n, i
   return ((size_t)of * (4 * Q) + n) * a.channels + c;
 }
 
+// Nothing is moved over this point: what a token needs, in registers or on its
+// way, does not pile up with the other tokens'.
+__device__ __forceinline__ void next_token() { __builtin_amdgcn_sched_barrier(0); }
+// ... and what these have come to is worked out here, not where it is used.
+template <int Q>
+__device__ __forceinline__ void settle(float (&x)[Q]) {
+#pragma unroll
+  for (int i = 0; i < Q; ++i) asm volatile("" : "+v"(x[i]));
+}
+
 // exp(delta A) = 2^(delta log2 e A): the steps are scaled, each with a rounding
 // of its own, and not the rates, whose rounding would be the same in every
 // factor of a product of decays.
 __device__ __forceinline__ float in_powers_of_two(float delta) { return delta * kLog2e; }
+// A rate of -infinity as the lowest number: a step above 2^-120 leaves nothing
+// of a state then, as it would with -infinity, but a step of zero (a tile's
+// tokens behind the sequence's end) leaves it as it is, where 0 (-infinity) is
+// NaN.  One instruction, which keeps a NaN (a comparison and a choice cost the
+// gradients two spilled registers, 627 us for 4 x 2048 x 4096 in place of 624).
+__device__ __forceinline__ float rate_of(float A) { return __builtin_elementwise_maximum(A, -FLT_MAX); }
+// A wave's rates as they lie in memory, and what they are taken as: the latter
+// once the first tile's loads are sent, since it waits (16384 x 2048 in segments
+// 259 us at the rates' load, 255 so).
 template <int Q>
 __device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, float (&A)[Q]) {
 #pragma unroll
@@ -104,6 +125,12 @@ __device__ __forceinline__ void load_rates(const SelectArgs& a, const Mine& m, f
     const int n = m.wave * Q + i;
     A[i] = n < a.d_state ? a.A[(size_t)m.c * a.d_state + n] : 0.f;
   }
+}
+template <int Q>
+__device__ __forceinline__ void take_rates(float (&A)[Q]) {
+  settle(A);
+#pragma unroll
+  for (int i = 0; i < Q; ++i) A[i] = rate_of(A[i]);
 }
 
 // The call's arguments, read again from where the launch put them: pointers and
@@ -212,16 +239,6 @@ __device__ __forceinline__ const T* in_row(const void* p, long long stride, int 
 template <typename T>
 __device__ __forceinline__ T* in_row(void* p, long long stride, int t, uint32_t at) {
   return reinterpret_cast<T*>(static_cast<char*>(p) + (long long)t * stride * (long long)sizeof(T) + at);
-}
-
-// Nothing is moved over this point: what a token needs, in registers or on its
-// way, does not pile up with the other tokens'.
-__device__ __forceinline__ void next_token() { __builtin_amdgcn_sched_barrier(0); }
-// ... and what these have come to is worked out here, not where it is used.
-template <int Q>
-__device__ __forceinline__ void settle(float (&x)[Q]) {
-#pragma unroll
-  for (int i = 0; i < Q; ++i) asm volatile("" : "+v"(x[i]));
 }
 
 template <typename T>

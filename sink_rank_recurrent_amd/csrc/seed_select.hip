@@ -135,6 +135,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
     row.load(m.group, t0 + kTile, t1);
     __syncthreads();
   }
+  take_rates(A);
   int turn = 0;
   for (int t = t0; t < t1; t += kTile, turn ^= 1) {
     load_raw(a, m, t + 2 * kTile, t1, gate, next);
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
-  const float A = a.A[(size_t)c * a.d_state + n];
+  const float A = rate_of(a.A[(size_t)c * a.d_state + n]);
   const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
   const size_t row = (size_t)NP * a.channels;
   for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
@@ -284,6 +285,8 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   };
   float A[4];
   four(a.A + (size_t)at * N + n0, A);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = rate_of(A[i]);
   const float bias = a.dt_bias ? a.dt_bias[at] : 0.f, D = a.D ? a.D[at] : 0.f;
   for (int b0 = (int)blockIdx.y * kRequests; b0 < a.n_seq; b0 += gridDim.y * kRequests) {
     float h[kRequests][4], x[kRequests], dt[kRequests], z[kRequests], B[kRequests][4], C[kRequests][4];

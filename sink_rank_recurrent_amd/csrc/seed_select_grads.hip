@@ -124,6 +124,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
   load_raw(m, r.t0 + kTile, r.t1, raw);
   row.load(m.group, r.t0 + kTile, r.t1);
   __syncthreads();
+  take_rates(A);
   float gone = 0.f;
   int turn = 0;
   for (int t = r.t0; t < r.t1; t += kTile, turn ^= 1) {
@@ -274,6 +275,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
         gone = *in_row<float>(reinterpret_cast<const float*>(q->ws + q->at.before) + tile * channels, 0, 0, in);
       };
       if (!none) load_tile(r.t0 + (tiles - 1) * kTile);
+      take_rates(A);
       for (int p = tiles - 1; p >= 0; --p) {
         const int t0 = r.t0 + p * kTile;
         float first[Q], hs[kTile][Q], d[kTile][Q];
