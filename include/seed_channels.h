@@ -103,7 +103,10 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void 
  * Steps, states and sums are fp32, y is rounded once.  Where a batch has few
  * sequences, they are run in segments that are joined through the workspace;
  * a segment's decay is exp(A sum(delta)).  An exponential is off by about
- * (1 + |delta A|) 2^-23 of its value; decays below 2^-126 are zero.  A NaN or
+ * (1 + |delta A|) 2^-23 of its value; decays below 2^-126, also products of
+ * them, are zero.  States may grow (A delta > 0), by any factor over a segment:
+ * where each step's exponential is finite, and the states (backwards, the
+ * gradients) are with the magnitudes of their terms, so are the results.  A NaN or
  * infinity of a token's x, dt or z stays in its channel (of B or C: in its
  * group) and in its sequence; an infinity may come out as NaN.  A rate of
  * -infinity is taken as the lowest fp32 number: its states keep nothing over a

@@ -239,7 +239,8 @@ def select_backward(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, dy, dS
             du, du_m, du_off = _read(Bc[t], g, M, E, N)
             rate, rate_m = g * a * h0, M * a * M0
             rate_off = a * (E * M0 + M * E0) + rate_m * (a_rel + 2 * u)
-            add("A", d * rate, d * rate_off + d * rate_m * (rel + u), d * rate_m)
+            size = np.abs(d)
+            add("A", d * rate, size * rate_off + size * rate_m * (rel + u), size * rate_m)
             step = x[t] * du + (A * rate).sum(-1)
             step_m = np.abs(x[t]) * du_m + np.abs(A * rate_m).sum(-1)
             step_off = np.abs(x[t]) * du_off + (np.abs(A) * rate_off).sum(-1) + (N + 6) * u * step_m
@@ -247,8 +248,9 @@ def select_backward(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, dy, dS
             ddt_off[t] = slope[t] * (step_off + step_m * (slope_rel[t] + u))
             add("dt_bias", ddt[t], ddt_off[t], slope[t] * step_m)
             dx[t] = delta[t] * du + Dv * ds
-            dx_off[t] = (delta[t] * (du_off + du_m * d_rel[t]) + np.abs(Dv) * ds_off
-                         + 3 * u * (delta[t] * du_m + np.abs(Dv * ds)))
+            size = np.abs(delta[t])
+            dx_off[t] = (size * (du_off + du_m * d_rel[t]) + np.abs(Dv) * ds_off
+                         + 3 * u * (size * du_m + np.abs(Dv * ds)))
             add("D", ds * x[t], ds_off * np.abs(x[t]), np.abs(ds * x[t]))
             g, E, M = a * g, a * E + a * M * (a_rel + u), a * M
         dS0[s], dS0_off[s] = g, E

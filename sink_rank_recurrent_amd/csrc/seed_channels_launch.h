@@ -62,6 +62,7 @@ struct SelectLayout {
   size_t carry;     // [slot][state][channel]: what a segment makes of zero, then its first state
   size_t back;      // the same for the gradient: what it passes back from zero, then that at its end
   size_t gone;      // [slot][channel]: sum of the scaled steps
+  size_t overflow;  // [slot][block of channels][wave]: whether states grew beyond fp32 (backward)
   size_t kept;      // [8 tokens][state][channel]: what a segment makes of zero before them (backward)
   size_t before;    // [8 tokens][channel]: sum of the scaled steps before them
   size_t sums;      // [set][token][group][wave]: parts of dB and dC

@@ -133,6 +133,18 @@ __device__ __forceinline__ void take_rates(float (&A)[Q]) {
   for (int i = 0; i < Q; ++i) A[i] = rate_of(A[i]);
 }
 
+// 2^e h + x.  Where a state grows, e > 127, 2^e overflows before what it makes
+// of a small h does, and is NaN with the zeros that h has before the first
+// input: in two factors then, with h between them.  (2^254 h is infinite for
+// every normal h, and so is 2^e h for e above.)
+__device__ __forceinline__ float grown(float e, float h, float x) {
+  const bool up = e > 127.f;
+  return fmaf(exp2_fast(!up ? e : e < 254.f ? e - 127.f : 127.f), up ? 0x1p127f * h : h, x);
+}
+// Whether states can grow: a step that went through softplus is positive.
+__device__ __forceinline__ bool may_grow(const SelectArgs& a, float A) { return !a.softplus || A > 0.f; }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+
 // The call's arguments, read again from where the launch put them: pointers and
 // strides of a dozen arrays, each used once a tile, would take the scalar
 // registers that the rows of B and C need.

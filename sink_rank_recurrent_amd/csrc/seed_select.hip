@@ -209,21 +209,74 @@ __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   }
 }
 
+// What a segment passes back to its first state, G = a_t (G + ds_t C_t) from its
+// last token on, for a state of a channel: one token after the other.
+template <typename T>
+__device__ __forceinline__ float passed_back(ArgsAgain a, int c, int n, float A, int t0, int t1) {
+  const int Q = a->at.quarter, group = c / (a->channels / a->groups);
+  const float bias = a->dt_bias ? a->dt_bias[c] : 0.f;
+  const float* rows = reinterpret_cast<const float*>(a->ws + a->at.rows) + n / Q * (2 * Q) + Q + n % Q;
+  const uint32_t in = (uint32_t)c * sizeof(T);
+  float G = 0.f;
+#pragma unroll 1
+  for (int t = t1 - 1; t >= t0; --t) {
+    const float delta = step_of(load_scalar(in_row<T>(a->dt.p, a->dt.stride, t, in)) + bias, a->softplus);
+    float ds = load_scalar(in_row<T>(a->dy.p, a->dy.stride, t, in));
+    if (a->z.p) {
+      const float z = load_scalar(in_row<T>(a->z.p, a->z.stride, t, in));
+      ds *= z * sigmoid(z);
+    }
+    G = exp2_fast(in_powers_of_two(delta) * A) * (G + ds * rows[((size_t)t * a->groups + group) * (8 * Q)]);
+  }
+  return G;
+}
+
+// Tokens t0 .. t1 of segment `at` (tiles from `tile` on) in a join with states
+// that grow: the state (or gradient) h before it is left in its place, that
+// behind it returned.  Backwards, where the product of decays overflowed within
+// the segment (seldom, and slow): what it passes back is made again, and the
+// states before its tiles get their part of h here, which is left as zero.
+template <bool BACK>
+__device__ __forceinline__ float join_grown(ArgsAgain a, int c, int n, float A, int at, size_t tile, int t0, int t1,
+                                         bool reverse, bool overflow, float h) {
+  const size_t channels = a->channels, row = 4 * a->at.quarter * channels, own = n * channels + c;
+  const float* gone = reinterpret_cast<const float*>(a->ws + a->at.gone) + c;
+  float* made = reinterpret_cast<float*>(a->ws + (reverse ? a->at.back : a->at.carry)) + at * row + own;
+  float x = *made;
+  *made = h;
+  if (BACK && overflow && reverse) {
+    if (!finite(x)) x = a->bf16 ? passed_back<bf16_t>(a, c, n, A, t0, t1) : passed_back<float>(a, c, n, A, t0, t1);
+  } else if (BACK && overflow) {
+    float* kept = reinterpret_cast<float*>(a->ws + a->at.kept) + tile * row + own;
+    const float* before = reinterpret_cast<const float*>(a->ws + a->at.before) + tile * channels + c;
+#pragma unroll 1
+    for (int t = t0; t < t1; t += kTile, kept += row, before += channels) *kept = grown(A * *before, h, *kept);
+    *made = 0.f;
+  }
+  return grown(A * gone[at * channels], h, x);
+}
+
 // The segments' first states, h' = exp(A gone) h + carry, in the carries'
 // places, and S; backwards also (blockIdx.z's upper half) the gradients at the
 // segments' ends, G' = exp(A gone) G + back, in theirs, and dS0.  A thread is a
 // state of a channel of a sequence; the values of kAhead segments are on their
 // way together.  Bound by latency, its sequence's segments in turn: 64 of one
-// sequence of 2048 channels of 16 states in 11 us, 4 x 16 of 4096 backward in 17.
+// sequence of 2048 channels of 16 states in 12 us, 4 x 16 of 4096 backward in 20
+// (17 without the way for states that grow, which takes scalar registers; eight
+// waves a SIMD, with six 22).
 constexpr int kAhead = 8;
 template <bool BACK>
-__global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
   const float A = rate_of(a.A[(size_t)c * a.d_state + n]);
   const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
   const size_t row = (size_t)NP * a.channels;
+  // of the channel's block and the state's wave
+  const int each = a.channels / a.groups, across = a.groups * a.at.blocks * kWaves;
+  const int* overflow = reinterpret_cast<const int*>(a.ws + a.at.overflow) +
+                        (c / each * a.at.blocks + c % each / 64) * kWaves + n / a.at.quarter;
   for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
     const int first = first_run(b, s), lo = first_token(b, s);
     const int end = b.cu ? first_token(b, s + 1) : lo + b.len;
@@ -242,11 +295,29 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SelectArgs a) {
         g[j] = gone[(size_t)at * a.channels];
         x[j] = made[(size_t)at * row];
       }
+      if (__any(may_grow(a, A))) {   // (looked at here: the rate has come with the others)
+        bool grows = false;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int at = from + way * (r + j < runs ? r + j : runs - 1);
+          grows |= A * g[j] > 127.f || (BACK && may_grow(a, A) && overflow[(size_t)at * across]);
+        }
+        if (__any(grows)) {
+#pragma unroll 1
+          for (int j = 0; j < kAhead && r + j < runs; ++j) {
+            const int at = from + way * (r + j), t0 = lo + ((at - first) << a.at.shift);
+            const int t1 = end - t0 > (1 << a.at.shift) ? t0 + (1 << a.at.shift) : end;
+            h = join_grown<BACK>(args_again(), c, n, A, at, (size_t)(lo >> 3) + s + ((t0 - lo) >> 3), t0, t1, reverse,
+                                 BACK && may_grow(a, A) && overflow[(size_t)at * across], h);
+          }
+          continue;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (r + j >= runs) break;
         made[(size_t)(from + way * (r + j)) * row] = h;
-        h = exp2_fast(A * g[j]) * h + x[j];
+        h = fmaf(exp2_fast(A * g[j]), h, x[j]);
       }
     }
     if (reverse) {
@@ -402,6 +473,7 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
     while (l.set > 1 && (long long)l.slots * groups * ((l.blocks + l.set - 1) / l.set) < 4096) l.set /= 2;
     l.sets = (l.blocks + l.set - 1) / l.set;
     l.back = take(l.slots * NP * C * 4);
+    l.overflow = take((size_t)l.slots * along * kWaves * 4);
     l.kept = take(tiles * NP * C * 4);
     l.before = take(tiles * C * 4);
     l.sums = take(l.sets * T * groups * 2 * NP * 4);

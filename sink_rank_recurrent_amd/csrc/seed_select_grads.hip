@@ -87,9 +87,11 @@ __device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (siz
 
 // Tiles of 8 tokens as in the forward pass.  The decays' product P goes with
 // the states, so that both directions' ends come out of one walk with one
-// exponential a state.  Bound by the vector unit: 4 x 2048 tokens x 4096 channels
-// of 16 states, bf16, in 190 us, busy 86 % with four-cycle instructions, 98 %
-// with all.
+// exponential a state.  P starts at two: where it does not overflow, 2^(A gone)
+// does not either, with a power of two between for the roundings; where it does,
+// what is passed back is infinite or NaN from there on, which the join finds
+// marked.  Bound by the vector unit: 4 x 2048 tokens x 4096 channels of 16 states,
+// bf16, in 190 us, busy 86 % with four-cycle instructions, 98 % with all.
 template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_kernel(SelectArgs a) {
   __shared__ Shared prep[2];
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     h[i] = G[i] = 0.f;
-    P[i] = 1.f;
+    P[i] = 2.f;
   }
   Raw<T, GATE> raw;
   auto prepare = [&](int t, Shared& to) {
@@ -175,6 +177,18 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_ke
     raw = next;
     row = next_row;
     __syncthreads();
+  }
+  bool over = false, may = false;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    G[i] *= 0.5f;
+    over |= !finite(G[i]);
+    may |= may_grow(a, A[i]);
+  }
+  if (__any(may)) {
+    const bool any = __any(over);
+    if (lane == 0)
+      reinterpret_cast<int*>(a.ws + a.at.overflow)[((size_t)slot * gridDim.y + blockIdx.y) * kWaves + m.wave] = any;
   }
   if (!m.live) return;
   float* carry = reinterpret_cast<float*>(a.ws + a.at.carry);
@@ -280,7 +294,8 @@ __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_k
         const int t0 = r.t0 + p * kTile;
         float first[Q], hs[kTile][Q], d[kTile][Q];
 #pragma unroll
-        for (int i = 0; i < Q; ++i) first[i] = exp2_fast(gone * A[i]) * H[i] + made[i];
+        for (int i = 0; i < Q; ++i)   // (from 2^127.75 on H is zero, and `made` all of the state)
+          first[i] = fmaf(exp2_fast(__builtin_elementwise_minimum(gone * A[i], 127.75f)), H[i], made[i]);
         Token own[kOwn];
         const int at = t0 + m.wave * kOwn;
         tokens_of<true>(raw, bias, args_again()->softplus, r.t1 - at, own);
