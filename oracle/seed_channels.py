@@ -184,7 +184,8 @@ def select(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, io_u=0.0):
 def select_backward(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, dy, dS, depth, io_u=0.0):
     """{name: (gradient, bound)} of x, dt, A, B, C, D, z, dt_bias, S0 (NaN in
     rows outside the sequences); `depth`: additions in a row of the sums over
-    tokens and over channels."""
+    tokens and of those over channels (one number: of both)."""
+    over_tokens, over_channels = depth if isinstance(depth, tuple) else (depth, depth)
     T, channels = x.shape
     N, n, G = A.shape[1], len(offsets) - 1, B.shape[1]
     delta, d_rel, slope, slope_rel, v, runs = _forward(x, dt, A, B, dt_bias, softplus, S0, offsets)
@@ -232,10 +233,10 @@ def select_backward(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, dy, dS
             E = E + u * M
             dC[t] = over(ds[:, None] * h)
             dC_off[t] = over(np.abs(ds)[:, None] * Eh + ds_off[:, None] * np.abs(h)
-                             + (depth + 1) * u * np.abs(ds[:, None] * h))
+                             + (over_channels + 1) * u * np.abs(ds[:, None] * h))
             put = d * x[t][:, None]
             dB[t] = over(g * put)
-            dB_off[t] = over(np.abs(put) * (E + M * (rel + (depth + 2) * u)))
+            dB_off[t] = over(np.abs(put) * (E + M * (rel + (over_channels + 2) * u)))
             du, du_m, du_off = _read(Bc[t], g, M, E, N)
             rate, rate_m = g * a * h0, M * a * M0
             rate_off = a * (E * M0 + M * E0) + rate_m * (a_rel + 2 * u)
@@ -258,7 +259,7 @@ def select_backward(x, dt, A, B, C, D, z, dt_bias, softplus, S0, offsets, dy, dS
     def io(value, off):
         return value, off + io_u * (np.abs(np.nan_to_num(value)) + off)
 
-    out = {k: (a, e + (depth + 1) * u * m) for k, (a, e, m) in sums.items()}
+    out = {k: (a, e + (over_tokens + 1) * u * m) for k, (a, e, m) in sums.items()}
     out.update(x=io(dx, dx_off), dt=io(ddt, ddt_off), z=io(dz, dz_off), B=io(dB, dB_off), C=io(dC, dC_off),
                S0=(dS0, dS0_off))
     return out
