@@ -59,8 +59,8 @@ __device__ __forceinline__ int ranked(const Batch& b, int number) {
     const int other = __builtin_amdgcn_readlane(len, s);
     longer += other > len || (other == len && s < lane);
   }
-  const uint64_t found = __ballot(lane < count && longer == rank);   // one: ranks differ
-  return found ? set + __builtin_ctzll(found) * sets : number;
+  // one lane: the ranks are 0 .. count - 1
+  return set + __builtin_ctzll(__ballot(lane < count && longer == rank)) * sets;
 }
 
 // MODE kWhole: a sequence from its first state to its last; kCarry: what a
