@@ -231,6 +231,17 @@ __device__ __forceinline__ float passed_back(ArgsAgain a, int c, int n, float A,
   return G;
 }
 
+// Whether states of n's wave and c's block overflowed, by segment.
+struct Overflow {
+  const int* found;
+  size_t across;
+  __device__ __forceinline__ Overflow(ArgsAgain a, int c, int n) : across((size_t)a->groups * a->at.blocks * kWaves) {
+    const int each = a->channels / a->groups, block = c / each * a->at.blocks + c % each / 64;
+    found = reinterpret_cast<const int*>(a->ws + a->at.overflow) + (size_t)block * kWaves + n / a->at.quarter;
+  }
+  __device__ __forceinline__ bool operator[](int at) const { return found[at * across] != 0; }
+};
+
 // Tokens t0 .. t1 of segment `at` (tiles from `tile` on) in a join with states
 // that grow: the state (or gradient) h before it is left in its place, that
 // behind it returned.  Backwards, where the product of decays overflowed within
@@ -238,7 +249,7 @@ __device__ __forceinline__ float passed_back(ArgsAgain a, int c, int n, float A,
 // states before its tiles get their part of h here, which is left as zero.
 template <bool BACK>
 __device__ __forceinline__ float join_grown(ArgsAgain a, int c, int n, float A, int at, size_t tile, int t0, int t1,
-                                         bool reverse, bool overflow, float h) {
+                                            bool reverse, bool overflow, float h) {
   const size_t channels = a->channels, row = 4 * a->at.quarter * channels, own = n * channels + c;
   const float* gone = reinterpret_cast<const float*>(a->ws + a->at.gone) + c;
   float* made = reinterpret_cast<float*>(a->ws + (reverse ? a->at.back : a->at.carry)) + at * row + own;
@@ -261,7 +272,7 @@ __device__ __forceinline__ float join_grown(ArgsAgain a, int c, int n, float A, 
 // segments' ends, G' = exp(A gone) G + back, in theirs, and dS0.  A thread is a
 // state of a channel of a sequence; the values of kAhead segments are on their
 // way together.  Bound by latency, its sequence's segments in turn: 64 of one
-// sequence of 2048 channels of 16 states in 12 us, 4 x 16 of 4096 backward in 20
+// sequence of 2048 channels of 16 states in 12 us, 4 x 16 of 4096 backward in 19
 // (17 without the way for states that grow, which takes scalar registers; eight
 // waves a SIMD, with six 22).
 constexpr int kAhead = 8;
@@ -273,10 +284,6 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
   const float A = rate_of(a.A[(size_t)c * a.d_state + n]);
   const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
   const size_t row = (size_t)NP * a.channels;
-  // of the channel's block and the state's wave
-  const int each = a.channels / a.groups, across = a.groups * a.at.blocks * kWaves;
-  const int* overflow = reinterpret_cast<const int*>(a.ws + a.at.overflow) +
-                        (c / each * a.at.blocks + c % each / 64) * kWaves + n / a.at.quarter;
   for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
     const int first = first_run(b, s), lo = first_token(b, s);
     const int end = b.cu ? first_token(b, s + 1) : lo + b.len;
@@ -298,9 +305,11 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
       if (__any(may_grow(a, A))) {   // (looked at here: the rate has come with the others)
         bool grows = false;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int at = from + way * (r + j < runs ? r + j : runs - 1);
-          grows |= A * g[j] > 127.f || (BACK && may_grow(a, A) && overflow[(size_t)at * across]);
+        for (int j = 0; j < kAhead; ++j) grows |= A * g[j] > 127.f;
+        if (BACK && may_grow(a, A)) {
+          const Overflow overflow(args_again(), c, n);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) grows |= overflow[from + way * (r + j < runs ? r + j : runs - 1)];
         }
         if (__any(grows)) {
 #pragma unroll 1
@@ -308,7 +317,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
             const int at = from + way * (r + j), t0 = lo + ((at - first) << a.at.shift);
             const int t1 = end - t0 > (1 << a.at.shift) ? t0 + (1 << a.at.shift) : end;
             h = join_grown<BACK>(args_again(), c, n, A, at, (size_t)(lo >> 3) + s + ((t0 - lo) >> 3), t0, t1, reverse,
-                                 BACK && may_grow(a, A) && overflow[(size_t)at * across], h);
+                                 BACK && may_grow(a, A) && Overflow(args_again(), c, n)[at], h);
           }
           continue;
         }
