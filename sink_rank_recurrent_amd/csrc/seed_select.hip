@@ -71,9 +71,9 @@ __device__ __forceinline__ int ranked(const Batch& b, int number) {
 // LDS, and each adds up the four waves' read-outs of its two; the loads of two
 // tiles are on their way.  One barrier a tile.  Bound by the vector unit's
 // issue slots: kWhole, 24 ragged sequences of 7919 tokens x 4096 channels of 16
-// states, bf16: 145 us with all launches, the unit busy 85 % of the cycles with
+// states, bf16: 147 us with all launches, the unit busy 86 % of the cycles with
 // four-cycle instructions and 99 % with all (1.9 TB/s).  In segments, 16384 x
-// 2048, fp32: kCarry 120 us (76 and 92 %), kRead 155 (76 and 89 %), 262 in all.
+// 2048, fp32: kCarry 115 us (78 and 94 %), kRead 135 (78 and 90 %), 264 in all.
 template <typename T, int Q, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_kernel(SelectArgs a) {
   __shared__ float2 prep[2][kTile][64];                           // the power of two of delta, delta x
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
   const int c = (int)blockIdx.x * kThreads + threadIdx.x, n = blockIdx.y, NP = 4 * a.at.quarter;
   if (c >= a.channels) return;
   const Batch b = batch_of(a.cu, a.n_seq, a.tokens, a.at.shift);
-  const float A = rate_of(a.A[(size_t)c * a.d_state + n]);
+  float A[1] = {a.A[(size_t)c * a.d_state + n]};
   const bool reverse = BACK && blockIdx.z >= gridDim.z / 2;
   const size_t row = (size_t)NP * a.channels;
   for (int s = reverse ? blockIdx.z - gridDim.z / 2 : blockIdx.z; s < a.n_seq; s += BACK ? gridDim.z / 2 : gridDim.z) {
@@ -302,11 +302,13 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
         g[j] = gone[(size_t)at * a.channels];
         x[j] = made[(size_t)at * row];
       }
-      if (__any(may_grow(a, A))) {   // (looked at here: the rate has come with the others)
+      take_rates(A);                    // (here: it has come with the others)
+      const float rate = A[0];
+      if (__any(may_grow(a, rate))) {
         bool grows = false;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) grows |= A * g[j] > 127.f;
-        if (BACK && may_grow(a, A)) {
+        for (int j = 0; j < kAhead; ++j) grows |= rate * g[j] > 127.f;
+        if (BACK && may_grow(a, rate)) {
           const Overflow overflow(args_again(), c, n);
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) grows |= overflow[from + way * (r + j < runs ? r + j : runs - 1)];
@@ -316,8 +318,8 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
           for (int j = 0; j < kAhead && r + j < runs; ++j) {
             const int at = from + way * (r + j), t0 = lo + ((at - first) << a.at.shift);
             const int t1 = end - t0 > (1 << a.at.shift) ? t0 + (1 << a.at.shift) : end;
-            h = join_grown<BACK>(args_again(), c, n, A, at, (size_t)(lo >> 3) + s + ((t0 - lo) >> 3), t0, t1, reverse,
-                                 BACK && may_grow(a, A) && Overflow(args_again(), c, n)[at], h);
+            h = join_grown<BACK>(args_again(), c, n, rate, at, (size_t)(lo >> 3) + s + ((t0 - lo) >> 3), t0, t1, reverse,
+                                 BACK && may_grow(a, rate) && Overflow(args_again(), c, n)[at], h);
           }
           continue;
         }
@@ -326,7 +328,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
       for (int j = 0; j < kAhead; ++j) {
         if (r + j >= runs) break;
         made[(size_t)(from + way * (r + j)) * row] = h;
-        h = fmaf(exp2_fast(A * g[j]), h, x[j]);
+        h = fmaf(exp2_fast(rate * g[j]), h, x[j]);
       }
     }
     if (reverse) {
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(SelectArgs a) {
 // loads on their way together, the channel's rates in registers.  Bound by the
 // states' bytes: 256 x 8192 channels of 16 in a call of 49 us, 5.8 TB/s (with
 // states through the caches 4 us more; four requests 1 more, eight 8); 64 x 4096
-// in 11, the kernel 10.
+// in 11, the kernel 9.
 constexpr int kRequests = 2;
 template <typename T, int LP, bool VEC>
 __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
@@ -365,8 +367,6 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
   };
   float A[4];
   four(a.A + (size_t)at * N + n0, A);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = rate_of(A[i]);
   const float bias = a.dt_bias ? a.dt_bias[at] : 0.f, D = a.D ? a.D[at] : 0.f;
   for (int b0 = (int)blockIdx.y * kRequests; b0 < a.n_seq; b0 += gridDim.y * kRequests) {
     float h[kRequests][4], x[kRequests], dt[kRequests], z[kRequests], B[kRequests][4], C[kRequests][4];
@@ -384,6 +384,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SelectArgs a) {
         C[r][i] = VEC || n0 + i < N ? load_scalar(pC + i) : 0.f;
       }
     }
+    take_rates(A);   // behind the loads' sending, since it waits (before it 51.2 us, 49.5 so)
 #pragma unroll
     for (int r = 0; r < kRequests; ++r) {
       const int b = b0 + r;
@@ -454,7 +455,10 @@ SelectLayout select_layout(int n_seq, int channels, int groups, int d_state, int
   // 210; 4 x 2048 364 and 274; 1 x 128 31 and 32; 1 x 512 96 and 45.
   // Segments of 256 tokens, and shorter ones where that leaves fewer than 2048
   // workgroups: 16384 x 2048 284 (128 tokens 297, 512 341), 4096 x 4096 185 (128
-  // tokens 156, 64 162), 512 x 4096 81 (128 tokens 58, 64 45).
+  // tokens 156, 64 162), 512 x 4096 81 (128 tokens 58, 64 45).  The lengths
+  // themselves are on the device: one sequence that is much longer than the mean
+  // of many is walked from end to end (4096 channels, 8192 tokens and 63 of one
+  // each: 1430 us; alone, in segments, 291).
   if (backward) l.shift = kBackShift;
   else if (n_seq * along >= 384 || tokens / n_seq <= 128) l.shift = -1;
   else
