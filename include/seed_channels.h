@@ -101,16 +101,21 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void 
  *   softplus     softplus(v) = log(1 + exp(v)), or 0: v itself
  *
  * Steps, states and sums are fp32, y is rounded once.  Where a batch has few
- * sequences, they are run in segments that are joined through the workspace;
- * a segment's decay is exp(A sum(delta)).  An exponential is off by about
- * (1 + |delta A|) 2^-23 of its value; decays below 2^-126, also products of
- * them, are zero.  States may grow (A delta > 0), by any factor over a segment:
- * where each step's exponential is finite, and the states (backwards, the
- * gradients) are with the magnitudes of their terms, so are the results.  A NaN or
- * infinity of a token's x, dt or z stays in its channel (of B or C: in its
- * group) and in its sequence; an infinity may come out as NaN.  A rate of
- * -infinity is taken as the lowest fp32 number: its states keep nothing over a
- * step (above 2^-120) but are left by a step of zero; gradients the same.
+ * sequences, they are run in segments that are joined through the workspace; a
+ * segment's decay is exp(A sum(delta)).  The choice goes by the number of
+ * sequences and their mean length: one that is much longer than the many others
+ * of its batch is run from end to end (0.18 us a token), and is faster in a call
+ * of its own.
+ *
+ * An exponential is off by about (1 + |delta A|) 2^-23 of its value; decays below
+ * 2^-126, also products of them, are zero.  States may grow (A delta > 0), by any
+ * factor over a segment: where each step's exponential is finite, and the states
+ * (backwards, the gradients) are with the magnitudes of their terms, so are the
+ * results.  A rate of -infinity is taken as the lowest fp32 number: its states
+ * keep nothing over a step (above 2^-120) but are left by a step of zero;
+ * gradients the same.  A NaN or infinity of a token's x, dt or z stays in its
+ * channel (of B or C: in its group) and in its sequence; an infinity may come out
+ * as NaN.
  * channels a multiple of groups and <= 2^20, d_state 1 .. 64.
  */
 seed_status seed_selective_scan(int n_seq, int channels, int groups, int d_state, int tokens,

@@ -9,7 +9,8 @@ namespace seed {
 namespace channels {
 
 // 1 / (1 + 2^(-x log2 e)) by the hardware's exponential and reciprocal (one
-// ulp each; the argument's rounding is |x| 2^-24 of the exponential).
+// ulp each; of the exponential the argument's rounding is at most |x| 2^-24, and
+// the constant's, 1.3e-8 of itself, |x| 1.3e-8).
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }

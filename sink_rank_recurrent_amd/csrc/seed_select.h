@@ -27,7 +27,7 @@
 // the vector unit bounds the scan, and what is not done for each state has to
 // be shared or taken off it.  us for 7919 ragged tokens x 4096 channels of 16
 // states, bf16, forward: 770 with a wave's channels to itself, 243 with the
-// states in quarters, 147 with the outer products on the matrix cores, 145 now.
+// states in quarters, 147 with the outer products on the matrix cores and now.
 #pragma once
 
 #include <float.h>
@@ -42,7 +42,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 8;        // tokens that go through LDS together
 constexpr int kOwn = kTile / kWaves;   // of them prepared by one wave
 // log2 of the tokens of a segment of the backward pass: 4 x 2048 tokens x 4096,
-// bf16, 640 us then (64 tokens 661, 256 tokens 797), now 623; 3001 x 2050, fp32,
+// bf16, 640 us then (64 tokens 661, 256 tokens 797), now 636; 3001 x 2050, fp32,
 // 115 then (120, 204), now 110.
 constexpr int kBackShift = 7;
 constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
@@ -107,7 +107,9 @@ __device__ __forceinline__ void settle(float (&x)[Q]) {
 
 // exp(delta A) = 2^(delta log2 e A): the steps are scaled, each with a rounding
 // of its own, and not the rates, whose rounding would be the same in every
-// factor of a product of decays.
+// factor of a product of decays.  The constant's own, 1.3e-8 of every exponent,
+// is: of a product of decays it takes 1.3e-8 of its logarithm, a fifth of a
+// rounding's half step.
 __device__ __forceinline__ float in_powers_of_two(float delta) { return delta * kLog2e; }
 // A rate of -infinity as the lowest number: a step above 2^-120 leaves nothing
 // of a state then, as it would with -infinity, but a step of zero (a tile's

@@ -91,7 +91,7 @@ __device__ __forceinline__ size_t tile_number(const Run& r, int t) { return (siz
 // does not either, with a power of two between for the roundings; where it does,
 // what is passed back is infinite or NaN from there on, which the join finds
 // marked.  Bound by the vector unit: 4 x 2048 tokens x 4096 channels of 16 states,
-// bf16, in 190 us, busy 86 % with four-cycle instructions, 98 % with all.
+// bf16, in 163 us, busy 87 % with four-cycle instructions, 98 % with all.
 template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads, Q <= 4 ? 4 : Q <= 8 ? 2 : 1) void ends_kernel(SelectArgs a) {
   __shared__ Shared prep[2];
@@ -233,11 +233,11 @@ __device__ __forceinline__ float fold16(float (&v)[16]) {
 // A set of blocks of channels of one group (blockIdx.y) over every
 // gridDim.x-th segment.  A wave keeps 8 tokens' decays and states of a quarter
 // in registers (three waves a SIMD), from the kept state before them, so that
-// nothing runs backwards through a decay.  Bound by the vector unit: 86
+// nothing runs backwards through a decay.  Bound by the vector unit: 87
 // instructions a token of four states, 46 of them the states' own formulas, 18
 // the sums of dB and dC over the lanes, the others the tokens' own (softplus,
 // gate, dx, ddt, dz), which the waves share.  4 x 2048 tokens x 4096 channels,
-// bf16: 490 us, busy 78 % with four-cycle instructions, 88 % with all.
+// bf16: 425 us, busy 80 % with four-cycle instructions, 90 % with all.
 template <typename T, int Q, bool GATE>
 __global__ __launch_bounds__(kThreads, Q <= 4 ? 3 : Q <= 8 ? 2 : 1) void grads_kernel(SelectArgs a) {
   // dB and dC of 8 tokens and a wave's states are summed over the lanes 16

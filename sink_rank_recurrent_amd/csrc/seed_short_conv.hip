@@ -91,9 +91,10 @@ __device__ __forceinline__ Run tokens_of(const Batch& b, int run) {
   return run_of(b, s, run);
 }
 
-// 64 x 512 tokens x 2048 channels, bf16, 4 taps, SiLU: 52 us, 5.2 TB/s of the
-// 6.1 that a large copy reaches (vector unit 48 %).  33 tokens: 6.5 us of a call
-// of 8, bound by the launch and one row's latency.
+// 64 x 512 tokens x 2048 channels, bf16, 4 taps, SiLU: 60 us, 4.5 TB/s of the
+// 6.1 that a large copy reaches (52 where the memory-side cache still has part of
+// the arrays; vector unit 47 %).  33 tokens: 5.6 us of a call of 8, bound by the
+// launch and one row's latency.
 template <int K, int VW, bool ONE, typename T>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, int runs, int tx) {
   constexpr int R = kRows<K>;
@@ -153,8 +154,10 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int shift, i
 // A block's threads take kThreads / tx runs at a time and keep their parts of
 // the weights' gradients in registers; the block adds them up in order through
 // LDS, and sums_kernel the blocks' parts.  The pre-activations are made again:
-// 4 x 2048 tokens x 4096 channels, bf16, 4 taps, SiLU: 49 us, 4.1 TB/s, the
-// vector unit busy 67 %; with the sums' launch 61.
+// 4 x 2048 tokens x 4096 channels, bf16, 4 taps, SiLU: 56 us, 3.6 TB/s (46 where
+// the memory-side cache still has the arrays), the vector unit busy 66 %; 1040
+// workgroups where registers leave room for 768 at once, so that the second round
+// is mostly empty; with the sums' launch 61.
 template <int K, int VW, bool ONE, typename T>
 __global__ __launch_bounds__(kThreads) void conv_backward_kernel(ConvArgs a, int shift, int runs, int tx) {
   constexpr int R = kBackRows<K>;
