@@ -102,10 +102,10 @@ seed_status seed_short_conv_step(int batch, int channels, int width, const void 
  *
  * Steps, states and sums are fp32, y is rounded once.  Where a batch has few
  * sequences, they are run in segments that are joined through the workspace; a
- * segment's decay is exp(A sum(delta)).  The choice goes by the number of
- * sequences and their mean length: one that is much longer than the many others
- * of its batch is run from end to end (0.18 us a token), and is faster in a call
- * of its own.
+ * segment's decay is exp(A sum(delta)), off by at most |A sum(delta)| 2^-17 of
+ * its value.  The choice goes by the number of sequences and their mean length:
+ * one that is much longer than the many others of its batch is run from end to
+ * end (0.18 us a token), and is faster in a call of its own.
  *
  * An exponential is off by about (1 + |delta A|) 2^-23 of its value; decays below
  * 2^-126, also products of them, are zero.  States may grow (A delta > 0), by any
